@@ -390,6 +390,48 @@ hg_status grouped_gemm(const uint8_t* a_fp8, const uint8_t* a_scale, bool a_scal
                : HG_ERR_CUDA;
 }
 
+// Limits of the few-token form: its block lists the slots by expert in shared
+// memory, and holds one input row there.
+constexpr int32_t kMatvecMaxSlots = 512;
+constexpr int32_t kMatvecMaxK = 32768;
+
+hg_status expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* topk_ids,
+                        const uint8_t* w_fp4, const uint8_t* w_scale, int32_t M, int32_t top_k,
+                        int32_t E, int32_t N, int32_t K, bool swiglu, uint16_t* out,
+                        hg_stream_t stream) {
+    if (M < 0 || top_k < 1 || E < 1 || N < 1 || K < 1) return HG_ERR_INVALID_ARG;
+    const long long slots = static_cast<long long>(M) * top_k;
+    if (x_rows != M && x_rows != slots) return HG_ERR_INVALID_ARG;
+    if (K % 128 != 0 || K > kMatvecMaxK || (swiglu && N % 2 != 0) || slots > kMatvecMaxSlots)
+        return HG_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<long long>(E) * N > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (!w_fp4 || !w_scale) return HG_ERR_INVALID_ARG;
+    if (!aligned(w_fp4, 32) || !aligned(w_scale, 4)) return HG_ERR_INVALID_ARG;
+    if (M == 0) return HG_OK;
+    if (!x_bf16 || !topk_ids || !out) return HG_ERR_INVALID_ARG;
+    if (!aligned(x_bf16, 16) || !aligned(topk_ids, 4) || !aligned(out, 2))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    MatvecArgs a;
+    a.x = x_bf16;
+    a.slots_per_row = x_rows == M ? top_k : 1;
+    a.ids = topk_ids;
+    a.w_fp4 = w_fp4;
+    a.w_scale = w_scale;
+    a.slots = static_cast<int>(slots);
+    a.E = E;
+    a.N = N;
+    a.K = K;
+    a.swiglu = swiglu;
+    a.out = out;
+    return launch_expert_matvec(a, d->num_sms, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -466,6 +508,164 @@ hg_status hg_combine_topk(const uint16_t* y_bf16, const int32_t* src_to_sorted,
     if (st != HG_OK) return st;
     return launch_combine_topk(y_bf16, src_to_sorted, topk_weights, M, top_k, N, out_bf16,
                                d->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status hg_dispatch_tokens(const uint16_t* x_bf16, const int32_t* src_to_sorted,
+                             const float* topk_weights, int32_t M, int32_t top_k, int32_t K,
+                             uint16_t* rows_bf16, hg_stream_t stream) {
+    if (M < 0 || top_k < 1 || K < 1) return HG_ERR_INVALID_ARG;
+    if (K % 8 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<long long>(M) * top_k > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return HG_OK;
+    if (!x_bf16 || !src_to_sorted || !rows_bf16) return HG_ERR_INVALID_ARG;
+    if (!aligned(x_bf16, 16) || !aligned(rows_bf16, 16) || !aligned(src_to_sorted, 4) ||
+        !aligned(topk_weights, 4))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    return launch_dispatch(x_bf16, src_to_sorted, topk_weights, M, top_k, K, rows_bf16, d->num_sms,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status hg_dispatch_tokens_bwd(const uint16_t* drows_bf16, const uint16_t* x_bf16,
+                                 const int32_t* src_to_sorted, const float* topk_weights,
+                                 int32_t M, int32_t top_k, int32_t K, uint16_t* dx_bf16,
+                                 float* dweights, hg_stream_t stream) {
+    if (M < 0 || top_k < 1 || K < 1) return HG_ERR_INVALID_ARG;
+    if (K % 8 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<long long>(M) * top_k > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
+    if ((x_bf16 == nullptr) != (dweights == nullptr)) return HG_ERR_INVALID_ARG;
+    if (M == 0) return HG_OK;
+    if (!drows_bf16 || !src_to_sorted || !dx_bf16) return HG_ERR_INVALID_ARG;
+    if (!aligned(drows_bf16, 16) || !aligned(x_bf16, 16) || !aligned(dx_bf16, 16) ||
+        !aligned(src_to_sorted, 4) || !aligned(topk_weights, 4) || !aligned(dweights, 4))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    return launch_dispatch_bwd(drows_bf16, x_bf16, src_to_sorted, topk_weights, M, top_k, K,
+                               dx_bf16, dweights, d->num_sms,
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status hg_combine_topk_bwd(const uint16_t* dout_bf16, const uint16_t* y_bf16,
+                              const int32_t* src_to_sorted, const float* topk_weights, int32_t M,
+                              int32_t top_k, int32_t N, uint16_t* dy_bf16, float* dweights,
+                              hg_stream_t stream) {
+    if (M < 0 || top_k < 1 || N < 1) return HG_ERR_INVALID_ARG;
+    if (N % 8 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<long long>(M) * top_k > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return HG_OK;
+    if (!dout_bf16 || !y_bf16 || !src_to_sorted || !topk_weights || !dy_bf16 || !dweights)
+        return HG_ERR_INVALID_ARG;
+    if (!aligned(dout_bf16, 16) || !aligned(y_bf16, 16) || !aligned(dy_bf16, 16) ||
+        !aligned(src_to_sorted, 4) || !aligned(topk_weights, 4) || !aligned(dweights, 4))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    return launch_combine_bwd(dout_bf16, y_bf16, src_to_sorted, topk_weights, M, top_k, N, dy_bf16,
+                              dweights, d->num_sms,
+                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status hg_swiglu_quantize(const uint16_t* z_bf16, int32_t rows, int32_t F, uint8_t* a_fp8,
+                             uint8_t* a_scale, uint8_t* z_fp8, uint8_t* z_scale,
+                             hg_stream_t stream) {
+    if (rows < 0 || F < 1) return HG_ERR_INVALID_ARG;
+    if (F % 128 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if ((z_fp8 == nullptr) != (z_scale == nullptr)) return HG_ERR_INVALID_ARG;
+    if (rows == 0) return HG_OK;
+    if (!z_bf16 || !a_fp8 || !a_scale) return HG_ERR_INVALID_ARG;
+    if (!aligned(z_bf16, 16) || !aligned(a_fp8, 16) || !aligned(z_fp8, 16))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    return launch_swiglu_quantize(z_bf16, rows, F, a_fp8, a_scale, z_fp8, z_scale, d->num_sms,
+                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status hg_swiglu_bwd(const uint16_t* dh_bf16, const uint8_t* z_fp8, const uint8_t* z_scale,
+                        int32_t rows, int32_t F, uint16_t* dz_bf16, hg_stream_t stream) {
+    if (rows < 0 || F < 1) return HG_ERR_INVALID_ARG;
+    if (F % 128 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return HG_OK;
+    if (!dh_bf16 || !z_fp8 || !z_scale || !dz_bf16) return HG_ERR_INVALID_ARG;
+    if (!aligned(dh_bf16, 16) || !aligned(z_fp8, 16) || !aligned(dz_bf16, 16))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    return launch_swiglu_bwd(dh_bf16, z_fp8, z_scale, rows, F, dz_bf16, d->num_sms,
+                             reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status hg_expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* topk_ids,
+                           const uint8_t* w_fp4, const uint8_t* w_scale, int32_t M, int32_t top_k,
+                           int32_t E, int32_t N, int32_t K, uint16_t* y_bf16,
+                           hg_stream_t stream) {
+    return expert_matvec(x_bf16, x_rows, topk_ids, w_fp4, w_scale, M, top_k, E, N, K, false,
+                         y_bf16, stream);
+}
+
+hg_status hg_expert_matvec_swiglu(const uint16_t* x_bf16, int32_t x_rows, const int32_t* topk_ids,
+                                  const uint8_t* w_fp4, const uint8_t* w_scale, int32_t M,
+                                  int32_t top_k, int32_t E, int32_t N, int32_t K,
+                                  uint16_t* h_bf16, hg_stream_t stream) {
+    return expert_matvec(x_bf16, x_rows, topk_ids, w_fp4, w_scale, M, top_k, E, N, K, true, h_bf16,
+                         stream);
+}
+
+hg_status hg_router_topk(const float* logits, int32_t M, int32_t E, int32_t top_k,
+                         int32_t renormalize, int32_t* topk_ids, float* topk_weights,
+                         hg_stream_t stream) {
+    if (M < 0 || E < 1 || top_k < 1 || top_k > E) return HG_ERR_INVALID_ARG;
+    if (top_k > router_max_top_k()) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return HG_OK;
+    if (!logits || !topk_ids || !topk_weights) return HG_ERR_INVALID_ARG;
+    if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    return launch_router_topk(logits, M, E, top_k, renormalize != 0, topk_ids, topk_weights,
+                              d->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status hg_router_topk_bwd(const float* logits, const int32_t* topk_ids,
+                             const float* topk_weights, const float* dweights, int32_t M,
+                             int32_t E, int32_t top_k, int32_t renormalize, float* dlogits,
+                             hg_stream_t stream) {
+    if (M < 0 || E < 1 || top_k < 1 || top_k > E) return HG_ERR_INVALID_ARG;
+    if (top_k > router_max_top_k()) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return HG_OK;
+    if (!topk_ids || !topk_weights || !dweights || !dlogits) return HG_ERR_INVALID_ARG;
+    if (!renormalize && !logits) return HG_ERR_INVALID_ARG;
+    if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+        !aligned(dweights, 4) || !aligned(dlogits, 4))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    return launch_router_topk_bwd(logits, topk_ids, topk_weights, dweights, M, E, top_k,
+                                  renormalize != 0, dlogits, d->num_sms,
+                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK
                : HG_ERR_CUDA;
 }

@@ -156,4 +156,39 @@ cudaError_t launch_combine_topk(const uint16_t* y, const int32_t* d2s, const flo
                                 int M, int top_k, int N, uint16_t* out, int num_sms,
                                 cudaStream_t stream);
 
+cudaError_t launch_dispatch(const uint16_t* x, const int32_t* d2s, const float* weights, int M,
+                            int top_k, int K, uint16_t* rows, int num_sms, cudaStream_t stream);
+cudaError_t launch_dispatch_bwd(const uint16_t* drows, const uint16_t* x, const int32_t* d2s,
+                                const float* weights, int M, int top_k, int K, uint16_t* dx,
+                                float* dw, int num_sms, cudaStream_t stream);
+cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, const int32_t* d2s,
+                               const float* weights, int M, int top_k, int N, uint16_t* dy,
+                               float* dw, int num_sms, cudaStream_t stream);
+
+cudaError_t launch_swiglu_quantize(const uint16_t* z, int rows, int F, uint8_t* a_fp8,
+                                   uint8_t* a_scale, uint8_t* z_fp8, uint8_t* z_scale, int num_sms,
+                                   cudaStream_t stream);
+cudaError_t launch_swiglu_bwd(const uint16_t* dh, const uint8_t* z_fp8, const uint8_t* z_scale,
+                              int rows, int F, uint16_t* dz, int num_sms, cudaStream_t stream);
+
+struct MatvecArgs {
+    const uint16_t* x;
+    int slots_per_row;      // consecutive slots that share an input row: 1 or top_k
+    const int32_t* ids;     // one expert id a slot
+    const uint8_t* w_fp4;
+    const uint8_t* w_scale;
+    int slots, E, N, K;
+    bool swiglu;
+    uint16_t* out;
+};
+cudaError_t launch_expert_matvec(const MatvecArgs& a, int num_sms, cudaStream_t stream);
+
+cudaError_t launch_router_topk(const float* logits, int M, int E, int top_k, int renormalize,
+                               int32_t* ids, float* weights, int num_sms, cudaStream_t stream);
+cudaError_t launch_router_topk_bwd(const float* logits, const int32_t* ids, const float* weights,
+                                   const float* dweights, int M, int E, int top_k,
+                                   int renormalize, float* dlogits, int num_sms,
+                                   cudaStream_t stream);
+int router_max_top_k();
+
 }  // namespace hg

@@ -16,36 +16,14 @@
 //    in FP32, j ascending, rounded once to BF16; terms whose id was dropped
 //    by the plan (src_to_sorted = -1) are skipped.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "hg_internal.cuh"
+#include "numeric.cuh"
 
 namespace hg {
 namespace {
 
 constexpr int kGroup = 128;
-
-// Smallest e with amax <= 448 * 2^e, from the bits of amax (exact, no
-// floating-point division or logarithm).  amax = f * 2^p with f in [1, 2):
-// amax <= 1.75 * 2^(8+e)  <=>  e >= p - 8 when f <= 1.75, else e >= p - 7.
-__device__ __forceinline__ int scale_exponent(float amax) {
-    if (amax == 0.0f) return 0;
-    const uint32_t bits = __float_as_uint(amax);
-    int p;
-    uint32_t mant;
-    const uint32_t be = (bits >> 23) & 0xFFu;
-    if (be == 0) {                         // subnormal: normalise
-        const uint32_t m = bits & 0x7FFFFFu;
-        const int lz = __clz(m) - 8;       // shift that brings the leading 1 to bit 23
-        p = -126 - lz;
-        mant = (m << lz) & 0x7FFFFFu;
-    } else {
-        p = static_cast<int>(be) - 127;
-        mant = bits & 0x7FFFFFu;
-    }
-    int e = p - 8 + (mant > 0x600000u ? 1 : 0);
-    return e < -127 ? -127 : (e > 127 ? 127 : e);
-}
 
 // One 256-thread block per sorted row and iteration: the row's source index is
 // read once, then each half-warp takes groups hw, hw+16, hw+32, ... of the row
@@ -54,54 +32,6 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 constexpr int kQThreads = 256;
 constexpr int kQHalves = kQThreads / 16;
 constexpr int kQMaxIter = 4;                       // groups per half-warp held in registers
-
-struct GroupCodes {
-    uint32_t lo, hi;        // this lane's 8 E4M3 codes
-    uint8_t scale;          // the group's E8M0 code
-};
-
-// Lane j of a half-warp holds elements 8j .. 8j+7 of one 128-element group;
-// every lane of the warp must call this (the amax reduction shuffles).
-__device__ __forceinline__ GroupCodes quantize_codes(const uint4 v) {
-    float f[8];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-    float amax = 0.0f;
-    bool nonfinite = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        amax = fmaxf(amax, fabsf(f[i]));
-        nonfinite |= !isfinite(f[i]);
-    }
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        nonfinite |= __shfl_xor_sync(0xFFFFFFFFu, nonfinite ? 1 : 0, o) != 0;
-    }
-    GroupCodes c;
-    if (nonfinite) {
-        c.scale = 0xFF;                            // E8M0 NaN
-        c.lo = c.hi = 0x7F7F7F7Fu;                 // E4M3 NaN
-    } else {
-        const int e = scale_exponent(amax);
-        c.scale = static_cast<uint8_t>(127 + e);
-        // 2^-e from its bits: finite BF16 inputs give e <= 120, so the
-        // biased exponent 127 - e stays in [7, 254] (a normal float).
-        const float inv = __int_as_float((127 - e) << 23);
-        uint32_t b[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            b[i] = __nv_cvt_float_to_fp8(f[i] * inv, __NV_SATFINITE, __NV_E4M3);
-        }
-        c.lo = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
-        c.hi = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
-    }
-    return c;
-}
 
 __device__ __forceinline__ void quantize_group(const uint4 v, uint8_t* dst, uint8_t* scale_dst,
                                                int j) {

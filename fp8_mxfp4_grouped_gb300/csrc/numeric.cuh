@@ -1,0 +1,126 @@
+// numeric.cuh -- element conversions shared by the kernels around the GEMM:
+// the E8M0 scale rule of the activations, and BF16 pairs in 32-bit words.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+namespace hg {
+
+// Value of an E8M0 code: 2^(code - 127); code 255 is NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t code) {
+    const uint32_t bits = code == 0u ? 0x00400000u : code << 23;   // 2^-127 is subnormal
+    return __uint_as_float(code == 255u ? 0x7FC00000u : bits);
+}
+
+// Values of eight E4M3 codes (byte i is element i).
+__device__ __forceinline__ void e4m3_unpack8(const uint2 v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = ((i < 2 ? v.x : v.y) >> (16 * (i & 1))) & 0xFFFFu;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two),
+                                                         __NV_E4M3);
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+    }
+}
+
+// Smallest e with amax <= 448 * 2^e, from the bits of amax (exact, no
+// floating-point division or logarithm).  amax = f * 2^p with f in [1, 2):
+// amax <= 1.75 * 2^(8+e)  <=>  e >= p - 8 when f <= 1.75, else e >= p - 7.
+__device__ __forceinline__ int scale_exponent(float amax) {
+    if (amax == 0.0f) return 0;
+    const uint32_t bits = __float_as_uint(amax);
+    int p;
+    uint32_t mant;
+    const uint32_t be = (bits >> 23) & 0xFFu;
+    if (be == 0) {                         // subnormal: normalise
+        const uint32_t m = bits & 0x7FFFFFu;
+        const int lz = __clz(m) - 8;       // shift that brings the leading 1 to bit 23
+        p = -126 - lz;
+        mant = (m << lz) & 0x7FFFFFu;
+    } else {
+        p = static_cast<int>(be) - 127;
+        mant = bits & 0x7FFFFFu;
+    }
+    int e = p - 8 + (mant > 0x600000u ? 1 : 0);
+    return e < -127 ? -127 : (e > 127 ? 127 : e);
+}
+
+// The two BF16 values of a 32-bit word (element 2i in the low half).
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two floats rounded to nearest even into one word of BF16.
+__device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void bf16_unpack8(const uint4 v, float (&f)[8]) {
+    f[0] = bf16_lo(v.x);
+    f[1] = bf16_hi(v.x);
+    f[2] = bf16_lo(v.y);
+    f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z);
+    f[5] = bf16_hi(v.z);
+    f[6] = bf16_lo(v.w);
+    f[7] = bf16_hi(v.w);
+}
+
+__device__ __forceinline__ uint4 bf16_pack8(const float (&f)[8]) {
+    return make_uint4(bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]),
+                      bf16_pack(f[6], f[7]));
+}
+
+struct GroupCodes {
+    uint32_t lo, hi;        // this lane's 8 E4M3 codes
+    uint8_t scale;          // the group's E8M0 code
+};
+
+// Lane j of a half-warp holds elements 8j .. 8j+7 of one 128-element group;
+// every lane of the warp must call this (the amax reduction shuffles).
+__device__ __forceinline__ GroupCodes quantize_codes(const float (&f)[8]) {
+    float amax = 0.0f;
+    bool nonfinite = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        amax = fmaxf(amax, fabsf(f[i]));
+        nonfinite |= !isfinite(f[i]);
+    }
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        nonfinite |= __shfl_xor_sync(0xFFFFFFFFu, nonfinite ? 1 : 0, o) != 0;
+    }
+    GroupCodes c;
+    if (nonfinite) {
+        c.scale = 0xFF;                            // E8M0 NaN
+        c.lo = c.hi = 0x7F7F7F7Fu;                 // E4M3 NaN
+    } else {
+        const int e = scale_exponent(amax);
+        c.scale = static_cast<uint8_t>(127 + e);
+        // 2^-e from its bits: finite inputs give e <= 120, so the biased
+        // exponent 127 - e stays in [7, 254] (a normal float).
+        const float inv = __int_as_float((127 - e) << 23);
+        uint32_t b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            b[i] = __nv_cvt_float_to_fp8(f[i] * inv, __NV_SATFINITE, __NV_E4M3);
+        }
+        c.lo = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+        c.hi = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
+    }
+    return c;
+}
+
+__device__ __forceinline__ GroupCodes quantize_codes(const uint4 v) {
+    float f[8];
+    bf16_unpack8(v, f);
+    return quantize_codes(f);
+}
+
+}  // namespace hg

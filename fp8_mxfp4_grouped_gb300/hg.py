@@ -69,6 +69,25 @@ lib.hg_grouped_w4a8_gemm_host.argtypes = [_p, _p, _p, _p, _p, _i32, _i32, _i32, 
                                           _p, _p, _p, _sz, _p]
 lib.hg_grouped_w4a8_gemm_host.restype = ctypes.c_int
 
+lib.hg_dispatch_tokens.argtypes = [_p, _p, _p, _i32, _i32, _i32, _p, _p]
+lib.hg_dispatch_tokens.restype = ctypes.c_int
+lib.hg_dispatch_tokens_bwd.argtypes = [_p, _p, _p, _p, _i32, _i32, _i32, _p, _p, _p]
+lib.hg_dispatch_tokens_bwd.restype = ctypes.c_int
+lib.hg_combine_topk_bwd.argtypes = [_p, _p, _p, _p, _i32, _i32, _i32, _p, _p, _p]
+lib.hg_combine_topk_bwd.restype = ctypes.c_int
+lib.hg_swiglu_quantize.argtypes = [_p, _i32, _i32, _p, _p, _p, _p, _p]
+lib.hg_swiglu_quantize.restype = ctypes.c_int
+lib.hg_swiglu_bwd.argtypes = [_p, _p, _p, _i32, _i32, _p, _p]
+lib.hg_swiglu_bwd.restype = ctypes.c_int
+lib.hg_expert_matvec.argtypes = [_p, _i32, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p, _p]
+lib.hg_expert_matvec.restype = ctypes.c_int
+lib.hg_expert_matvec_swiglu.argtypes = lib.hg_expert_matvec.argtypes
+lib.hg_expert_matvec_swiglu.restype = ctypes.c_int
+lib.hg_router_topk.argtypes = [_p, _i32, _i32, _i32, _i32, _p, _p, _p]
+lib.hg_router_topk.restype = ctypes.c_int
+lib.hg_router_topk_bwd.argtypes = [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _p, _p]
+lib.hg_router_topk_bwd.restype = ctypes.c_int
+
 HG_OK = 0
 HG_ERR_INVALID_ARG = 1
 HG_ERR_UNSUPPORTED_SHAPE = 2
@@ -98,6 +117,17 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _out(given, shape, dtype, like, stream):
+    """The caller's output tensor, checked, or a new one that belongs to `stream`."""
+    if given is not None:
+        assert given.dtype == dtype and given.shape == shape and given.is_contiguous()
+        return given
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def hg_shutdown() -> None:
@@ -262,6 +292,163 @@ def hg_combine_topk(y_bf16: torch.Tensor, src_to_sorted: torch.Tensor, topk_weig
                              _ptr(out), _stream(stream))
     _check(st, "hg_combine_topk")
     return out
+
+
+def hg_dispatch_tokens(x_bf16: torch.Tensor, top_k: int, src_to_sorted: torch.Tensor,
+                       topk_weights=None, out=None, stream=None) -> torch.Tensor:
+    """rows[src_to_sorted[t*k + j]] = w[t, j] * x[t] (w = 1 without weights), BF16 [M*top_k, K].
+    Rows that no entry names are not written."""
+    M, K = x_bf16.shape
+    assert x_bf16.dtype == torch.bfloat16 and x_bf16.is_contiguous()
+    assert src_to_sorted.dtype == torch.int32 and src_to_sorted.numel() == M * top_k
+    assert src_to_sorted.is_contiguous()
+    assert topk_weights is None or (topk_weights.dtype == torch.float32 and
+                                    topk_weights.shape == (M, top_k) and
+                                    topk_weights.is_contiguous())
+    out = _out(out, (M * top_k, K), torch.bfloat16, x_bf16, stream)
+    st = lib.hg_dispatch_tokens(_ptr(x_bf16), _ptr(src_to_sorted), _ptr(topk_weights), M, top_k, K,
+                                _ptr(out), _stream(stream))
+    _check(st, "hg_dispatch_tokens")
+    return out
+
+
+def hg_dispatch_tokens_bwd(drows: torch.Tensor, top_k: int, src_to_sorted: torch.Tensor,
+                           topk_weights=None, x_bf16=None, dx=None, dweights=None, stream=None):
+    """Gradient of hg_dispatch_tokens: (dx [M, K] BF16, dweights [M, top_k] float32).
+    dweights is None unless the forward input x_bf16 is given."""
+    R, K = drows.shape
+    M = src_to_sorted.numel() // top_k
+    assert drows.dtype == torch.bfloat16 and drows.is_contiguous() and R == M * top_k
+    assert src_to_sorted.dtype == torch.int32 and src_to_sorted.numel() == R
+    assert src_to_sorted.is_contiguous()
+    assert topk_weights is None or (topk_weights.dtype == torch.float32 and
+                                    topk_weights.shape == (M, top_k) and
+                                    topk_weights.is_contiguous())
+    dx = _out(dx, (M, K), torch.bfloat16, drows, stream)
+    if x_bf16 is not None:
+        assert x_bf16.dtype == torch.bfloat16 and x_bf16.shape == (M, K) and x_bf16.is_contiguous()
+        dweights = _out(dweights, (M, top_k), torch.float32, drows, stream)
+    else:
+        assert dweights is None
+    st = lib.hg_dispatch_tokens_bwd(_ptr(drows), _ptr(x_bf16), _ptr(src_to_sorted),
+                                    _ptr(topk_weights), M, top_k, K, _ptr(dx), _ptr(dweights),
+                                    _stream(stream))
+    _check(st, "hg_dispatch_tokens_bwd")
+    return dx, dweights
+
+
+def hg_combine_topk_bwd(dout: torch.Tensor, y_bf16: torch.Tensor, src_to_sorted: torch.Tensor,
+                        topk_weights: torch.Tensor, dy=None, dweights=None, stream=None):
+    """Gradient of hg_combine_topk: (dy [M*top_k, N] BF16, dweights [M, top_k] float32)."""
+    M, k = topk_weights.shape
+    N = dout.shape[1]
+    assert dout.dtype == torch.bfloat16 and dout.shape == (M, N) and dout.is_contiguous()
+    assert y_bf16.dtype == torch.bfloat16 and y_bf16.shape == (M * k, N) and y_bf16.is_contiguous()
+    assert topk_weights.dtype == torch.float32 and topk_weights.is_contiguous()
+    assert src_to_sorted.dtype == torch.int32 and src_to_sorted.numel() == M * k
+    assert src_to_sorted.is_contiguous()
+    dy = _out(dy, (M * k, N), torch.bfloat16, dout, stream)
+    dweights = _out(dweights, (M, k), torch.float32, dout, stream)
+    st = lib.hg_combine_topk_bwd(_ptr(dout), _ptr(y_bf16), _ptr(src_to_sorted), _ptr(topk_weights),
+                                 M, k, N, _ptr(dy), _ptr(dweights), _stream(stream))
+    _check(st, "hg_combine_topk_bwd")
+    return dy, dweights
+
+
+def hg_swiglu_quantize(z_bf16: torch.Tensor, checkpoint: bool = True, a_fp8=None, a_scale=None,
+                       z_fp8=None, z_scale=None, stream=None):
+    """silu(g) * u of z = (g, u) [rows, 2F] as the next GEMM's (a_fp8, a_scale), and with
+    `checkpoint` z itself in 8 bits (z_fp8, z_scale), else None in their places."""
+    rows, F2 = z_bf16.shape
+    assert z_bf16.dtype == torch.bfloat16 and z_bf16.is_contiguous() and F2 % 2 == 0
+    F = F2 // 2
+    a_fp8 = _out(a_fp8, (rows, F), torch.uint8, z_bf16, stream)
+    a_scale = _out(a_scale, (rows, F // 128), torch.uint8, z_bf16, stream)
+    if checkpoint:
+        z_fp8 = _out(z_fp8, (rows, F2), torch.uint8, z_bf16, stream)
+        z_scale = _out(z_scale, (rows, F2 // 128), torch.uint8, z_bf16, stream)
+    else:
+        assert z_fp8 is None and z_scale is None
+    st = lib.hg_swiglu_quantize(_ptr(z_bf16), rows, F, _ptr(a_fp8), _ptr(a_scale), _ptr(z_fp8),
+                                _ptr(z_scale), _stream(stream))
+    _check(st, "hg_swiglu_quantize")
+    return a_fp8, a_scale, z_fp8, z_scale
+
+
+def hg_swiglu_bwd(dh: torch.Tensor, z_fp8: torch.Tensor, z_scale: torch.Tensor, dz=None,
+                  stream=None) -> torch.Tensor:
+    """Gradient of silu(g) * u from the 8-bit checkpoint of (g, u): dz [rows, 2F] BF16."""
+    rows, F = dh.shape
+    assert dh.dtype == torch.bfloat16 and dh.is_contiguous()
+    assert z_fp8.dtype == torch.uint8 and z_fp8.shape == (rows, 2 * F) and z_fp8.is_contiguous()
+    assert z_scale.dtype == torch.uint8 and z_scale.shape == (rows, 2 * F // 128)
+    assert z_scale.is_contiguous()
+    dz = _out(dz, (rows, 2 * F), torch.bfloat16, dh, stream)
+    st = lib.hg_swiglu_bwd(_ptr(dh), _ptr(z_fp8), _ptr(z_scale), rows, F, _ptr(dz),
+                           _stream(stream))
+    _check(st, "hg_swiglu_bwd")
+    return dz
+
+
+def _expert_matvec(fn, what, cols, x_bf16, topk_ids, w_fp4, w_scale, out, stream):
+    M, k = topk_ids.shape
+    E, N, K2 = w_fp4.shape
+    K = 2 * K2
+    assert x_bf16.dtype == torch.bfloat16 and x_bf16.is_contiguous() and x_bf16.shape[1] == K
+    assert topk_ids.dtype == torch.int32 and topk_ids.is_contiguous()
+    assert w_fp4.dtype == torch.uint8 and w_fp4.is_contiguous()
+    assert w_scale.dtype == torch.uint8 and w_scale.is_contiguous()
+    assert w_scale.shape == (E, N, K // 32)
+    out = _out(out, (M * k, cols(N)), torch.bfloat16, x_bf16, stream)
+    st = fn(_ptr(x_bf16), x_bf16.shape[0], _ptr(topk_ids), _ptr(w_fp4), _ptr(w_scale), M, k, E, N,
+            K, _ptr(out), _stream(stream))
+    _check(st, what)
+    return out
+
+
+def hg_expert_matvec(x_bf16: torch.Tensor, topk_ids: torch.Tensor, w_fp4: torch.Tensor,
+                     w_scale: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """y[t*k + j] = W[topk_ids[t, j]] x: BF16 [M*top_k, N].  x_bf16 has M rows (shared by a
+    token's slots) or M*top_k (one a slot)."""
+    return _expert_matvec(lib.hg_expert_matvec, "hg_expert_matvec", lambda N: N, x_bf16, topk_ids,
+                          w_fp4, w_scale, out, stream)
+
+
+def hg_expert_matvec_swiglu(x_bf16: torch.Tensor, topk_ids: torch.Tensor, w_fp4: torch.Tensor,
+                            w_scale: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """silu(y[:, :N/2]) * y[:, N/2:] of hg_expert_matvec's y: BF16 [M*top_k, N/2]."""
+    return _expert_matvec(lib.hg_expert_matvec_swiglu, "hg_expert_matvec_swiglu",
+                          lambda N: N // 2, x_bf16, topk_ids, w_fp4, w_scale, out, stream)
+
+
+def hg_router_topk(logits: torch.Tensor, top_k: int, renormalize: bool = True, ids=None,
+                   weights=None, stream=None):
+    """(topk_ids int32 [M, top_k], topk_weights float32 [M, top_k]) of float32 logits [M, E]."""
+    M, E = logits.shape
+    assert logits.dtype == torch.float32 and logits.is_contiguous()
+    ids = _out(ids, (M, top_k), torch.int32, logits, stream)
+    weights = _out(weights, (M, top_k), torch.float32, logits, stream)
+    st = lib.hg_router_topk(_ptr(logits), M, E, top_k, int(renormalize), _ptr(ids), _ptr(weights),
+                            _stream(stream))
+    _check(st, "hg_router_topk")
+    return ids, weights
+
+
+def hg_router_topk_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                       dweights: torch.Tensor, renormalize: bool = True, dlogits=None,
+                       stream=None) -> torch.Tensor:
+    """Gradient of hg_router_topk with respect to the logits: float32 [M, E]."""
+    M, E = logits.shape
+    k = topk_ids.shape[1]
+    assert logits.dtype == torch.float32 and logits.is_contiguous()
+    assert topk_ids.dtype == torch.int32 and topk_ids.shape == (M, k) and topk_ids.is_contiguous()
+    for t in (topk_weights, dweights):
+        assert t.dtype == torch.float32 and t.shape == (M, k) and t.is_contiguous()
+    dlogits = _out(dlogits, (M, E), torch.float32, logits, stream)
+    st = lib.hg_router_topk_bwd(_ptr(logits), _ptr(topk_ids), _ptr(topk_weights), _ptr(dweights),
+                                M, E, k, int(renormalize), _ptr(dlogits), _stream(stream))
+    _check(st, "hg_router_topk_bwd")
+    return dlogits
 
 
 def hg_get_device_status(stream=None):

@@ -320,6 +320,194 @@ hg_status hg_combine_topk(const uint16_t* y_bf16, const int32_t* src_to_sorted,
                           const float* topk_weights, int32_t M, int32_t top_k, int32_t N,
                           uint16_t* out_bf16, hg_stream_t stream);
 
+/* ----------------------------------- tokens by expert, and gradients -- */
+
+/*
+ * BF16 token rows copied into the plan's sorted order, with or without the
+ * router's weights [H129 first section: the rows of one expert are one
+ * contiguous range]:
+ *
+ *   rows[src_to_sorted[t*top_k + j], :] = bf16_rne( w[t, j] * x[t, :] )
+ *
+ *   x_bf16         uint16 [M, K] BF16, 16-byte aligned.
+ *   src_to_sorted  int32 [M*top_k] from hg_plan_expert_offsets; entries outside
+ *                  [0, M*top_k) are skipped (ids the plan dropped are -1).
+ *   topk_weights   float32 [M, top_k], or NULL for a plain copy (w = 1).
+ *   rows_bf16      uint16 [M*top_k, K] out, 16-byte aligned; rows no entry names
+ *                  are not written.
+ * K % 8 == 0.  Every token is read once.  One kernel on `stream`; no host
+ * synchronisation.
+ */
+hg_status hg_dispatch_tokens(const uint16_t* x_bf16, const int32_t* src_to_sorted,
+                             const float* topk_weights, int32_t M, int32_t top_k, int32_t K,
+                             uint16_t* rows_bf16, hg_stream_t stream);
+
+/*
+ * Gradient of hg_dispatch_tokens (and of hg_quantize_scatter_acts, taken as
+ * the identity):
+ *
+ *   dx[t, :]       = bf16_rne( sum_j w[t, j] * drows[src_to_sorted[t*top_k + j], :] )
+ *   dweights[t, j] = sum_k drows[src_to_sorted[t*top_k + j], k] * x[t, k]
+ *
+ * the first sum in FP32 over j ascending, the second in FP32 in an order that
+ * depends on K alone; terms whose entry is outside [0, M*top_k) are
+ * skipped, and their dweights are 0.
+ *
+ *   drows_bf16    uint16 [M*top_k, K] BF16, 16-byte aligned.
+ *   x_bf16        uint16 [M, K] the forward input, with dweights; else NULL.
+ *   topk_weights  float32 [M, top_k], or NULL (w = 1).
+ *   dx_bf16       uint16 [M, K] out, 16-byte aligned.
+ *   dweights      float32 [M, top_k] out, with x_bf16; else NULL.
+ * K % 8 == 0.  One kernel on `stream`; no host synchronisation.
+ */
+hg_status hg_dispatch_tokens_bwd(const uint16_t* drows_bf16, const uint16_t* x_bf16,
+                                 const int32_t* src_to_sorted, const float* topk_weights,
+                                 int32_t M, int32_t top_k, int32_t K, uint16_t* dx_bf16,
+                                 float* dweights, hg_stream_t stream);
+
+/*
+ * Gradient of hg_combine_topk:
+ *
+ *   dy[src_to_sorted[t*top_k + j], :] = bf16_rne( w[t, j] * dout[t, :] )
+ *   dweights[t, j] = sum_n y[src_to_sorted[t*top_k + j], n] * dout[t, n]   (FP32)
+ *
+ * Entries outside [0, M*top_k) are skipped: their dweights are 0, and rows of
+ * dy that no entry names are not written.
+ *
+ *   dout_bf16      uint16 [M, N] BF16, 16-byte aligned.
+ *   y_bf16         uint16 [M*top_k, N] BF16, the forward input, 16-byte aligned.
+ *   src_to_sorted  int32 [M*top_k]; topk_weights float32 [M, top_k].
+ *   dy_bf16        uint16 [M*top_k, N] out, 16-byte aligned (not y_bf16).
+ *   dweights       float32 [M, top_k] out.
+ * N % 8 == 0.  One kernel on `stream`; no host synchronisation.
+ */
+hg_status hg_combine_topk_bwd(const uint16_t* dout_bf16, const uint16_t* y_bf16,
+                              const int32_t* src_to_sorted, const float* topk_weights, int32_t M,
+                              int32_t top_k, int32_t N, uint16_t* dy_bf16, float* dweights,
+                              hg_stream_t stream);
+
+/* ------------------------------------------- between the projections -- */
+
+/*
+ * SwiGLU of the gate/up projection's output, quantised as the down
+ * projection's input, with an 8-bit checkpoint of its own input for
+ * hg_swiglu_bwd.  Row r of z holds g in columns [0, F) and u in [F, 2F):
+ *
+ *   h[r, f] = g / (1 + exp(-g)) * u                            (FP32)
+ *   (a_fp8, a_scale) = h, (z_fp8, z_scale) = z in E4M3 with one E8M0 scale per
+ *   128 elements of a row, by the rule of hg_quantize_gather_acts (a group of
+ *   h that holds an Inf or NaN becomes the NaN codes, as there).
+ *
+ *   z_bf16   uint16 [rows, 2F] BF16, 16-byte aligned.
+ *   a_fp8    uint8 [rows, F] out, 16-byte aligned; a_scale uint8 [rows, F/128] out.
+ *   z_fp8    uint8 [rows, 2F] out, 16-byte aligned, and z_scale uint8
+ *            [rows, 2F/128] out; both NULL when no backward pass follows.
+ * F % 128 == 0.  h is quantised from FP32, without a BF16 rounding between.
+ * One kernel on `stream`; no host synchronisation.
+ */
+hg_status hg_swiglu_quantize(const uint16_t* z_bf16, int32_t rows, int32_t F, uint8_t* a_fp8,
+                             uint8_t* a_scale, uint8_t* z_fp8, uint8_t* z_scale,
+                             hg_stream_t stream);
+
+/*
+ * Gradient of the SwiGLU from the 8-bit checkpoint: with g and u decoded from
+ * (z_fp8, z_scale) and s = 1 / (1 + exp(-g)),
+ *
+ *   dz[r, f]     = bf16_rne( dh[r, f] * u * s * (1 + g * (1 - s)) )
+ *   dz[r, F + f] = bf16_rne( dh[r, f] * g * s )
+ *
+ *   dh_bf16  uint16 [rows, F] BF16, 16-byte aligned.
+ *   z_fp8    uint8 [rows, 2F], 16-byte aligned; z_scale uint8 [rows, 2F/128].
+ *   dz_bf16  uint16 [rows, 2F] out, 16-byte aligned.
+ * F % 128 == 0.  One kernel on `stream`; no host synchronisation.
+ */
+hg_status hg_swiglu_bwd(const uint16_t* dh_bf16, const uint8_t* z_fp8, const uint8_t* z_scale,
+                        int32_t rows, int32_t F, uint16_t* dz_bf16, hg_stream_t stream);
+
+/* ------------------------------------------------- few-token experts -- */
+
+/*
+ * Few tokens times their experts' MXFP4 weights on BF16 activations: what the
+ * plan, the quantisation and hg_grouped_w4a8_gemm do together, for the tokens
+ * of a decoding step, in one launch and without rounding the activations to
+ * 8 bits.  Slot s = t*top_k + j, e = topk_ids[s]:
+ *
+ *   y[s, n] = bf16_rne( sum_k x[row(s), k] * W(e, n, k) )     (FP32 sum)
+ *
+ * with W as for hg_grouped_w4a8_gemm.  y is in slot order (token-major):
+ * hg_combine_topk takes it with src_to_sorted[s] = s.  The row of a slot whose
+ * id is outside [0, E) is written as zeros.
+ *
+ *   x_bf16    uint16 [x_rows, K] BF16, 16-byte aligned; x_rows = M (row(s) =
+ *             s / top_k: a token's slots share its row) or M*top_k (row(s) = s).
+ *   topk_ids  int32 [M, top_k].
+ *   w_fp4     uint8 [E, N, K/2], 32-byte aligned; w_scale uint8 [E, N, K/32],
+ *             4-byte aligned.
+ *   y_bf16    uint16 [M*top_k, N] out.
+ * Supported: K % 128 == 0, K <= 32768, M*top_k <= 512, any N and E with
+ * E*N < 2^31.  Each expert's weights are read once per eight slots (fewer
+ * for large K), so that beyond some tens of tokens the grouped GEMM is the
+ * faster way.  The result does not vary from run to run.  One kernel on
+ * `stream`; no host synchronisation.
+ */
+hg_status hg_expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* topk_ids,
+                           const uint8_t* w_fp4, const uint8_t* w_scale, int32_t M, int32_t top_k,
+                           int32_t E, int32_t N, int32_t K, uint16_t* y_bf16, hg_stream_t stream);
+
+/*
+ * The same with the SwiGLU as epilogue, for a gate/up projection whose rows
+ * [0, F) are the gate's and [F, 2F) the up projection's, F = N/2 (N even):
+ *
+ *   h[s, f] = bf16_rne( silu(y[s, f]) * y[s, F + f] ),  y in FP32
+ *
+ *   h_bf16  uint16 [M*top_k, N/2] out.
+ */
+hg_status hg_expert_matvec_swiglu(const uint16_t* x_bf16, int32_t x_rows, const int32_t* topk_ids,
+                                  const uint8_t* w_fp4, const uint8_t* w_scale, int32_t M,
+                                  int32_t top_k, int32_t E, int32_t N, int32_t K,
+                                  uint16_t* h_bf16, hg_stream_t stream);
+
+/* ------------------------------------------------------------- router -- */
+
+/*
+ * The router's gate: the top_k largest of each token's E logits, largest
+ * first, ties to the lower index, and their softmax weights
+ *
+ *   w[t, j] = p[t, id_j]                          (renormalize = 0)
+ *   w[t, j] = p[t, id_j] / sum_i p[t, id_i]       (renormalize != 0)
+ *
+ * with p = softmax(logits[t, :]) over all E experts, in FP32.  A logit of
+ * -inf closes an expert to the token; places for which no open expert is left
+ * get id -1 (dropped by hg_plan_expert_offsets, which counts it) and weight 0.
+ * A NaN logit is never chosen; a NaN or +inf among a token's logits makes its
+ * weights NaN.
+ *
+ *   logits        float32 [M, E].
+ *   topk_ids      int32 [M, top_k] out; topk_weights float32 [M, top_k] out.
+ * 1 <= top_k <= min(E, 32).  One kernel on `stream`; no host synchronisation.
+ */
+hg_status hg_router_topk(const float* logits, int32_t M, int32_t E, int32_t top_k,
+                         int32_t renormalize, int32_t* topk_ids, float* topk_weights,
+                         hg_stream_t stream);
+
+/*
+ * Gradient of hg_router_topk with respect to the logits, the choice held
+ * fixed.  With c = sum_j w[t, j] * dweights[t, j] over the valid choices:
+ *
+ *   dlogits[t, e] = [e chosen] w[t, e] * dweights[t, e] - p[t, e] * c   (renormalize = 0)
+ *   dlogits[t, e] = [e chosen] w[t, e] * (dweights[t, e] - c)           (renormalize != 0)
+ *
+ *   logits        float32 [M, E]: the forward input; may be NULL when renormalize != 0.
+ *   topk_ids, topk_weights  what hg_router_topk returned; ids outside [0, E)
+ *                 take no part.
+ *   dweights      float32 [M, top_k]; dlogits float32 [M, E] out (every element).
+ * One kernel on `stream`; no host synchronisation.
+ */
+hg_status hg_router_topk_bwd(const float* logits, const int32_t* topk_ids,
+                             const float* topk_weights, const float* dweights, int32_t M,
+                             int32_t E, int32_t top_k, int32_t renormalize, float* dlogits,
+                             hg_stream_t stream);
+
 /* ------------------------------------------------- from host buffers -- */
 
 /*
