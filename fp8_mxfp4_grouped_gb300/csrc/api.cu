@@ -103,9 +103,11 @@ struct OMapEntry {
     CUtensorMap map;
 };
 WMapEntry g_wmap[kMapCacheEntries];
+WMapEntry g_wbytes_map[kMapCacheEntries];
 AMapEntry g_amap[kMapCacheEntries];
 OMapEntry g_omap[kMapCacheEntries];
 int g_wmap_next = 0;
+int g_wbytes_map_next = 0;
 int g_amap_next = 0;
 int g_omap_next = 0;
 std::mutex g_map_mu;
@@ -114,10 +116,11 @@ void map_cache_reset() {
     std::lock_guard<std::mutex> lock(g_map_mu);
     for (int i = 0; i < kMapCacheEntries; ++i) {
         g_wmap[i].p = nullptr;
+        g_wbytes_map[i].p = nullptr;
         g_amap[i].p = nullptr;
         g_omap[i].p = nullptr;
     }
-    g_wmap_next = g_amap_next = g_omap_next = 0;
+    g_wmap_next = g_wbytes_map_next = g_amap_next = g_omap_next = 0;
 }
 
 // Weights: [E*N rows, K elements] of E2M1, unpacked by the TMA into one
@@ -144,6 +147,37 @@ hg_status weight_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* w_
         return HG_ERR_CUDA;
     WMapEntry& slot = g_wmap[g_wmap_next];
     g_wmap_next = (g_wmap_next + 1) % kMapCacheEntries;
+    slot.p = w_fp4;
+    slot.E = E;
+    slot.N = N;
+    slot.K = K;
+    slot.map = *out;
+    return HG_OK;
+}
+
+// Weights as packed bytes: [E*N rows, K/2 bytes], 128-byte swizzle, boxes of
+// 8 rows x 128 bytes (zeros past the end of a row and of the last row).
+hg_status weight_bytes_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* w_fp4,
+                           int32_t E, int32_t N, int32_t K, CUtensorMap* out) {
+    std::lock_guard<std::mutex> lock(g_map_mu);
+    for (int i = 0; i < kMapCacheEntries; ++i) {
+        const WMapEntry& c = g_wbytes_map[i];
+        if (c.p == w_fp4 && c.E == E && c.N == N && c.K == K) {
+            *out = c.map;
+            return HG_OK;
+        }
+    }
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2),
+                          static_cast<cuuint64_t>(E) * static_cast<cuuint64_t>(N)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+    cuuint32_t box[2] = {128, 8};
+    cuuint32_t estr[2] = {1, 1};
+    if (encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w_fp4), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return HG_ERR_CUDA;
+    WMapEntry& slot = g_wbytes_map[g_wbytes_map_next];
+    g_wbytes_map_next = (g_wbytes_map_next + 1) % kMapCacheEntries;
     slot.p = w_fp4;
     slot.E = E;
     slot.N = N;
@@ -390,11 +424,6 @@ hg_status grouped_gemm(const uint8_t* a_fp8, const uint8_t* a_scale, bool a_scal
                : HG_ERR_CUDA;
 }
 
-// Limits of the few-token form: its block lists the slots by expert in shared
-// memory, and holds one input row there.
-constexpr int32_t kMatvecMaxSlots = 512;
-constexpr int32_t kMatvecMaxK = 32768;
-
 hg_status expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* topk_ids,
                         const uint8_t* w_fp4, const uint8_t* w_scale, int32_t M, int32_t top_k,
                         int32_t E, int32_t N, int32_t K, bool swiglu, uint16_t* out,
@@ -402,9 +431,10 @@ hg_status expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* t
     if (M < 0 || top_k < 1 || E < 1 || N < 1 || K < 1) return HG_ERR_INVALID_ARG;
     const long long slots = static_cast<long long>(M) * top_k;
     if (x_rows != M && x_rows != slots) return HG_ERR_INVALID_ARG;
-    if (K % 128 != 0 || K > kMatvecMaxK || (swiglu && N % 2 != 0) || slots > kMatvecMaxSlots)
+    if (K % 128 != 0 || (swiglu && N % 2 != 0) || slots > kMatvecMaxSlots || K > kMatvecMaxK)
         return HG_ERR_UNSUPPORTED_SHAPE;
-    if (static_cast<long long>(E) * N > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<long long>(E) * N > 0x7FFFFFFFll || slots * N > 0x7FFFFFFFll)
+        return HG_ERR_UNSUPPORTED_SHAPE;
     if (!w_fp4 || !w_scale) return HG_ERR_INVALID_ARG;
     if (!aligned(w_fp4, 32) || !aligned(w_scale, 4)) return HG_ERR_INVALID_ARG;
     if (M == 0) return HG_OK;
@@ -420,13 +450,22 @@ hg_status expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* t
     a.ids = topk_ids;
     a.w_fp4 = w_fp4;
     a.w_scale = w_scale;
+    a.tokens = M;
     a.slots = static_cast<int>(slots);
     a.E = E;
     a.N = N;
     a.K = K;
     a.swiglu = swiglu;
     a.out = out;
-    return launch_expert_matvec(a, d->num_sms, reinterpret_cast<cudaStream_t>(stream)) ==
+    a.status = d->status;
+    a.timeout_ns = g_timeout_ns.load();
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    st = encoder(&encode);
+    if (st != HG_OK) return st;
+    CUtensorMap map_w;
+    st = weight_bytes_map(encode, w_fp4, E, N, K, &map_w);
+    if (st != HG_OK) return st;
+    return launch_expert_matvec(a, map_w, d->num_sms, reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? HG_OK
                : HG_ERR_CUDA;

@@ -34,6 +34,7 @@ enum WaitRole : uint32_t {
     kRoleTeardown = 5,
     kRoleSelftest = 6,
     kRoleRelay = 7,
+    kRoleMatvec = 8,
 };
 
 struct WaitCtx {
@@ -177,11 +178,19 @@ struct MatvecArgs {
     const int32_t* ids;     // one expert id a slot
     const uint8_t* w_fp4;
     const uint8_t* w_scale;
-    int slots, E, N, K;
+    int tokens, slots, E, N, K;
     bool swiglu;
     uint16_t* out;
+    uint32_t* status;
+    uint64_t timeout_ns;
 };
-cudaError_t launch_expert_matvec(const MatvecArgs& a, int num_sms, cudaStream_t stream);
+// map_w: the weights' bytes [E*N, K/2], 128-byte swizzle, boxes of 8 rows x 128 bytes.
+cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, int num_sms,
+                                 cudaStream_t stream);
+// Limits of the few-token product: a block lists the slots by expert in shared
+// memory, and holds at least one input row there.
+constexpr int kMatvecMaxSlots = 512;
+constexpr int kMatvecMaxK = 32768;
 
 cudaError_t launch_router_topk(const float* logits, int M, int E, int top_k, int renormalize,
                                int32_t* ids, float* weights, int num_sms, cudaStream_t stream);
