@@ -95,13 +95,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// The same load without a cache hint.
-__device__ __forceinline__ void tma_load_2d_nohint(uint32_t dst, const CUtensorMap* map, int32_t x,
-                                                   int32_t y, uint32_t bar) {
+// 3-D tiled bulk tensor load global -> shared, without a cache hint.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x,
+                                            int32_t y, int32_t z, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -110,6 +110,12 @@ __device__ __forceinline__ void tma_load_2d_nohint(uint32_t dst, const CUtensorM
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
                  "r"(valid ? 4u : 0u)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 8u : 0u)
                  : "memory");
 }
 
@@ -144,6 +150,28 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
         : "r"(w));
 }
 
+// Two E8M0 codes (the low 16 bits) as floats.
+__device__ __forceinline__ float2 e8m0x2_to_f32(uint32_t codes) {
+    uint32_t two;                            // a pair of BF16, exact
+    asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, p;\n\t}"
+        : "=r"(two)
+        : "r"(codes));
+    return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u));
+}
+
+// Four E8M0 codes as floats (2^(code - 127); code 255 is NaN).
+__device__ __forceinline__ void e8m0x4_to_f32(uint32_t codes, float (&f)[4]) {
+    uint32_t lo, hi;                         // pairs of BF16, exact
+    asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, p;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %1, q;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+    f[0] = __uint_as_float(lo << 16);
+    f[1] = __uint_as_float(lo & 0xFFFF0000u);
+    f[2] = __uint_as_float(hi << 16);
+    f[3] = __uint_as_float(hi & 0xFFFF0000u);
+}
+
 // d += a * b: 16 x 8 += 16 x 16 times 16 x 8, FP16 operands, FP32 sums.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -152,11 +180,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Barrier `id` over `threads` threads (whole warps) of the CTA.
-__device__ __forceinline__ void named_barrier(uint32_t id, uint32_t threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // The same load issued for a CTA pair: the data lands in the executing CTA's

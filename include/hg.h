@@ -445,7 +445,7 @@ hg_status hg_swiglu_bwd(const uint16_t* dh_bf16, const uint8_t* z_fp8, const uin
  *             4-byte aligned.
  *   y_bf16    uint16 [M*top_k, N] out.
  * Supported: K % 128 == 0, K <= 32768, M*top_k <= 512, any N and E with
- * E*N and M*top_k*N below 2^31.  Each expert's weights are read once per eight slots (fewer
+ * E*N and M*top_k*N below 2^31.  Each expert's weights are read once per sixteen slots (fewer
  * for large K), so that beyond some tens of tokens the grouped GEMM is the
  * faster way.  The result does not vary from run to run.  One kernel on
  * `stream`; no host synchronisation.
