@@ -92,6 +92,12 @@ struct WMapEntry {
     int32_t E = 0, N = 0, K = 0;
     CUtensorMap map;
 };
+struct WBytesMapEntry {
+    const void* p = nullptr;
+    int32_t E = 0, N = 0, K = 0, rows = 0;
+    bool pair = false;
+    CUtensorMap map;
+};
 struct AMapEntry {
     const void* p = nullptr;
     int32_t rows = 0, K = 0;
@@ -103,11 +109,11 @@ struct OMapEntry {
     CUtensorMap map;
 };
 WMapEntry g_wmap[kMapCacheEntries];
-WMapEntry g_wbytes_map[2][kMapCacheEntries];   // plain, gate/up pairs
+WBytesMapEntry g_wbytes_map[kMapCacheEntries];
 AMapEntry g_amap[kMapCacheEntries];
 OMapEntry g_omap[kMapCacheEntries];
 int g_wmap_next = 0;
-int g_wbytes_map_next[2] = {0, 0};
+int g_wbytes_map_next = 0;
 int g_amap_next = 0;
 int g_omap_next = 0;
 std::mutex g_map_mu;
@@ -116,13 +122,11 @@ void map_cache_reset() {
     std::lock_guard<std::mutex> lock(g_map_mu);
     for (int i = 0; i < kMapCacheEntries; ++i) {
         g_wmap[i].p = nullptr;
-        g_wbytes_map[0][i].p = nullptr;
-        g_wbytes_map[1][i].p = nullptr;
+        g_wbytes_map[i].p = nullptr;
         g_amap[i].p = nullptr;
         g_omap[i].p = nullptr;
     }
-    g_wmap_next = g_wbytes_map_next[0] = g_wbytes_map_next[1] = 0;
-    g_amap_next = g_omap_next = 0;
+    g_wmap_next = g_wbytes_map_next = g_amap_next = g_omap_next = 0;
 }
 
 // Weights: [E*N rows, K elements] of E2M1, unpacked by the TMA into one
@@ -157,17 +161,17 @@ hg_status weight_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* w_
     return HG_OK;
 }
 
-// Weights as packed bytes, 128-byte swizzle, 16 rows x 128 bytes a box (zeros
-// past the end of a row and of an expert): [E, N rows, K/2 bytes] with 16
+// Weights as packed bytes, 128-byte swizzle, `rows` x 128 bytes a box (zeros
+// past the end of a row and of an expert): [E, N rows, K/2 bytes] with
 // consecutive rows, or for a gate/up pair [E * 2, N/2 rows, K/2 bytes] with
-// 8 rows of each.
+// half of the box's rows from each.
 hg_status weight_bytes_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* w_fp4,
-                           int32_t E, int32_t N, int32_t K, bool pair, CUtensorMap* out) {
+                           int32_t E, int32_t N, int32_t K, bool pair, int32_t rows,
+                           CUtensorMap* out) {
     std::lock_guard<std::mutex> lock(g_map_mu);
-    WMapEntry* cache = g_wbytes_map[pair];
     for (int i = 0; i < kMapCacheEntries; ++i) {
-        const WMapEntry& c = cache[i];
-        if (c.p == w_fp4 && c.E == E && c.N == N && c.K == K) {
+        const WBytesMapEntry& c = g_wbytes_map[i];
+        if (c.p == w_fp4 && c.E == E && c.N == N && c.K == K && c.pair == pair && c.rows == rows) {
             *out = c.map;
             return HG_OK;
         }
@@ -177,18 +181,21 @@ hg_status weight_bytes_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8
                           static_cast<cuuint64_t>(E) * split};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(K / 2),
                              static_cast<cuuint64_t>(K / 2) * static_cast<cuuint64_t>(N / split)};
-    cuuint32_t box[3] = {128, static_cast<cuuint32_t>(16 / split), static_cast<cuuint32_t>(split)};
+    cuuint32_t box[3] = {128, static_cast<cuuint32_t>(rows / split),
+                         static_cast<cuuint32_t>(split)};
     cuuint32_t estr[3] = {1, 1, 1};
     if (encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(w_fp4), dims, strides,
                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return HG_ERR_CUDA;
-    WMapEntry& slot = cache[g_wbytes_map_next[pair]];
-    g_wbytes_map_next[pair] = (g_wbytes_map_next[pair] + 1) % kMapCacheEntries;
+    WBytesMapEntry& slot = g_wbytes_map[g_wbytes_map_next];
+    g_wbytes_map_next = (g_wbytes_map_next + 1) % kMapCacheEntries;
     slot.p = w_fp4;
     slot.E = E;
     slot.N = N;
     slot.K = K;
+    slot.rows = rows;
+    slot.pair = pair;
     slot.map = *out;
     return HG_OK;
 }
@@ -470,7 +477,7 @@ hg_status expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* t
     st = encoder(&encode);
     if (st != HG_OK) return st;
     CUtensorMap map_w;
-    st = weight_bytes_map(encode, w_fp4, E, N, K, swiglu, &map_w);
+    st = weight_bytes_map(encode, w_fp4, E, N, K, swiglu, matvec_unit_rows(K, a.slots, M), &map_w);
     if (st != HG_OK) return st;
     return launch_expert_matvec(a, map_w, d->num_sms, reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess

@@ -184,8 +184,10 @@ struct MatvecArgs {
     uint32_t* status;
     uint64_t timeout_ns;
 };
-// map_w: the weights' bytes, 128-byte swizzle, boxes of 16 rows x 128 bytes; with swiglu
-// 8 rows of the gate's half and the same 8 of the up projection's.
+// Weight rows of a work unit for these sizes.
+int matvec_unit_rows(int K, int slots, int tokens);
+// map_w: the weights' bytes, 128-byte swizzle, boxes of a unit's rows x 128
+// bytes; with swiglu half of them the gate's and half the up projection's.
 cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, int num_sms,
                                  cudaStream_t stream);
 // Limits of the few-token product: a block lists the slots by expert in shared

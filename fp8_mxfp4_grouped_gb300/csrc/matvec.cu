@@ -10,20 +10,21 @@
 //
 // What bounds it: the weights, N * K * 17/32 bytes per expert in use, read
 // once from HBM.  Every block first lists the slots by expert in shared
-// memory, in chunks of up to eight slots (the columns of one MMA), so that an
-// expert's weights are read once for all of a chunk's slots; a work unit is
-// (chunk, 16 weight rows), and each block takes one contiguous range of units.
+// memory, in chunks of up to sixteen slots (the columns of two MMAs), so that
+// an expert's weights are read once for all of a chunk's slots; a work unit is
+// (chunk, 16 or 32 weight rows), and each block takes one contiguous range of
+// units.
 //
-// Warps stream: each warp owns a ring of 16-row x 256-K boxes that its lane 0
+// Warps stream: each warp owns a ring of 4-KB boxes of weights that its lane 0
 // fills by TMA, and runs ahead of its own use of them by the ring's depth.  The
-// boxes of a block's units, in order, go to its 16 warps in turn, so that all
+// boxes of a block's units, in order, go to its warps in turn, so that all
 // have the same work whatever K is; a unit's partial sums meet in shared memory,
 // in a fixed order (the result does not depend on timing), and the warp of the
 // unit's last box writes the outputs.  Nobody else waits for that: the sums of
 // several units may be under way at once.
 //
 // Arithmetic: a box's E2M1 codes become FP16 (exact) in registers and meet x
-// in mma.sync m16n8k16: with eight columns at most the tensor work is small,
+// in mma.sync m16n8k16: with sixteen columns at most the tensor work is small,
 // and tcgen05 would want the 16-bit weights written back to shared memory
 // first.  x is BF16, wider than FP16's range: each row's 256 elements of a box
 // are scaled by the power of two that takes their largest magnitude into
@@ -39,47 +40,57 @@
 namespace hg {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = kWarps * 32;
-static_assert(kThreads >= kMatvecMaxSlots, "a thread lists one slot");
-constexpr int kRows = 16;                    // weight rows of a unit: the MMA's M
 constexpr int kTileCols = 8;                 // slots of an MMA: its N
 constexpr int kMaxCols = 16;                 // slots of a chunk: at most two MMAs
-constexpr int kHalfK = 256;                  // elements of 128 bytes of a weight row
-constexpr int kHalfBytes = kRows * kHalfK / 2;
-constexpr int kHalfScaleBytes = kRows * kHalfK / 32;
-constexpr int kMaxRing = 4;                  // boxes in flight per warp
+constexpr int kPartK = 256;                  // elements of 128 bytes of a weight row
+constexpr int kBlockBytes = 8 * kPartK / 2;  // 8 rows of a part: one swizzle pattern
+constexpr int kBoxBlocks = 4;
+constexpr int kBoxBytes = kBoxBlocks * kBlockBytes;
+constexpr int kBoxScaleBytes = kBoxBytes / 16;
 constexpr int kMaxUnderWay = 4;              // units whose partial sums are kept at once
 constexpr int kSmemLimit = 232448 - 256;     // beside a few static bytes
+
+// The forms of the kernel.  A single column's MMAs are light, and its boxes
+// are long in K: 16 rows x 512 K.  With more columns the fragments of x weigh
+// more than the weights, and 32 rows x 256 K share each of them between two
+// MMAs; eight warps then have registers for it, and leave room for x.
+// The ring is no deeper than the memory's latency needs: 128 KB in flight per
+// SM; half as much again takes a token's gate/up product (E = 32, top-8,
+// N = 4096, K = 6144) from 22.4 to 24.1 us.
+struct Form {
+    int warps, row_tiles, parts, ring;       // parts: of 256 K in a box; ring: boxes in flight
+};
+__host__ __device__ constexpr Form form_of(bool single) {
+    return single ? Form{16, 1, 2, 2} : Form{8, 2, 1, 4};
+}
 
 // The slots by expert: an entry per slot or chunk (there are at most as many
 // chunks as slots).
 struct Tables {
-    int* id;
-    int* expert;             // of a chunk
+    int* count;              // [0] chunks, [1] slots without an expert
+    int* id;                 // of a slot; -1 without an expert
+    int* rank;               // of a slot among its expert's
+    int2* key;               // of a chunk: expert, and which of the expert's chunks
     int* ncols;              // of a chunk
-    uint16_t* chunk_of;      // of a chunk's first slot
     uint16_t* slot;          // of a chunk's columns: chunk * cols + column
-    uint8_t* same_rows;      // the chunk's input rows are those of the one before
-    int* warp_count;
+    uint8_t* same_row;       // the chunk's input row is that of the one before (single columns)
 };
 
-// For n slots; in multiples of 4 bytes.
 __host__ __device__ inline int table_bytes(int slots, int cols) {
     const int n = (slots + 3) & ~3;
-    return n * (3 * 4 + 2 + 2 * cols + 1) + kWarps * 4;
+    return 16 + n * (5 * 4 + 2 * cols + 1);
 }
 
 __device__ inline Tables tables_at(uint8_t* p, int slots, int cols) {
     const int n = (slots + 3) & ~3;
     Tables t;
-    t.warp_count = reinterpret_cast<int*>(p);
-    t.id = t.warp_count + kWarps;
-    t.expert = t.id + n;
-    t.ncols = t.expert + n;
-    t.chunk_of = reinterpret_cast<uint16_t*>(t.ncols + n);
-    t.slot = t.chunk_of + n;
-    t.same_rows = reinterpret_cast<uint8_t*>(t.slot + n * cols);
+    t.count = reinterpret_cast<int*>(p);
+    t.id = t.count + 4;
+    t.rank = t.id + n;
+    t.key = reinterpret_cast<int2*>(t.rank + n);
+    t.ncols = reinterpret_cast<int*>(t.key + n);
+    t.slot = reinterpret_cast<uint16_t*>(t.ncols + n);
+    t.same_row = reinterpret_cast<uint8_t*>(t.slot + n * cols);
     return t;
 }
 
@@ -90,14 +101,12 @@ struct Layout {
     int scales, partial, x, x_scale, zeros, bars, tables, total;   // byte offsets
 };
 
-// 256-K halves of a box: a single column's work is light, and two at a time
-// halve what a box costs besides.
-__host__ __device__ constexpr int box_halves(int cols) { return cols == 1 ? 2 : 1; }
-
-// Partial sums of the units under way: a float per weight row of a single
-// column, 16 x 8 floats per MMA otherwise, from every warp.
+// Partial sums of the units under way, from every warp: a float per weight row
+// of a single column; 32 x 8 floats per MMA column tile otherwise, of four
+// units (two with two tiles).
 int partial_bytes(int cols) {
-    return kWarps * (cols == 1 ? kMaxUnderWay * kRows * 4 : kMaxUnderWay * kRows * kTileCols * 4);
+    return cols == 1 ? form_of(true).warps * kMaxUnderWay * 16 * 4
+                     : form_of(false).warps * kMaxUnderWay * 32 * kTileCols * 4;
 }
 
 // As many columns as fit beside a ring of at least two boxes a warp, then as
@@ -105,30 +114,32 @@ int partial_bytes(int cols) {
 // that the eight lanes of a 16-byte load phase (two columns) meet no bank
 // twice.
 bool make_layout(int K, int slots, int tokens, Layout* out) {
-    const int halves = (K + kHalfK - 1) / kHalfK + 1;   // a box may reach one past the end
+    const int parts = (K + kPartK - 1) / kPartK + 1;     // a box may reach one past the end
     Layout l;
-    l.x_stride = halves * kHalfK * 2 + 64;
-    auto box = [](int cols) { return kWarps * box_halves(cols) * (kHalfBytes + kHalfScaleBytes); };
+    l.x_stride = parts * kPartK * 2 + 64;
+    auto box = [](int cols) { return form_of(cols == 1).warps * (kBoxBytes + kBoxScaleBytes); };
     auto needs = [&](int cols) {
-        return 1024 + partial_bytes(cols) + cols * l.x_stride + halves * kMaxCols * 4 +
-               2 * kHalfK + (kWarps * kMaxRing + 2 * kMaxUnderWay) * 8 + table_bytes(slots, cols);
+        return 1024 + partial_bytes(cols) + cols * l.x_stride + parts * kMaxCols * 4 + 2 * kPartK +
+               (form_of(cols == 1).warps * form_of(cols == 1).ring + 2 * kMaxUnderWay) * 8 +
+               table_bytes(slots, cols);
     };
     int cols = tokens < kMaxCols ? tokens : kMaxCols;   // a token's choices are distinct experts
     if (cols > slots) cols = slots;
     while (cols > 1 && needs(cols) + 2 * box(cols) > kSmemLimit) --cols;
     l.cols = cols;
     l.ring = (kSmemLimit - needs(cols)) / box(cols);
-    if (l.ring > kMaxRing) l.ring = kMaxRing;
+    if (l.ring > form_of(cols == 1).ring) l.ring = form_of(cols == 1).ring;
     if (l.ring < 1) return false;
-    const int ring = kWarps * l.ring * box_halves(cols);
-    l.scales = ring * kHalfBytes;
-    l.partial = l.scales + ring * kHalfScaleBytes;
+    const int ring = form_of(cols == 1).warps * l.ring;
+    l.scales = ring * kBoxBytes;
+    l.partial = l.scales + ring * kBoxScaleBytes;
     l.x = l.partial + partial_bytes(cols);
     l.x_scale = l.x + cols * l.x_stride;
-    l.zeros = l.x_scale + halves * kMaxCols * 4;
-    l.bars = l.zeros + 2 * kHalfK;
-    l.tables = l.bars + (kWarps * l.ring + 2 * kMaxUnderWay) * 8;
-    l.total = l.tables + table_bytes(slots, cols) + 1024;
+    l.zeros = l.x_scale + parts * kMaxCols * 4;
+    l.bars = l.zeros + 2 * kPartK;
+    l.tables = l.bars + (ring + 2 * kMaxUnderWay) * 8;
+    l.tables = (l.tables + 15) & ~15;
+    l.total = l.tables + table_bytes(slots, cols) + 1024 - 16;
     *out = l;
     return true;
 }
@@ -144,142 +155,154 @@ struct KernelArgs {
     Layout l;
 };
 
-// List the slots by expert in chunks of up to `cols`: thread s handles slot s.
-// Returns the number of chunks.
+// List the slots by expert in chunks of up to `cols`, in the order of the
+// chunks' first slots.  Returns the number of chunks.
+template <int kThreads>
 __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
-    const int s = threadIdx.x;
-    const bool mine = s < a.slots;
+    const int tid = threadIdx.x;
+    const int cols = a.l.cols;
+    auto expert_of = [&](int s) {
+        const int e = s < a.slots ? __ldg(a.ids + s) : -1;
+        return e >= 0 && e < a.E ? e : -1;
+    };
     if (a.slots <= 32) {                     // one warp sees all slots at once
-        if (s < 32) {
-            const int e = mine ? __ldg(a.ids + s) : -1;
-            const bool valid = e >= 0 && e < a.E;
-            const uint32_t below = (1u << s) - 1u;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, valid ? e : -1);
+        if (tid < 32) {
+            const int e = expert_of(tid);
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+            const uint32_t below = (1u << tid) - 1u;
             const int rank = __popc(same & below);
-            const int col = rank % a.l.cols;
-            const uint32_t leads = __ballot_sync(0xFFFFFFFFu, valid && col == 0);
-            // the chunk's first slot: the last leader of this expert up to here
-            const int lead = 31 - __clz(same & leads & (below | (1u << s)));
-            const int c = __popc(leads & ((1u << (lead & 31)) - 1u));
-            if (mine) tb.id[s] = e;
-            if (valid) tb.slot[c * a.l.cols + col] = static_cast<uint16_t>(s);
-            const int cols_here = min(a.l.cols, __popc(same) - (rank - col));
-            if (valid && col == 0) {
-                tb.expert[c] = e;
-                tb.ncols[c] = cols_here;
+            const int nth = rank / cols, col = rank - nth * cols;
+            const uint32_t leads = __ballot_sync(0xFFFFFFFFu, e >= 0 && col == 0);
+            const uint32_t valid = __ballot_sync(0xFFFFFFFFu, e >= 0);
+            if (tid < a.slots) tb.id[tid] = e;
+            if (e >= 0) {
+                // the chunk's first slot: the last leader of this expert up to here
+                const int lead = 31 - __clz(same & leads & (below | (1u << tid)));
+                const int c = __popc(leads & ((1u << lead) - 1u));
+                tb.slot[c * cols + col] = static_cast<uint16_t>(tid);
+                if (col == 0) {
+                    tb.key[c] = make_int2(e, nth);
+                    tb.ncols[c] = min(cols, __popc(same) - rank);
+                }
             }
             __syncwarp();
             const int total = __popc(leads);
-            if (s < total) {
-                bool rows = s > 0 && tb.ncols[s] == tb.ncols[s - 1];
-                for (int i = 0; rows && i < tb.ncols[s]; ++i) {
-                    rows = tb.slot[s * a.l.cols + i] / a.slots_per_row ==
-                           tb.slot[(s - 1) * a.l.cols + i] / a.slots_per_row;
-                }
-                tb.same_rows[s] = rows;
+            if (tid < total)
+                tb.same_row[tid] = tid > 0 && tb.slot[tid * cols] / a.slots_per_row ==
+                                                  tb.slot[(tid - 1) * cols] / a.slots_per_row;
+            if (tid == 0) {
+                tb.count[0] = total;
+                tb.count[1] = a.slots - __popc(valid);
             }
-            if (s == 0) tb.warp_count[0] = total;
         }
         __syncthreads();
-        return tb.warp_count[0];
+        return tb.count[0];
     }
-    if (mine) {
-        tb.id[s] = __ldg(a.ids + s);
-        tb.ncols[s] = 0;
-    }
+    const int n = (a.slots + 3) & ~3;
+    for (int s = tid; s < n; s += kThreads) tb.id[s] = expert_of(s);
     __syncthreads();
-    // rank among the slots of the same expert; the first slot of this one's chunk
-    int rank = 0, lead = s;
-    const int e = mine ? tb.id[s] : -1;
-    const bool valid = mine && e >= 0 && e < a.E;
-    if (valid) {
-        for (int j = 0; j < s; ++j) {
-            if (tb.id[j] == e) {
-                if (rank % a.l.cols == 0) lead = j;
-                ++rank;
-            }
+    for (int s = tid; s < a.slots; s += kThreads) {
+        const int e = tb.id[s];
+        int rank = 0;
+        const int4* four = reinterpret_cast<const int4*>(tb.id);
+#pragma unroll 4
+        for (int j = 0; j < s >> 2; ++j) {
+            const int4 v = four[j];
+            rank += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
         }
-        if (rank % a.l.cols == 0) lead = s;
-    }
-    const bool leads = valid && lead == s;
-    const uint32_t vote = __ballot_sync(0xFFFFFFFFu, leads);
-    const int lane = s & 31, warp = s >> 5;
-    if (lane == 0) tb.warp_count[warp] = __popc(vote);
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int i = 0; i < kWarps; ++i) {
-        const int c = tb.warp_count[i];
-        if (i < warp) before += c;
-        total += c;
-    }
-    if (leads) {
-        const int c = before + __popc(vote & ((1u << lane) - 1u));
-        tb.chunk_of[s] = static_cast<uint16_t>(c);
-        tb.expert[c] = e;
+        const int4 v = four[s >> 2];
+        rank += (s % 4 > 0 && v.x == e) + (s % 4 > 1 && v.y == e) + (s % 4 > 2 && v.z == e);
+        tb.rank[s] = rank;
     }
     __syncthreads();
-    if (valid) {
-        const int c = tb.chunk_of[lead];
-        tb.slot[c * a.l.cols + rank % a.l.cols] = static_cast<uint16_t>(s);
+    if (tid < 32) {                          // number the chunks in order of their first slots
+        int total = 0, valid = 0;
+        for (int s0 = 0; s0 < a.slots; s0 += 32) {
+            const int s = s0 + tid;
+            const int e = s < a.slots ? tb.id[s] : -1;
+            const int nth = e >= 0 ? tb.rank[s] / cols : 0;
+            const bool leads = e >= 0 && tb.rank[s] == nth * cols;
+            const uint32_t vote = __ballot_sync(0xFFFFFFFFu, leads);
+            valid += __popc(__ballot_sync(0xFFFFFFFFu, e >= 0));
+            if (leads) {
+                const int c = total + __popc(vote & ((1u << tid) - 1u));
+                tb.key[c] = make_int2(e, nth);
+                tb.ncols[c] = 0;
+            }
+            total += __popc(vote);
+        }
+        if (tid == 0) {
+            tb.count[0] = total;
+            tb.count[1] = a.slots - valid;
+        }
+    }
+    __syncthreads();
+    const int total = tb.count[0];
+    for (int s = tid; s < a.slots; s += kThreads) {
+        const int e = tb.id[s];
+        const int nth = tb.rank[s] / cols;
+        int c = -1;
+#pragma unroll 4
+        for (int i = 0; i < total; ++i) {
+            const int2 k = tb.key[i];
+            if (k.x == e && k.y == nth) c = i;
+        }
+        if (c < 0) continue;                 // no expert
+        tb.slot[c * cols + tb.rank[s] - nth * cols] = static_cast<uint16_t>(s);
         atomicAdd(&tb.ncols[c], 1);
     }
     __syncthreads();
-    if (s < total) {
-        bool same = s > 0 && tb.ncols[s] == tb.ncols[s - 1];
-        for (int i = 0; same && i < tb.ncols[s]; ++i) {
-            same = tb.slot[s * a.l.cols + i] / a.slots_per_row ==
-                   tb.slot[(s - 1) * a.l.cols + i] / a.slots_per_row;
-        }
-        tb.same_rows[s] = same;
+    if (cols == 1) {
+        for (int c = tid; c < total; c += kThreads)
+            tb.same_row[c] = c > 0 && tb.slot[c] / a.slots_per_row ==
+                                          tb.slot[c - 1] / a.slots_per_row;
+        __syncthreads();
     }
-    __syncthreads();
     return total;
 }
 
-// The chunk's input rows into shared memory as scaled FP16, with one scale per
-// row and 256 elements: a warp handles these at a time, eight a lane.
-__device__ void load_x(const KernelArgs& a, const Tables& tb, uint8_t* smem, int chunk, int halves) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int ncols = tb.ncols[chunk];
-    float* scale = reinterpret_cast<float*>(smem + a.l.x_scale);
-    for (int i = threadIdx.x; i < halves * kMaxCols; i += kThreads) {
-        if (i % kMaxCols >= ncols) scale[i] = 0.0f;
+// A chunk's input rows go to shared memory in pieces of 256 elements, eight a
+// lane: piece p is part p % parts of column p / parts, and belongs to warp
+// p % warps.  All pieces are asked for at once, and each is rewritten in place
+// as scaled FP16 by the lanes that asked for it.
+__device__ __forceinline__ void load_piece(const KernelArgs& a, uint32_t base, int col, int part,
+                                           int row, int lane) {
+    const int k = part * kPartK + 8 * lane;
+    const uint16_t* src = a.x + static_cast<long long>(row) * a.K;
+    ptx::cp_async_16(base + a.l.x + col * a.l.x_stride + 2 * k, src + (k < a.K ? k : 0), k < a.K);
+}
+
+__device__ __forceinline__ void scale_piece(const KernelArgs& a, uint8_t* smem, int col, int part,
+                                            int lane) {
+    uint4* at = reinterpret_cast<uint4*>(smem + a.l.x + col * a.l.x_stride + part * (2 * kPartK) +
+                                         16 * lane);
+    float f[8];
+    bf16_unpack8(*at, f);
+    uint32_t top = 0;                        // largest magnitude's bits; NaN counts as the largest
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    int be = static_cast<int>(top >> 23);
+    float mult, back;
+    if (be == 255) {
+        // an Inf or NaN decides the sum: the finite elements may be dropped
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = isfinite(f[e]) ? 0.0f : f[e];
+        mult = back = 1.0f;
+    } else {
+        be = max(be, 15);                    // both factors stay normal numbers
+        mult = __uint_as_float(static_cast<uint32_t>(268 - be) << 23);   // 2^(14 - (be - 127))
+        back = __uint_as_float(static_cast<uint32_t>(be - 14) << 23);
     }
-    for (int i = warp; i < halves * ncols; i += kWarps) {
-        const int c = i / halves, b = i - c * halves;
-        const int row = tb.slot[chunk * a.l.cols + c] / a.slots_per_row;
-        const int k = b * kHalfK + 8 * lane;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (k < a.K)
-            v = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<long long>(row) * a.K + k));
-        float f[8];
-        bf16_unpack8(v, f);
-        uint32_t top = 0;                    // largest magnitude's bits; NaN counts as the largest
+    uint32_t h[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        int be = static_cast<int>(top >> 23);
-        float mult, back;
-        if (be == 255) {
-            // an Inf or NaN decides the sum: the finite elements may be dropped
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = isfinite(f[e]) ? 0.0f : f[e];
-            mult = back = 1.0f;
-        } else {
-            be = max(be, 15);                // both factors stay normal numbers
-            mult = __uint_as_float(static_cast<uint32_t>(268 - be) << 23);   // 2^(14 - (be - 127))
-            back = __uint_as_float(static_cast<uint32_t>(be - 14) << 23);
-        }
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __half2 p = __floats2half2_rn(f[2 * e] * mult, f[2 * e + 1] * mult);
-            h[e] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-        *reinterpret_cast<uint4*>(smem + a.l.x + c * a.l.x_stride + 2 * k) =
-            make_uint4(h[0], h[1], h[2], h[3]);
-        if (lane == 0) scale[b * kMaxCols + c] = back;
+    for (int e = 0; e < 4; ++e) {
+        const __half2 p = __floats2half2_rn(f[2 * e] * mult, f[2 * e + 1] * mult);
+        h[e] = *reinterpret_cast<const uint32_t*>(&p);
     }
+    *at = make_uint4(h[0], h[1], h[2], h[3]);
+    if (lane == 0)
+        reinterpret_cast<float*>(smem + a.l.x_scale)[part * kMaxCols + col] = back;
 }
 
 // 256 K of 16 weight rows times one column.  Were the column alone in the
@@ -288,7 +311,7 @@ __device__ void load_x(const KernelArgs& a, const Tables& tb, uint8_t* smem, int
 // all eight groups, and of group g's product only column g is kept: a lane
 // keeps groups 2q and 2q + 1 of its two rows, and scales four sums in place of
 // thirty-two.
-__device__ __forceinline__ void single_half(uint32_t w_at, uint32_t x_at, uint32_t code_lo,
+__device__ __forceinline__ void single_part(uint32_t w_at, uint32_t x_at, uint32_t code_lo,
                                             uint32_t code_hi, float sx, int lane,
                                             float (&acc)[2]) {
     const int q = lane & 3;
@@ -304,8 +327,7 @@ __device__ __forceinline__ void single_half(uint32_t w_at, uint32_t x_at, uint32
             uint32_t lo[4], hi[4];
             ptx::e2m1x8_to_f16(w[2 * i], lo);
             ptx::e2m1x8_to_f16(w[2 * i + 1], hi);
-            d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.0f;
-            ptx::mma_f16_16816(d[i], lo[0], hi[0], lo[1], hi[1], xv.x, xv.y);
+            ptx::mma_f16_16816_first(d[i], lo[0], hi[0], lo[1], hi[1], xv.x, xv.y);
             ptx::mma_f16_16816(d[i], lo[2], hi[2], lo[3], hi[3], xv.z, xv.w);
         }
         if (p == 0 || q == p) {
@@ -324,29 +346,37 @@ __device__ __forceinline__ void single_half(uint32_t w_at, uint32_t x_at, uint32
 
 // kTiles: MMAs side by side, eight slots each; 0: a single slot.
 template <bool kSwiglu, int kTiles>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(form_of(kTiles == 0).warps * 32, 1)
 expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_abort;
     constexpr bool kSingle = kTiles == 0;
     constexpr int kT = kSingle ? 1 : kTiles;
+    constexpr int kWarps = form_of(kSingle).warps;
+    constexpr int kThreads = kWarps * 32;
+    constexpr int kR = form_of(kSingle).row_tiles;
+    constexpr int kRows = 16 * kR;
+    constexpr int kParts = form_of(kSingle).parts;
+    constexpr int kBoxK = kParts * kPartK;
     constexpr int kUnderWay = kMaxUnderWay / kT;
-    constexpr int kHalves = box_halves(kSingle ? 1 : kTileCols);
-    constexpr int kBoxK = kHalves * kHalfK;
-    constexpr int kBoxBytes = kHalves * kHalfBytes;
-    constexpr int kBoxScaleBytes = kHalves * kHalfScaleBytes;
+    static_assert(2 * kR * kParts == kBoxBlocks, "a box is four blocks of 8 rows x 128 bytes");
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
     const Tables tb = tables_at(smem + a.l.tables, a.slots, a.l.cols);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t bars = base + a.l.bars + 8 * warp * a.l.ring;
+    const uint32_t full = base + a.l.bars + 8 * kWarps * a.l.ring;
+    const uint32_t empty = full + 8 * kMaxUnderWay;
+
     const int nb = (a.K + kBoxK - 1) / kBoxK;
     const int sharers = min(nb, kWarps);                     // warps that work on one unit
     const int out_cols = kSwiglu ? a.N / 2 : a.N;
     const int tile_cols = kSwiglu ? kRows / 2 : kRows;       // outputs of a unit
     const int tiles = (out_cols + tile_cols - 1) / tile_cols;
-    const uint32_t bars = base + a.l.bars + 8 * warp * a.l.ring;
-    const uint32_t full = base + a.l.bars + 8 * kWarps * a.l.ring;
-    const uint32_t empty = full + 8 * kMaxUnderWay;
+    // Boxes of a run in order, box b of unit u at (u - run) * nb + b: this warp
+    // takes every kWarps-th.
+    const int step_u = kWarps / nb, step_b = kWarps - step_u * nb;
+    const int first_u = warp / nb, first_b = warp - first_u * nb;
 
     if (lane == 0) {
         for (int i = 0; i < a.l.ring; ++i) ptx::mbar_init(bars + 8 * i, 33);
@@ -360,49 +390,72 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         }
         ptx::fence_barrier_init();
     }
-    if (!kSingle && threadIdx.x < kHalfK / 2)
+    if (!kSingle && threadIdx.x < kPartK / 2)
         reinterpret_cast<uint32_t*>(smem + a.l.zeros)[threadIdx.x] = 0;
-    const int chunks = list_slots(a, tb);    // has block barriers
+    ptx::griddep_wait();                     // nothing global is read or written before
+    ptx::griddep_launch_dependents();
 
-    const long long units = static_cast<long long>(chunks) * tiles;
-    const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x);
-    const int u1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    // x goes ahead of the weights, behind which it would wait for the whole
+    // ring; with one row for all slots, ahead of the ids, too.
+    const int parts = kParts * nb;
+    const bool one_row = kSingle && a.slots_per_row == a.slots;
+    if (one_row) {
+        for (int p = warp; p < parts; p += kWarps) load_piece(a, base, 0, p, 0, lane);
+        ptx::cp_async_commit();
+    }
+    const int chunks = list_slots<kThreads>(a, tb);          // has block barriers
 
-    // End of the run of units from `u` that share their input rows.
-    auto run_end = [&](int u) {
-        int c = u / tiles + 1;
-        while (c < chunks && tb.same_rows[c]) ++c;
+    const int units = chunks * tiles;
+    const int each = units / static_cast<int>(gridDim.x);
+    const int left = units - each * static_cast<int>(gridDim.x);
+    const int u0 = static_cast<int>(blockIdx.x) * each + min(static_cast<int>(blockIdx.x), left);
+    const int u1 = u0 + each + (static_cast<int>(blockIdx.x) < left);
+    const int chunk0 = u0 / tiles;
+
+    // End of the run of units, from one of chunk c, that share their input rows.
+    auto run_end = [&](int c) {
+        do ++c;
+        while (kSingle && c < chunks && tb.same_row[c]);
         return min(c * tiles, u1);
     };
-
-    // Boxes of a run in order, box b of unit u at (u - run) * nb + b: this warp
-    // takes every 16th.
-    const int step_u = kWarps / nb, step_b = kWarps % nb;
-    const int first_u = warp / nb, first_b = warp % nb;
+    auto load_x = [&](int chunk) {
+        for (int p = warp, col = 0, part = warp; p < parts * tb.ncols[chunk]; p += kWarps) {
+            while (part >= parts) {
+                part -= parts;
+                ++col;
+            }
+            load_piece(a, base, col, part, tb.slot[chunk * a.l.cols + col] / a.slots_per_row, lane);
+            part += kWarps;
+        }
+        ptx::cp_async_commit();
+    };
+    if (!one_row && u0 < u1) load_x(chunk0);
 
     // What this warp has asked for so far.
     const int groups = a.K / 32;
     const uint32_t ring_w = base + warp * a.l.ring * kBoxBytes;
     const uint32_t ring_s = base + a.l.scales + warp * a.l.ring * kBoxScaleBytes;
-    int p_u = u0 + first_u, p_b = first_b, p_end = u0 < u1 ? run_end(u0) : u0;
-    int p_chunk = u0 / tiles, p_known = -1, p_n0 = 0, p_expert = 0, p_at = 0, issued = 0;
+    int p_u = u0 + first_u, p_b = first_b, p_end = u0 < u1 ? run_end(chunk0) : u0;
+    int p_chunk = chunk0, p_known = -1, p_n0 = 0, p_expert = 0, p_at = 0, issued = 0;
     const uint8_t* p_scale = nullptr;
     auto issue = [&]() {
         while (p_u >= p_end) {
             if (p_end >= u1) return;
             p_u = p_end + first_u;
             p_b = first_b;
-            p_end = run_end(p_end);
+            while (p_end >= (p_chunk + 1) * tiles) ++p_chunk;
+            p_end = run_end(p_chunk);
         }
         if (p_u != p_known) {
             p_known = p_u;
             while (p_u >= (p_chunk + 1) * tiles) ++p_chunk;
             p_n0 = (p_u - p_chunk * tiles) * tile_cols;
-            p_expert = tb.expert[p_chunk];
-            // lane l copies half of row l / 2's scales; rows past the end of the
+            p_expert = tb.key[p_chunk].x;
+            // the row whose scales this lane copies; rows past the end of the
             // expert's are not used
-            const int r = lane >> 1;
-            const int n = kSwiglu ? min(p_n0 + (r & 7), out_cols - 1) + (r >> 3) * out_cols
+            const int r = kSingle ? lane >> 1 : lane;
+            const int n = kSwiglu ? min(p_n0 + r % (kRows / 2), out_cols - 1) +
+                                        r / (kRows / 2) * out_cols
                                   : min(p_n0 + r, out_cols - 1);
             p_scale = a.w_scale + (static_cast<long long>(p_expert) * a.N + n) * groups;
         }
@@ -412,15 +465,14 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             const int z = kSwiglu ? 2 * p_expert : p_expert;
             ptx::mbar_arrive_expect_tx(bar, kBoxBytes);
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-                ptx::tma_load_3d(dst + h * kHalfBytes, &map_w, (kHalves * p_b + h) * (kHalfK / 2),
-                                 p_n0, z, bar);
+            for (int h = 0; h < kParts; ++h)
+                ptx::tma_load_3d(dst + h * (kBoxBytes / kParts), &map_w,
+                                 (kParts * p_b + h) * (kPartK / 2), p_n0, z, bar);
         }
-        const int g = kHalves * (8 * p_b + 4 * (lane & 1));
-        const uint32_t to = ring_s + p_at * kBoxScaleBytes + 4 * kHalves * lane;
-        if (kHalves == 1) {
-            ptx::cp_async_4(to, p_scale + (g < groups ? g : 0), g < groups);
-        } else if (groups & 7) {             // rows of scales start at multiples of 4 bytes
+        // eight scales a lane: a row's 256 K, or half of a row's 512 K
+        const int g = kSingle ? 16 * p_b + 8 * (lane & 1) : 8 * p_b;
+        const uint32_t to = ring_s + p_at * kBoxScaleBytes + 8 * lane;
+        if (groups & 7) {                    // rows of scales start at multiples of 4 bytes
             ptx::cp_async_4(to, p_scale + (g < groups ? g : 0), g < groups);
             ptx::cp_async_4(to + 4, p_scale + (g + 4 < groups ? g + 4 : 0), g + 4 < groups);
         } else {
@@ -439,90 +491,133 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     for (int i = 0; i < a.l.ring; ++i) issue();
 
     // slots without an expert: zeros, spread over the grid
-    for (int s = 0; s < a.slots; ++s) {
-        if (tb.id[s] >= 0 && tb.id[s] < a.E) continue;
+    for (int s = 0; tb.count[1] > 0 && s < a.slots; ++s) {
+        if (tb.id[s] >= 0) continue;
         for (int n = blockIdx.x * kThreads + threadIdx.x; n < out_cols; n += gridDim.x * kThreads)
             a.out[static_cast<long long>(s) * out_cols + n] = 0;
     }
 
     const WaitCtx ctx{a.status, &s_abort, a.timeout_ns};
-    const float* x_scale = reinterpret_cast<const float*>(smem + a.l.x_scale);
+    float* x_scale = reinterpret_cast<float*>(smem + a.l.x_scale);
     float* partial = reinterpret_cast<float*>(smem + a.l.partial);
     const int q = lane & 3, g8 = lane >> 2;
-    // ldmatrix: lane l addresses row l % 8 of matrix l / 8: rows 0-7 and 8-15
-    // of one group, then of the next; 16-byte chunks are XOR-swizzled by row
-    const uint32_t lm_row = ring_w + ((lane >> 3) & 1) * (kHalfBytes / 2) + (lane & 7) * 128;
-    const uint8_t* my_scales = smem + a.l.scales + warp * a.l.ring * kBoxScaleBytes;
+    // ldmatrix: lane l addresses row l % 8 of matrix l / 8: the MMA's rows 0-7
+    // and 8-15 of one group, then of the next; 16-byte chunks are XOR-swizzled
+    // by row.  The 8-row blocks of a box follow one another; MMA r takes blocks
+    // 2r and 2r + 1, or with SwiGLU block r of the gate's and of the up rows.
+    constexpr int kHiBlock = kSwiglu ? kR : 1, kTileBlock = kSwiglu ? 1 : 2;
+    const uint32_t lm_row = ring_w + ((lane >> 3) & 1) * (kHiBlock * kBlockBytes) + (lane & 7) * 128;
+    constexpr int kScaleRow = 8 * kParts;
+    const uint8_t* my_scales = smem + a.l.scales + warp * a.l.ring * kBoxScaleBytes +
+                               g8 * kScaleRow;
     int at = 0;
     uint32_t phase = 0;
-    for (int run = u0, before = 0; run < u1;) {              // before: units of earlier runs
-        const int end = run_end(run);
-        const int ncols = tb.ncols[run / tiles];
-        if (run > u0) __syncthreads();       // everybody is done with the rows before
-        load_x(a, tb, smem, run / tiles, kHalves * nb);
+    for (int run = u0, chunk = chunk0, before = 0; run < u1;) {   // before: units of earlier runs
+        while (run >= (chunk + 1) * tiles) ++chunk;
+        const int end = run_end(chunk);
+        const int ncols = tb.ncols[chunk];
+        if (run > u0) {
+            __syncthreads();                 // everybody is done with the rows before
+            load_x(chunk);
+        }
+        if (!kSingle) {
+            for (int i = threadIdx.x; i < parts * kMaxCols; i += kThreads) {
+                if (i % kMaxCols >= ncols) x_scale[i] = 0.0f;
+            }
+        }
+        ptx::cp_async_wait_all_groups();
+        __syncwarp();
+        for (int p = warp, col = 0, part = warp; p < parts * ncols; p += kWarps) {
+            while (part >= parts) {
+                part -= parts;
+                ++col;
+            }
+            scale_piece(a, smem, col, part, lane);
+            part += kWarps;
+        }
         __syncthreads();
-        int chunk = run / tiles;
         // lanes of columns that the chunk does not have read zeros
         uint32_t x_at[kT], x_step[kT];
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
             const bool there = 8 * t + g8 < ncols;
             x_at[t] = base + (there ? a.l.x + (8 * t + g8) * a.l.x_stride : a.l.zeros) + 16 * q;
-            x_step[t] = there ? 2 * kHalfK : 0;
+            x_step[t] = there ? 2 * kPartK : 0;
         }
-        float acc[kT][4];
+        uint64_t acc[kR][kT][2];             // rows g8 and g8 + 8, each of columns 2q and 2q + 1
 #pragma unroll
-        for (int i = 0; i < 4 * kT; ++i) acc[i >> 2][i & 3] = 0.0f;
+        for (int i = 0; i < kR * kT * 2; ++i) acc[i / (2 * kT)][i / 2 % kT][i % 2] = 0;
         float one[2] = {0.0f, 0.0f};
         for (int u = run + first_u, b = first_b; u < end;) {
             const bool ok = __all_sync(0xFFFFFFFFu,
                                        wait_bounded(bars + 8 * at, phase, ctx, kRoleMatvec, at));
             if (ok) {
-                const uint8_t* codes = my_scales + at * kBoxScaleBytes + 8 * kHalves * g8;
+                const uint8_t* codes = my_scales + at * kBoxScaleBytes;
                 if (kSingle) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        single_half(lm_row + at * kBoxBytes + h * kHalfBytes,
-                                    base + a.l.x + (2 * b + h) * (2 * kHalfK),
-                                    *reinterpret_cast<const uint16_t*>(codes + 8 * h + 2 * q),
-                                    *reinterpret_cast<const uint16_t*>(codes + 128 + 8 * h + 2 * q),
-                                    x_scale[(2 * b + h) * kMaxCols], lane, one);
+                    for (int h = 0; h < kParts; ++h) {
+                        const uint8_t* c = codes + 8 * h + 2 * q;
+                        single_part(lm_row + at * kBoxBytes + h * (kBoxBytes / kParts),
+                                    base + a.l.x + (kParts * b + h) * (2 * kPartK),
+                                    *reinterpret_cast<const uint16_t*>(c),
+                                    *reinterpret_cast<const uint16_t*>(c + 8 * kScaleRow),
+                                    x_scale[(kParts * b + h) * kMaxCols], lane, one);
                     }
                 } else {
-                    const uint2 code_lo = *reinterpret_cast<const uint2*>(codes);
-                    const uint2 code_hi = *reinterpret_cast<const uint2*>(codes + 64);
-                    const uint32_t w_at = lm_row + at * kBoxBytes;
-                    float2 sx[kT];
+                    uint64_t sx[kT];
 #pragma unroll
                     for (int t = 0; t < kT; ++t)
-                        sx[t] = *reinterpret_cast<const float2*>(x_scale + b * kMaxCols + 8 * t +
-                                                                 2 * q);
-                    float s_lo[4], s_hi[4];
+                        sx[t] = *reinterpret_cast<const uint64_t*>(x_scale + b * kMaxCols + 8 * t +
+                                                                   2 * q);
+                    uint2 code[kR][2];
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) {
+#pragma unroll
+                        for (int hi = 0; hi < 2; ++hi)
+                            code[r][hi] = *reinterpret_cast<const uint2*>(
+                                codes + (r * kTileBlock + hi * kHiBlock) * 8 * kScaleRow);
+                    }
 #pragma unroll
                     for (int g = 0; g < 8; g += 2) {
-                        if (g % 4 == 0) {
-                            ptx::e8m0x4_to_f32(g ? code_lo.y : code_lo.x, s_lo);
-                            ptx::e8m0x4_to_f32(g ? code_hi.y : code_hi.x, s_hi);
-                        }
-                        uint32_t w[4];
-                        ptx::ldmatrix_x4(w_at + (((g + (lane >> 4)) ^ (lane & 7)) << 4), w);
+                        uint4 xf[2][kT];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            uint32_t lo[4], hi[4];
-                            ptx::e2m1x8_to_f16(w[2 * i], lo);
-                            ptx::e2m1x8_to_f16(w[2 * i + 1], hi);
 #pragma unroll
-                            for (int t = 0; t < kT; ++t) {
-                                const uint4 xv =
-                                    ptx::lds_v4(x_at[t] + b * x_step[t] + 64 * (g + i));
-                                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                ptx::mma_f16_16816(d, lo[0], hi[0], lo[1], hi[1], xv.x, xv.y);
-                                ptx::mma_f16_16816(d, lo[2], hi[2], lo[3], hi[3], xv.z, xv.w);
-                                const float a_lo = s_lo[g % 4 + i], a_hi = s_hi[g % 4 + i];
-                                acc[t][0] = fmaf(d[0], a_lo * sx[t].x, acc[t][0]);
-                                acc[t][1] = fmaf(d[1], a_lo * sx[t].y, acc[t][1]);
-                                acc[t][2] = fmaf(d[2], a_hi * sx[t].x, acc[t][2]);
-                                acc[t][3] = fmaf(d[3], a_hi * sx[t].y, acc[t][3]);
+                            for (int t = 0; t < kT; ++t)
+                                xf[i][t] = ptx::lds_v4(x_at[t] + b * x_step[t] + 64 * (g + i));
+                        }
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            uint32_t w[4];
+                            ptx::ldmatrix_x4(lm_row + at * kBoxBytes +
+                                                 r * kTileBlock * kBlockBytes +
+                                                 (((g + (lane >> 4)) ^ (lane & 7)) << 4), w);
+                            const uint2 c0 = code[r][0], c1 = code[r][1];
+                            const float2 s0 = ptx::e8m0x2_to_f32((g < 4 ? c0.x : c0.y) >> (g & 2) * 8);
+                            const float2 s1 = ptx::e8m0x2_to_f32((g < 4 ? c1.x : c1.y) >> (g & 2) * 8);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t lo[4], hi[4];
+                                ptx::e2m1x8_to_f16(w[2 * i], lo);
+                                ptx::e2m1x8_to_f16(w[2 * i + 1], hi);
+                                const uint64_t s_lo = i ? ptx::f32x2(s0.y, s0.y)
+                                                        : ptx::f32x2(s0.x, s0.x);
+                                const uint64_t s_hi = i ? ptx::f32x2(s1.y, s1.y)
+                                                        : ptx::f32x2(s1.x, s1.x);
+#pragma unroll
+                                for (int t = 0; t < kT; ++t) {
+                                    float d[4];
+                                    ptx::mma_f16_16816_first(d, lo[0], hi[0], lo[1], hi[1],
+                                                             xf[i][t].x, xf[i][t].y);
+                                    ptx::mma_f16_16816(d, lo[2], hi[2], lo[3], hi[3], xf[i][t].z,
+                                                       xf[i][t].w);
+                                    acc[r][t][0] =
+                                        ptx::fma_f32x2(ptx::f32x2(d[0], d[1]),
+                                                       ptx::mul_f32x2(s_lo, sx[t]), acc[r][t][0]);
+                                    acc[r][t][1] =
+                                        ptx::fma_f32x2(ptx::f32x2(d[2], d[3]),
+                                                       ptx::mul_f32x2(s_hi, sx[t]), acc[r][t][1]);
+                                }
                             }
                         }
                     }
@@ -580,40 +675,44 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                     a.out[static_cast<long long>(tb.slot[chunk]) * out_cols + n] =
                         __bfloat16_as_ushort(__float2bfloat16_rn(y));
             } else {
-                float4* part = reinterpret_cast<float4*>(partial) + place * kWarps * kT * 32 + lane;
+                constexpr int kA = kR * kT;
+                ulonglong2* part = reinterpret_cast<ulonglong2*>(partial) +
+                                   place * kWarps * kA * 32 + lane;
 #pragma unroll
-                for (int t = 0; t < kT; ++t) {
-                    part[(warp * kT + t) * 32] =
-                        make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-                    acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+                for (int i = 0; i < kA; ++i) {
+                    part[(warp * kA + i) * 32] =
+                        make_ulonglong2(acc[i / kT][i % kT][0], acc[i / kT][i % kT][1]);
+                    acc[i / kT][i % kT][0] = acc[i / kT][i % kT][1] = 0;
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(full + 8 * place);
                 if (!last_box) continue;
                 wait_bounded(full + 8 * place, round, ctx, kRoleMatvec, 0x200 + place);
                 while (done >= (chunk + 1) * tiles) ++chunk;
-                const int n0 = (done - chunk * tiles) * tile_cols + g8;
-                float4 sum[kT];
+                float4 sum[kA];
 #pragma unroll
-                for (int t = 0; t < kT; ++t) {
-                    sum[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i = 0; i < kA; ++i) {
+                    sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
                     for (int j = 0; j < sharers; ++j) {
-                        const float4 v = part[(((w0 + j) & (kWarps - 1)) * kT + t) * 32];
-                        sum[t].x += v.x;
-                        sum[t].y += v.y;
-                        sum[t].z += v.z;
-                        sum[t].w += v.w;
+                        const float4 v = *reinterpret_cast<const float4*>(
+                            part + (((w0 + j) & (kWarps - 1)) * kA + i) * 32);
+                        sum[i].x += v.x;
+                        sum[i].y += v.y;
+                        sum[i].z += v.z;
+                        sum[i].w += v.w;
                     }
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(empty + 8 * place);
 #pragma unroll
-                for (int t = 0; t < kT; ++t) {
-                    const float y[4] = {sum[t].x, sum[t].y, sum[t].z, sum[t].w};
+                for (int j = 0; j < kA; ++j) {
+                    const float y[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
+                    const int n0 = (done - chunk * tiles) * tile_cols +
+                                   j / kT * (kSwiglu ? 8 : 16) + g8;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int c = 8 * t + 2 * q + i;
+                        const int c = 8 * (j % kT) + 2 * q + i;
                         if (c >= ncols) continue;
                         uint16_t* o = a.out + static_cast<long long>(
                                                   tb.slot[chunk * a.l.cols + c]) * out_cols + n0;
@@ -648,12 +747,22 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 
 template <bool kSwiglu, int kTiles>
 cudaError_t launch(const CUtensorMap& map, const KernelArgs& k, int grid, cudaStream_t stream) {
-    const cudaError_t err = cudaFuncSetAttribute(expert_matvec_kernel<kSwiglu, kTiles>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 kSmemLimit);
+    cudaError_t err = cudaFuncSetAttribute(expert_matvec_kernel<kSwiglu, kTiles>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (err != cudaSuccess) return err;
-    expert_matvec_kernel<kSwiglu, kTiles><<<grid, kThreads, k.l.total, stream>>>(map, k);
-    return cudaGetLastError();
+    // The set-up of the block may overlap the end of the kernel before.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(form_of(kTiles == 0).warps * 32);
+    cfg.dynamicSmemBytes = k.l.total;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, expert_matvec_kernel<kSwiglu, kTiles>, map, k);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 template <bool kSwiglu>
@@ -665,6 +774,11 @@ cudaError_t launch_cols(const CUtensorMap& map, const KernelArgs& k, int grid,
 }
 
 }  // namespace
+
+int matvec_unit_rows(int K, int slots, int tokens) {
+    Layout l;
+    return make_layout(K, slots, tokens, &l) ? 16 * form_of(l.cols == 1).row_tiles : 0;
+}
 
 cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, int num_sms,
                                  cudaStream_t stream) {
@@ -681,7 +795,7 @@ cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, 
     k.N = a.N;
     k.K = a.K;
     if (!make_layout(a.K, a.slots, a.tokens, &k.l)) return cudaErrorInvalidValue;
-    const int tile_cols = a.swiglu ? kRows / 2 : kRows;
+    const int tile_cols = 16 * form_of(k.l.cols == 1).row_tiles / (a.swiglu ? 2 : 1);
     const long long tiles = ((a.swiglu ? a.N / 2 : a.N) + tile_cols - 1) / tile_cols;
     const long long units = tiles * a.slots;
     const int grid = static_cast<int>(units < num_sms ? units : num_sms);
