@@ -477,7 +477,7 @@ hg_status expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* t
     st = encoder(&encode);
     if (st != HG_OK) return st;
     CUtensorMap map_w;
-    st = weight_bytes_map(encode, w_fp4, E, N, K, swiglu, matvec_unit_rows(K, a.slots, M), &map_w);
+    st = weight_bytes_map(encode, w_fp4, E, N, K, swiglu, matvec_unit_rows(a), &map_w);
     if (st != HG_OK) return st;
     return launch_expert_matvec(a, map_w, d->num_sms, reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess

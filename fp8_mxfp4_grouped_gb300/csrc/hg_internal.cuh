@@ -185,7 +185,7 @@ struct MatvecArgs {
     uint64_t timeout_ns;
 };
 // Weight rows of a work unit for these sizes.
-int matvec_unit_rows(int K, int slots, int tokens);
+int matvec_unit_rows(const MatvecArgs& a);
 // map_w: the weights' bytes, 128-byte swizzle, boxes of a unit's rows x 128
 // bytes; with swiglu half of them the gate's and half the up projection's.
 cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, int num_sms,

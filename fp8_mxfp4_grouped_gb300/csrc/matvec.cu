@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kTileCols = 8;                 // slots of an MMA: its N
 constexpr int kMaxCols = 16;                 // slots of a chunk: at most two MMAs
+constexpr int kSingleRows = 4;               // input rows held for single columns
 constexpr int kPartK = 256;                  // elements of 128 bytes of a weight row
 constexpr int kBlockBytes = 8 * kPartK / 2;  // 8 rows of a part: one swizzle pattern
 constexpr int kBoxBlocks = 4;
@@ -73,12 +74,11 @@ struct Tables {
     int2* key;               // of a chunk: expert, and which of the expert's chunks
     int* ncols;              // of a chunk
     uint16_t* slot;          // of a chunk's columns: chunk * cols + column
-    uint8_t* same_row;       // the chunk's input row is that of the one before (single columns)
 };
 
 __host__ __device__ inline int table_bytes(int slots, int cols) {
     const int n = (slots + 3) & ~3;
-    return 16 + n * (5 * 4 + 2 * cols + 1);
+    return 16 + n * (5 * 4 + 2 * cols);
 }
 
 __device__ inline Tables tables_at(uint8_t* p, int slots, int cols) {
@@ -90,14 +90,14 @@ __device__ inline Tables tables_at(uint8_t* p, int slots, int cols) {
     t.key = reinterpret_cast<int2*>(t.rank + n);
     t.ncols = reinterpret_cast<int*>(t.key + n);
     t.slot = reinterpret_cast<uint16_t*>(t.ncols + n);
-    t.same_row = reinterpret_cast<uint8_t*>(t.slot + n * cols);
     return t;
 }
 
 struct Layout {
     int ring;          // boxes per warp
     int cols;          // most slots of a chunk
-    int x_stride;      // bytes between the columns of x
+    int x_rows;        // input rows held at once
+    int x_stride;      // bytes between them
     int scales, partial, x, x_scale, zeros, bars, tables, total;   // byte offsets
 };
 
@@ -109,36 +109,44 @@ int partial_bytes(int cols) {
                      : form_of(false).warps * kMaxUnderWay * 32 * kTileCols * 4;
 }
 
-// As many columns as fit beside a ring of at least two boxes a warp, then as
-// deep a ring as fits.  Columns stay 64 bytes off a multiple of 128 apart, so
-// that the eight lanes of a 16-byte load phase (two columns) meet no bank
-// twice.
-bool make_layout(int K, int slots, int tokens, Layout* out) {
+// Columns: up to eight (one MMA) where an expert has few slots on average, up
+// to sixteen otherwise: a second MMA costs half as much again, and reading the
+// weights of an expert with more slots twice costs twice.  Input rows: as many
+// as fit beside a ring of two boxes a warp.  They stay 64 bytes off a multiple
+// of 128 apart, so that the eight lanes of a 16-byte load phase (two columns,
+// whose rows mostly follow one another) meet no bank twice.
+bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     const int parts = (K + kPartK - 1) / kPartK + 1;     // a box may reach one past the end
     Layout l;
     l.x_stride = parts * kPartK * 2 + 64;
     auto box = [](int cols) { return form_of(cols == 1).warps * (kBoxBytes + kBoxScaleBytes); };
-    auto needs = [&](int cols) {
-        return 1024 + partial_bytes(cols) + cols * l.x_stride + parts * kMaxCols * 4 + 2 * kPartK +
+    auto needs = [&](int cols, int rows) {
+        return 1024 + partial_bytes(cols) + rows * (l.x_stride + parts * 4) + 16 + 2 * kPartK +
                (form_of(cols == 1).warps * form_of(cols == 1).ring + 2 * kMaxUnderWay) * 8 +
                table_bytes(slots, cols);
     };
-    int cols = tokens < kMaxCols ? tokens : kMaxCols;   // a token's choices are distinct experts
-    if (cols > slots) cols = slots;
-    while (cols > 1 && needs(cols) + 2 * box(cols) > kSmemLimit) --cols;
+    int cols = tokens < slots ? tokens : slots;          // a token's choices are distinct experts
+    const int most = slots > 6ll * E ? kMaxCols : kTileCols;
+    if (cols > most) cols = most;
+    while (cols > 1 && needs(cols, cols) + 2 * box(cols) > kSmemLimit) --cols;
     l.cols = cols;
-    l.ring = (kSmemLimit - needs(cols)) / box(cols);
+    const int room = kSmemLimit - 2 * box(cols) - needs(cols, 0);
+    l.x_rows = room / (l.x_stride + parts * 4);
+    const int useful = cols == 1 ? kSingleRows : 3 * kMaxCols;
+    if (l.x_rows > useful) l.x_rows = useful;
+    if (l.x_rows > x_rows) l.x_rows = x_rows;
+    if (l.x_rows < cols) l.x_rows = cols;
+    l.ring = (kSmemLimit - needs(cols, l.x_rows)) / box(cols);
     if (l.ring > form_of(cols == 1).ring) l.ring = form_of(cols == 1).ring;
     if (l.ring < 1) return false;
     const int ring = form_of(cols == 1).warps * l.ring;
     l.scales = ring * kBoxBytes;
     l.partial = l.scales + ring * kBoxScaleBytes;
     l.x = l.partial + partial_bytes(cols);
-    l.x_scale = l.x + cols * l.x_stride;
-    l.zeros = l.x_scale + parts * kMaxCols * 4;
+    l.x_scale = l.x + l.x_rows * l.x_stride;
+    l.zeros = (l.x_scale + l.x_rows * parts * 4 + 15) & ~15;
     l.bars = l.zeros + 2 * kPartK;
-    l.tables = l.bars + (ring + 2 * kMaxUnderWay) * 8;
-    l.tables = (l.tables + 15) & ~15;
+    l.tables = (l.bars + (ring + 2 * kMaxUnderWay) * 8 + 15) & ~15;
     l.total = l.tables + table_bytes(slots, cols) + 1024 - 16;
     *out = l;
     return true;
@@ -151,7 +159,7 @@ struct KernelArgs {
     uint16_t* out;
     uint32_t* status;
     uint64_t timeout_ns;
-    int slots_per_row, slots, E, N, K;
+    int x_rows, slots_per_row, slots, E, N, K;
     Layout l;
 };
 
@@ -185,13 +193,8 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
                     tb.ncols[c] = min(cols, __popc(same) - rank);
                 }
             }
-            __syncwarp();
-            const int total = __popc(leads);
-            if (tid < total)
-                tb.same_row[tid] = tid > 0 && tb.slot[tid * cols] / a.slots_per_row ==
-                                                  tb.slot[(tid - 1) * cols] / a.slots_per_row;
             if (tid == 0) {
-                tb.count[0] = total;
+                tb.count[0] = __popc(leads);
                 tb.count[1] = a.slots - __popc(valid);
             }
         }
@@ -252,29 +255,23 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
         atomicAdd(&tb.ncols[c], 1);
     }
     __syncthreads();
-    if (cols == 1) {
-        for (int c = tid; c < total; c += kThreads)
-            tb.same_row[c] = c > 0 && tb.slot[c] / a.slots_per_row ==
-                                          tb.slot[c - 1] / a.slots_per_row;
-        __syncthreads();
-    }
     return total;
 }
 
-// A chunk's input rows go to shared memory in pieces of 256 elements, eight a
-// lane: piece p is part p % parts of column p / parts, and belongs to warp
-// p % warps.  All pieces are asked for at once, and each is rewritten in place
-// as scaled FP16 by the lanes that asked for it.
-__device__ __forceinline__ void load_piece(const KernelArgs& a, uint32_t base, int col, int part,
+// Input rows go to shared memory in pieces of 256 elements, eight a lane: piece
+// p is part p % parts of held row p / parts, and belongs to warp p % warps.  All
+// pieces are asked for at once, and each is rewritten in place as scaled FP16 by
+// the lanes that asked for it.
+__device__ __forceinline__ void load_piece(const KernelArgs& a, uint32_t base, int held, int part,
                                            int row, int lane) {
     const int k = part * kPartK + 8 * lane;
     const uint16_t* src = a.x + static_cast<long long>(row) * a.K;
-    ptx::cp_async_16(base + a.l.x + col * a.l.x_stride + 2 * k, src + (k < a.K ? k : 0), k < a.K);
+    ptx::cp_async_16(base + a.l.x + held * a.l.x_stride + 2 * k, src + (k < a.K ? k : 0), k < a.K);
 }
 
-__device__ __forceinline__ void scale_piece(const KernelArgs& a, uint8_t* smem, int col, int part,
-                                            int lane) {
-    uint4* at = reinterpret_cast<uint4*>(smem + a.l.x + col * a.l.x_stride + part * (2 * kPartK) +
+__device__ __forceinline__ void scale_piece(const KernelArgs& a, uint8_t* smem, int held, int part,
+                                            int parts, int lane) {
+    uint4* at = reinterpret_cast<uint4*>(smem + a.l.x + held * a.l.x_stride + part * (2 * kPartK) +
                                          16 * lane);
     float f[8];
     bf16_unpack8(*at, f);
@@ -302,7 +299,7 @@ __device__ __forceinline__ void scale_piece(const KernelArgs& a, uint8_t* smem, 
     }
     *at = make_uint4(h[0], h[1], h[2], h[3]);
     if (lane == 0)
-        reinterpret_cast<float*>(smem + a.l.x_scale)[part * kMaxCols + col] = back;
+        reinterpret_cast<float*>(smem + a.l.x_scale)[held * parts + part] = back;
 }
 
 // 256 K of 16 weight rows times one column.  Were the column alone in the
@@ -315,7 +312,7 @@ __device__ __forceinline__ void single_part(uint32_t w_at, uint32_t x_at, uint32
                                             uint32_t code_hi, float sx, int lane,
                                             float (&acc)[2]) {
     const int q = lane & 3;
-    const uint4 xv = ptx::lds_v4(x_at + 16 * lane);
+    const uint4 xv = ptx::lds_v4(x_at);
     float v[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {                            // groups 2p and 2p + 1
@@ -390,19 +387,27 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         }
         ptx::fence_barrier_init();
     }
-    if (!kSingle && threadIdx.x < kPartK / 2)
+    if (threadIdx.x < kPartK / 2)
         reinterpret_cast<uint32_t*>(smem + a.l.zeros)[threadIdx.x] = 0;
     ptx::griddep_wait();                     // nothing global is read or written before
     ptx::griddep_launch_dependents();
 
     // x goes ahead of the weights, behind which it would wait for the whole
-    // ring; with one row for all slots, ahead of the ids, too.
+    // ring; where all rows are held, ahead of the ids, too.
     const int parts = kParts * nb;
-    const bool one_row = kSingle && a.slots_per_row == a.slots;
-    if (one_row) {
-        for (int p = warp; p < parts; p += kWarps) load_piece(a, base, 0, p, 0, lane);
+    const bool hold_all = a.x_rows <= a.l.x_rows;
+    auto load_all = [&](int rows, auto row_of) {
+        for (int p = warp, held = 0, part = warp; p < parts * rows; p += kWarps) {
+            while (part >= parts) {
+                part -= parts;
+                ++held;
+            }
+            load_piece(a, base, held, part, row_of(held), lane);
+            part += kWarps;
+        }
         ptx::cp_async_commit();
-    }
+    };
+    if (hold_all) load_all(a.x_rows, [](int held) { return held; });
     const int chunks = list_slots<kThreads>(a, tb);          // has block barriers
 
     const int units = chunks * tiles;
@@ -412,24 +417,26 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     const int u1 = u0 + each + (static_cast<int>(blockIdx.x) < left);
     const int chunk0 = u0 / tiles;
 
-    // End of the run of units, from one of chunk c, that share their input rows.
+    // A run: the units of as many chunks, from chunk c on, as rows can be held.
     auto run_end = [&](int c) {
-        do ++c;
-        while (kSingle && c < chunks && tb.same_row[c]);
+        if (hold_all) return u1;
+        int rows = 0;
+        while (c * tiles < u1 && rows + tb.ncols[c] <= a.l.x_rows) rows += tb.ncols[c++];
         return min(c * tiles, u1);
     };
-    auto load_x = [&](int chunk) {
-        for (int p = warp, col = 0, part = warp; p < parts * tb.ncols[chunk]; p += kWarps) {
-            while (part >= parts) {
-                part -= parts;
-                ++col;
-            }
-            load_piece(a, base, col, part, tb.slot[chunk * a.l.cols + col] / a.slots_per_row, lane);
-            part += kWarps;
-        }
-        ptx::cp_async_commit();
+    auto run_rows = [&](int c, int end) {
+        int rows = 0;
+        for (; c * tiles < end; ++c) rows += tb.ncols[c];
+        return rows;
     };
-    if (!one_row && u0 < u1) load_x(chunk0);
+    auto load_run = [&](int c, int end) {
+        int before = 0;                      // rows of the run's chunks before c
+        load_all(run_rows(c, end), [&](int held) {
+            while (held >= before + tb.ncols[c]) before += tb.ncols[c++];
+            return tb.slot[c * a.l.cols + held - before] / a.slots_per_row;
+        });
+    };
+    if (!hold_all && u0 < u1) load_run(chunk0, run_end(chunk0));
 
     // What this warp has asked for so far.
     const int groups = a.K / 32;
@@ -515,40 +522,57 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     for (int run = u0, chunk = chunk0, before = 0; run < u1;) {   // before: units of earlier runs
         while (run >= (chunk + 1) * tiles) ++chunk;
         const int end = run_end(chunk);
-        const int ncols = tb.ncols[chunk];
         if (run > u0) {
             __syncthreads();                 // everybody is done with the rows before
-            load_x(chunk);
-        }
-        if (!kSingle) {
-            for (int i = threadIdx.x; i < parts * kMaxCols; i += kThreads) {
-                if (i % kMaxCols >= ncols) x_scale[i] = 0.0f;
-            }
+            load_run(chunk, end);
         }
         ptx::cp_async_wait_all_groups();
         __syncwarp();
-        for (int p = warp, col = 0, part = warp; p < parts * ncols; p += kWarps) {
+        const int rows = hold_all ? a.x_rows : run_rows(chunk, end);
+        for (int p = warp, held = 0, part = warp; p < parts * rows; p += kWarps) {
             while (part >= parts) {
                 part -= parts;
-                ++col;
+                ++held;
             }
-            scale_piece(a, smem, col, part, lane);
+            scale_piece(a, smem, held, part, parts, lane);
             part += kWarps;
         }
         __syncthreads();
-        // lanes of columns that the chunk does not have read zeros
+        // Where this lane's columns of the current chunk lie; lanes of columns
+        // that the chunk does not have read zeros.
+        int ncols = 0, rows_before = 0, x_chunk = chunk - 1;
         uint32_t x_at[kT], x_step[kT];
+        const float* s_at[kT][2];
+        int s_step[kT][2];
+        auto next_chunk = [&]() {
+            rows_before += ncols;
+            ncols = tb.ncols[++x_chunk];
+            auto held_row = [&](int c) {
+                return hold_all ? tb.slot[x_chunk * a.l.cols + c] / a.slots_per_row
+                                : rows_before + c;
+            };
+            const uint32_t zeros = base + a.l.zeros;
+            const float* no_scale = reinterpret_cast<const float*>(smem + a.l.zeros);
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            const bool there = 8 * t + g8 < ncols;
-            x_at[t] = base + (there ? a.l.x + (8 * t + g8) * a.l.x_stride : a.l.zeros) + 16 * q;
-            x_step[t] = there ? 2 * kPartK : 0;
-        }
+            for (int t = 0; t < kT; ++t) {
+                const int c = kSingle ? 0 : 8 * t + g8;
+                x_step[t] = c < ncols ? 2 * kPartK : 0;
+                x_at[t] = (c < ncols ? base + a.l.x + held_row(c) * a.l.x_stride : zeros) +
+                          16 * (kSingle ? lane : q);
+#pragma unroll
+                for (int i = 0; i < (kSingle ? 1 : 2); ++i) {
+                    const int d = kSingle ? 0 : 8 * t + 2 * q + i;
+                    s_step[t][i] = d < ncols;
+                    s_at[t][i] = d < ncols ? x_scale + held_row(d) * parts : no_scale;
+                }
+            }
+        };
         uint64_t acc[kR][kT][2];             // rows g8 and g8 + 8, each of columns 2q and 2q + 1
 #pragma unroll
         for (int i = 0; i < kR * kT * 2; ++i) acc[i / (2 * kT)][i / 2 % kT][i % 2] = 0;
         float one[2] = {0.0f, 0.0f};
         for (int u = run + first_u, b = first_b; u < end;) {
+            while (u >= (x_chunk + 1) * tiles) next_chunk();
             const bool ok = __all_sync(0xFFFFFFFFu,
                                        wait_bounded(bars + 8 * at, phase, ctx, kRoleMatvec, at));
             if (ok) {
@@ -558,17 +582,17 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                     for (int h = 0; h < kParts; ++h) {
                         const uint8_t* c = codes + 8 * h + 2 * q;
                         single_part(lm_row + at * kBoxBytes + h * (kBoxBytes / kParts),
-                                    base + a.l.x + (kParts * b + h) * (2 * kPartK),
+                                    x_at[0] + (kParts * b + h) * (2 * kPartK),
                                     *reinterpret_cast<const uint16_t*>(c),
                                     *reinterpret_cast<const uint16_t*>(c + 8 * kScaleRow),
-                                    x_scale[(kParts * b + h) * kMaxCols], lane, one);
+                                    s_at[0][0][kParts * b + h], lane, one);
                     }
                 } else {
                     uint64_t sx[kT];
 #pragma unroll
                     for (int t = 0; t < kT; ++t)
-                        sx[t] = *reinterpret_cast<const uint64_t*>(x_scale + b * kMaxCols + 8 * t +
-                                                                   2 * q);
+                        sx[t] = ptx::f32x2(s_at[t][0][b * s_step[t][0]],
+                                           s_at[t][1][b * s_step[t][1]]);
                     uint2 code[kR][2];
 #pragma unroll
                     for (int r = 0; r < kR; ++r) {
@@ -665,14 +689,13 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                     y += part[((w0 + j) & (kWarps - 1)) * kRows + (lane & 15)];
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(empty + 8 * place);
-                while (done >= (chunk + 1) * tiles) ++chunk;
-                const int n = (done - chunk * tiles) * tile_cols + lane;
+                const int n = (done - x_chunk * tiles) * tile_cols + lane;
                 if (kSwiglu) {
                     const float up = __shfl_down_sync(0xFFFFFFFFu, y, 8);
                     y = y / (1.0f + expf(-y)) * up;
                 }
                 if (lane < tile_cols && n < out_cols)
-                    a.out[static_cast<long long>(tb.slot[chunk]) * out_cols + n] =
+                    a.out[static_cast<long long>(tb.slot[x_chunk]) * out_cols + n] =
                         __bfloat16_as_ushort(__float2bfloat16_rn(y));
             } else {
                 constexpr int kA = kR * kT;
@@ -688,7 +711,6 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 if (lane == 0) ptx::mbar_arrive(full + 8 * place);
                 if (!last_box) continue;
                 wait_bounded(full + 8 * place, round, ctx, kRoleMatvec, 0x200 + place);
-                while (done >= (chunk + 1) * tiles) ++chunk;
                 float4 sum[kA];
 #pragma unroll
                 for (int i = 0; i < kA; ++i) {
@@ -708,14 +730,14 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 #pragma unroll
                 for (int j = 0; j < kA; ++j) {
                     const float y[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
-                    const int n0 = (done - chunk * tiles) * tile_cols +
+                    const int n0 = (done - x_chunk * tiles) * tile_cols +
                                    j / kT * (kSwiglu ? 8 : 16) + g8;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int c = 8 * (j % kT) + 2 * q + i;
                         if (c >= ncols) continue;
                         uint16_t* o = a.out + static_cast<long long>(
-                                                  tb.slot[chunk * a.l.cols + c]) * out_cols + n0;
+                                                  tb.slot[x_chunk * a.l.cols + c]) * out_cols + n0;
                         if (kSwiglu) {
                             if (n0 < out_cols)
                                 o[0] = __bfloat16_as_ushort(
@@ -775,9 +797,11 @@ cudaError_t launch_cols(const CUtensorMap& map, const KernelArgs& k, int grid,
 
 }  // namespace
 
-int matvec_unit_rows(int K, int slots, int tokens) {
+int matvec_unit_rows(const MatvecArgs& a) {
     Layout l;
-    return make_layout(K, slots, tokens, &l) ? 16 * form_of(l.cols == 1).row_tiles : 0;
+    return make_layout(a.K, a.slots, a.tokens, a.E, a.slots / a.slots_per_row, &l)
+               ? 16 * form_of(l.cols == 1).row_tiles
+               : 0;
 }
 
 cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, int num_sms,
@@ -789,12 +813,13 @@ cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, 
     k.out = a.out;
     k.status = a.status;
     k.timeout_ns = a.timeout_ns;
+    k.x_rows = a.slots / a.slots_per_row;
     k.slots_per_row = a.slots_per_row;
     k.slots = a.slots;
     k.E = a.E;
     k.N = a.N;
     k.K = a.K;
-    if (!make_layout(a.K, a.slots, a.tokens, &k.l)) return cudaErrorInvalidValue;
+    if (!make_layout(a.K, a.slots, a.tokens, a.E, k.x_rows, &k.l)) return cudaErrorInvalidValue;
     const int tile_cols = 16 * form_of(k.l.cols == 1).row_tiles / (a.swiglu ? 2 : 1);
     const long long tiles = ((a.swiglu ? a.N / 2 : a.N) + tile_cols - 1) / tile_cols;
     const long long units = tiles * a.slots;
