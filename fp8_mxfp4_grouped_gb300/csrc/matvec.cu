@@ -45,9 +45,6 @@ constexpr int kMaxCols = 16;                 // slots of a chunk: at most two MM
 constexpr int kSingleRows = 4;               // input rows held for single columns
 constexpr int kPartK = 256;                  // elements of 128 bytes of a weight row
 constexpr int kBlockBytes = 8 * kPartK / 2;  // 8 rows of a part: one swizzle pattern
-constexpr int kBoxBlocks = 4;
-constexpr int kBoxBytes = kBoxBlocks * kBlockBytes;
-constexpr int kBoxScaleBytes = kBoxBytes / 16;
 constexpr int kMaxUnderWay = 4;              // units whose partial sums are kept at once
 constexpr int kSmemLimit = 232448 - 256;     // beside a few static bytes
 
@@ -60,6 +57,9 @@ constexpr int kSmemLimit = 232448 - 256;     // beside a few static bytes
 // N = 4096, K = 6144) from 22.4 to 24.1 us.
 struct Form {
     int warps, row_tiles, parts, ring;       // parts: of 256 K in a box; ring: boxes in flight
+    __host__ __device__ constexpr int rows() const { return 16 * row_tiles; }
+    __host__ __device__ constexpr int box_bytes() const { return 2 * row_tiles * parts * kBlockBytes; }
+    __host__ __device__ constexpr int box_scale_bytes() const { return box_bytes() / 16; }
 };
 __host__ __device__ constexpr Form form_of(bool single) {
     return single ? Form{16, 1, 2, 2} : Form{8, 2, 1, 4};
@@ -105,8 +105,8 @@ struct Layout {
 // of a single column; 32 x 8 floats per MMA column tile otherwise, of four
 // units (two with two tiles).
 int partial_bytes(int cols) {
-    return cols == 1 ? form_of(true).warps * kMaxUnderWay * 16 * 4
-                     : form_of(false).warps * kMaxUnderWay * 32 * kTileCols * 4;
+    const Form f = form_of(cols == 1);
+    return f.warps * kMaxUnderWay * f.rows() * (cols == 1 ? 1 : kTileCols) * 4;
 }
 
 // Columns: up to eight (one MMA) where an expert has few slots on average, up
@@ -119,7 +119,10 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     const int parts = (K + kPartK - 1) / kPartK + 1;     // a box may reach one past the end
     Layout l;
     l.x_stride = parts * kPartK * 2 + 64;
-    auto box = [](int cols) { return form_of(cols == 1).warps * (kBoxBytes + kBoxScaleBytes); };
+    auto box = [](int cols) {
+        const Form f = form_of(cols == 1);
+        return f.warps * (f.box_bytes() + f.box_scale_bytes());
+    };
     auto needs = [&](int cols, int rows) {
         return 1024 + partial_bytes(cols) + rows * (l.x_stride + parts * 4) + 16 + 2 * kPartK +
                (form_of(cols == 1).warps * form_of(cols == 1).ring + 2 * kMaxUnderWay) * 8 +
@@ -140,8 +143,8 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     if (l.ring > form_of(cols == 1).ring) l.ring = form_of(cols == 1).ring;
     if (l.ring < 1) return false;
     const int ring = form_of(cols == 1).warps * l.ring;
-    l.scales = ring * kBoxBytes;
-    l.partial = l.scales + ring * kBoxScaleBytes;
+    l.scales = ring * form_of(cols == 1).box_bytes();
+    l.partial = l.scales + ring * form_of(cols == 1).box_scale_bytes();
     l.x = l.partial + partial_bytes(cols);
     l.x_scale = l.x + l.x_rows * l.x_stride;
     l.zeros = (l.x_scale + l.x_rows * parts * 4 + 15) & ~15;
@@ -308,22 +311,24 @@ __device__ __forceinline__ void scale_piece(const KernelArgs& a, uint8_t* smem, 
 // all eight groups, and of group g's product only column g is kept: a lane
 // keeps groups 2q and 2q + 1 of its two rows, and scales four sums in place of
 // thirty-two.
-__device__ __forceinline__ void single_part(uint32_t w_at, uint32_t x_at, uint32_t code_lo,
+__device__ __forceinline__ void single_part(uint32_t w_at, const uint8_t* x_at, uint32_t code_lo,
                                             uint32_t code_hi, float sx, int lane,
                                             float (&acc)[2]) {
     const int q = lane & 3;
-    const uint4 xv = ptx::lds_v4(x_at);
+    const uint4 xv = *reinterpret_cast<const uint4*>(x_at);
     float v[4];
+    uint32_t w[2][4];
+    ptx::ldmatrix_x4(w_at + (((lane >> 4) ^ (lane & 7)) << 4), w[0]);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {                            // groups 2p and 2p + 1
-        uint32_t w[4];
-        ptx::ldmatrix_x4(w_at + (((2 * p + (lane >> 4)) ^ (lane & 7)) << 4), w);
+        if (p < 3)
+            ptx::ldmatrix_x4(w_at + (((2 * p + 2 + (lane >> 4)) ^ (lane & 7)) << 4), w[~p & 1]);
         float d[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint32_t lo[4], hi[4];
-            ptx::e2m1x8_to_f16(w[2 * i], lo);
-            ptx::e2m1x8_to_f16(w[2 * i + 1], hi);
+            ptx::e2m1x8_to_f16(w[p & 1][2 * i], lo);
+            ptx::e2m1x8_to_f16(w[p & 1][2 * i + 1], hi);
             ptx::mma_f16_16816_first(d[i], lo[0], hi[0], lo[1], hi[1], xv.x, xv.y);
             ptx::mma_f16_16816(d[i], lo[2], hi[2], lo[3], hi[3], xv.z, xv.w);
         }
@@ -341,6 +346,25 @@ __device__ __forceinline__ void single_part(uint32_t w_at, uint32_t x_at, uint32
     acc[1] = fmaf(v[3], s_hi.y * sx, acc[1]);
 }
 
+// Wait until the shared counter has reached `target`, with the limits of
+// wait_bounded.  (Counts, not a barrier's phase parity: a warp may pass over
+// several rounds that it takes no part in.)
+__device__ __forceinline__ void wait_count(const volatile int* count, int target,
+                                           const WaitCtx& ctx, uint32_t where) {
+    if (*count < target) {
+        const uint64_t t0 = ptx::globaltimer_ns();
+        for (uint32_t it = 1; *count < target; ++it) {
+            if (*ctx.abort) return;
+            if ((it & 7u) == 0u && ptx::globaltimer_ns() - t0 > ctx.timeout_ns) {
+                *ctx.abort = 1u;
+                record_error(ctx.status, HG_ERR_TIMEOUT, (kRoleMatvec << 24) | where);
+                return;
+            }
+        }
+    }
+    __threadfence_block();
+}
+
 // kTiles: MMAs side by side, eight slots each; 0: a single slot.
 template <bool kSwiglu, int kTiles>
 __global__ void __launch_bounds__(form_of(kTiles == 0).warps * 32, 1)
@@ -356,14 +380,19 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     constexpr int kParts = form_of(kSingle).parts;
     constexpr int kBoxK = kParts * kPartK;
     constexpr int kUnderWay = kMaxUnderWay / kT;
-    static_assert(2 * kR * kParts == kBoxBlocks, "a box is four blocks of 8 rows x 128 bytes");
+    constexpr int kBoxBytes = form_of(kSingle).box_bytes();
+    constexpr int kBoxScaleBytes = form_of(kSingle).box_scale_bytes();
+    constexpr int kScaleLanes = kRows * kParts;              // eight scales a lane
+    static_assert(kScaleLanes <= 32, "a warp copies a box's scales at once");
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
     const Tables tb = tables_at(smem + a.l.tables, a.slots, a.l.cols);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t bars = base + a.l.bars + 8 * warp * a.l.ring;
     const uint32_t full = base + a.l.bars + 8 * kWarps * a.l.ring;
-    const uint32_t empty = full + 8 * kMaxUnderWay;
+    // rounds of each place of the partial sums that have been joined
+    volatile int* joined = reinterpret_cast<volatile int*>(smem + a.l.bars + 8 * kWarps * a.l.ring +
+                                                           8 * kMaxUnderWay);
 
     const int nb = (a.K + kBoxK - 1) / kBoxK;
     const int sharers = min(nb, kWarps);                     // warps that work on one unit
@@ -382,7 +411,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             s_abort = 0;
             for (int i = 0; i < kUnderWay; ++i) {
                 ptx::mbar_init(full + 8 * i, sharers);
-                ptx::mbar_init(empty + 8 * i, 1);
+                joined[i] = 0;
             }
         }
         ptx::fence_barrier_init();
@@ -460,7 +489,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             p_expert = tb.key[p_chunk].x;
             // the row whose scales this lane copies; rows past the end of the
             // expert's are not used
-            const int r = kSingle ? lane >> 1 : lane;
+            const int r = lane / kParts % kRows;
             const int n = kSwiglu ? min(p_n0 + r % (kRows / 2), out_cols - 1) +
                                         r / (kRows / 2) * out_cols
                                   : min(p_n0 + r, out_cols - 1);
@@ -477,9 +506,10 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                                  (kParts * p_b + h) * (kPartK / 2), p_n0, z, bar);
         }
         // eight scales a lane: a row's 256 K, or half of a row's 512 K
-        const int g = kSingle ? 16 * p_b + 8 * (lane & 1) : 8 * p_b;
+        const int g = 8 * (kParts * p_b + lane % kParts);
         const uint32_t to = ring_s + p_at * kBoxScaleBytes + 8 * lane;
-        if (groups & 7) {                    // rows of scales start at multiples of 4 bytes
+        if (lane >= kScaleLanes) {
+        } else if (groups & 7) {             // rows of scales start at multiples of 4 bytes
             ptx::cp_async_4(to, p_scale + (g < groups ? g : 0), g < groups);
             ptx::cp_async_4(to + 4, p_scale + (g + 4 < groups ? g + 4 : 0), g + 4 < groups);
         } else {
@@ -541,7 +571,8 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         // Where this lane's columns of the current chunk lie; lanes of columns
         // that the chunk does not have read zeros.
         int ncols = 0, rows_before = 0, x_chunk = chunk - 1;
-        uint32_t x_at[kT], x_step[kT];
+        const uint8_t* x_at[kT];
+        int x_step[kT];
         const float* s_at[kT][2];
         int s_step[kT][2];
         auto next_chunk = [&]() {
@@ -551,13 +582,13 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 return hold_all ? tb.slot[x_chunk * a.l.cols + c] / a.slots_per_row
                                 : rows_before + c;
             };
-            const uint32_t zeros = base + a.l.zeros;
+            const uint8_t* zeros = smem + a.l.zeros;
             const float* no_scale = reinterpret_cast<const float*>(smem + a.l.zeros);
 #pragma unroll
             for (int t = 0; t < kT; ++t) {
                 const int c = kSingle ? 0 : 8 * t + g8;
                 x_step[t] = c < ncols ? 2 * kPartK : 0;
-                x_at[t] = (c < ncols ? base + a.l.x + held_row(c) * a.l.x_stride : zeros) +
+                x_at[t] = (c < ncols ? smem + a.l.x + held_row(c) * a.l.x_stride : zeros) +
                           16 * (kSingle ? lane : q);
 #pragma unroll
                 for (int i = 0; i < (kSingle ? 1 : 2); ++i) {
@@ -608,14 +639,18 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                         for (int i = 0; i < 2; ++i) {
 #pragma unroll
                             for (int t = 0; t < kT; ++t)
-                                xf[i][t] = ptx::lds_v4(x_at[t] + b * x_step[t] + 64 * (g + i));
+                                xf[i][t] = *reinterpret_cast<const uint4*>(
+                                    x_at[t] + b * x_step[t] + 64 * (g + i));
                         }
+                        uint32_t ws[kR][4];
 #pragma unroll
-                        for (int r = 0; r < kR; ++r) {
-                            uint32_t w[4];
+                        for (int r = 0; r < kR; ++r)
                             ptx::ldmatrix_x4(lm_row + at * kBoxBytes +
                                                  r * kTileBlock * kBlockBytes +
-                                                 (((g + (lane >> 4)) ^ (lane & 7)) << 4), w);
+                                                 (((g + (lane >> 4)) ^ (lane & 7)) << 4), ws[r]);
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            const uint32_t(&w)[4] = ws[r];
                             const uint2 c0 = code[r][0], c1 = code[r][1];
                             const float2 s0 = ptx::e8m0x2_to_f32((g < 4 ? c0.x : c0.y) >> (g & 2) * 8);
                             const float2 s1 = ptx::e8m0x2_to_f32((g < 4 ? c1.x : c1.y) >> (g & 2) * 8);
@@ -667,9 +702,9 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             // unit's last box was here, join the parts and write the outputs.
             const int n_unit = before + done - run;
             const int place = n_unit % kUnderWay;
-            const uint32_t round = (n_unit / kUnderWay) & 1;
+            const int round = n_unit / kUnderWay;
             const int w0 = warp - (sharers - 1);             // the unit's first sharer, cyclically
-            wait_bounded(empty + 8 * place, round ^ 1, ctx, kRoleMatvec, 0x100 + place);
+            wait_count(joined + place, round, ctx, 0x100 + place);
             if (kSingle) {
                 float* part = partial + place * kWarps * kRows;
 #pragma unroll
@@ -682,13 +717,16 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(full + 8 * place);
                 if (!last_box) continue;
-                wait_bounded(full + 8 * place, round, ctx, kRoleMatvec, 0x200 + place);
+                wait_bounded(full + 8 * place, round & 1, ctx, kRoleMatvec, 0x200 + place);
                 float y = 0.0f;
 #pragma unroll 4
                 for (int j = 0; j < sharers; ++j)
                     y += part[((w0 + j) & (kWarps - 1)) * kRows + (lane & 15)];
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(empty + 8 * place);
+                if (lane == 0) {
+                    __threadfence_block();
+                    joined[place] = round + 1;
+                }
                 const int n = (done - x_chunk * tiles) * tile_cols + lane;
                 if (kSwiglu) {
                     const float up = __shfl_down_sync(0xFFFFFFFFu, y, 8);
@@ -710,7 +748,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(full + 8 * place);
                 if (!last_box) continue;
-                wait_bounded(full + 8 * place, round, ctx, kRoleMatvec, 0x200 + place);
+                wait_bounded(full + 8 * place, round & 1, ctx, kRoleMatvec, 0x200 + place);
                 float4 sum[kA];
 #pragma unroll
                 for (int i = 0; i < kA; ++i) {
@@ -726,7 +764,10 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                     }
                 }
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(empty + 8 * place);
+                if (lane == 0) {
+                    __threadfence_block();
+                    joined[place] = round + 1;
+                }
 #pragma unroll
                 for (int j = 0; j < kA; ++j) {
                     const float y[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
@@ -800,7 +841,7 @@ cudaError_t launch_cols(const CUtensorMap& map, const KernelArgs& k, int grid,
 int matvec_unit_rows(const MatvecArgs& a) {
     Layout l;
     return make_layout(a.K, a.slots, a.tokens, a.E, a.slots / a.slots_per_row, &l)
-               ? 16 * form_of(l.cols == 1).row_tiles
+               ? form_of(l.cols == 1).rows()
                : 0;
 }
 
@@ -820,7 +861,7 @@ cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, 
     k.N = a.N;
     k.K = a.K;
     if (!make_layout(a.K, a.slots, a.tokens, a.E, k.x_rows, &k.l)) return cudaErrorInvalidValue;
-    const int tile_cols = 16 * form_of(k.l.cols == 1).row_tiles / (a.swiglu ? 2 : 1);
+    const int tile_cols = form_of(k.l.cols == 1).rows() / (a.swiglu ? 2 : 1);
     const long long tiles = ((a.swiglu ? a.N / 2 : a.N) + tile_cols - 1) / tile_cols;
     const long long units = tiles * a.slots;
     const int grid = static_cast<int>(units < num_sms ? units : num_sms);
