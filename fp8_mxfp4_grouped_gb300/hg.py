@@ -119,6 +119,20 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# The calls of a decoding step take a few microseconds on the GPU: what they do
+# on the host is kept as short.  Addresses go to ctypes as plain integers, and
+# the current stream's handle is asked for without building a Stream.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _handle(stream, like):
+    return _raw_stream(like.get_device()) if stream is None else stream.cuda_stream
+
+
 def _out(given, shape, dtype, like, stream):
     """The caller's output tensor, checked, or a new one that belongs to `stream`."""
     if given is not None:
@@ -306,8 +320,8 @@ def hg_dispatch_tokens(x_bf16: torch.Tensor, top_k: int, src_to_sorted: torch.Te
                                     topk_weights.shape == (M, top_k) and
                                     topk_weights.is_contiguous())
     out = _out(out, (M * top_k, K), torch.bfloat16, x_bf16, stream)
-    st = lib.hg_dispatch_tokens(_ptr(x_bf16), _ptr(src_to_sorted), _ptr(topk_weights), M, top_k, K,
-                                _ptr(out), _stream(stream))
+    st = lib.hg_dispatch_tokens(_addr(x_bf16), _addr(src_to_sorted), _addr(topk_weights), M, top_k,
+                                K, _addr(out), _handle(stream, x_bf16))
     _check(st, "hg_dispatch_tokens")
     return out
 
@@ -330,9 +344,9 @@ def hg_dispatch_tokens_bwd(drows: torch.Tensor, top_k: int, src_to_sorted: torch
         dweights = _out(dweights, (M, top_k), torch.float32, drows, stream)
     else:
         assert dweights is None
-    st = lib.hg_dispatch_tokens_bwd(_ptr(drows), _ptr(x_bf16), _ptr(src_to_sorted),
-                                    _ptr(topk_weights), M, top_k, K, _ptr(dx), _ptr(dweights),
-                                    _stream(stream))
+    st = lib.hg_dispatch_tokens_bwd(_addr(drows), _addr(x_bf16), _addr(src_to_sorted),
+                                    _addr(topk_weights), M, top_k, K, _addr(dx), _addr(dweights),
+                                    _handle(stream, drows))
     _check(st, "hg_dispatch_tokens_bwd")
     return dx, dweights
 
@@ -349,8 +363,8 @@ def hg_combine_topk_bwd(dout: torch.Tensor, y_bf16: torch.Tensor, src_to_sorted:
     assert src_to_sorted.is_contiguous()
     dy = _out(dy, (M * k, N), torch.bfloat16, dout, stream)
     dweights = _out(dweights, (M, k), torch.float32, dout, stream)
-    st = lib.hg_combine_topk_bwd(_ptr(dout), _ptr(y_bf16), _ptr(src_to_sorted), _ptr(topk_weights),
-                                 M, k, N, _ptr(dy), _ptr(dweights), _stream(stream))
+    st = lib.hg_combine_topk_bwd(_addr(dout), _addr(y_bf16), _addr(src_to_sorted),
+                                 _addr(topk_weights), M, k, N, _addr(dy), _addr(dweights), _handle(stream, dout))
     _check(st, "hg_combine_topk_bwd")
     return dy, dweights
 
@@ -369,8 +383,8 @@ def hg_swiglu_quantize(z_bf16: torch.Tensor, checkpoint: bool = True, a_fp8=None
         z_scale = _out(z_scale, (rows, F2 // 128), torch.uint8, z_bf16, stream)
     else:
         assert z_fp8 is None and z_scale is None
-    st = lib.hg_swiglu_quantize(_ptr(z_bf16), rows, F, _ptr(a_fp8), _ptr(a_scale), _ptr(z_fp8),
-                                _ptr(z_scale), _stream(stream))
+    st = lib.hg_swiglu_quantize(_addr(z_bf16), rows, F, _addr(a_fp8), _addr(a_scale), _addr(z_fp8),
+                                _addr(z_scale), _handle(stream, z_bf16))
     _check(st, "hg_swiglu_quantize")
     return a_fp8, a_scale, z_fp8, z_scale
 
@@ -384,8 +398,8 @@ def hg_swiglu_bwd(dh: torch.Tensor, z_fp8: torch.Tensor, z_scale: torch.Tensor, 
     assert z_scale.dtype == torch.uint8 and z_scale.shape == (rows, 2 * F // 128)
     assert z_scale.is_contiguous()
     dz = _out(dz, (rows, 2 * F), torch.bfloat16, dh, stream)
-    st = lib.hg_swiglu_bwd(_ptr(dh), _ptr(z_fp8), _ptr(z_scale), rows, F, _ptr(dz),
-                           _stream(stream))
+    st = lib.hg_swiglu_bwd(_addr(dh), _addr(z_fp8), _addr(z_scale), rows, F, _addr(dz),
+                           _handle(stream, dh))
     _check(st, "hg_swiglu_bwd")
     return dz
 
@@ -400,8 +414,8 @@ def _expert_matvec(fn, what, cols, x_bf16, topk_ids, w_fp4, w_scale, out, stream
     assert w_scale.dtype == torch.uint8 and w_scale.is_contiguous()
     assert w_scale.shape == (E, N, K // 32)
     out = _out(out, (M * k, cols(N)), torch.bfloat16, x_bf16, stream)
-    st = fn(_ptr(x_bf16), x_bf16.shape[0], _ptr(topk_ids), _ptr(w_fp4), _ptr(w_scale), M, k, E, N,
-            K, _ptr(out), _stream(stream))
+    st = fn(_addr(x_bf16), x_bf16.shape[0], _addr(topk_ids), _addr(w_fp4), _addr(w_scale), M, k, E,
+            N, K, _addr(out), _handle(stream, x_bf16))
     _check(st, what)
     return out
 
@@ -428,8 +442,8 @@ def hg_router_topk(logits: torch.Tensor, top_k: int, renormalize: bool = True, i
     assert logits.dtype == torch.float32 and logits.is_contiguous()
     ids = _out(ids, (M, top_k), torch.int32, logits, stream)
     weights = _out(weights, (M, top_k), torch.float32, logits, stream)
-    st = lib.hg_router_topk(_ptr(logits), M, E, top_k, int(renormalize), _ptr(ids), _ptr(weights),
-                            _stream(stream))
+    st = lib.hg_router_topk(_addr(logits), M, E, top_k, int(renormalize), _addr(ids),
+                            _addr(weights), _handle(stream, logits))
     _check(st, "hg_router_topk")
     return ids, weights
 
@@ -445,8 +459,8 @@ def hg_router_topk_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, topk_weight
     for t in (topk_weights, dweights):
         assert t.dtype == torch.float32 and t.shape == (M, k) and t.is_contiguous()
     dlogits = _out(dlogits, (M, E), torch.float32, logits, stream)
-    st = lib.hg_router_topk_bwd(_ptr(logits), _ptr(topk_ids), _ptr(topk_weights), _ptr(dweights),
-                                M, E, k, int(renormalize), _ptr(dlogits), _stream(stream))
+    st = lib.hg_router_topk_bwd(_addr(logits), _addr(topk_ids), _addr(topk_weights),
+                                _addr(dweights), M, E, k, int(renormalize), _addr(dlogits), _handle(stream, logits))
     _check(st, "hg_router_topk_bwd")
     return dlogits
 
