@@ -15,17 +15,49 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
     return __uint_as_float(code == 255u ? 0x7FC00000u : bits);
 }
 
-// Values of eight E4M3 codes (byte i is element i).
-__device__ __forceinline__ void e4m3_unpack8(const uint2 v, float (&f)[8]) {
+// Values of four E4M3 codes (byte i is element i).
+__device__ __forceinline__ void e4m3_unpack4(uint32_t v, float (&f)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t two = ((i < 2 ? v.x : v.y) >> (16 * (i & 1))) & 0xFFFFu;
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two),
-                                                         __NV_E4M3);
+    for (int i = 0; i < 2; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>((v >> (16 * i)) & 0xFFFFu), __NV_E4M3);
         const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h));
         f[2 * i] = p.x;
         f[2 * i + 1] = p.y;
     }
+}
+
+// Four floats as E4M3 codes, round to nearest even; finite values beyond the
+// range saturate, NaN becomes NaN.
+__device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// Larger of two floats; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// Largest magnitude over the warp; NaN if any is.
+__device__ __forceinline__ float warp_abs_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// E8M0 code of the scale of a group whose largest magnitude is amax: 127 + e
+// with e the smallest integer such that amax <= 448 * 2^e = 1.75 * 2^(e + 8),
+// clamped to codes from 0 (the carry of the addition is the step from 1.75 to
+// the next power of two); 127 for amax = 0, 255 (NaN) for an Inf or NaN.
+__device__ __forceinline__ uint32_t e8m0_scale_code(float amax) {
+    const uint32_t bits = __float_as_uint(amax) & 0x7FFFFFFFu;
+    const int code = static_cast<int>((bits + 0x1FFFFFu) >> 23) - 8;
+    if (bits >= 0x7F800000u) return 255u;
+    return bits == 0u ? 127u : static_cast<uint32_t>(max(code, 0));
 }
 
 // Smallest e with amax <= 448 * 2^e, from the bits of amax (exact, no
