@@ -15,16 +15,11 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
     return __uint_as_float(code == 255u ? 0x7FC00000u : bits);
 }
 
-// Values of four E4M3 codes (byte i is element i).
-__device__ __forceinline__ void e4m3_unpack4(uint32_t v, float (&f)[4]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-            static_cast<__nv_fp8x2_storage_t>((v >> (16 * i)) & 0xFFFFu), __NV_E4M3);
-        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        f[2 * i] = p.x;
-        f[2 * i + 1] = p.y;
-    }
+// Values of the two E4M3 codes of the low 16 bits (the low byte first).
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(codes & 0xFFFFu), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // Four floats as E4M3 codes, round to nearest even; finite values beyond the

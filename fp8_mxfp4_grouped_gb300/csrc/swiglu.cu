@@ -10,9 +10,10 @@
 //
 // What bounds both is memory, once the arithmetic is short enough: per element
 // of h the forward moves 7 bytes (5 without the checkpoint), the backward 8.  A
-// group of 128 belongs to one warp, four elements a lane, so that its largest
-// magnitude is one warp-wide reduction instruction away and nothing is read
-// twice; each warp has two groups under way.  exp is 2^x of the hardware and
+// group of 128 belongs to half a warp, eight elements a lane, so that its
+// largest magnitude is a reduction instruction away and nothing is read twice
+// (four elements a lane of a whole warp pay twice for addresses and scales:
+// 390 us in place of REPLACE for 131072 x 2048 with the checkpoint).  exp is 2^x of the hardware and
 // the reciprocal its approximation: off by some 2^-22 of the value, and by
 // |g| * 2^-24 of it for the rounding of the exponent, against the formats'
 // 2^-4 and 2^-8.
@@ -24,23 +25,46 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kGroup = 128;
-constexpr int kUnder = 2;                    // groups under way per warp
+constexpr int kBlockGroups = kThreads / 16;
 
-// 1 / (1 + exp(-g)).  exp overflows to infinity below g = -88 and the result
-// is 0 there; between -87.3 and -88 it is subnormal, which rcp keeps.
-__device__ __forceinline__ float sigmoid(float g) {
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-    return s;
+// 1 / (1 + exp(-g)) of two values.  0 from about g = -87.3 down, where the
+// result leaves FP32's normal numbers.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+    const float2 t = ptx::f32x2_parts(
+        ptx::mul_f32x2(g, ptx::f32x2(-1.4426950408889634f, -1.4426950408889634f)));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    const float2 d = ptx::f32x2_parts(ptx::add_f32x2(ptx::f32x2(e.x, e.y), ptx::f32x2(1.0f, 1.0f)));
+    float2 s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+    return ptx::f32x2(s.x, s.y);
 }
 
-// Where the warps' walk over groups (row r, group g) has come to: every
-// `step`-th group of the rows in order.
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t w) {
+    return ptx::f32x2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ uint32_t bf16_pack_pair(uint64_t v) {
+    const float2 f = ptx::f32x2_parts(v);
+    return hg::bf16_pack(f.x, f.y);
+}
+
+// The two E4M3 codes of the low 16 bits.
+__device__ __forceinline__ uint64_t e4m3_pair(uint32_t codes) {
+    const float2 f = e4m3x2_to_f32(codes);
+    return ptx::f32x2(f.x, f.y);
+}
+
+// Where a half-warp's walk over the groups of all rows, in order, has come to:
+// group i of all, of row r.  An element of h lies at 128 i, of the gate at
+// 128 i + r F.
 struct Walk {
-    int r, g;
-    __device__ Walk(int first, int G) : r(first / G), g(first - first / G * G) {}
-    __device__ void next(int step_r, int step_g, int G) {
+    long long i, r;
+    int g;
+    __device__ Walk(int first, int G) : i(first), r(first / G), g(first - first / G * G) {}
+    __device__ void next(int step, int step_r, int step_g, int G) {
+        i += step;
         r += step_r;
         g += step_g;
         if (g >= G) {
@@ -50,14 +74,25 @@ struct Walk {
     }
 };
 
-// Four elements a lane of a group -> four E4M3 codes and the group's scale.
-__device__ __forceinline__ uint32_t quantize4(const float (&f)[4], uint32_t& scale) {
-    const float top = warp_abs_max(max_nan(max_nan(fabsf(f[0]), fabsf(f[1])),
-                                           max_nan(fabsf(f[2]), fabsf(f[3]))));
-    scale = e8m0_scale_code(top);
+// Eight elements a lane of each half-warp's group -> eight E4M3 codes and the
+// group's scale.  Every lane of the warp takes part.
+__device__ __forceinline__ uint2 quantize8(const uint64_t (&f)[4], int half, uint32_t& scale) {
+    float top = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const float2 v = ptx::f32x2_parts(f[p]);
+        top = max_nan(top, max_nan(fabsf(v.x), fabsf(v.y)));
+    }
+    const float top0 = warp_abs_max(half ? 0.0f : top), top1 = warp_abs_max(half ? top : 0.0f);
+    scale = e8m0_scale_code(half ? top1 : top0);
     const float inv = scale == 255u ? __uint_as_float(0x7FC00000u)      // every code becomes NaN
                                     : __uint_as_float((254u - scale) << 23);
-    return e4m3_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+    const uint64_t inv2 = ptx::f32x2(inv, inv);
+    float2 q[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) q[p] = ptx::f32x2_parts(ptx::mul_f32x2(f[p], inv2));
+    return make_uint2(e4m3_pack4(q[0].x, q[0].y, q[1].x, q[1].y),
+                      e4m3_pack4(q[2].x, q[2].y, q[3].x, q[3].y));
 }
 
 template <bool kCheckpoint>
@@ -66,49 +101,38 @@ swiglu_quantize_kernel(const uint16_t* __restrict__ z, int rows, int F,
                        uint8_t* __restrict__ a_fp8, uint8_t* __restrict__ a_scale,
                        uint8_t* __restrict__ z_fp8, uint8_t* __restrict__ z_scale) {
     const int G = F / kGroup;
-    const int lane = threadIdx.x & 31;
-    const int step = gridDim.x * (kThreads / 32);
+    const int half = (threadIdx.x >> 4) & 1, j = threadIdx.x & 15;
+    const int step = gridDim.x * kBlockGroups;
     const int step_r = step / G, step_g = step - step_r * G;
-    Walk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), G);
-    while (at.r < rows) {
-        int r[kUnder], g[kUnder];
-        uint2 vg[kUnder], vu[kUnder];
-#pragma unroll
-        for (int k = 0; k < kUnder; ++k) {
-            r[k] = at.r;
-            g[k] = at.g;
-            at.next(step_r, step_g, G);
-            vg[k] = vu[k] = make_uint2(0, 0);
-            if (r[k] < rows) {
-                const uint16_t* p = z + 2ll * r[k] * F + g[k] * kGroup + 4 * lane;
-                vg[k] = __ldcs(reinterpret_cast<const uint2*>(p));
-                vu[k] = __ldcs(reinterpret_cast<const uint2*>(p + F));
-            }
+    const long long groups = static_cast<long long>(rows) * G;
+    Walk at(blockIdx.x * kBlockGroups + (threadIdx.x >> 4), G);
+    for (; at.i - half < groups; at.next(step, step_r, step_g, G)) {
+        const bool real = at.i < groups;     // the last group may have no partner
+        const long long z_at = at.i * kGroup + at.r * F + 8 * j;
+        uint4 vg = make_uint4(0, 0, 0, 0), vu = vg;
+        if (real) {
+            vg = __ldcs(reinterpret_cast<const uint4*>(z + z_at));
+            vu = __ldcs(reinterpret_cast<const uint4*>(z + z_at + F));
         }
+        const uint64_t g[4] = {bf16_pair(vg.x), bf16_pair(vg.y), bf16_pair(vg.z), bf16_pair(vg.w)};
+        const uint64_t u[4] = {bf16_pair(vu.x), bf16_pair(vu.y), bf16_pair(vu.z), bf16_pair(vu.w)};
+        uint64_t h[4];
 #pragma unroll
-        for (int k = 0; k < kUnder; ++k) {
-            const float fg[4] = {bf16_lo(vg[k].x), bf16_hi(vg[k].x), bf16_lo(vg[k].y),
-                                 bf16_hi(vg[k].y)};
-            const float fu[4] = {bf16_lo(vu[k].x), bf16_hi(vu[k].x), bf16_lo(vu[k].y),
-                                 bf16_hi(vu[k].y)};
-            float h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = fg[e] * sigmoid(fg[e]) * fu[e];
-            if (r[k] >= rows) break;         // the whole warp
-            const long long row = r[k];
-            uint32_t scale;
-            const uint32_t codes = quantize4(h, scale);
-            *reinterpret_cast<uint32_t*>(a_fp8 + row * F + g[k] * kGroup + 4 * lane) = codes;
-            if (lane == 0) a_scale[row * G + g[k]] = static_cast<uint8_t>(scale);
-            if (kCheckpoint) {
-                uint32_t sg, su;
-                const uint32_t cg = quantize4(fg, sg);
-                const uint32_t cu = quantize4(fu, su);
-                uint8_t* q = z_fp8 + 2 * row * F + g[k] * kGroup + 4 * lane;
-                *reinterpret_cast<uint32_t*>(q) = cg;
-                *reinterpret_cast<uint32_t*>(q + F) = cu;
-                if (lane < 2)
-                    z_scale[(2 * row + lane) * G + g[k]] = static_cast<uint8_t>(lane ? su : sg);
+        for (int p = 0; p < 4; ++p)
+            h[p] = ptx::mul_f32x2(ptx::mul_f32x2(g[p], sigmoid2(g[p])), u[p]);
+        uint32_t scale, sg, su;
+        const uint2 codes = quantize8(h, half, scale);
+        if (real) {
+            *reinterpret_cast<uint2*>(a_fp8 + at.i * kGroup + 8 * j) = codes;
+            if (j == 0) a_scale[at.i] = static_cast<uint8_t>(scale);
+        }
+        if (kCheckpoint) {
+            const uint2 cg = quantize8(g, half, sg);
+            const uint2 cu = quantize8(u, half, su);
+            if (real) {
+                *reinterpret_cast<uint2*>(z_fp8 + z_at) = cg;
+                *reinterpret_cast<uint2*>(z_fp8 + z_at + F) = cu;
+                if (j < 2) z_scale[at.i + (at.r + j) * G] = static_cast<uint8_t>(j ? su : sg);
             }
         }
     }
@@ -119,58 +143,36 @@ swiglu_bwd_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restrict__ z
                   const uint8_t* __restrict__ z_scale, int rows, int F,
                   uint16_t* __restrict__ dz) {
     const int G = F / kGroup;
-    const int lane = threadIdx.x & 31;
-    const int step = gridDim.x * (kThreads / 32);
+    const int j = threadIdx.x & 15;
+    const int step = gridDim.x * kBlockGroups;
     const int step_r = step / G, step_g = step - step_r * G;
-    Walk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), G);
-    while (at.r < rows) {
-        int r[kUnder], g[kUnder];
-        uint2 vd[kUnder];
-        uint32_t vg[kUnder], vu[kUnder], sg[kUnder], su[kUnder];
+    const uint64_t one = ptx::f32x2(1.0f, 1.0f), minus = ptx::f32x2(-1.0f, -1.0f);
+    Walk at(blockIdx.x * kBlockGroups + (threadIdx.x >> 4), G);
+    for (; at.r < rows; at.next(step, step_r, step_g, G)) {
+        const long long z_at = at.i * kGroup + at.r * F + 8 * j;
+        const uint8_t* s_at = z_scale + (at.i + at.r * G);
+        const uint4 vd = __ldcs(reinterpret_cast<const uint4*>(dh + at.i * kGroup + 8 * j));
+        const uint2 vg = __ldcs(reinterpret_cast<const uint2*>(z_fp8 + z_at));
+        const uint2 vu = __ldcs(reinterpret_cast<const uint2*>(z_fp8 + z_at + F));
+        const float scale_g = e8m0_value(__ldg(s_at)), scale_u = e8m0_value(__ldg(s_at + G));
+        const uint64_t sg = ptx::f32x2(scale_g, scale_g), su = ptx::f32x2(scale_u, scale_u);
+        uint32_t og[4], ou[4];
 #pragma unroll
-        for (int k = 0; k < kUnder; ++k) {
-            r[k] = at.r;
-            g[k] = at.g;
-            at.next(step_r, step_g, G);
-            vd[k] = make_uint2(0, 0);
-            vg[k] = vu[k] = sg[k] = su[k] = 0;
-            if (r[k] < rows) {
-                const long long row = r[k];
-                const int col = g[k] * kGroup + 4 * lane;
-                vd[k] = __ldcs(reinterpret_cast<const uint2*>(dh + row * F + col));
-                vg[k] = __ldcs(reinterpret_cast<const uint32_t*>(z_fp8 + 2 * row * F + col));
-                vu[k] = __ldcs(reinterpret_cast<const uint32_t*>(z_fp8 + (2 * row + 1) * F + col));
-                sg[k] = __ldg(z_scale + 2 * row * G + g[k]);
-                su[k] = __ldg(z_scale + (2 * row + 1) * G + g[k]);
-            }
+        for (int p = 0; p < 4; ++p) {
+            const uint64_t d = bf16_pair(p == 0 ? vd.x : p == 1 ? vd.y : p == 2 ? vd.z : vd.w);
+            const uint64_t g = ptx::mul_f32x2(e4m3_pair((p < 2 ? vg.x : vg.y) >> 16 * (p & 1)), sg);
+            const uint64_t u = ptx::mul_f32x2(e4m3_pair((p < 2 ? vu.x : vu.y) >> 16 * (p & 1)), su);
+            const uint64_t s = sigmoid2(g);
+            const uint64_t slope = ptx::fma_f32x2(g, ptx::fma_f32x2(s, minus, one), one);
+            og[p] = bf16_pack_pair(ptx::mul_f32x2(ptx::mul_f32x2(ptx::mul_f32x2(d, u), s), slope));
+            ou[p] = bf16_pack_pair(ptx::mul_f32x2(ptx::mul_f32x2(d, g), s));
         }
-#pragma unroll
-        for (int k = 0; k < kUnder; ++k) {
-            if (r[k] >= rows) break;
-            const float d[4] = {bf16_lo(vd[k].x), bf16_hi(vd[k].x), bf16_lo(vd[k].y),
-                                bf16_hi(vd[k].y)};
-            float fg[4], fu[4], og[4], ou[4];
-            e4m3_unpack4(vg[k], fg);
-            e4m3_unpack4(vu[k], fu);
-            const float scale_g = e8m0_value(sg[k]), scale_u = e8m0_value(su[k]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float gv = fg[e] * scale_g;
-                const float uv = fu[e] * scale_u;
-                const float s = sigmoid(gv);
-                og[e] = d[e] * uv * s * (1.0f + gv * (1.0f - s));
-                ou[e] = d[e] * gv * s;
-            }
-            uint16_t* o = dz + 2ll * r[k] * F + g[k] * kGroup + 4 * lane;
-            *reinterpret_cast<uint2*>(o) = make_uint2(bf16_pack(og[0], og[1]),
-                                                      bf16_pack(og[2], og[3]));
-            *reinterpret_cast<uint2*>(o + F) = make_uint2(bf16_pack(ou[0], ou[1]),
-                                                          bf16_pack(ou[2], ou[3]));
-        }
+        *reinterpret_cast<uint4*>(dz + z_at) = make_uint4(og[0], og[1], og[2], og[3]);
+        *reinterpret_cast<uint4*>(dz + z_at + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
     }
 }
 
-// Blocks: a warp for each pair of groups, at most what is resident at once.
+// Blocks: a half-warp for each group, at most what is resident at once.
 int grid_blocks(int rows, int F, const void* kernel, int num_sms) {
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0) !=
@@ -178,8 +180,7 @@ int grid_blocks(int rows, int F, const void* kernel, int num_sms) {
         per_sm < 1)
         per_sm = 1;
     const long long groups = static_cast<long long>(rows) * (F / kGroup);
-    const long long per_block = kThreads / 32 * kUnder;
-    const long long blocks = (groups + per_block - 1) / per_block;
+    const long long blocks = (groups + kBlockGroups - 1) / kBlockGroups;
     const long long cap = static_cast<long long>(num_sms) * per_sm;
     return static_cast<int>(blocks < cap ? blocks : cap);
 }
