@@ -692,11 +692,8 @@ hg_status hg_router_topk(const float* logits, int32_t M, int32_t E, int32_t top_
     if (!logits || !topk_ids || !topk_weights) return HG_ERR_INVALID_ARG;
     if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
         return HG_ERR_INVALID_ARG;
-    DeviceInfo* d = nullptr;
-    hg_status st = device_info(&d);
-    if (st != HG_OK) return st;
     return launch_router_topk(logits, M, E, top_k, renormalize != 0, topk_ids, topk_weights,
-                              d->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK
                : HG_ERR_CUDA;
 }
@@ -713,11 +710,8 @@ hg_status hg_router_topk_bwd(const float* logits, const int32_t* topk_ids,
     if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
         !aligned(dweights, 4) || !aligned(dlogits, 4))
         return HG_ERR_INVALID_ARG;
-    DeviceInfo* d = nullptr;
-    hg_status st = device_info(&d);
-    if (st != HG_OK) return st;
     return launch_router_topk_bwd(logits, topk_ids, topk_weights, dweights, M, E, top_k,
-                                  renormalize != 0, dlogits, d->num_sms,
+                                  renormalize != 0, dlogits,
                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK
                : HG_ERR_CUDA;

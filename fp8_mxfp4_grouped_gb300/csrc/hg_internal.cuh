@@ -196,11 +196,10 @@ constexpr int kMatvecMaxSlots = 512;
 constexpr int kMatvecMaxK = 32768;
 
 cudaError_t launch_router_topk(const float* logits, int M, int E, int top_k, int renormalize,
-                               int32_t* ids, float* weights, int num_sms, cudaStream_t stream);
+                               int32_t* ids, float* weights, cudaStream_t stream);
 cudaError_t launch_router_topk_bwd(const float* logits, const int32_t* ids, const float* weights,
                                    const float* dweights, int M, int E, int top_k,
-                                   int renormalize, float* dlogits, int num_sms,
-                                   cudaStream_t stream);
+                                   int renormalize, float* dlogits, cudaStream_t stream);
 int router_max_top_k();
 
 }  // namespace hg

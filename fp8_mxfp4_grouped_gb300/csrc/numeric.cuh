@@ -37,6 +37,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return m;
 }
 
+// Largest value over the warp, NaN aside.
+__device__ __forceinline__ float warp_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
 // Largest magnitude over the warp; NaN if any is.
 __device__ __forceinline__ float warp_abs_max(float v) {
     float m;

@@ -10,16 +10,27 @@
 // it is never chosen, and a token with fewer than top_k open experts gets id -1
 // (which the routing plan drops) and weight 0 in the places left over.  A NaN
 // or +inf among a token's logits makes its weights NaN; a NaN logit itself is
-// never chosen.  One warp a token; everything is FP32.
+// never chosen.
+//
+// One warp a token, everything in FP32.  Both passes move one row of logits (the
+// gradient also writes one), 640 bytes for 160 experts: little enough that
+// instructions count.  The row stays in registers (up to 512 experts); a choice
+// is a warp-wide maximum and a warp-wide minimum of the index, one reduction
+// instruction each, and only the lane that owned it looks at its values again.
+// The gradient needs no softmax of its own: the first choice is the row's
+// largest logit and its weight 1 / sum, so that p_e = exp(l_e - l_first) *
+// w_first.
 #include <math_constants.h>
 
 #include "hg_internal.cuh"
+#include "numeric.cuh"
 
 namespace hg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxTopK = 32;       // one choice a lane
+constexpr int kMaxHeld = 16;       // logits a lane holds in registers
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -27,76 +38,93 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// The row of a token, lane l holding experts l, l + 32, ...: in registers
+// (kHeld of them), or read again each time (kHeld = 0).  NaN reads as -inf.
+template <int kHeld>
+struct Row {
+    const float* at;
+    int E, lane;
+    float v[kHeld ? kHeld : 1];
+    bool nan = false;
+
+    __device__ Row(const float* row, int E_, int lane_) : at(row), E(E_), lane(lane_) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-}
-
-// Largest logit (NaN aside) and the sum of exp(logit - largest), NaN included;
-// a row of -inf gives (-inf, 0).
-__device__ __forceinline__ void softmax_stats(const float* row, int E, int lane, float& top,
-                                              float& sum) {
-    top = -CUDART_INF_F;
-    for (int e = lane; e < E; e += 32) top = fmaxf(top, __ldg(row + e));
-    top = warp_max(top);
-    sum = 0.0f;
-    for (int e = lane; e < E; e += 32) {
-        const float l = __ldg(row + e);
-        if (l != -CUDART_INF_F) sum += expf(l - top);
+        for (int i = 0; i < kHeld; ++i) v[i] = read(i);
+        if (kHeld == 0) {
+            for (int i = 0; lane + 32 * i < E; ++i) read(i);
+        }
     }
-    sum = warp_sum(sum);
-}
+    __device__ float read(int i) {
+        if (lane + 32 * i >= E) return -CUDART_INF_F;
+        const float l = __ldg(at + lane + 32 * i);
+        nan |= isnan(l);
+        return isnan(l) ? -CUDART_INF_F : l;
+    }
+    template <class F>
+    __device__ void each(F f) {
+        if (kHeld) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) f(lane + 32 * i, v[i]);
+        } else {
+            for (int i = 0; lane + 32 * i < E; ++i) f(lane + 32 * i, read(i));
+        }
+    }
+};
 
+template <int kHeld>
 __global__ void __launch_bounds__(kThreads)
 router_topk_kernel(const float* __restrict__ logits, int M, int E, int top_k, int renormalize,
                    int32_t* __restrict__ ids, float* __restrict__ weights) {
     const int lane = threadIdx.x & 31;
-    const long long nw = (static_cast<long long>(gridDim.x) * kThreads) >> 5;
-    for (long long t = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5; t < M;
-         t += nw) {
-        const float* row = logits + t * E;
-        float top, sum;
-        softmax_stats(row, E, lane, top, sum);
-        // the largest logit below the one chosen before, in the order (value
-        // descending, index ascending)
-        float last = CUDART_INF_F, mine = 0.0f;
-        int last_e = -1, mine_e = -1;
-        for (int c = 0; c < top_k; ++c) {
-            float best = -CUDART_INF_F;
-            int best_e = 0x7FFFFFFF;
-            for (int e = lane; e < E; e += 32) {
-                const float l = __ldg(row + e);
-                if ((l < last || (l == last && e > last_e)) &&
-                    (l > best || (l == best && e < best_e))) {
-                    best = l;
-                    best_e = e;
-                }
+    const long long t = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (t >= M) return;
+    Row<kHeld> row(logits + t * E, E, lane);
+
+    // This lane's largest logit below what it has given away (last, last_e), in
+    // the order (value descending, index ascending).
+    float best, last = CUDART_INF_F;
+    int best_e, last_e = -1;
+    auto look = [&]() {
+        best = -CUDART_INF_F;
+        best_e = 0x7FFFFFFF;
+        row.each([&](int e, float l) {
+            if (l > best && (l < last || (l == last && e > last_e))) {
+                best = l;
+                best_e = e;
             }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) {
-                const float l = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-                const int e = __shfl_xor_sync(0xFFFFFFFFu, best_e, o);
-                if (l > best || (l == best && e < best_e)) {
-                    best = l;
-                    best_e = e;
-                }
-            }
-            if (best == -CUDART_INF_F) break;      // no open expert is left
-            last = best;
-            last_e = best_e;
-            if (lane == c) {
-                mine = best;
-                mine_e = best_e;
-            }
+        });
+    };
+    look();
+    const float top = warp_max(best);
+    float sum = 0.0f;
+    row.each([&](int e, float l) {
+        if (l != -CUDART_INF_F) sum += expf(l - top);
+    });
+    sum = warp_sum(sum);
+    if (__any_sync(0xFFFFFFFFu, row.nan)) sum = CUDART_NAN_F;
+
+    float mine = 0.0f;
+    int mine_e = -1;
+    for (int c = 0; c < top_k; ++c) {
+        const float l = warp_max(best);
+        if (l == -CUDART_INF_F) break;       // no open expert is left
+        const int e = __reduce_min_sync(0xFFFFFFFFu, best == l ? best_e : 0x7FFFFFFF);
+        if (lane == c) {
+            mine = l;
+            mine_e = e;
         }
-        float w = mine_e >= 0 ? expf(mine - top) : 0.0f;
-        const float den = renormalize && !isnan(sum) ? warp_sum(w) : sum;
-        if (mine_e >= 0) w /= den;
-        if (lane < top_k) {
-            ids[t * top_k + lane] = mine_e;
-            weights[t * top_k + lane] = w;
+        if (best_e == e) {
+            last = l;
+            last_e = e;
+            look();
         }
+    }
+    float w = mine_e >= 0 ? expf(mine - top) : 0.0f;
+    const float den = renormalize && !isnan(sum) ? warp_sum(w) : sum;
+    if (mine_e >= 0) w /= den;
+    if (lane < top_k) {
+        ids[t * top_k + lane] = mine_e;
+        weights[t * top_k + lane] = w;
     }
 }
 
@@ -105,44 +133,42 @@ router_topk_bwd_kernel(const float* __restrict__ logits, const int32_t* __restri
                        const float* __restrict__ weights, const float* __restrict__ dweights,
                        int M, int E, int top_k, int renormalize, float* __restrict__ dlogits) {
     const int lane = threadIdx.x & 31;
-    const long long nw = (static_cast<long long>(gridDim.x) * kThreads) >> 5;
-    for (long long t = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5; t < M;
-         t += nw) {
-        int id = -1;
-        float w = 0.0f, dw = 0.0f;
-        if (lane < top_k) {
-            id = __ldg(ids + t * top_k + lane);
-            if (id >= 0 && id < E) {
-                w = __ldg(weights + t * top_k + lane);
-                dw = __ldg(dweights + t * top_k + lane);
-            } else {
-                id = -1;
-            }
-        }
-        const float inner = warp_sum(w * dw);
-        float top = 0.0f, sum = 1.0f;
-        if (!renormalize) softmax_stats(logits + t * E, E, lane, top, sum);
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            float d = 0.0f;
-            if (!renormalize && e < E) {
-                const float l = __ldg(logits + t * E + e);
-                if (l != -CUDART_INF_F) d = -(expf(l - top) / sum) * inner;
-            }
-            for (int c = 0; c < top_k; ++c) {
-                const int ic = __shfl_sync(0xFFFFFFFFu, id, c);
-                const float wc = __shfl_sync(0xFFFFFFFFu, w, c);
-                const float dc = __shfl_sync(0xFFFFFFFFu, dw, c);
-                if (ic == e) d += renormalize ? wc * (dc - inner) : wc * dc;
-            }
-            if (e < E) dlogits[t * E + e] = d;
+    const long long t = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (t >= M) return;
+    int id = -1;
+    float w = 0.0f, dw = 0.0f;
+    if (lane < top_k) {
+        id = __ldg(ids + t * top_k + lane);
+        if (id >= 0 && id < E) {
+            w = __ldg(weights + t * top_k + lane);
+            dw = __ldg(dweights + t * top_k + lane);
+        } else {
+            id = -1;
         }
     }
+    const float inner = warp_sum(w * dw);
+    const int first = __shfl_sync(0xFFFFFFFFu, id, 0);
+    float* out = dlogits + t * E;
+    if (renormalize || first < 0) {
+        for (int e = lane; e < E; e += 32) out[e] = 0.0f;
+    } else {
+        const float* row = logits + t * E;
+        const float top = __ldg(row + first);
+        const float scale = -__shfl_sync(0xFFFFFFFFu, w, 0) * inner;
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) out[e] = expf(__ldg(row + e) - top) * scale;
+    }
+    __syncwarp();                            // the chosen ones' values come last
+    if (id >= 0) out[id] = w * (dw - inner);
 }
 
-int grid_blocks(int M, int num_sms) {
-    const int blocks = (M + kThreads / 32 - 1) / (kThreads / 32);
-    return blocks < num_sms * 8 ? blocks : num_sms * 8;
+template <int kHeld>
+cudaError_t launch_topk(const float* logits, int M, int E, int top_k, int renormalize,
+                        int32_t* ids, float* weights, cudaStream_t stream) {
+    const int grid = (M + kThreads / 32 - 1) / (kThreads / 32);
+    router_topk_kernel<kHeld><<<grid, kThreads, 0, stream>>>(logits, M, E, top_k, renormalize, ids,
+                                                             weights);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -150,18 +176,23 @@ int grid_blocks(int M, int num_sms) {
 int router_max_top_k() { return kMaxTopK; }
 
 cudaError_t launch_router_topk(const float* logits, int M, int E, int top_k, int renormalize,
-                               int32_t* ids, float* weights, int num_sms, cudaStream_t stream) {
-    router_topk_kernel<<<grid_blocks(M, num_sms), kThreads, 0, stream>>>(logits, M, E, top_k,
-                                                                         renormalize, ids, weights);
-    return cudaGetLastError();
+                               int32_t* ids, float* weights, cudaStream_t stream) {
+    const int held = (E + 31) / 32;
+    const auto launch = held <= 1    ? launch_topk<1>
+                        : held <= 2  ? launch_topk<2>
+                        : held <= 4  ? launch_topk<4>
+                        : held <= 8  ? launch_topk<8>
+                        : held <= kMaxHeld ? launch_topk<kMaxHeld>
+                                           : launch_topk<0>;
+    return launch(logits, M, E, top_k, renormalize, ids, weights, stream);
 }
 
 cudaError_t launch_router_topk_bwd(const float* logits, const int32_t* ids, const float* weights,
                                    const float* dweights, int M, int E, int top_k,
-                                   int renormalize, float* dlogits, int num_sms,
-                                   cudaStream_t stream) {
-    router_topk_bwd_kernel<<<grid_blocks(M, num_sms), kThreads, 0, stream>>>(
-        logits, ids, weights, dweights, M, E, top_k, renormalize, dlogits);
+                                   int renormalize, float* dlogits, cudaStream_t stream) {
+    const int grid = (M + kThreads / 32 - 1) / (kThreads / 32);
+    router_topk_bwd_kernel<<<grid, kThreads, 0, stream>>>(logits, ids, weights, dweights, M, E,
+                                                          top_k, renormalize, dlogits);
     return cudaGetLastError();
 }
 
