@@ -20,6 +20,7 @@ constexpr int kMaxDevices = 64;
 constexpr int kPlanMaxThreads = 512;
 constexpr int kPlanIdsPerBlock = 2048;
 constexpr int kPlanMaxBlocks = 256;
+constexpr int32_t kMaxRowElements = 1 << 30;     // of a token row: kernels index it with int32
 
 struct DeviceInfo {
     bool ready = false;
@@ -569,17 +570,14 @@ hg_status hg_dispatch_tokens(const uint16_t* x_bf16, const int32_t* src_to_sorte
                              const float* topk_weights, int32_t M, int32_t top_k, int32_t K,
                              uint16_t* rows_bf16, hg_stream_t stream) {
     if (M < 0 || top_k < 1 || K < 1) return HG_ERR_INVALID_ARG;
-    if (K % 8 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (K % 8 != 0 || K > kMaxRowElements) return HG_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<long long>(M) * top_k > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return HG_OK;
     if (!x_bf16 || !src_to_sorted || !rows_bf16) return HG_ERR_INVALID_ARG;
     if (!aligned(x_bf16, 16) || !aligned(rows_bf16, 16) || !aligned(src_to_sorted, 4) ||
         !aligned(topk_weights, 4))
         return HG_ERR_INVALID_ARG;
-    DeviceInfo* d = nullptr;
-    hg_status st = device_info(&d);
-    if (st != HG_OK) return st;
-    return launch_dispatch(x_bf16, src_to_sorted, topk_weights, M, top_k, K, rows_bf16, d->num_sms,
+    return launch_dispatch(x_bf16, src_to_sorted, topk_weights, M, top_k, K, rows_bf16,
                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK
                : HG_ERR_CUDA;
@@ -590,7 +588,7 @@ hg_status hg_dispatch_tokens_bwd(const uint16_t* drows_bf16, const uint16_t* x_b
                                  int32_t M, int32_t top_k, int32_t K, uint16_t* dx_bf16,
                                  float* dweights, hg_stream_t stream) {
     if (M < 0 || top_k < 1 || K < 1) return HG_ERR_INVALID_ARG;
-    if (K % 8 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (K % 8 != 0 || K > kMaxRowElements) return HG_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<long long>(M) * top_k > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
     if ((x_bf16 == nullptr) != (dweights == nullptr)) return HG_ERR_INVALID_ARG;
     if (M == 0) return HG_OK;
@@ -598,12 +596,8 @@ hg_status hg_dispatch_tokens_bwd(const uint16_t* drows_bf16, const uint16_t* x_b
     if (!aligned(drows_bf16, 16) || !aligned(x_bf16, 16) || !aligned(dx_bf16, 16) ||
         !aligned(src_to_sorted, 4) || !aligned(topk_weights, 4) || !aligned(dweights, 4))
         return HG_ERR_INVALID_ARG;
-    DeviceInfo* d = nullptr;
-    hg_status st = device_info(&d);
-    if (st != HG_OK) return st;
     return launch_dispatch_bwd(drows_bf16, x_bf16, src_to_sorted, topk_weights, M, top_k, K,
-                               dx_bf16, dweights, d->num_sms,
-                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                               dx_bf16, dweights, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK
                : HG_ERR_CUDA;
 }
@@ -613,7 +607,7 @@ hg_status hg_combine_topk_bwd(const uint16_t* dout_bf16, const uint16_t* y_bf16,
                               int32_t top_k, int32_t N, uint16_t* dy_bf16, float* dweights,
                               hg_stream_t stream) {
     if (M < 0 || top_k < 1 || N < 1) return HG_ERR_INVALID_ARG;
-    if (N % 8 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (N % 8 != 0 || N > kMaxRowElements) return HG_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<long long>(M) * top_k > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return HG_OK;
     if (!dout_bf16 || !y_bf16 || !src_to_sorted || !topk_weights || !dy_bf16 || !dweights)
@@ -621,12 +615,8 @@ hg_status hg_combine_topk_bwd(const uint16_t* dout_bf16, const uint16_t* y_bf16,
     if (!aligned(dout_bf16, 16) || !aligned(y_bf16, 16) || !aligned(dy_bf16, 16) ||
         !aligned(src_to_sorted, 4) || !aligned(topk_weights, 4) || !aligned(dweights, 4))
         return HG_ERR_INVALID_ARG;
-    DeviceInfo* d = nullptr;
-    hg_status st = device_info(&d);
-    if (st != HG_OK) return st;
     return launch_combine_bwd(dout_bf16, y_bf16, src_to_sorted, topk_weights, M, top_k, N, dy_bf16,
-                              dweights, d->num_sms,
-                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                              dweights, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK
                : HG_ERR_CUDA;
 }

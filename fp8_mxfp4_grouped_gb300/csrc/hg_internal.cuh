@@ -158,13 +158,13 @@ cudaError_t launch_combine_topk(const uint16_t* y, const int32_t* d2s, const flo
                                 cudaStream_t stream);
 
 cudaError_t launch_dispatch(const uint16_t* x, const int32_t* d2s, const float* weights, int M,
-                            int top_k, int K, uint16_t* rows, int num_sms, cudaStream_t stream);
+                            int top_k, int K, uint16_t* rows, cudaStream_t stream);
 cudaError_t launch_dispatch_bwd(const uint16_t* drows, const uint16_t* x, const int32_t* d2s,
                                 const float* weights, int M, int top_k, int K, uint16_t* dx,
-                                float* dw, int num_sms, cudaStream_t stream);
+                                float* dw, cudaStream_t stream);
 cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, const int32_t* d2s,
                                const float* weights, int M, int top_k, int N, uint16_t* dy,
-                               float* dw, int num_sms, cudaStream_t stream);
+                               float* dw, cudaStream_t stream);
 
 cudaError_t launch_swiglu_quantize(const uint16_t* z, int rows, int F, uint8_t* a_fp8,
                                    uint8_t* a_scale, uint8_t* z_fp8, uint8_t* z_scale, int num_sms,

@@ -335,7 +335,7 @@ hg_status hg_combine_topk(const uint16_t* y_bf16, const int32_t* src_to_sorted,
  *   topk_weights   float32 [M, top_k], or NULL for a plain copy (w = 1).
  *   rows_bf16      uint16 [M*top_k, K] out, 16-byte aligned; rows no entry names
  *                  are not written.
- * K % 8 == 0.  Every token is read once.  One kernel on `stream`; no host
+ * K % 8 == 0, K <= 2^30.  Every token is read once.  One kernel on `stream`; no host
  * synchronisation.
  */
 hg_status hg_dispatch_tokens(const uint16_t* x_bf16, const int32_t* src_to_sorted,
@@ -358,7 +358,7 @@ hg_status hg_dispatch_tokens(const uint16_t* x_bf16, const int32_t* src_to_sorte
  *   topk_weights  float32 [M, top_k], or NULL (w = 1).
  *   dx_bf16       uint16 [M, K] out, 16-byte aligned.
  *   dweights      float32 [M, top_k] out, with x_bf16; else NULL.
- * K % 8 == 0.  One kernel on `stream`; no host synchronisation.
+ * K % 8 == 0, K <= 2^30.  One kernel on `stream`; no host synchronisation.
  */
 hg_status hg_dispatch_tokens_bwd(const uint16_t* drows_bf16, const uint16_t* x_bf16,
                                  const int32_t* src_to_sorted, const float* topk_weights,
@@ -379,7 +379,7 @@ hg_status hg_dispatch_tokens_bwd(const uint16_t* drows_bf16, const uint16_t* x_b
  *   src_to_sorted  int32 [M*top_k]; topk_weights float32 [M, top_k].
  *   dy_bf16        uint16 [M*top_k, N] out, 16-byte aligned (not y_bf16).
  *   dweights       float32 [M, top_k] out.
- * N % 8 == 0.  One kernel on `stream`; no host synchronisation.
+ * N % 8 == 0, N <= 2^30.  One kernel on `stream`; no host synchronisation.
  */
 hg_status hg_combine_topk_bwd(const uint16_t* dout_bf16, const uint16_t* y_bf16,
                               const int32_t* src_to_sorted, const float* topk_weights, int32_t M,
