@@ -130,15 +130,15 @@ __device__ __forceinline__ float warp_sum8(const float (&d)[8]) {
 
 // kSum: the gradient of the dispatch (out[t] = sum of the weighted rows);
 // otherwise the gradient of the combine (out rows = w * token row).
-// kDots: dw as well (always with the combine).
-template <bool kSum, bool kDots, int kPieces>
-__global__ void __launch_bounds__(kThreads)
+// kDots: dw as well (always with the combine).  kFlight: rows in flight; kBlocks:
+// blocks per SM.
+template <bool kSum, bool kDots, int kPieces, int kFlight, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks)
 token_grad_kernel(const uint16_t* __restrict__ rows, const uint16_t* __restrict__ token,
                   const int32_t* __restrict__ place, const float* __restrict__ weights, int M,
                   int top_k, int N, int team_warps, uint16_t* __restrict__ out,
                   float* __restrict__ dw) {
     __shared__ float s_part[kWarps * kBatch];
-    constexpr int kFlight = kPieces < 3 ? 8 / kPieces : kPieces == 3 ? 4 : 2;   // rows in flight
     static_assert(kBatch % kFlight == 0, "a batch is whole groups of rows in flight");
     const Team team(team_warps);
     const bool real = team.token < M;        // a block's last teams may have no token
@@ -262,18 +262,34 @@ struct Shape {
     }
 };
 
+// Two rows in flight and three or four blocks per SM against four rows and two
+// blocks: 489 against 504 us for the combine's gradient (M = 16384, N = 6144,
+// top-8), 353 against 365 for the dispatch's with dw, 63 against 77 without (M
+// = 4096), where the sums alone leave registers for a fourth block.  With
+// one choice a second row would be no row.
+template <bool kSum, bool kDots, int kPieces>
+cudaError_t launch_pieces(const Shape& s, const uint16_t* rows, const uint16_t* token,
+                          const int32_t* d2s, const float* weights, int M, int top_k, int N,
+                          uint16_t* out, float* dw, cudaStream_t stream) {
+    constexpr int kBlocks = kPieces == 4 ? (kSum ? 2 : 3) : kDots && kPieces == 3 ? 3 : 4;
+    constexpr int kSingleBlocks = kPieces < 3 ? 4 : kSum && kPieces == 4 ? 2 : 3;
+    const auto kernel = top_k == 1 ? token_grad_kernel<kSum, kDots, kPieces, 1, kSingleBlocks>
+                                   : token_grad_kernel<kSum, kDots, kPieces, 2, kBlocks>;
+    kernel<<<s.blocks(M), kThreads, 0, stream>>>(rows, token, d2s, weights, M, top_k, N,
+                                                 s.team_warps, out, dw);
+    return cudaGetLastError();
+}
+
 template <bool kSum, bool kDots>
 cudaError_t launch_grad(const uint16_t* rows, const uint16_t* token, const int32_t* d2s,
                         const float* weights, int M, int top_k, int N, uint16_t* out, float* dw,
                         cudaStream_t stream) {
     const Shape s(N);
-    const auto kernel = s.pieces == 1   ? token_grad_kernel<kSum, kDots, 1>
-                        : s.pieces == 2 ? token_grad_kernel<kSum, kDots, 2>
-                        : s.pieces == 3 ? token_grad_kernel<kSum, kDots, 3>
-                                        : token_grad_kernel<kSum, kDots, 4>;
-    kernel<<<s.blocks(M), kThreads, 0, stream>>>(rows, token, d2s, weights, M, top_k, N,
-                                                 s.team_warps, out, dw);
-    return cudaGetLastError();
+    const auto launch = s.pieces == 1   ? launch_pieces<kSum, kDots, 1>
+                        : s.pieces == 2 ? launch_pieces<kSum, kDots, 2>
+                        : s.pieces == 3 ? launch_pieces<kSum, kDots, 3>
+                                        : launch_pieces<kSum, kDots, 4>;
+    return launch(s, rows, token, d2s, weights, M, top_k, N, out, dw, stream);
 }
 
 }  // namespace
