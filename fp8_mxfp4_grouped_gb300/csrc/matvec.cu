@@ -34,6 +34,8 @@
 // added up in FP32 times the product of the two scales.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "hg_internal.cuh"
 #include "numeric.cuh"
 
@@ -65,20 +67,36 @@ __host__ __device__ constexpr Form form_of(bool single) {
     return single ? Form{16, 1, 2, 2} : Form{8, 2, 1, 4};
 }
 
+struct __align__(8) Entry {
+    int expert;                              // -1: free
+    int first;                               // the expert's first slot
+    uint8_t slots[kMatvecMaxSlots / 32];     // how many it has in each 32 slots
+};
+
 // The slots by expert: an entry per slot or chunk (there are at most as many
-// chunks as slots).
+// chunks as slots), and a hash table of the experts.
 struct Tables {
     int* count;              // [0] chunks, [1] slots without an expert
     int* id;                 // of a slot; -1 without an expert
-    int* rank;               // of a slot among its expert's
-    int2* key;               // of a chunk: expert, and which of the expert's chunks
+    int* expert;             // of a chunk
     int* ncols;              // of a chunk
     uint16_t* slot;          // of a chunk's columns: chunk * cols + column
+    // more than 32 slots only
+    uint32_t* leads;         // a bit per slot: the first of a chunk
+    Entry* hash;             // by expert
 };
+
+// A power of two, twice the slots at least.
+__host__ __device__ inline int hash_entries(int slots) {
+    int n = 64;
+    while (n < 2 * slots) n *= 2;
+    return n;
+}
 
 __host__ __device__ inline int table_bytes(int slots, int cols) {
     const int n = (slots + 3) & ~3;
-    return 16 + n * (5 * 4 + 2 * cols);
+    const int hash = static_cast<int>(sizeof(Entry)) * hash_entries(slots);
+    return 16 + n * (3 * 4 + 2 * cols) + (slots > 32 ? kMatvecMaxSlots / 8 + hash : 0);
 }
 
 __device__ inline Tables tables_at(uint8_t* p, int slots, int cols) {
@@ -86,10 +104,11 @@ __device__ inline Tables tables_at(uint8_t* p, int slots, int cols) {
     Tables t;
     t.count = reinterpret_cast<int*>(p);
     t.id = t.count + 4;
-    t.rank = t.id + n;
-    t.key = reinterpret_cast<int2*>(t.rank + n);
-    t.ncols = reinterpret_cast<int*>(t.key + n);
+    t.expert = t.id + n;
+    t.ncols = t.expert + n;
     t.slot = reinterpret_cast<uint16_t*>(t.ncols + n);
+    t.leads = reinterpret_cast<uint32_t*>(t.slot + n * cols);
+    t.hash = reinterpret_cast<Entry*>(t.leads + kMatvecMaxSlots / 32);
     return t;
 }
 
@@ -167,7 +186,8 @@ struct KernelArgs {
 };
 
 // List the slots by expert in chunks of up to `cols`, in the order of the
-// chunks' first slots.  Returns the number of chunks.
+// chunks' first slots: every block makes the same list.  Returns the number of
+// chunks.
 template <int kThreads>
 __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
     const int tid = threadIdx.x;
@@ -192,7 +212,7 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
                 const int c = __popc(leads & ((1u << lead) - 1u));
                 tb.slot[c * cols + col] = static_cast<uint16_t>(tid);
                 if (col == 0) {
-                    tb.key[c] = make_int2(e, nth);
+                    tb.expert[c] = e;
                     tb.ncols[c] = min(cols, __popc(same) - rank);
                 }
             }
@@ -204,85 +224,97 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
         __syncthreads();
         return tb.count[0];
     }
-    const int n = (a.slots + 3) & ~3;
-    for (int s = tid; s < n; s += kThreads) tb.id[s] = expert_of(s);
-    __syncthreads();
-    for (int s = tid; s < a.slots; s += kThreads) {
-        const int e = tb.id[s];
-        int rank = 0;
-        const int4* four = reinterpret_cast<const int4*>(tb.id);
-#pragma unroll 4
-        for (int j = 0; j < s >> 2; ++j) {
-            const int4 v = four[j];
-            rank += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
-        }
-        const int4 v = four[s >> 2];
-        rank += (s % 4 > 0 && v.x == e) + (s % 4 > 1 && v.y == e) + (s % 4 > 2 && v.z == e);
-        tb.rank[s] = rank;
+    constexpr int kTurns = kMatvecMaxSlots / kThreads;       // slots per thread
+    const int mask = hash_entries(a.slots) - 1, words = (a.slots + 31) / 32;
+    int e[kTurns], h[kTurns], rank[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) e[i] = expert_of(tid + i * kThreads);
+    for (int i = tid; i <= mask; i += kThreads) {
+        Entry& t = tb.hash[i];
+        t.expert = -1;
+        t.first = kMatvecMaxSlots;
+#pragma unroll
+        for (int w = 0; w < kMatvecMaxSlots / 32; w += 4)
+            *reinterpret_cast<uint32_t*>(t.slots + w) = 0;
     }
+    for (int i = tid; i < a.slots; i += kThreads) tb.ncols[i] = 0;
+    if (tid == 0) tb.count[1] = 0;
     __syncthreads();
-    if (tid < 32) {                          // number the chunks in order of their first slots
-        int total = 0, valid = 0;
-        for (int s0 = 0; s0 < a.slots; s0 += 32) {
-            const int s = s0 + tid;
-            const int e = s < a.slots ? tb.id[s] : -1;
-            const int nth = e >= 0 ? tb.rank[s] / cols : 0;
-            const bool leads = e >= 0 && tb.rank[s] == nth * cols;
-            const uint32_t vote = __ballot_sync(0xFFFFFFFFu, leads);
-            valid += __popc(__ballot_sync(0xFFFFFFFFu, e >= 0));
-            if (leads) {
-                const int c = total + __popc(vote & ((1u << tid) - 1u));
-                tb.key[c] = make_int2(e, nth);
-                tb.ncols[c] = 0;
+    // each expert's slots of each 32, by the first lane that has it
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int s = tid + i * kThreads, lane = tid & 31;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e[i]);
+        const int leader = __ffs(same) - 1;
+        rank[i] = __popc(same & ((1u << lane) - 1u));
+        h[i] = 0;
+        if (e[i] >= 0 && lane == leader) {
+            h[i] = static_cast<int>((static_cast<uint32_t>(e[i]) * 2654435761u) >> 16) & mask;
+            for (;; h[i] = (h[i] + 1) & mask) {              // at most half of the entries are used
+                const int there = atomicCAS(&tb.hash[h[i]].expert, -1, e[i]);
+                if (there == -1 || there == e[i]) break;
             }
-            total += __popc(vote);
+            atomicMin(&tb.hash[h[i]].first, s);
+            tb.hash[h[i]].slots[s >> 5] = static_cast<uint8_t>(__popc(same));
         }
-        if (tid == 0) {
-            tb.count[0] = total;
-            tb.count[1] = a.slots - valid;
+        h[i] = __shfl_sync(0xFFFFFFFFu, h[i], leader);
+        if (s < a.slots) tb.id[s] = e[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int s = tid + i * kThreads;
+        if (e[i] >= 0) {
+            for (int w = 0; w < s >> 5; ++w) rank[i] += tb.hash[h[i]].slots[w];
+        }
+        const uint32_t leads = __ballot_sync(0xFFFFFFFFu, e[i] >= 0 && rank[i] % cols == 0);
+        const uint32_t none = __ballot_sync(0xFFFFFFFFu, s < a.slots && e[i] < 0);
+        if ((tid & 31) == 0 && s < a.slots) {
+            tb.leads[s >> 5] = leads;
+            if (none) atomicAdd(&tb.count[1], __popc(none));
         }
     }
     __syncthreads();
-    const int total = tb.count[0];
-    for (int s = tid; s < a.slots; s += kThreads) {
-        const int e = tb.id[s];
-        const int nth = tb.rank[s] / cols;
-        int c = -1;
-#pragma unroll 4
-        for (int i = 0; i < total; ++i) {
-            const int2 k = tb.key[i];
-            if (k.x == e && k.y == nth) c = i;
-        }
-        if (c < 0) continue;                 // no expert
-        tb.slot[c * cols + tb.rank[s] - nth * cols] = static_cast<uint16_t>(s);
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        if (e[i] < 0) continue;
+        int lead = tb.hash[h[i]].first, skip = rank[i] / cols * cols;
+        const int col = rank[i] - skip;
+        for (; skip > 0; ++lead) skip -= tb.id[lead] == e[i];    // a later chunk of the expert
+        while (tb.id[lead] != e[i]) ++lead;
+        int c = __popc(tb.leads[lead >> 5] & ((1u << (lead & 31)) - 1u));
+        for (int w = 0; w < lead >> 5; ++w) c += __popc(tb.leads[w]);
+        tb.slot[c * cols + col] = static_cast<uint16_t>(tid + i * kThreads);
         atomicAdd(&tb.ncols[c], 1);
+        if (col == 0) tb.expert[c] = e[i];
+    }
+    if (tid == 0) {
+        int total = 0;
+        for (int w = 0; w < words; ++w) total += __popc(tb.leads[w]);
+        tb.count[0] = total;
     }
     __syncthreads();
-    return total;
+    return tb.count[0];
 }
 
-// Input rows go to shared memory in pieces of 256 elements, eight a lane: piece
-// p is part p % parts of held row p / parts, and belongs to warp p % warps.  All
-// pieces are asked for at once, and each is rewritten in place as scaled FP16 by
-// the lanes that asked for it.
-__device__ __forceinline__ void load_piece(const KernelArgs& a, uint32_t base, int held, int part,
-                                           int row, int lane) {
-    const int k = part * kPartK + 8 * lane;
-    const uint16_t* src = a.x + static_cast<long long>(row) * a.K;
-    ptx::cp_async_16(base + a.l.x + held * a.l.x_stride + 2 * k, src + (k < a.K ? k : 0), k < a.K);
-}
-
+// Input rows come to shared memory as they are and are rewritten in place as
+// scaled FP16, 256 elements of a row at a time, eight a lane: piece p is part
+// p % parts of held row p / parts, and belongs to warp p % warps.  The one to four
+// rows of single columns come by cp.async of the lanes that rewrite them (a
+// dense 500 x 640 takes 3.8 us so, 4.3 with bulk copies), the many rows of the
+// other forms by a bulk copy each (13 tokens on 12 experts: 50.7 against 52.1 us).
 __device__ __forceinline__ void scale_piece(const KernelArgs& a, uint8_t* smem, int held, int part,
                                             int parts, int lane) {
     uint4* at = reinterpret_cast<uint4*>(smem + a.l.x + held * a.l.x_stride + part * (2 * kPartK) +
                                          16 * lane);
+    const uint4 v = *at;
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;   // BF16 magnitudes compare as integers, NaN the largest
+    const uint32_t two = __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs),
+                                  __vmaxu2(v.z & kAbs, v.w & kAbs));
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(two & 0xFFFFu, two >> 16));
     float f[8];
-    bf16_unpack8(*at, f);
-    uint32_t top = 0;                        // largest magnitude's bits; NaN counts as the largest
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    int be = static_cast<int>(top >> 23);
+    bf16_unpack8(v, f);
+    int be = static_cast<int>(top >> 7);
     float mult, back;
     if (be == 255) {
         // an Inf or NaN decides the sum: the finite elements may be dropped
@@ -394,6 +426,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     volatile int* joined = reinterpret_cast<volatile int*>(smem + a.l.bars + 8 * kWarps * a.l.ring +
                                                            8 * kMaxUnderWay);
 
+    const uint32_t x_bar = full + 8 * kMaxUnderWay + 4 * kMaxUnderWay;   // behind `joined`
     const int nb = (a.K + kBoxK - 1) / kBoxK;
     const int sharers = min(nb, kWarps);                     // warps that work on one unit
     const int out_cols = kSwiglu ? a.N / 2 : a.N;
@@ -409,6 +442,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         if (warp == 0) {
             ptx::prefetch_tensormap(&map_w);
             s_abort = 0;
+            ptx::mbar_init(x_bar, 1);
             for (int i = 0; i < kUnderWay; ++i) {
                 ptx::mbar_init(full + 8 * i, sharers);
                 joined[i] = 0;
@@ -425,25 +459,66 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     // ring; where all rows are held, ahead of the ids, too.
     const int parts = kParts * nb;
     const bool hold_all = a.x_rows <= a.l.x_rows;
-    auto load_all = [&](int rows, auto row_of) {
+    auto each_piece = [&](int rows, auto f) {
         for (int p = warp, held = 0, part = warp; p < parts * rows; p += kWarps) {
             while (part >= parts) {
                 part -= parts;
                 ++held;
             }
-            load_piece(a, base, held, part, row_of(held), lane);
+            f(held, part);
             part += kWarps;
         }
-        ptx::cp_async_commit();
     };
-    if (hold_all) load_all(a.x_rows, [](int held) { return held; });
+    auto load_rows = [&](int rows, auto row_of) {
+        if (kSingle) {
+            each_piece(rows, [&](int held, int part) {
+                const int k = part * kPartK + 8 * lane;
+                const uint16_t* src = a.x + static_cast<long long>(row_of(held)) * a.K;
+                ptx::cp_async_16(base + a.l.x + held * a.l.x_stride + 2 * k,
+                                 src + (k < a.K ? k : 0), k < a.K);
+            });
+            ptx::cp_async_commit();
+            return;
+        }
+        if (warp != 0) return;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(x_bar, rows * 2 * a.K);
+        __syncwarp();
+        ptx::fence_proxy_async_smem();       // the rows before were rewritten in place
+        for (int held = lane; held < rows; held += 32)
+            ptx::bulk_load(base + a.l.x + held * a.l.x_stride,
+                           a.x + static_cast<long long>(row_of(held)) * a.K, 2 * a.K, x_bar);
+    };
+    if (hold_all) load_rows(a.x_rows, [](int held) { return held; });
+    // zeros behind the rows, up to the end of their last box (cp.async writes them itself)
+    const int tail = kSingle ? 0 : (2 * kPartK * parts - 2 * a.K) / 16;
+    for (int i = threadIdx.x; i < tail * a.l.x_rows; i += kThreads)
+        *reinterpret_cast<uint4*>(smem + a.l.x + i / tail * a.l.x_stride + 2 * a.K +
+                                  16 * (i % tail)) = make_uint4(0, 0, 0, 0);
     const int chunks = list_slots<kThreads>(a, tb);          // has block barriers
 
     const int units = chunks * tiles;
     const int each = units / static_cast<int>(gridDim.x);
     const int left = units - each * static_cast<int>(gridDim.x);
-    const int u0 = static_cast<int>(blockIdx.x) * each + min(static_cast<int>(blockIdx.x), left);
-    const int u1 = u0 + each + (static_cast<int>(blockIdx.x) < left);
+    int u0 = static_cast<int>(blockIdx.x) * each + min(static_cast<int>(blockIdx.x), left);
+    int u1 = u0 + each + (static_cast<int>(blockIdx.x) < left);
+    if (kTiles == 2 && chunks <= 32) {
+        // A unit of a chunk with two MMAs a row tile takes about 5/4 of the
+        // time of one with one: blocks get equal shares of that.
+        const bool wide = lane < chunks && tb.ncols[lane] > kTileCols;
+        const uint32_t wides = __ballot_sync(0xFFFFFFFFu, wide);
+        const long long cost = 4 * lane + __popc(wides & ((1u << lane) - 1u));   // chunks before
+        const long long all = static_cast<long long>(tiles) * (4 * chunks + __popc(wides));
+        auto unit_at = [&](long long target) {
+            const int c = __popc(__ballot_sync(0xFFFFFFFFu, lane < chunks &&
+                                                                tiles * cost <= target)) - 1;
+            const int weight = (wides >> c) & 1u ? 5 : 4;
+            const int inside = static_cast<int>(
+                target - tiles * __shfl_sync(0xFFFFFFFFu, cost, c));
+            return c * tiles + min(tiles, (inside + weight - 1) / weight);
+        };
+        u0 = chunks ? unit_at(all * blockIdx.x / gridDim.x) : 0;
+        u1 = chunks ? unit_at(all * (blockIdx.x + 1) / gridDim.x) : 0;
+    }
     const int chunk0 = u0 / tiles;
 
     // A run: the units of as many chunks, from chunk c on, as rows can be held.
@@ -460,7 +535,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     };
     auto load_run = [&](int c, int end) {
         int before = 0;                      // rows of the run's chunks before c
-        load_all(run_rows(c, end), [&](int held) {
+        load_rows(run_rows(c, end), [&](int held) {
             while (held >= before + tb.ncols[c]) before += tb.ncols[c++];
             return tb.slot[c * a.l.cols + held - before] / a.slots_per_row;
         });
@@ -486,7 +561,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             p_known = p_u;
             while (p_u >= (p_chunk + 1) * tiles) ++p_chunk;
             p_n0 = (p_u - p_chunk * tiles) * tile_cols;
-            p_expert = tb.key[p_chunk].x;
+            p_expert = tb.expert[p_chunk];
             // the row whose scales this lane copies; rows past the end of the
             // expert's are not used
             const int r = lane / kParts % kRows;
@@ -548,7 +623,11 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     const uint8_t* my_scales = smem + a.l.scales + warp * a.l.ring * kBoxScaleBytes +
                                g8 * kScaleRow;
     int at = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, x_phase = 0;
+    if (!kSingle && hold_all && u0 >= u1) {  // no work here, but rows are on their way
+        wait_bounded(x_bar, x_phase, ctx, kRoleMatvec, 0x300);
+        x_phase ^= 1;
+    }
     for (int run = u0, chunk = chunk0, before = 0; run < u1;) {   // before: units of earlier runs
         while (run >= (chunk + 1) * tiles) ++chunk;
         const int end = run_end(chunk);
@@ -556,17 +635,15 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             __syncthreads();                 // everybody is done with the rows before
             load_run(chunk, end);
         }
-        ptx::cp_async_wait_all_groups();
-        __syncwarp();
-        const int rows = hold_all ? a.x_rows : run_rows(chunk, end);
-        for (int p = warp, held = 0, part = warp; p < parts * rows; p += kWarps) {
-            while (part >= parts) {
-                part -= parts;
-                ++held;
-            }
-            scale_piece(a, smem, held, part, parts, lane);
-            part += kWarps;
+        if (kSingle) {
+            ptx::cp_async_wait_all_groups();
+            __syncwarp();
+        } else {
+            wait_bounded(x_bar, x_phase, ctx, kRoleMatvec, 0x300);
+            x_phase ^= 1;
         }
+        each_piece(hold_all ? a.x_rows : run_rows(chunk, end),
+                   [&](int held, int part) { scale_piece(a, smem, held, part, parts, lane); });
         __syncthreads();
         // Where this lane's columns of the current chunk lie; lanes of columns
         // that the chunk does not have read zeros.
@@ -602,6 +679,64 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 #pragma unroll
         for (int i = 0; i < kR * kT * 2; ++i) acc[i / (2 * kT)][i / 2 % kT][i % 2] = 0;
         float one[2] = {0.0f, 0.0f};
+        // 256 K of kRows weight rows times the chunk's columns, in `tiles_here`
+        // MMAs side by side.
+        auto multiply = [&](auto tiles_here, int b, const uint8_t* codes) {
+            constexpr int kHere = decltype(tiles_here)::value;
+            uint64_t sx[kHere];
+#pragma unroll
+            for (int t = 0; t < kHere; ++t)
+                sx[t] = ptx::f32x2(s_at[t][0][b * s_step[t][0]], s_at[t][1][b * s_step[t][1]]);
+            uint2 code[kR][2];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi)
+                    code[r][hi] = *reinterpret_cast<const uint2*>(
+                        codes + (r * kTileBlock + hi * kHiBlock) * 8 * kScaleRow);
+            }
+#pragma unroll
+            for (int g = 0; g < 8; g += 2) {
+                uint4 xf[2][kHere];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int t = 0; t < kHere; ++t)
+                        xf[i][t] = *reinterpret_cast<const uint4*>(x_at[t] + b * x_step[t] +
+                                                                   64 * (g + i));
+                }
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    uint32_t w[4];
+                    ptx::ldmatrix_x4(lm_row + at * kBoxBytes + r * kTileBlock * kBlockBytes +
+                                         (((g + (lane >> 4)) ^ (lane & 7)) << 4), w);
+                    const uint2 c0 = code[r][0], c1 = code[r][1];
+                    const float2 s0 = ptx::e8m0x2_to_f32((g < 4 ? c0.x : c0.y) >> (g & 2) * 8);
+                    const float2 s1 = ptx::e8m0x2_to_f32((g < 4 ? c1.x : c1.y) >> (g & 2) * 8);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t lo[4], hi[4];
+                        ptx::e2m1x8_to_f16(w[2 * i], lo);
+                        ptx::e2m1x8_to_f16(w[2 * i + 1], hi);
+                        const uint64_t s_lo = i ? ptx::f32x2(s0.y, s0.y) : ptx::f32x2(s0.x, s0.x);
+                        const uint64_t s_hi = i ? ptx::f32x2(s1.y, s1.y) : ptx::f32x2(s1.x, s1.x);
+#pragma unroll
+                        for (int t = 0; t < kHere; ++t) {
+                            const uint4 x = xf[i][t];
+                            float d[4];
+                            ptx::mma_f16_16816_first(d, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+                            ptx::mma_f16_16816(d, lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+                            acc[r][t][0] = ptx::fma_f32x2(ptx::f32x2(d[0], d[1]),
+                                                          ptx::mul_f32x2(s_lo, sx[t]),
+                                                          acc[r][t][0]);
+                            acc[r][t][1] = ptx::fma_f32x2(ptx::f32x2(d[2], d[3]),
+                                                          ptx::mul_f32x2(s_hi, sx[t]),
+                                                          acc[r][t][1]);
+                        }
+                    }
+                }
+            }
+        };
         for (int u = run + first_u, b = first_b; u < end;) {
             while (u >= (x_chunk + 1) * tiles) next_chunk();
             const bool ok = __all_sync(0xFFFFFFFFu,
@@ -618,68 +753,10 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                                     *reinterpret_cast<const uint16_t*>(c + 8 * kScaleRow),
                                     s_at[0][0][kParts * b + h], lane, one);
                     }
+                } else if (kT == 2 && ncols > kTileCols) {
+                    multiply(std::integral_constant<int, kT>(), b, codes);
                 } else {
-                    uint64_t sx[kT];
-#pragma unroll
-                    for (int t = 0; t < kT; ++t)
-                        sx[t] = ptx::f32x2(s_at[t][0][b * s_step[t][0]],
-                                           s_at[t][1][b * s_step[t][1]]);
-                    uint2 code[kR][2];
-#pragma unroll
-                    for (int r = 0; r < kR; ++r) {
-#pragma unroll
-                        for (int hi = 0; hi < 2; ++hi)
-                            code[r][hi] = *reinterpret_cast<const uint2*>(
-                                codes + (r * kTileBlock + hi * kHiBlock) * 8 * kScaleRow);
-                    }
-#pragma unroll
-                    for (int g = 0; g < 8; g += 2) {
-                        uint4 xf[2][kT];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                            for (int t = 0; t < kT; ++t)
-                                xf[i][t] = *reinterpret_cast<const uint4*>(
-                                    x_at[t] + b * x_step[t] + 64 * (g + i));
-                        }
-                        uint32_t ws[kR][4];
-#pragma unroll
-                        for (int r = 0; r < kR; ++r)
-                            ptx::ldmatrix_x4(lm_row + at * kBoxBytes +
-                                                 r * kTileBlock * kBlockBytes +
-                                                 (((g + (lane >> 4)) ^ (lane & 7)) << 4), ws[r]);
-#pragma unroll
-                        for (int r = 0; r < kR; ++r) {
-                            const uint32_t(&w)[4] = ws[r];
-                            const uint2 c0 = code[r][0], c1 = code[r][1];
-                            const float2 s0 = ptx::e8m0x2_to_f32((g < 4 ? c0.x : c0.y) >> (g & 2) * 8);
-                            const float2 s1 = ptx::e8m0x2_to_f32((g < 4 ? c1.x : c1.y) >> (g & 2) * 8);
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                uint32_t lo[4], hi[4];
-                                ptx::e2m1x8_to_f16(w[2 * i], lo);
-                                ptx::e2m1x8_to_f16(w[2 * i + 1], hi);
-                                const uint64_t s_lo = i ? ptx::f32x2(s0.y, s0.y)
-                                                        : ptx::f32x2(s0.x, s0.x);
-                                const uint64_t s_hi = i ? ptx::f32x2(s1.y, s1.y)
-                                                        : ptx::f32x2(s1.x, s1.x);
-#pragma unroll
-                                for (int t = 0; t < kT; ++t) {
-                                    float d[4];
-                                    ptx::mma_f16_16816_first(d, lo[0], hi[0], lo[1], hi[1],
-                                                             xf[i][t].x, xf[i][t].y);
-                                    ptx::mma_f16_16816(d, lo[2], hi[2], lo[3], hi[3], xf[i][t].z,
-                                                       xf[i][t].w);
-                                    acc[r][t][0] =
-                                        ptx::fma_f32x2(ptx::f32x2(d[0], d[1]),
-                                                       ptx::mul_f32x2(s_lo, sx[t]), acc[r][t][0]);
-                                    acc[r][t][1] =
-                                        ptx::fma_f32x2(ptx::f32x2(d[2], d[3]),
-                                                       ptx::mul_f32x2(s_hi, sx[t]), acc[r][t][1]);
-                                }
-                            }
-                        }
-                    }
+                    multiply(std::integral_constant<int, 1>(), b, codes);
                 }
             }
             __syncwarp();                    // the box is read: its place may be refilled
@@ -800,11 +877,13 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     // again with a limit, before the shared memory is given back.
     if (*ctx.abort) {
         const uint64_t t0 = ptx::globaltimer_ns();
-        for (int i = max(0, issued - a.l.ring); i < issued; ++i) {
-            while (!ptx::mbar_try_wait(bars + 8 * (i % a.l.ring), (i / a.l.ring) & 1) &&
-                   ptx::globaltimer_ns() - t0 < a.timeout_ns) {
+        auto drain = [&](uint32_t bar, uint32_t parity) {
+            while (!ptx::mbar_try_wait(bar, parity) && ptx::globaltimer_ns() - t0 < a.timeout_ns) {
             }
-        }
+        };
+        for (int i = max(0, issued - a.l.ring); i < issued; ++i)
+            drain(bars + 8 * (i % a.l.ring), (i / a.l.ring) & 1);
+        if (!kSingle) drain(x_bar, x_phase ^ 1);             // the last rows asked for
     }
 }
 

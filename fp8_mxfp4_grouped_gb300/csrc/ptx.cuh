@@ -132,6 +132,16 @@ __device__ __forceinline__ void cp_async_wait_all_groups() {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Bulk copy global -> shared of `bytes` (a multiple of 16, both addresses on
+// 16-byte boundaries), completion counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
 // One arrival on `bar` (counted in its expected arrivals) once this thread's
 // earlier cp.async copies have landed.
 __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
