@@ -116,6 +116,8 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, const CUtensorMap& map_w, con
 size_t gemm_smem_bytes(int variant, int32_t E);
 long long gemm_launch_ctas(const GemmArgs& a);   // CTAs the launch would use
 int gemm_max_experts();
+// Set a kernel's dynamic shared-memory limit on the current device, once.
+cudaError_t kernel_smem_limit(const void* kernel, size_t bytes);
 // Forget the per-device kernel settings and occupancy answers (hg_shutdown).
 void gemm_reset_caches();
 // Forget the plan scratch array's per-device addresses (hg_shutdown).

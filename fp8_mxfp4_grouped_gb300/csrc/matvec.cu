@@ -889,8 +889,8 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 
 template <bool kSwiglu, int kTiles>
 cudaError_t launch(const CUtensorMap& map, const KernelArgs& k, int grid, cudaStream_t stream) {
-    cudaError_t err = cudaFuncSetAttribute(expert_matvec_kernel<kSwiglu, kTiles>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    cudaError_t err = kernel_smem_limit(
+        reinterpret_cast<const void*>(&expert_matvec_kernel<kSwiglu, kTiles>), kSmemLimit);
     if (err != cudaSuccess) return err;
     // The set-up of the block may overlap the end of the kernel before.
     cudaLaunchAttribute attr[1];

@@ -18,6 +18,8 @@
 // the reciprocal its approximation: off by some 2^-22 of the value, and by
 // |g| * 2^-24 of it for the rounding of the exponent, against the formats'
 // 2^-4 and 2^-8.
+#include <atomic>
+
 #include "hg_internal.cuh"
 #include "numeric.cuh"
 
@@ -182,13 +184,17 @@ swiglu_bwd_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restrict__ z
     }
 }
 
-// Blocks: a half-warp for each group, at most what is resident at once.
-int grid_blocks(int rows, int F, const void* kernel, int num_sms) {
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0) !=
-            cudaSuccess ||
-        per_sm < 1)
-        per_sm = 1;
+// Blocks: a half-warp for each group, at most what is resident at once (asked
+// for once per kernel: it is a property of the code and of sm_103a).
+int grid_blocks(int rows, int F, const void* kernel, std::atomic<int>& known, int num_sms) {
+    int per_sm = known.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0) !=
+                cudaSuccess ||
+            per_sm < 1)
+            per_sm = 1;
+        known.store(per_sm, std::memory_order_relaxed);
+    }
     const long long groups = static_cast<long long>(rows) * (F / kGroup);
     const long long blocks = (groups + kBlockGroups - 1) / kBlockGroups;
     const long long cap = static_cast<long long>(num_sms) * per_sm;
@@ -201,14 +207,17 @@ cudaError_t launch_swiglu_quantize(const uint16_t* z, int rows, int F, uint8_t* 
                                    uint8_t* a_scale, uint8_t* z_fp8, uint8_t* z_scale, int num_sms,
                                    cudaStream_t stream) {
     const auto kernel = z_fp8 ? swiglu_quantize_kernel<true> : swiglu_quantize_kernel<false>;
-    const int grid = grid_blocks(rows, F, reinterpret_cast<const void*>(kernel), num_sms);
+    static std::atomic<int> known[2];
+    const int grid = grid_blocks(rows, F, reinterpret_cast<const void*>(kernel),
+                                 known[z_fp8 != nullptr], num_sms);
     kernel<<<grid, kThreads, 0, stream>>>(z, rows, F, a_fp8, a_scale, z_fp8, z_scale);
     return cudaGetLastError();
 }
 
 cudaError_t launch_swiglu_bwd(const uint16_t* dh, const uint8_t* z_fp8, const uint8_t* z_scale,
                               int rows, int F, uint16_t* dz, int num_sms, cudaStream_t stream) {
-    const int grid = grid_blocks(rows, F, reinterpret_cast<const void*>(swiglu_bwd_kernel),
+    static std::atomic<int> known;
+    const int grid = grid_blocks(rows, F, reinterpret_cast<const void*>(swiglu_bwd_kernel), known,
                                  num_sms);
     swiglu_bwd_kernel<<<grid, kThreads, 0, stream>>>(dh, z_fp8, z_scale, rows, F, dz);
     return cudaGetLastError();
