@@ -93,12 +93,6 @@ struct WMapEntry {
     int32_t E = 0, N = 0, K = 0;
     CUtensorMap map;
 };
-struct WBytesMapEntry {
-    const void* p = nullptr;
-    int32_t E = 0, N = 0, K = 0, rows = 0;
-    bool pair = false;
-    CUtensorMap map;
-};
 struct AMapEntry {
     const void* p = nullptr;
     int32_t rows = 0, K = 0;
@@ -110,11 +104,9 @@ struct OMapEntry {
     CUtensorMap map;
 };
 WMapEntry g_wmap[kMapCacheEntries];
-WBytesMapEntry g_wbytes_map[kMapCacheEntries];
 AMapEntry g_amap[kMapCacheEntries];
 OMapEntry g_omap[kMapCacheEntries];
 int g_wmap_next = 0;
-int g_wbytes_map_next = 0;
 int g_amap_next = 0;
 int g_omap_next = 0;
 std::mutex g_map_mu;
@@ -123,11 +115,10 @@ void map_cache_reset() {
     std::lock_guard<std::mutex> lock(g_map_mu);
     for (int i = 0; i < kMapCacheEntries; ++i) {
         g_wmap[i].p = nullptr;
-        g_wbytes_map[i].p = nullptr;
         g_amap[i].p = nullptr;
         g_omap[i].p = nullptr;
     }
-    g_wmap_next = g_wbytes_map_next = g_amap_next = g_omap_next = 0;
+    g_wmap_next = g_amap_next = g_omap_next = 0;
 }
 
 // Weights: [E*N rows, K elements] of E2M1, unpacked by the TMA into one
@@ -165,18 +156,11 @@ hg_status weight_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* w_
 // Weights as packed bytes, 128-byte swizzle, `rows` x 128 bytes a box (zeros
 // past the end of a row and of an expert): [E, N rows, K/2 bytes] with
 // consecutive rows, or for a gate/up pair [E * 2, N/2 rows, K/2 bytes] with
-// half of the box's rows from each.
+// half of the box's rows from each.  Encoded at every call (one map, where the
+// GEMM needs five).
 hg_status weight_bytes_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* w_fp4,
                            int32_t E, int32_t N, int32_t K, bool pair, int32_t rows,
                            CUtensorMap* out) {
-    std::lock_guard<std::mutex> lock(g_map_mu);
-    for (int i = 0; i < kMapCacheEntries; ++i) {
-        const WBytesMapEntry& c = g_wbytes_map[i];
-        if (c.p == w_fp4 && c.E == E && c.N == N && c.K == K && c.pair == pair && c.rows == rows) {
-            *out = c.map;
-            return HG_OK;
-        }
-    }
     const int32_t split = pair ? 2 : 1;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(N / split),
                           static_cast<cuuint64_t>(E) * split};
@@ -185,20 +169,12 @@ hg_status weight_bytes_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8
     cuuint32_t box[3] = {128, static_cast<cuuint32_t>(rows / split),
                          static_cast<cuuint32_t>(split)};
     cuuint32_t estr[3] = {1, 1, 1};
-    if (encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(w_fp4), dims, strides,
-               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return HG_ERR_CUDA;
-    WBytesMapEntry& slot = g_wbytes_map[g_wbytes_map_next];
-    g_wbytes_map_next = (g_wbytes_map_next + 1) % kMapCacheEntries;
-    slot.p = w_fp4;
-    slot.E = E;
-    slot.N = N;
-    slot.K = K;
-    slot.rows = rows;
-    slot.pair = pair;
-    slot.map = *out;
-    return HG_OK;
+    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(w_fp4), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? HG_OK
+               : HG_ERR_CUDA;
 }
 
 // Activations: [rows, K] bytes, 128-byte swizzle; boxes of 16, 32, 64 and

@@ -28,8 +28,8 @@
 // and tcgen05 would want the 16-bit weights written back to shared memory
 // first.  x is BF16, wider than FP16's range: each row's 256 elements of a box
 // are scaled by the power of two that takes their largest magnitude into
-// [2^14, 2^15).  An element keeps its 8 bits down to 2^-32 of that largest,
-// and what lies below is off by 2^-40 of it at most, far below the FP32 sum's
+// [2^14, 2^15).  An element keeps its 8 bits down to 2^-31 of that largest,
+// and what lies below is off by 2^-39 of it at most, far below the FP32 sum's
 // own rounding.  The sums of a 32-K group come out of the MMA in FP32 and are
 // added up in FP32 times the product of the two scales.
 #include <cuda_fp16.h>

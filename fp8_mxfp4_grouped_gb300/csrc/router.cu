@@ -165,7 +165,7 @@ router_topk_bwd_kernel(const float* __restrict__ logits, const int32_t* __restri
 template <int kHeld>
 cudaError_t launch_topk(const float* logits, int M, int E, int top_k, int renormalize,
                         int32_t* ids, float* weights, cudaStream_t stream) {
-    const int grid = (M + kThreads / 32 - 1) / (kThreads / 32);
+    const int grid = (M - 1) / (kThreads / 32) + 1;
     router_topk_kernel<kHeld><<<grid, kThreads, 0, stream>>>(logits, M, E, top_k, renormalize, ids,
                                                              weights);
     return cudaGetLastError();
@@ -196,7 +196,7 @@ cudaError_t launch_router_topk(const float* logits, int M, int E, int top_k, int
 cudaError_t launch_router_topk_bwd(const float* logits, const int32_t* ids, const float* weights,
                                    const float* dweights, int M, int E, int top_k,
                                    int renormalize, float* dlogits, cudaStream_t stream) {
-    const int grid = (M + kThreads / 32 - 1) / (kThreads / 32);
+    const int grid = (M - 1) / (kThreads / 32) + 1;
     router_topk_bwd_kernel<<<grid, kThreads, 0, stream>>>(logits, ids, weights, dweights, M, E,
                                                           top_k, renormalize, dlogits);
     return cudaGetLastError();

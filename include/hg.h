@@ -578,7 +578,7 @@ hg_status hg_get_device_status(hg_stream_t stream, uint32_t* detail);
 hg_status hg_selftest_wait_timeout(uint32_t timeout_us, hg_stream_t stream);
 
 /*
- * Per-wait limit of the GEMM's barrier waits in microseconds (default
+ * Per-wait limit of the GEMM's and the few-token product's waits in microseconds (default
  * 1000000).  Host-side setting, applied to later launches.  0 restores the
  * default.
  */
