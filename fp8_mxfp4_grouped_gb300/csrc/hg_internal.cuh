@@ -71,6 +71,32 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, cons
 
 // ------------------------------------------------- host-side launchers --
 
+// Launch with programmatic dependent launch: blocks may start while the kernel
+// before on the stream drains.  The kernel calls start_dependent first of all,
+// so that stream order holds for everything it reads and writes.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int block, size_t smem,
+                             cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// Wait until the kernel before has completed, and let the one after be launched.
+__device__ __forceinline__ void start_dependent() {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+}
+
 struct GemmArgs {
     const uint8_t* a_fp8;
     const uint8_t* a_scale;

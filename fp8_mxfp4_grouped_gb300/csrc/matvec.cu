@@ -452,8 +452,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     }
     if (threadIdx.x < kPartK / 2)
         reinterpret_cast<uint32_t*>(smem + a.l.zeros)[threadIdx.x] = 0;
-    ptx::griddep_wait();                     // nothing global is read or written before
-    ptx::griddep_launch_dependents();
+    start_dependent();                       // nothing global is read or written before
 
     // x goes ahead of the weights, behind which it would wait for the whole
     // ring; where all rows are held, ahead of the ids, too.
@@ -889,22 +888,11 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 
 template <bool kSwiglu, int kTiles>
 cudaError_t launch(const CUtensorMap& map, const KernelArgs& k, int grid, cudaStream_t stream) {
-    cudaError_t err = kernel_smem_limit(
+    const cudaError_t err = kernel_smem_limit(
         reinterpret_cast<const void*>(&expert_matvec_kernel<kSwiglu, kTiles>), kSmemLimit);
     if (err != cudaSuccess) return err;
-    // The set-up of the block may overlap the end of the kernel before.
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(form_of(kTiles == 0).warps * 32);
-    cfg.dynamicSmemBytes = k.l.total;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, expert_matvec_kernel<kSwiglu, kTiles>, map, k);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    return launch_dependent(expert_matvec_kernel<kSwiglu, kTiles>, grid,
+                            form_of(kTiles == 0).warps * 32, k.l.total, stream, map, k);
 }
 
 template <bool kSwiglu>

@@ -77,6 +77,7 @@ router_topk_kernel(const float* __restrict__ logits, int M, int E, int top_k, in
                    int32_t* __restrict__ ids, float* __restrict__ weights) {
     const int lane = threadIdx.x & 31;
     const long long t = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    start_dependent();
     if (t >= M) return;
     Row<kHeld> row(logits + t * E, E, lane);
 
@@ -134,6 +135,7 @@ router_topk_bwd_kernel(const float* __restrict__ logits, const int32_t* __restri
                        int M, int E, int top_k, int renormalize, float* __restrict__ dlogits) {
     const int lane = threadIdx.x & 31;
     const long long t = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    start_dependent();
     if (t >= M) return;
     int id = -1;
     float w = 0.0f, dw = 0.0f;
@@ -166,9 +168,8 @@ template <int kHeld>
 cudaError_t launch_topk(const float* logits, int M, int E, int top_k, int renormalize,
                         int32_t* ids, float* weights, cudaStream_t stream) {
     const int grid = (M - 1) / (kThreads / 32) + 1;
-    router_topk_kernel<kHeld><<<grid, kThreads, 0, stream>>>(logits, M, E, top_k, renormalize, ids,
-                                                             weights);
-    return cudaGetLastError();
+    return launch_dependent(router_topk_kernel<kHeld>, grid, kThreads, 0, stream, logits, M, E,
+                            top_k, renormalize, ids, weights);
 }
 
 }  // namespace
@@ -197,9 +198,8 @@ cudaError_t launch_router_topk_bwd(const float* logits, const int32_t* ids, cons
                                    const float* dweights, int M, int E, int top_k,
                                    int renormalize, float* dlogits, cudaStream_t stream) {
     const int grid = (M - 1) / (kThreads / 32) + 1;
-    router_topk_bwd_kernel<<<grid, kThreads, 0, stream>>>(logits, ids, weights, dweights, M, E,
-                                                          top_k, renormalize, dlogits);
-    return cudaGetLastError();
+    return launch_dependent(router_topk_bwd_kernel, grid, kThreads, 0, stream, logits, ids,
+                            weights, dweights, M, E, top_k, renormalize, dlogits);
 }
 
 }  // namespace hg

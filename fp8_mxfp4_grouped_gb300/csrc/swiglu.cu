@@ -109,6 +109,7 @@ swiglu_quantize_kernel(const uint16_t* __restrict__ z, int rows, int F,
     const int step_r = step / G, step_g = step - step_r * G;
     const long long groups = static_cast<long long>(rows) * G;
     Walk at(blockIdx.x * kBlockGroups + (threadIdx.x >> 4), G);
+    start_dependent();
     // the group after this one is asked for before this one is worked on
     uint4 next_g = make_uint4(0, 0, 0, 0), next_u = next_g;
     auto load = [&]() {
@@ -158,6 +159,7 @@ swiglu_bwd_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restrict__ z
     const int step_r = step / G, step_g = step - step_r * G;
     const uint64_t one = ptx::f32x2(1.0f, 1.0f), minus = ptx::f32x2(-1.0f, -1.0f);
     Walk at(blockIdx.x * kBlockGroups + (threadIdx.x >> 4), G);
+    start_dependent();
     // eight elements of three inputs are enough loads under way: asking ahead as
     // above costs registers and with them warps (24.7 -> 25.9 us at 9223 x 2048)
     for (; at.r < rows; at.next(step, step_r, step_g, G)) {
@@ -210,8 +212,8 @@ cudaError_t launch_swiglu_quantize(const uint16_t* z, int rows, int F, uint8_t* 
     static std::atomic<int> known[2];
     const int grid = grid_blocks(rows, F, reinterpret_cast<const void*>(kernel),
                                  known[z_fp8 != nullptr], num_sms);
-    kernel<<<grid, kThreads, 0, stream>>>(z, rows, F, a_fp8, a_scale, z_fp8, z_scale);
-    return cudaGetLastError();
+    return launch_dependent(kernel, grid, kThreads, 0, stream, z, rows, F, a_fp8, a_scale, z_fp8,
+                            z_scale);
 }
 
 cudaError_t launch_swiglu_bwd(const uint16_t* dh, const uint8_t* z_fp8, const uint8_t* z_scale,
@@ -219,8 +221,8 @@ cudaError_t launch_swiglu_bwd(const uint16_t* dh, const uint8_t* z_fp8, const ui
     static std::atomic<int> known;
     const int grid = grid_blocks(rows, F, reinterpret_cast<const void*>(swiglu_bwd_kernel), known,
                                  num_sms);
-    swiglu_bwd_kernel<<<grid, kThreads, 0, stream>>>(dh, z_fp8, z_scale, rows, F, dz);
-    return cudaGetLastError();
+    return launch_dependent(swiglu_bwd_kernel, grid, kThreads, 0, stream, dh, z_fp8, z_scale, rows,
+                            F, dz);
 }
 
 }  // namespace hg

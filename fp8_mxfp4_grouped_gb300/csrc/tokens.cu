@@ -68,6 +68,7 @@ dispatch_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ plac
                 const float* __restrict__ weights, int M, int top_k, int K, int team_warps,
                 uint16_t* __restrict__ rows) {
     const Team team(team_warps);
+    start_dependent();
     if (team.token >= M) return;
     const uint16_t* xt = x + team.token * K;
     for (int pass = 0; pass * team.pass_elements(kPieces) < K; ++pass) {
@@ -141,6 +142,7 @@ token_grad_kernel(const uint16_t* __restrict__ rows, const uint16_t* __restrict_
     __shared__ float s_part[kWarps * kBatch];
     static_assert(kBatch % kFlight == 0, "a batch is whole groups of rows in flight");
     const Team team(team_warps);
+    start_dependent();
     const bool real = team.token < M;        // a block's last teams may have no token
     const long long first = team.token * top_k;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -275,9 +277,8 @@ cudaError_t launch_pieces(const Shape& s, const uint16_t* rows, const uint16_t* 
     constexpr int kSingleBlocks = kPieces < 3 ? 4 : kSum && kPieces == 4 ? 2 : 3;
     const auto kernel = top_k == 1 ? token_grad_kernel<kSum, kDots, kPieces, 1, kSingleBlocks>
                                    : token_grad_kernel<kSum, kDots, kPieces, 2, kBlocks>;
-    kernel<<<s.blocks(M), kThreads, 0, stream>>>(rows, token, d2s, weights, M, top_k, N,
-                                                 s.team_warps, out, dw);
-    return cudaGetLastError();
+    return launch_dependent(kernel, s.blocks(M), kThreads, 0, stream, rows, token, d2s, weights, M,
+                            top_k, N, s.team_warps, out, dw);
 }
 
 template <bool kSum, bool kDots>
@@ -301,8 +302,8 @@ cudaError_t launch_dispatch(const uint16_t* x, const int32_t* d2s, const float* 
                         : s.pieces == 2 ? dispatch_kernel<2>
                         : s.pieces == 3 ? dispatch_kernel<3>
                                         : dispatch_kernel<4>;
-    kernel<<<s.blocks(M), kThreads, 0, stream>>>(x, d2s, weights, M, top_k, K, s.team_warps, rows);
-    return cudaGetLastError();
+    return launch_dependent(kernel, s.blocks(M), kThreads, 0, stream, x, d2s, weights, M, top_k, K,
+                            s.team_warps, rows);
 }
 
 cudaError_t launch_dispatch_bwd(const uint16_t* drows, const uint16_t* x, const int32_t* d2s,

@@ -585,3 +585,59 @@ def test_empty_problems(cuda_lib):
     l0 = torch.empty(0, 4, **dev)
     ids, wt = cuda_lib.hg_router_topk(l0, 2)
     assert cuda_lib.hg_router_topk_bwd(l0, ids, wt, wt).shape == (0, 4)
+
+
+def test_calls_back_to_back_see_each_others_results(cuda_lib):
+    # each call may be launched while the one before drains: a chain of calls on
+    # shared buffers, with inputs that change from pass to pass and nothing
+    # waited for, gives what the same calls give with a wait after each
+    hg = cuda_lib
+    M, k, E, D, F = 8, 2, 8, 512, 256
+    gu = [t.cuda() for t in make_weights(E, 2 * F, D, seed=5)]
+    dn = [t.cuda() for t in make_weights(E, D, F, seed=6)]
+    xs = [_normal(30 + i, M, D).to(torch.bfloat16).cuda() for i in range(3)]
+    ls = [_normal(40 + i, M, E).cuda() for i in range(3)]
+    slots = torch.arange(M * k, dtype=torch.int32, device="cuda")
+    buf = dict(x=torch.empty_like(xs[0]), l=torch.empty_like(ls[0]),
+               ids=torch.empty(M, k, dtype=torch.int32, device="cuda"),
+               w=torch.empty(M, k, device="cuda"),
+               h=torch.empty(M * k, F, dtype=torch.bfloat16, device="cuda"),
+               y=torch.empty(M * k, D, dtype=torch.bfloat16, device="cuda"),
+               o=torch.empty(M, D, dtype=torch.bfloat16, device="cuda"),
+               dy=torch.empty(M * k, D, dtype=torch.bfloat16, device="cuda"),
+               dw=torch.empty(M, k, device="cuda"),
+               dl=torch.empty(M, E, device="cuda"),
+               z=torch.empty(M * k, 2 * F, dtype=torch.bfloat16, device="cuda"),
+               q=torch.empty(M * k, F, dtype=torch.uint8, device="cuda"),
+               qs=torch.empty(M * k, F // 128, dtype=torch.uint8, device="cuda"),
+               z8=torch.empty(M * k, 2 * F, dtype=torch.uint8, device="cuda"),
+               zs=torch.empty(M * k, 2 * F // 128, dtype=torch.uint8, device="cuda"),
+               dz=torch.empty(M * k, 2 * F, dtype=torch.bfloat16, device="cuda"))
+    b = buf
+
+    def chain(i, wait):
+        steps = [lambda: (b["x"].copy_(xs[i]), b["l"].copy_(ls[i])),
+                 lambda: hg.hg_router_topk(b["l"], k, True, b["ids"], b["w"]),
+                 lambda: hg.hg_expert_matvec_swiglu(b["x"], b["ids"], *gu, out=b["h"]),
+                 lambda: hg.hg_expert_matvec(b["h"], b["ids"], *dn, out=b["y"]),
+                 lambda: hg.hg_combine_topk(b["y"], slots, b["w"], b["o"]),
+                 lambda: hg.hg_combine_topk_bwd(b["o"], b["y"], slots, b["w"], b["dy"], b["dw"]),
+                 lambda: hg.hg_router_topk_bwd(b["l"], b["ids"], b["w"], b["dw"], True, b["dl"]),
+                 lambda: hg.hg_expert_matvec(b["x"], b["ids"], *gu, out=b["z"]),
+                 lambda: hg.hg_swiglu_quantize(b["z"], True, b["q"], b["qs"], b["z8"], b["zs"]),
+                 lambda: hg.hg_swiglu_bwd(b["h"], b["z8"], b["zs"], b["dz"]),
+                 lambda: hg.hg_dispatch_tokens(b["o"], k, slots, b["w"], out=b["dy"]),
+                 lambda: hg.hg_dispatch_tokens_bwd(b["dy"], k, slots, b["w"], b["o"], b["x"],
+                                                   b["dw"])]
+        for f in steps:
+            f()
+            if wait:
+                torch.cuda.synchronize()
+        return [b[n].clone() for n in ("h", "o", "dl", "dz", "x", "dw")]
+
+    want = [chain(i, True) for i in range(3)]
+    got = [(i % 3, chain(i % 3, False)) for i in range(30)]
+    torch.cuda.synchronize()
+    for i, outs in got:
+        for a, w in zip(outs, want[i]):
+            assert torch.equal(a, w)
