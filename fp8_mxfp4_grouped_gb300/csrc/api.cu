@@ -276,6 +276,7 @@ hg_status hg_shutdown(void) {
     }
     gemm_reset_caches();
     plan_noalloc_reset();
+    matvec_reset_caches();
     map_cache_reset();
     return HG_OK;
 }

@@ -1384,7 +1384,19 @@ std::mutex g_attr_mu;
 
 template <class Kern>
 cudaError_t set_smem_attr(Kern* fn, size_t bytes) {
-    return kernel_smem_limit(reinterpret_cast<const void*>(fn), bytes);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    const void* key = reinterpret_cast<const void*>(fn);
+    std::lock_guard<std::mutex> lock(g_attr_mu);
+    for (int i = 0; i < g_attr_used; ++i) {
+        const AttrEntry& c = g_attr_cache[i];
+        if (c.fn == key && c.dev == dev && c.bytes == bytes) return c.err;
+    }
+    const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(bytes));
+    if (err != cudaSuccess) cudaGetLastError();
+    if (g_attr_used < 64) g_attr_cache[g_attr_used++] = AttrEntry{key, dev, bytes, err};
+    return err;
 }
 
 // CTAs one launch uses (0: nothing to do).  Persistent grids: C CTAs per SM,
@@ -1497,21 +1509,6 @@ cudaError_t launch_pair(const GemmArgs& a, const CUtensorMap& map_w, const AMaps
 }
 
 }  // namespace
-
-cudaError_t kernel_smem_limit(const void* key, size_t bytes) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lock(g_attr_mu);
-    for (int i = 0; i < g_attr_used; ++i) {
-        const AttrEntry& c = g_attr_cache[i];
-        if (c.fn == key && c.dev == dev && c.bytes == bytes) return c.err;
-    }
-    const cudaError_t err = cudaFuncSetAttribute(key, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(bytes));
-    if (err != cudaSuccess) cudaGetLastError();
-    if (g_attr_used < 64) g_attr_cache[g_attr_used++] = AttrEntry{key, dev, bytes, err};
-    return err;
-}
 
 int gemm_max_experts() { return kMaxE; }
 

@@ -34,6 +34,7 @@
 // added up in FP32 times the product of the two scales.
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "hg_internal.cuh"
@@ -886,11 +887,22 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     }
 }
 
+// Devices (a bit each) on which a kernel's shared-memory limit has been set.
+std::atomic<uint64_t> g_ready[2][3];
+
 template <bool kSwiglu, int kTiles>
 cudaError_t launch(const CUtensorMap& map, const KernelArgs& k, int grid, cudaStream_t stream) {
-    const cudaError_t err = kernel_smem_limit(
-        reinterpret_cast<const void*>(&expert_matvec_kernel<kSwiglu, kTiles>), kSmemLimit);
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
+    std::atomic<uint64_t>& ready = g_ready[kSwiglu][kTiles];
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load() & bit)) {
+        err = cudaFuncSetAttribute(expert_matvec_kernel<kSwiglu, kTiles>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (err != cudaSuccess) return err;
+        ready.fetch_or(bit);
+    }
     return launch_dependent(expert_matvec_kernel<kSwiglu, kTiles>, grid,
                             form_of(kTiles == 0).warps * 32, k.l.total, stream, map, k);
 }
@@ -904,6 +916,12 @@ cudaError_t launch_cols(const CUtensorMap& map, const KernelArgs& k, int grid,
 }
 
 }  // namespace
+
+void matvec_reset_caches() {
+    for (auto& form : g_ready) {
+        for (auto& ready : form) ready.store(0);
+    }
+}
 
 int matvec_unit_rows(const MatvecArgs& a) {
     Layout l;
