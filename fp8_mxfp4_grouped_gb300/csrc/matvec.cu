@@ -32,6 +32,12 @@
 // and what lies below is off by 2^-39 of it at most, far below the FP32 sum's
 // own rounding.  The sums of a 32-K group come out of the MMA in FP32 and are
 // added up in FP32 times the product of the two scales.
+//
+// Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 22.6
+// us for 107 MB, of which 3.5 pass before the first weights arrive; from there
+// on the weights stream at the measured copy rate.  Down, 6144 x 2048: 14.5 us
+// for 54 MB.  13 tokens on 12 experts, 6144 x 3584: 47.7 us for 142 MB, bound by
+// the latency of conversion, MMA and scaling with two warps per scheduler.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -151,7 +157,11 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     int cols = tokens < slots ? tokens : slots;          // a token's choices are distinct experts
     const int most = slots > 6ll * E ? kMaxCols : kTileCols;
     if (cols > most) cols = most;
+    const int wanted = cols;
     while (cols > 1 && needs(cols, cols) + 2 * box(cols) > kSmemLimit) --cols;
+    // where not all of an expert's slots fit, two chunks of one MMA take less
+    // than one of two and one of one
+    if (cols < wanted && cols > kTileCols) cols = kTileCols;
     l.cols = cols;
     const int room = kSmemLimit - 2 * box(cols) - needs(cols, 0);
     l.x_rows = room / (l.x_stride + parts * 4);

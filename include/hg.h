@@ -323,6 +323,15 @@ hg_status hg_combine_topk(const uint16_t* y_bf16, const int32_t* src_to_sorted,
 /* ----------------------------------- tokens by expert, and gradients -- */
 
 /*
+ * This section and the three after it hold the operators of an MoE layer
+ * around the plan and the GEMM.  Each call is one kernel, launched with
+ * programmatic dependent launch: its blocks may start while the kernel before
+ * on `stream` drains, and read and write nothing until that has completed, so
+ * stream order holds as with a plain launch.  All of them can be captured
+ * into CUDA graphs.
+ */
+
+/*
  * BF16 token rows copied into the plan's sorted order, with or without the
  * router's weights [H129 first section: the rows of one expert are one
  * contiguous range]:

@@ -30,6 +30,9 @@ Modules:
 * ``gemm``     -- per-expert float64 dequantise + matmul, BF16 rounding once;
   and a sampled variant computing chosen output elements one by one.
 
+* ``moe_layer`` -- dispatch and combine with gradients, SwiGLU with its 8-bit
+  checkpoint, the few-token expert product, the router's gate, in float64.
+
 Every function here is pinned by ``tests/test_oracle_*.py`` against facts
 fixed independently of this code (exhaustive decode against closed forms and
 library conversions, identity / one-hot / all-ones weights with closed-form
