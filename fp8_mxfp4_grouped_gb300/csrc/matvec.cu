@@ -54,25 +54,41 @@ constexpr int kMaxCols = 16;                 // slots of a chunk: at most two MM
 constexpr int kSingleRows = 4;               // input rows held for single columns
 constexpr int kPartK = 256;                  // elements of 128 bytes of a weight row
 constexpr int kBlockBytes = 8 * kPartK / 2;  // 8 rows of a part: one swizzle pattern
-constexpr int kMaxUnderWay = 4;              // units whose partial sums are kept at once
+constexpr int kMaxUnderWay = 4;              // units whose partial sums are kept at once, at most
 constexpr int kSmemLimit = 232448 - 256;     // beside a few static bytes
 
 // The forms of the kernel.  A single column's MMAs are light, and its boxes
 // are long in K: 16 rows x 512 K.  With more columns the fragments of x weigh
 // more than the weights, and 32 rows x 256 K share each of them between two
-// MMAs; eight warps then have registers for it, and leave room for x.
+// MMAs.  There twelve warps where they leave room for x, else eight: what
+// bounds them is the latency of each warp's chain of instructions (8 tokens on
+// 32 experts, 6144 x 2048: twelve warps 36.6 us, eight 48.9, sixteen, short of
+// registers, 41.8).
 // The ring is no deeper than the memory's latency needs: 128 KB in flight per
 // SM; half as much again takes a token's gate/up product (E = 32, top-8,
 // N = 4096, K = 6144) from 22.4 to 24.1 us.
 struct Form {
-    int warps, row_tiles, parts, ring;       // parts: of 256 K in a box; ring: boxes in flight
+    int warps, row_tiles, parts;             // parts: of 256 K in a box
+    int ring;                                // boxes in flight per warp, at most
+    int under_way;                           // units whose partial sums are kept, times MMAs
     __host__ __device__ constexpr int rows() const { return 16 * row_tiles; }
     __host__ __device__ constexpr int box_bytes() const { return 2 * row_tiles * parts * kBlockBytes; }
     __host__ __device__ constexpr int box_scale_bytes() const { return box_bytes() / 16; }
+    __host__ __device__ constexpr int partial_bytes() const {
+        return warps * under_way * rows() * (row_tiles == 1 ? 1 : kTileCols) * 4;
+    }
 };
-__host__ __device__ constexpr Form form_of(bool single) {
-    return single ? Form{16, 1, 2, 2} : Form{8, 2, 1, 4};
+// tiles: MMAs side by side, 0 for a single column.  Two units under way at least
+// (one: 54.6 in place of 48 us for 13 tokens on 12 experts, 6144 x 3584).
+__host__ __device__ constexpr Form form_of(int tiles, int warps) {
+    return tiles == 0 ? Form{warps, 1, 2, 2, 4}
+                      : Form{warps, 2, 1, 4, tiles == 2 || warps == 8 ? 4 : 2};
 }
+__host__ __device__ constexpr int tiles_of(int cols) {
+    return cols == 1 ? 0 : cols <= kTileCols ? 1 : 2;
+}
+constexpr int kSingleWarps = 16;
+constexpr int kWarpChoices[2] = {12, 8};             // with more columns
 
 struct __align__(8) Entry {
     int expert;                              // -1: free
@@ -120,6 +136,7 @@ __device__ inline Tables tables_at(uint8_t* p, int slots, int cols) {
 }
 
 struct Layout {
+    int warps;
     int ring;          // boxes per warp
     int cols;          // most slots of a chunk
     int x_rows;        // input rows held at once
@@ -127,57 +144,58 @@ struct Layout {
     int scales, partial, x, x_scale, zeros, bars, tables, total;   // byte offsets
 };
 
-// Partial sums of the units under way, from every warp: a float per weight row
-// of a single column; 32 x 8 floats per MMA column tile otherwise, of four
-// units (two with two tiles).
-int partial_bytes(int cols) {
-    const Form f = form_of(cols == 1);
-    return f.warps * kMaxUnderWay * f.rows() * (cols == 1 ? 1 : kTileCols) * 4;
-}
-
 // Columns: up to eight (one MMA) where an expert has few slots on average, up
-// to sixteen otherwise: a second MMA costs half as much again, and reading the
-// weights of an expert with more slots twice costs twice.  Input rows: as many
-// as fit beside a ring of two boxes a warp.  They stay 64 bytes off a multiple
-// of 128 apart, so that the eight lanes of a 16-byte load phase (two columns,
-// whose rows mostly follow one another) meet no bank twice.
+// to sixteen otherwise: a second MMA costs a quarter more, and reading the
+// weights of an expert with more slots twice costs twice.  Warps: as many as
+// leave a ring of two boxes each beside that.  Input rows: as many as still fit.
+// They stay 64 bytes off a multiple of 128 apart, so that the eight lanes of a
+// 16-byte load phase (two columns, whose rows mostly follow one another) meet
+// no bank twice.
 bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
-    const int parts = (K + kPartK - 1) / kPartK + 1;     // a box may reach one past the end
+    const int pieces = (K + kPartK - 1) / kPartK + 1;    // a box may reach one past the end
     Layout l;
-    l.x_stride = parts * kPartK * 2 + 64;
-    auto box = [](int cols) {
-        const Form f = form_of(cols == 1);
-        return f.warps * (f.box_bytes() + f.box_scale_bytes());
+    l.x_stride = pieces * kPartK * 2 + 64;
+    Form f;
+    auto box = [&]() { return f.warps * (f.box_bytes() + f.box_scale_bytes()); };
+    auto needs = [&](int rows) {
+        return 1024 + f.partial_bytes() + rows * (l.x_stride + pieces * 4) + 16 +
+               2 * kPartK + (f.warps * f.ring + 2 * kMaxUnderWay) * 8 + table_bytes(slots, l.cols);
     };
-    auto needs = [&](int cols, int rows) {
-        return 1024 + partial_bytes(cols) + rows * (l.x_stride + parts * 4) + 16 + 2 * kPartK +
-               (form_of(cols == 1).warps * form_of(cols == 1).ring + 2 * kMaxUnderWay) * 8 +
-               table_bytes(slots, cols);
+    auto fits = [&]() { return needs(l.cols) + 2 * box() <= kSmemLimit; };
+    auto choose = [&](int cols) {            // the most warps with which so many columns fit
+        l.cols = cols;
+        if (cols == 1) {
+            f = form_of(0, kSingleWarps);
+            return fits();
+        }
+        for (int warps : kWarpChoices) {
+            f = form_of(tiles_of(cols), warps);
+            if (fits()) return true;
+        }
+        return false;
     };
     int cols = tokens < slots ? tokens : slots;          // a token's choices are distinct experts
     const int most = slots > 6ll * E ? kMaxCols : kTileCols;
     if (cols > most) cols = most;
-    const int wanted = cols;
-    while (cols > 1 && needs(cols, cols) + 2 * box(cols) > kSmemLimit) --cols;
     // where not all of an expert's slots fit, two chunks of one MMA take less
     // than one of two and one of one
-    if (cols < wanted && cols > kTileCols) cols = kTileCols;
-    l.cols = cols;
-    const int room = kSmemLimit - 2 * box(cols) - needs(cols, 0);
-    l.x_rows = room / (l.x_stride + parts * 4);
+    if (!choose(cols) && cols > kTileCols) cols = kTileCols;
+    while (!choose(cols) && cols > 1) --cols;
+    l.warps = f.warps;
     const int useful = cols == 1 ? kSingleRows : 3 * kMaxCols;
+    l.x_rows = (kSmemLimit - 2 * box() - needs(0)) / (l.x_stride + pieces * 4);
     if (l.x_rows > useful) l.x_rows = useful;
     if (l.x_rows > x_rows) l.x_rows = x_rows;
     if (l.x_rows < cols) l.x_rows = cols;
-    l.ring = (kSmemLimit - needs(cols, l.x_rows)) / box(cols);
-    if (l.ring > form_of(cols == 1).ring) l.ring = form_of(cols == 1).ring;
+    l.ring = (kSmemLimit - needs(l.x_rows)) / box();
+    if (l.ring > f.ring) l.ring = f.ring;
     if (l.ring < 1) return false;
-    const int ring = form_of(cols == 1).warps * l.ring;
-    l.scales = ring * form_of(cols == 1).box_bytes();
-    l.partial = l.scales + ring * form_of(cols == 1).box_scale_bytes();
-    l.x = l.partial + partial_bytes(cols);
+    const int ring = f.warps * l.ring;
+    l.scales = ring * f.box_bytes();
+    l.partial = l.scales + ring * f.box_scale_bytes();
+    l.x = l.partial + f.partial_bytes();
     l.x_scale = l.x + l.x_rows * l.x_stride;
-    l.zeros = (l.x_scale + l.x_rows * parts * 4 + 15) & ~15;
+    l.zeros = (l.x_scale + l.x_rows * pieces * 4 + 15) & ~15;
     l.bars = l.zeros + 2 * kPartK;
     l.tables = (l.bars + (ring + 2 * kMaxUnderWay) * 8 + 15) & ~15;
     l.total = l.tables + table_bytes(slots, cols) + 1024 - 16;
@@ -235,7 +253,7 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
         __syncthreads();
         return tb.count[0];
     }
-    constexpr int kTurns = kMatvecMaxSlots / kThreads;       // slots per thread
+    constexpr int kTurns = (kMatvecMaxSlots + kThreads - 1) / kThreads;      // slots per thread
     const int mask = hash_entries(a.slots) - 1, words = (a.slots + 31) / 32;
     int e[kTurns], h[kTurns], rank[kTurns];
 #pragma unroll
@@ -409,22 +427,22 @@ __device__ __forceinline__ void wait_count(const volatile int* count, int target
 }
 
 // kTiles: MMAs side by side, eight slots each; 0: a single slot.
-template <bool kSwiglu, int kTiles>
-__global__ void __launch_bounds__(form_of(kTiles == 0).warps * 32, 1)
+template <bool kSwiglu, int kTiles, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 1)
 expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_abort;
     constexpr bool kSingle = kTiles == 0;
     constexpr int kT = kSingle ? 1 : kTiles;
-    constexpr int kWarps = form_of(kSingle).warps;
+    constexpr Form kForm = form_of(kTiles, kWarps);
     constexpr int kThreads = kWarps * 32;
-    constexpr int kR = form_of(kSingle).row_tiles;
+    constexpr int kR = kForm.row_tiles;
     constexpr int kRows = 16 * kR;
-    constexpr int kParts = form_of(kSingle).parts;
+    constexpr int kParts = kForm.parts;
     constexpr int kBoxK = kParts * kPartK;
-    constexpr int kUnderWay = kMaxUnderWay / kT;
-    constexpr int kBoxBytes = form_of(kSingle).box_bytes();
-    constexpr int kBoxScaleBytes = form_of(kSingle).box_scale_bytes();
+    constexpr int kUnderWay = kForm.under_way / kT;
+    constexpr int kBoxBytes = kForm.box_bytes();
+    constexpr int kBoxScaleBytes = kForm.box_scale_bytes();
     constexpr int kScaleLanes = kRows * kParts;              // eight scales a lane
     static_assert(kScaleLanes <= 32, "a warp copies a box's scales at once");
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -790,7 +808,9 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             const int n_unit = before + done - run;
             const int place = n_unit % kUnderWay;
             const int round = n_unit / kUnderWay;
-            const int w0 = warp - (sharers - 1);             // the unit's first sharer, cyclically
+            // the unit's sharers in the order of their boxes: from w0 on, cyclically
+            const int w0 = warp + 1 - sharers + (warp + 1 < sharers ? kWarps : 0);
+            auto sharer = [&](int j) { return w0 + j - (w0 + j >= kWarps ? kWarps : 0); };
             wait_count(joined + place, round, ctx, 0x100 + place);
             if (kSingle) {
                 float* part = partial + place * kWarps * kRows;
@@ -808,7 +828,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 float y = 0.0f;
 #pragma unroll 4
                 for (int j = 0; j < sharers; ++j)
-                    y += part[((w0 + j) & (kWarps - 1)) * kRows + (lane & 15)];
+                    y += part[sharer(j) * kRows + (lane & 15)];
                 __syncwarp();
                 if (lane == 0) {
                     __threadfence_block();
@@ -843,7 +863,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 #pragma unroll 4
                     for (int j = 0; j < sharers; ++j) {
                         const float4 v = *reinterpret_cast<const float4*>(
-                            part + (((w0 + j) & (kWarps - 1)) * kA + i) * 32);
+                            part + (sharer(j) * kA + i) * 32);
                         sum[i].x += v.x;
                         sum[i].y += v.y;
                         sum[i].z += v.z;
@@ -897,46 +917,59 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     }
 }
 
-// Devices (a bit each) on which a kernel's shared-memory limit has been set.
-std::atomic<uint64_t> g_ready[2][3];
+// Devices (a bit each) on which a kernel's shared-memory limit has been set:
+// by epilogue, MMAs, warps / 4.
+std::atomic<uint64_t> g_ready[2][3][5];
 
-template <bool kSwiglu, int kTiles>
+template <bool kSwiglu, int kTiles, int kWarps>
 cudaError_t launch(const CUtensorMap& map, const KernelArgs& k, int grid, cudaStream_t stream) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
-    std::atomic<uint64_t>& ready = g_ready[kSwiglu][kTiles];
+    std::atomic<uint64_t>& ready = g_ready[kSwiglu][kTiles][kWarps / 4];
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {
-        err = cudaFuncSetAttribute(expert_matvec_kernel<kSwiglu, kTiles>,
+        err = cudaFuncSetAttribute(expert_matvec_kernel<kSwiglu, kTiles, kWarps>,
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (err != cudaSuccess) return err;
         ready.fetch_or(bit);
     }
-    return launch_dependent(expert_matvec_kernel<kSwiglu, kTiles>, grid,
-                            form_of(kTiles == 0).warps * 32, k.l.total, stream, map, k);
+    return launch_dependent(expert_matvec_kernel<kSwiglu, kTiles, kWarps>, grid, kWarps * 32,
+                            k.l.total, stream, map, k);
+}
+
+template <bool kSwiglu, int kTiles>
+cudaError_t launch_warps(const CUtensorMap& map, const KernelArgs& k, int grid,
+                         cudaStream_t stream) {
+    return k.l.warps == kWarpChoices[0]
+               ? launch<kSwiglu, kTiles, kWarpChoices[0]>(map, k, grid, stream)
+               : launch<kSwiglu, kTiles, kWarpChoices[1]>(map, k, grid, stream);
 }
 
 template <bool kSwiglu>
 cudaError_t launch_cols(const CUtensorMap& map, const KernelArgs& k, int grid,
                         cudaStream_t stream) {
-    if (k.l.cols == 1) return launch<kSwiglu, 0>(map, k, grid, stream);
-    if (k.l.cols <= kTileCols) return launch<kSwiglu, 1>(map, k, grid, stream);
-    return launch<kSwiglu, 2>(map, k, grid, stream);
+    switch (tiles_of(k.l.cols)) {
+        case 0: return launch<kSwiglu, 0, kSingleWarps>(map, k, grid, stream);
+        case 1: return launch_warps<kSwiglu, 1>(map, k, grid, stream);
+        default: return launch_warps<kSwiglu, 2>(map, k, grid, stream);
+    }
 }
 
 }  // namespace
 
 void matvec_reset_caches() {
-    for (auto& form : g_ready) {
-        for (auto& ready : form) ready.store(0);
+    for (auto& epilogue : g_ready) {
+        for (auto& tiles : epilogue) {
+            for (auto& ready : tiles) ready.store(0);
+        }
     }
 }
 
 int matvec_unit_rows(const MatvecArgs& a) {
     Layout l;
     return make_layout(a.K, a.slots, a.tokens, a.E, a.slots / a.slots_per_row, &l)
-               ? form_of(l.cols == 1).rows()
+               ? form_of(tiles_of(l.cols), l.warps).rows()
                : 0;
 }
 
@@ -956,7 +989,7 @@ cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, 
     k.N = a.N;
     k.K = a.K;
     if (!make_layout(a.K, a.slots, a.tokens, a.E, k.x_rows, &k.l)) return cudaErrorInvalidValue;
-    const int tile_cols = form_of(k.l.cols == 1).rows() / (a.swiglu ? 2 : 1);
+    const int tile_cols = form_of(tiles_of(k.l.cols), k.l.warps).rows() / (a.swiglu ? 2 : 1);
     const long long tiles = ((a.swiglu ? a.N / 2 : a.N) + tile_cols - 1) / tile_cols;
     const long long units = tiles * a.slots;
     const int grid = static_cast<int>(units < num_sms ? units : num_sms);
