@@ -20,9 +20,8 @@
 // several passes); a block holds eight warps of whole teams.  The token's own
 // pieces stay in registers while the rows of its choices go by.  Measured: the
 // combine's gradient of 16384 x 6144, top-8, 489 us for 3424 MB (7.0 TB/s); the
-// dispatch's with dw at that size 351 us for 2015 MB (5.7 TB/s: each token waits
-// for its ids first and for the join of its dot products last); the dispatch
-// of 768 x 6144, top-8, 14.7 us for 85 MB.
+// dispatch's with dw at that size 320 us for 2015 MB (6.3 TB/s); the dispatch of
+// 768 x 6144, top-8, 14.7 us for 85 MB.
 #include "hg_internal.cuh"
 #include "numeric.cuh"
 
@@ -254,12 +253,12 @@ token_grad_kernel(const uint16_t* __restrict__ rows, const uint16_t* __restrict_
 // Warps per token and pieces per lane for rows of n elements.
 struct Shape {
     int team_warps, pieces;
-    explicit Shape(int n) {
+    explicit Shape(int n, int most_warps = kWarps, int most_pieces = kMaxPieces) {
         const int chunks = (n + 7) / 8;
         team_warps = 1;
-        while (team_warps < kWarps && 32 * team_warps * kMaxPieces < chunks) team_warps *= 2;
+        while (team_warps < most_warps && 32 * team_warps * most_pieces < chunks) team_warps *= 2;
         pieces = (chunks + 32 * team_warps - 1) / (32 * team_warps);
-        if (pieces > kMaxPieces) pieces = kMaxPieces;
+        if (pieces > most_pieces) pieces = most_pieces;
     }
     int blocks(int M) const {
         const int teams = kWarps / team_warps;
@@ -267,10 +266,23 @@ struct Shape {
     }
 };
 
+// With tokens enough for every SM's warps (16 a SM), a warp for itself takes a
+// token in several passes where a team would mostly wait: for one choice's row
+// (16384 x 2056: 42 us, a team 46 to 55), and for the dispatch's gradient with
+// dw, whose dot products join across a team's warps (16384 x 6144, top-8: 320
+// us, a team 352; 8004 x 3336, top-3: 54 and 65).
+constexpr int kManyTokens = 16 * 152;
+template <bool kSum, bool kDots>
+Shape grad_shape(int M, int top_k, int N) {
+    if (M >= kManyTokens && top_k == 1) return Shape(N, 1);
+    if (M >= kManyTokens && kSum && kDots) return Shape(N, 1, 2);
+    return Shape(N);
+}
+
 // Two rows in flight and three or four blocks per SM against four rows and two
 // blocks: 489 against 504 us for the combine's gradient (M = 16384, N = 6144,
-// top-8), 353 against 365 for the dispatch's with dw, 63 against 77 without (M
-// = 4096), where the sums alone leave registers for a fourth block.  With
+// top-8), 63 against 77 for the dispatch's without dw (M = 4096), where the sums
+// alone leave registers for a fourth block.  With
 // one choice a second row would be no row.
 template <bool kSum, bool kDots, int kPieces>
 cudaError_t launch_pieces(const Shape& s, const uint16_t* rows, const uint16_t* token,
@@ -288,7 +300,7 @@ template <bool kSum, bool kDots>
 cudaError_t launch_grad(const uint16_t* rows, const uint16_t* token, const int32_t* d2s,
                         const float* weights, int M, int top_k, int N, uint16_t* out, float* dw,
                         cudaStream_t stream) {
-    const Shape s(N);
+    const Shape s = grad_shape<kSum, kDots>(M, top_k, N);
     const auto launch = s.pieces == 1   ? launch_pieces<kSum, kDots, 1>
                         : s.pieces == 2 ? launch_pieces<kSum, kDots, 2>
                         : s.pieces == 3 ? launch_pieces<kSum, kDots, 3>

@@ -359,7 +359,7 @@ hg_status hg_dispatch_tokens(const uint16_t* x_bf16, const int32_t* src_to_sorte
  *   dweights[t, j] = sum_k drows[src_to_sorted[t*top_k + j], k] * x[t, k]
  *
  * the first sum in FP32 over j ascending, the second in FP32 in an order that
- * depends on K alone; terms whose entry is outside [0, M*top_k) are
+ * depends on the sizes alone; terms whose entry is outside [0, M*top_k) are
  * skipped, and their dweights are 0.
  *
  *   drows_bf16    uint16 [M*top_k, K] BF16, 16-byte aligned.

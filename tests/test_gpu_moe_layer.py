@@ -109,6 +109,29 @@ def test_combine_topk_bwd(cuda_lib, M, N, k, E, drop):
     _close(dw.double().cpu().numpy(), want, N * FP32 * mag, "dw")
 
 
+# tokens enough for a warp each: several passes over a row, one choice, more
+# choices than are reduced together
+@pytest.mark.parametrize("M,N,k,E,drop", [(2500, 2056, 1, 8, 40), (2433, 1032, 9, 16, 300),
+                                          (2600, 520, 3, 8, 0)])
+def test_token_gradients_of_many_tokens(cuda_lib, M, N, k, E, drop):
+    place = _place(M, E, k, M + N + 3, drop)
+    p, d2s = place.reshape(M, k), torch.from_numpy(place).cuda()
+    x = _normal(15, M, N).to(torch.bfloat16)
+    rows = _normal(16, M * k, N).to(torch.bfloat16)
+    w = _normal(17, M, k)
+    xf, rf, wf = _f64(x), _f64(rows), w.double().numpy()
+    dx, dw = cuda_lib.hg_dispatch_tokens_bwd(rows.cuda(), k, d2s, w.cuda(), x.cuda())
+    want, mag = L.combine(rf, p, wf)
+    _close(_f64(dx), want, BF16 * np.abs(want) + k * FP32 * mag + 2.0 ** -134, "dx")
+    dots, mag = L.row_dots(rf, xf, p)
+    _close(dw.double().cpu().numpy(), dots, N * FP32 * mag, "dw")
+    dy = torch.full((M * k, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, dw = cuda_lib.hg_combine_topk_bwd(x.cuda(), rows.cuda(), d2s, w.cuda(), dy=dy)
+    _close(dw.double().cpu().numpy(), dots, N * FP32 * mag, "dw of the combine")
+    want = L.dispatch(xf, p, wf, np.full((M * k, N), 7.0))
+    _close(_f64(dy), want, (BF16 + FP32) * np.abs(want), "dy")
+
+
 def test_tokens_with_every_choice_dropped_and_entries_out_of_range(cuda_lib):
     M, K, k = 6, 136, 2
     place = np.array([-1, -1, 3, 12, -5, 0, 1 << 30, -1, 2, 1, -2 ** 31, 4], dtype=np.int32)
