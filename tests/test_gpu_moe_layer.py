@@ -384,6 +384,27 @@ def test_expert_matvec_ids_out_of_range_give_zeros(cuda_lib, swiglu):
     assert float(out.abs().max()) == 0
 
 
+@pytest.mark.parametrize("M,k,E,N,K,per_slot", [(20, 4, 6, 40, 384, False), (40, 2, 300, 16, 128, True),
+                                                (33, 1, 2, 70, 512, False), (64, 8, 5, 24, 256, True),
+                                                (100, 5, 1 << 20, 2, 128, False)])
+def test_expert_matvec_many_slots_with_ids_out_of_range(cuda_lib, M, k, E, N, K, per_slot):
+    # more than 32 slots: experts met once and often, a choice met twice by a
+    # token, ids out of range anywhere among them
+    rng = np.random.default_rng(M + E)
+    few = rng.integers(0, E, 5) if E > 100 else np.arange(E)
+    ids = rng.choice(few, (M, k)).astype(np.int32)
+    ids[rng.random((M, k)) < 0.15] = -1
+    ids[rng.random((M, k)) < 0.1] = E
+    ids[0, 0], ids[-1, -1] = 2 ** 31 - 1, -2 ** 31
+    x = torch.from_numpy(rng.standard_normal((M * k if per_slot else M, K))).to(torch.bfloat16)
+    w = torch.from_numpy(rng.integers(0, 256, (E, N, K // 2), dtype=np.uint8))
+    ws = torch.from_numpy(rng.integers(120, 130, (E, N, K // 32), dtype=np.uint8))
+    out = torch.full((M * k, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    _check_matvec(cuda_lib, M, k, E, N, K, per_slot, False, ids=ids, x=x, w=(w, ws), out=out)
+    bad = (ids.reshape(-1) < 0) | (ids.reshape(-1) >= E)
+    assert bad.any() and float(out[torch.from_numpy(bad).cuda()].abs().max()) == 0
+
+
 def test_expert_matvec_wide_range(cuda_lib):
     # rows whose elements span many powers of two, and weight scales from 2^-127
     # to 2^60: what is small beside the row's largest element still counts where
