@@ -20,8 +20,8 @@
 // boxes of a block's units, in order, go to its warps in turn, so that all
 // have the same work whatever K is; a unit's partial sums meet in shared memory,
 // in a fixed order (the result does not depend on timing), and the warp of the
-// unit's last box writes the outputs.  Nobody else waits for that: the sums of
-// several units may be under way at once.
+// unit's last box writes the outputs.  The sums of several units may be under
+// way at once.
 //
 // Arithmetic: a box's E2M1 codes become FP16 (exact) in registers and meet x
 // in mma.sync m16n8k16: with sixteen columns at most the tensor work is small,
@@ -36,8 +36,9 @@
 // Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 22.6
 // us for 107 MB, of which 3.5 pass before the first weights arrive; from there
 // on the weights stream at the measured copy rate.  Down, 6144 x 2048: 14.5 us
-// for 54 MB.  13 tokens on 12 experts, 6144 x 3584: 47.7 us for 142 MB, bound by
-// the latency of conversion, MMA and scaling with two warps per scheduler.
+// for 54 MB.  4 tokens, gate/up: 48.6 us for 293 MB.  13 tokens on 12 experts,
+// 6144 x 3584: 47.4 us for 142 MB, bound by the latency of conversion, MMA and
+// scaling with three warps per scheduler.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -54,35 +55,34 @@ constexpr int kMaxCols = 16;                 // slots of a chunk: at most two MM
 constexpr int kSingleRows = 4;               // input rows held for single columns
 constexpr int kPartK = 256;                  // elements of 128 bytes of a weight row
 constexpr int kBlockBytes = 8 * kPartK / 2;  // 8 rows of a part: one swizzle pattern
-constexpr int kMaxUnderWay = 4;              // units whose partial sums are kept at once, at most
+constexpr int kUnderWay = 4;                 // units whose sums are kept at once
 constexpr int kSmemLimit = 232448 - 256;     // beside a few static bytes
 
 // The forms of the kernel.  A single column's MMAs are light, and its boxes
 // are long in K: 16 rows x 512 K.  With more columns the fragments of x weigh
 // more than the weights, and 32 rows x 256 K share each of them between two
 // MMAs.  There twelve warps where they leave room for x, else eight: what
-// bounds them is the latency of each warp's chain of instructions (8 tokens on
-// 32 experts, 6144 x 2048: twelve warps 36.6 us, eight 48.9, sixteen, short of
-// registers, 41.8).
+// bounds them is the latency of each warp's chain of instructions (4 tokens on
+// 32 experts, gate/up 4096 x 6144: twelve warps 48.6 us, eight 58; sixteen are
+// short of registers).
 // The ring is no deeper than the memory's latency needs: 128 KB in flight per
 // SM; half as much again takes a token's gate/up product (E = 32, top-8,
 // N = 4096, K = 6144) from 22.4 to 24.1 us.
 struct Form {
     int warps, row_tiles, parts;             // parts: of 256 K in a box
     int ring;                                // boxes in flight per warp, at most
-    int under_way;                           // units whose partial sums are kept, times MMAs
     __host__ __device__ constexpr int rows() const { return 16 * row_tiles; }
     __host__ __device__ constexpr int box_bytes() const { return 2 * row_tiles * parts * kBlockBytes; }
     __host__ __device__ constexpr int box_scale_bytes() const { return box_bytes() / 16; }
-    __host__ __device__ constexpr int partial_bytes() const {
-        return warps * under_way * rows() * (row_tiles == 1 ? 1 : kTileCols) * 4;
-    }
 };
-// tiles: MMAs side by side, 0 for a single column.  Two units under way at least
-// (one: 54.6 in place of 48 us for 13 tokens on 12 experts, 6144 x 3584).
+// tiles: MMAs side by side, 0 for a single column.
 __host__ __device__ constexpr Form form_of(int tiles, int warps) {
-    return tiles == 0 ? Form{warps, 1, 2, 2, 4}
-                      : Form{warps, 2, 1, 4, tiles == 2 || warps == 8 ? 4 : 2};
+    return tiles == 0 ? Form{warps, 1, 2, 2} : Form{warps, 2, 1, 4};
+}
+// Sums of the units under way: of a single column a float per weight row from
+// every warp, else one running sum per row and column.
+__host__ __device__ constexpr int partial_bytes(int tiles, const Form& f) {
+    return kUnderWay * f.rows() * 4 * (tiles == 0 ? f.warps : tiles * kTileCols);
 }
 __host__ __device__ constexpr int tiles_of(int cols) {
     return cols == 1 ? 0 : cols <= kTileCols ? 1 : 2;
@@ -158,8 +158,8 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     Form f;
     auto box = [&]() { return f.warps * (f.box_bytes() + f.box_scale_bytes()); };
     auto needs = [&](int rows) {
-        return 1024 + f.partial_bytes() + rows * (l.x_stride + pieces * 4) + 16 +
-               2 * kPartK + (f.warps * f.ring + 2 * kMaxUnderWay) * 8 + table_bytes(slots, l.cols);
+        return 1024 + partial_bytes(tiles_of(l.cols), f) + rows * (l.x_stride + pieces * 4) + 16 +
+               2 * kPartK + (f.warps * f.ring + 2 * kUnderWay) * 8 + table_bytes(slots, l.cols);
     };
     auto fits = [&]() { return needs(l.cols) + 2 * box() <= kSmemLimit; };
     auto choose = [&](int cols) {            // the most warps with which so many columns fit
@@ -193,11 +193,11 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     const int ring = f.warps * l.ring;
     l.scales = ring * f.box_bytes();
     l.partial = l.scales + ring * f.box_scale_bytes();
-    l.x = l.partial + f.partial_bytes();
+    l.x = l.partial + partial_bytes(tiles_of(cols), f);
     l.x_scale = l.x + l.x_rows * l.x_stride;
     l.zeros = (l.x_scale + l.x_rows * pieces * 4 + 15) & ~15;
     l.bars = l.zeros + 2 * kPartK;
-    l.tables = (l.bars + (ring + 2 * kMaxUnderWay) * 8 + 15) & ~15;
+    l.tables = (l.bars + (ring + 2 * kUnderWay) * 8 + 15) & ~15;
     l.total = l.tables + table_bytes(slots, cols) + 1024 - 16;
     *out = l;
     return true;
@@ -440,7 +440,6 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     constexpr int kRows = 16 * kR;
     constexpr int kParts = kForm.parts;
     constexpr int kBoxK = kParts * kPartK;
-    constexpr int kUnderWay = kForm.under_way / kT;
     constexpr int kBoxBytes = kForm.box_bytes();
     constexpr int kBoxScaleBytes = kForm.box_scale_bytes();
     constexpr int kScaleLanes = kRows * kParts;              // eight scales a lane
@@ -451,11 +450,12 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t bars = base + a.l.bars + 8 * warp * a.l.ring;
     const uint32_t full = base + a.l.bars + 8 * kWarps * a.l.ring;
-    // rounds of each place of the partial sums that have been joined
+    // of each place of the sums: the rounds that have been joined (single
+    // column), or the parts that have been added
     volatile int* joined = reinterpret_cast<volatile int*>(smem + a.l.bars + 8 * kWarps * a.l.ring +
-                                                           8 * kMaxUnderWay);
+                                                           8 * kUnderWay);
 
-    const uint32_t x_bar = full + 8 * kMaxUnderWay + 4 * kMaxUnderWay;   // behind `joined`
+    const uint32_t x_bar = full + 8 * kUnderWay + 4 * kUnderWay;   // behind `joined`
     const int nb = (a.K + kBoxK - 1) / kBoxK;
     const int sharers = min(nb, kWarps);                     // warps that work on one unit
     const int out_cols = kSwiglu ? a.N / 2 : a.N;
@@ -793,8 +793,8 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 at = 0;
                 phase ^= 1;
             }
-            const int done = u;
-            const bool last_box = b == nb - 1;
+            const int done = u, boxes_left = nb - 1 - b;     // of unit u
+            const bool last_box = boxes_left == 0;
             u += step_u;
             b += step_b;
             if (b >= nb) {
@@ -808,11 +808,11 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             const int n_unit = before + done - run;
             const int place = n_unit % kUnderWay;
             const int round = n_unit / kUnderWay;
-            // the unit's sharers in the order of their boxes: from w0 on, cyclically
-            const int w0 = warp + 1 - sharers + (warp + 1 < sharers ? kWarps : 0);
-            auto sharer = [&](int j) { return w0 + j - (w0 + j >= kWarps ? kWarps : 0); };
-            wait_count(joined + place, round, ctx, 0x100 + place);
             if (kSingle) {
+                // the unit's sharers in the order of their boxes: from w0 on, cyclically
+                const int w0 = warp + 1 - sharers + (warp + 1 < sharers ? kWarps : 0);
+                auto sharer = [&](int j) { return w0 + j - (w0 + j >= kWarps ? kWarps : 0); };
+                wait_count(joined + place, round, ctx, 0x100 + place);
                 float* part = partial + place * kWarps * kRows;
 #pragma unroll
                 for (int o = 1; o <= 2; o <<= 1) {
@@ -843,41 +843,37 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                     a.out[static_cast<long long>(tb.slot[x_chunk]) * out_cols + n] =
                         __bfloat16_as_ushort(__float2bfloat16_rn(y));
             } else {
+                // The parts are added to one sum in the order of the boxes,
+                // which is that of their arrival, more or less: each warp
+                // waits for its turn.  (A copy per warp would take the room
+                // of two to four warps' rings.)
                 constexpr int kA = kR * kT;
-                ulonglong2* part = reinterpret_cast<ulonglong2*>(partial) +
-                                   place * kWarps * kA * 32 + lane;
+                ulonglong2* sum = reinterpret_cast<ulonglong2*>(partial) + place * kA * 32 + lane;
+                const int turn = sharers - 1 - boxes_left;
+                wait_count(joined + place, round * sharers + turn, ctx, 0x100 + place);
+                float4 total[kA];
 #pragma unroll
                 for (int i = 0; i < kA; ++i) {
-                    part[(warp * kA + i) * 32] =
-                        make_ulonglong2(acc[i / kT][i % kT][0], acc[i / kT][i % kT][1]);
-                    acc[i / kT][i % kT][0] = acc[i / kT][i % kT][1] = 0;
-                }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(full + 8 * place);
-                if (!last_box) continue;
-                wait_bounded(full + 8 * place, round & 1, ctx, kRoleMatvec, 0x200 + place);
-                float4 sum[kA];
-#pragma unroll
-                for (int i = 0; i < kA; ++i) {
-                    sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int j = 0; j < sharers; ++j) {
-                        const float4 v = *reinterpret_cast<const float4*>(
-                            part + (sharer(j) * kA + i) * 32);
-                        sum[i].x += v.x;
-                        sum[i].y += v.y;
-                        sum[i].z += v.z;
-                        sum[i].w += v.w;
+                    uint64_t(&mine)[2] = acc[i / kT][i % kT];
+                    if (turn > 0) {
+                        const ulonglong2 v = sum[i * 32];
+                        mine[0] = ptx::add_f32x2(v.x, mine[0]);
+                        mine[1] = ptx::add_f32x2(v.y, mine[1]);
                     }
+                    if (!last_box) sum[i * 32] = make_ulonglong2(mine[0], mine[1]);
+                    const float2 lo = ptx::f32x2_parts(mine[0]), hi = ptx::f32x2_parts(mine[1]);
+                    total[i] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                    mine[0] = mine[1] = 0;
                 }
                 __syncwarp();
                 if (lane == 0) {
                     __threadfence_block();
-                    joined[place] = round + 1;
+                    joined[place] = round * sharers + turn + 1;
                 }
+                if (!last_box) continue;
 #pragma unroll
                 for (int j = 0; j < kA; ++j) {
-                    const float y[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
+                    const float y[4] = {total[j].x, total[j].y, total[j].z, total[j].w};
                     const int n0 = (done - x_chunk * tiles) * tile_cols +
                                    j / kT * (kSwiglu ? 8 : 16) + g8;
 #pragma unroll
