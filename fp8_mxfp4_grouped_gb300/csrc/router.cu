@@ -149,7 +149,16 @@ router_topk_bwd_kernel(const float* __restrict__ logits, const int32_t* __restri
             id = -1;
         }
     }
-    const float inner = warp_sum(w * dw);
+    // dw - sum_j w_j dw_j; renormalised weights add up to 1, and sum_j w_j (dw -
+    // dw_j) does not cancel where one weight is nearly all of it
+    float inner = 0.0f, rise = 0.0f;
+    if (renormalize) {
+        for (int j = 0; j < top_k; ++j)
+            rise = fmaf(__shfl_sync(0xFFFFFFFFu, w, j), dw - __shfl_sync(0xFFFFFFFFu, dw, j), rise);
+    } else {
+        inner = warp_sum(w * dw);
+        rise = dw - inner;
+    }
     const int first = __shfl_sync(0xFFFFFFFFu, id, 0);
     float* out = dlogits + t * E;
     if (renormalize || first < 0) {
@@ -162,7 +171,7 @@ router_topk_bwd_kernel(const float* __restrict__ logits, const int32_t* __restri
         for (int e = lane; e < E; e += 32) out[e] = expf(__ldg(row + e) - top) * scale;
     }
     __syncwarp();                            // the chosen ones' values come last
-    if (id >= 0) out[id] = w * (dw - inner);
+    if (id >= 0) out[id] = w * rise;
 }
 
 template <int kHeld>
