@@ -72,7 +72,9 @@ struct Form {
     int warps, row_tiles, parts;             // parts: of 256 K in a box
     int ring;                                // boxes in flight per warp, at most
     __host__ __device__ constexpr int rows() const { return 16 * row_tiles; }
-    __host__ __device__ constexpr int box_bytes() const { return 2 * row_tiles * parts * kBlockBytes; }
+    __host__ __device__ constexpr int box_bytes() const {
+        return 2 * row_tiles * parts * kBlockBytes;
+    }
     __host__ __device__ constexpr int box_scale_bytes() const { return box_bytes() / 16; }
 };
 // tiles: MMAs side by side, 0 for a single column.
@@ -646,7 +648,8 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     // by row.  The 8-row blocks of a box follow one another; MMA r takes blocks
     // 2r and 2r + 1, or with SwiGLU block r of the gate's and of the up rows.
     constexpr int kHiBlock = kSwiglu ? kR : 1, kTileBlock = kSwiglu ? 1 : 2;
-    const uint32_t lm_row = ring_w + ((lane >> 3) & 1) * (kHiBlock * kBlockBytes) + (lane & 7) * 128;
+    const uint32_t lm_row =
+        ring_w + ((lane >> 3) & 1) * (kHiBlock * kBlockBytes) + (lane & 7) * 128;
     constexpr int kScaleRow = 8 * kParts;
     const uint8_t* my_scales = smem + a.l.scales + warp * a.l.ring * kBoxScaleBytes +
                                g8 * kScaleRow;

@@ -165,26 +165,13 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
         : "r"(w));
 }
 
-// Two E8M0 codes (the low 16 bits) as floats.
+// Two E8M0 codes (the low 16 bits) as floats (2^(code - 127); code 255 is NaN).
 __device__ __forceinline__ float2 e8m0x2_to_f32(uint32_t codes) {
     uint32_t two;                            // a pair of BF16, exact
     asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, p;\n\t}"
         : "=r"(two)
         : "r"(codes));
     return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u));
-}
-
-// Four E8M0 codes as floats (2^(code - 127); code 255 is NaN).
-__device__ __forceinline__ void e8m0x4_to_f32(uint32_t codes, float (&f)[4]) {
-    uint32_t lo, hi;                         // pairs of BF16, exact
-    asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, p;\n\t"
-        "cvt.rn.bf16x2.ue8m0x2 %1, q;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(codes));
-    f[0] = __uint_as_float(lo << 16);
-    f[1] = __uint_as_float(lo & 0xFFFF0000u);
-    f[2] = __uint_as_float(hi << 16);
-    f[3] = __uint_as_float(hi & 0xFFFF0000u);
 }
 
 // d = a * b and d += a * b: 16 x 16 times 16 x 8, FP16 operands, FP32 sums.

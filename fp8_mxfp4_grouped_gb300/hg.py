@@ -364,7 +364,8 @@ def hg_combine_topk_bwd(dout: torch.Tensor, y_bf16: torch.Tensor, src_to_sorted:
     dy = _out(dy, (M * k, N), torch.bfloat16, dout, stream)
     dweights = _out(dweights, (M, k), torch.float32, dout, stream)
     st = lib.hg_combine_topk_bwd(_addr(dout), _addr(y_bf16), _addr(src_to_sorted),
-                                 _addr(topk_weights), M, k, N, _addr(dy), _addr(dweights), _handle(stream, dout))
+                                 _addr(topk_weights), M, k, N, _addr(dy), _addr(dweights),
+                                 _handle(stream, dout))
     _check(st, "hg_combine_topk_bwd")
     return dy, dweights
 
@@ -460,7 +461,8 @@ def hg_router_topk_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, topk_weight
         assert t.dtype == torch.float32 and t.shape == (M, k) and t.is_contiguous()
     dlogits = _out(dlogits, (M, E), torch.float32, logits, stream)
     st = lib.hg_router_topk_bwd(_addr(logits), _addr(topk_ids), _addr(topk_weights),
-                                _addr(dweights), M, E, k, int(renormalize), _addr(dlogits), _handle(stream, logits))
+                                _addr(dweights), M, E, k, int(renormalize), _addr(dlogits),
+                                _handle(stream, logits))
     _check(st, "hg_router_topk_bwd")
     return dlogits
 

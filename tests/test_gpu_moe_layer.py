@@ -85,7 +85,8 @@ def test_dispatch_tokens_bwd(cuda_lib, M, K, k, E, drop, weighted, dots):
     dx, dw = cuda_lib.hg_dispatch_tokens_bwd(rows.cuda(), k, torch.from_numpy(place).cuda(),
                                              None if w is None else w.cuda(),
                                              x.cuda() if dots else None)
-    want, mag = L.combine(_f64(rows), place.reshape(M, k), None if w is None else w.double().numpy())
+    want, mag = L.combine(_f64(rows), place.reshape(M, k),
+                          None if w is None else w.double().numpy())
     _close(_f64(dx), want, BF16 * np.abs(want) + k * FP32 * mag + 2.0 ** -134, "dx")
     if not dots:
         assert dw is None
@@ -376,17 +377,17 @@ def test_expert_matvec_ids_out_of_range_give_zeros(cuda_lib, swiglu):
     assert float(out[[0, 3, 4, 5, 7, 8]].abs().max()) == 0
     # no slot with an expert at all
     out.fill_(float("nan"))
-    _check = np.full((4, 3), -1, dtype=np.int32)
+    none = np.full((4, 3), -1, dtype=np.int32)
     f = cuda_lib.hg_expert_matvec_swiglu if swiglu else cuda_lib.hg_expert_matvec
     w, ws = make_weights(4, 20, 256, seed=0)
-    f(torch.ones(4, 256, dtype=torch.bfloat16).cuda(), torch.from_numpy(_check).cuda(), w.cuda(),
+    f(torch.ones(4, 256, dtype=torch.bfloat16).cuda(), torch.from_numpy(none).cuda(), w.cuda(),
       ws.cuda(), out=out)
     assert float(out.abs().max()) == 0
 
 
-@pytest.mark.parametrize("M,k,E,N,K,per_slot", [(20, 4, 6, 40, 384, False), (40, 2, 300, 16, 128, True),
-                                                (33, 1, 2, 70, 512, False), (64, 8, 5, 24, 256, True),
-                                                (100, 5, 1 << 20, 2, 128, False)])
+@pytest.mark.parametrize("M,k,E,N,K,per_slot", [
+    (20, 4, 6, 40, 384, False), (40, 2, 300, 16, 128, True), (33, 1, 2, 70, 512, False),
+    (64, 8, 5, 24, 256, True), (100, 5, 1 << 20, 2, 128, False)])
 def test_expert_matvec_many_slots_with_ids_out_of_range(cuda_lib, M, k, E, N, K, per_slot):
     # more than 32 slots: experts met once and often, a choice met twice by a
     # token, ids out of range anywhere among them
