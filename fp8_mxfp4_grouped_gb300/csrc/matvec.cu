@@ -17,11 +17,14 @@
 //
 // Warps stream: each warp owns a ring of 4-KB boxes of weights that its lane 0
 // fills by TMA, and runs ahead of its own use of them by the ring's depth.  The
-// boxes of a block's units, in order, go to its warps in turn, so that all
-// have the same work whatever K is; a unit's partial sums meet in shared memory,
-// in a fixed order (the result does not depend on timing), and the warp of the
-// unit's last box writes the outputs.  The sums of several units may be under
-// way at once.
+// boxes of a block's units, in order, are cut into one contiguous range per
+// warp, so that all have the same work whatever K is.  A warp leaves the sums
+// of a unit that began before its range in shared memory; the warp of a unit's
+// first box adds those to its own, in the order of the warps (the result does
+// not depend on timing), and writes the outputs.  It does so at the end of its
+// range, and the others did theirs at the start: nobody waits, mostly.  (Boxes
+// dealt to the warps in turn, and sums added in the order of the boxes, had the
+// warps wait a third of their time: 13 tokens on 12 experts 47.4 us.)
 //
 // Arithmetic: a box's E2M1 codes become FP16 (exact) in registers and meet x
 // in mma.sync m16n8k16: with sixteen columns at most the tensor work is small,
@@ -33,12 +36,12 @@
 // own rounding.  The sums of a 32-K group come out of the MMA in FP32 and are
 // added up in FP32 times the product of the two scales.
 //
-// Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 22.6
+// Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 20.8
 // us for 107 MB, of which 3.5 pass before the first weights arrive; from there
-// on the weights stream at the measured copy rate.  Down, 6144 x 2048: 14.5 us
-// for 54 MB.  4 tokens, gate/up: 48.6 us for 293 MB.  13 tokens on 12 experts,
-// 6144 x 3584: 47.4 us for 142 MB, bound by the latency of conversion, MMA and
-// scaling with three warps per scheduler.
+// on the weights stream at the measured copy rate.  Down, 6144 x 2048: 13.3 us
+// for 54 MB.  4 tokens, gate/up: 43.1 us for 293 MB; 8 tokens, down: 29.0 us
+// for 194 MB.  13 tokens on 12 experts, 6144 x 3584: 42.7 us for 142 MB, bound by
+// the instructions issued: conversion, MMA and scaling.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -55,19 +58,16 @@ constexpr int kMaxCols = 16;                 // slots of a chunk: at most two MM
 constexpr int kSingleRows = 4;               // input rows held for single columns
 constexpr int kPartK = 256;                  // elements of 128 bytes of a weight row
 constexpr int kBlockBytes = 8 * kPartK / 2;  // 8 rows of a part: one swizzle pattern
-constexpr int kUnderWay = 4;                 // units whose sums are kept at once
 constexpr int kSmemLimit = 232448 - 256;     // beside a few static bytes
 
 // The forms of the kernel.  A single column's MMAs are light, and its boxes
 // are long in K: 16 rows x 512 K.  With more columns the fragments of x weigh
 // more than the weights, and 32 rows x 256 K share each of them between two
 // MMAs.  There twelve warps where they leave room for x, else eight: what
-// bounds them is the latency of each warp's chain of instructions (4 tokens on
-// 32 experts, gate/up 4096 x 6144: twelve warps 48.6 us, eight 58; sixteen are
-// short of registers).
-// The ring is no deeper than the memory's latency needs: 128 KB in flight per
-// SM; half as much again takes a token's gate/up product (E = 32, top-8,
-// N = 4096, K = 6144) from 22.4 to 24.1 us.
+// bounds them is the instructions they issue, and eight leave gaps between
+// them; sixteen are short of registers (13 tokens on 12 experts 45.5 us, twelve
+// 42.4).  Two boxes a warp cover the memory's latency; three or four change
+// nothing.
 struct Form {
     int warps, row_tiles, parts;             // parts: of 256 K in a box
     int ring;                                // boxes in flight per warp, at most
@@ -75,16 +75,16 @@ struct Form {
     __host__ __device__ constexpr int box_bytes() const {
         return 2 * row_tiles * parts * kBlockBytes;
     }
-    __host__ __device__ constexpr int box_scale_bytes() const { return box_bytes() / 16; }
+    // of two boxes
+    __host__ __device__ constexpr int scale_bytes() const { return box_bytes() / 8; }
 };
 // tiles: MMAs side by side, 0 for a single column.
 __host__ __device__ constexpr Form form_of(int tiles, int warps) {
-    return tiles == 0 ? Form{warps, 1, 2, 2} : Form{warps, 2, 1, 4};
+    return tiles == 0 ? Form{warps, 1, 2, 2} : Form{warps, 2, 1, 2};
 }
-// Sums of the units under way: of a single column a float per weight row from
-// every warp, else one running sum per row and column.
+// The sums that each warp leaves: a float per weight row and column.
 __host__ __device__ constexpr int partial_bytes(int tiles, const Form& f) {
-    return kUnderWay * f.rows() * 4 * (tiles == 0 ? f.warps : tiles * kTileCols);
+    return f.warps * f.rows() * 4 * (tiles == 0 ? 1 : tiles * kTileCols);
 }
 __host__ __device__ constexpr int tiles_of(int cols) {
     return cols == 1 ? 0 : cols <= kTileCols ? 1 : 2;
@@ -108,7 +108,7 @@ struct Tables {
     uint16_t* slot;          // of a chunk's columns: chunk * cols + column
     // more than 32 slots only
     uint32_t* leads;         // a bit per slot: the first of a chunk
-    Entry* hash;             // by expert
+    Entry* hash;             // by expert; where the warps' sums come later
 };
 
 // A power of two, twice the slots at least.
@@ -120,11 +120,14 @@ __host__ __device__ inline int hash_entries(int slots) {
 
 __host__ __device__ inline int table_bytes(int slots, int cols) {
     const int n = (slots + 3) & ~3;
-    const int hash = static_cast<int>(sizeof(Entry)) * hash_entries(slots);
-    return 16 + n * (3 * 4 + 2 * cols) + (slots > 32 ? kMatvecMaxSlots / 8 + hash : 0);
+    return 16 + n * (3 * 4 + 2 * cols) + (slots > 32 ? kMatvecMaxSlots / 8 : 0);
 }
 
-__device__ inline Tables tables_at(uint8_t* p, int slots, int cols) {
+__host__ __device__ inline int hash_bytes(int slots) {
+    return slots > 32 ? static_cast<int>(sizeof(Entry)) * hash_entries(slots) : 0;
+}
+
+__device__ inline Tables tables_at(uint8_t* p, uint8_t* hash, int slots, int cols) {
     const int n = (slots + 3) & ~3;
     Tables t;
     t.count = reinterpret_cast<int*>(p);
@@ -133,7 +136,7 @@ __device__ inline Tables tables_at(uint8_t* p, int slots, int cols) {
     t.ncols = t.expert + n;
     t.slot = reinterpret_cast<uint16_t*>(t.ncols + n);
     t.leads = reinterpret_cast<uint32_t*>(t.slot + n * cols);
-    t.hash = reinterpret_cast<Entry*>(t.leads + kMatvecMaxSlots / 32);
+    t.hash = reinterpret_cast<Entry*>(hash);
     return t;
 }
 
@@ -154,14 +157,21 @@ struct Layout {
 // 16-byte load phase (two columns, whose rows mostly follow one another) meet
 // no bank twice.
 bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
-    const int pieces = (K + kPartK - 1) / kPartK + 1;    // a box may reach one past the end
-    Layout l;
-    l.x_stride = pieces * kPartK * 2 + 64;
+    int pieces = 0;
+    Layout l{};
     Form f;
-    auto box = [&]() { return f.warps * (f.box_bytes() + f.box_scale_bytes()); };
+    auto box = [&]() { return f.warps * (f.box_bytes() + f.scale_bytes()); };
+    auto sums = [&]() {
+        const int left = partial_bytes(tiles_of(l.cols), f), hash = hash_bytes(slots);
+        return left > hash ? left : hash;
+    };
+    auto bars = [&](int ring) { return (f.warps * ring + f.warps + 1) * 8 + (f.warps + 1) * 4; };
     auto needs = [&](int rows) {
-        return 1024 + partial_bytes(tiles_of(l.cols), f) + rows * (l.x_stride + pieces * 4) + 16 +
-               2 * kPartK + (f.warps * f.ring + 2 * kUnderWay) * 8 + table_bytes(slots, l.cols);
+        const int parts = f.parts * kPartK;              // the rows reach to the end of a box
+        pieces = (K + parts - 1) / parts * f.parts;
+        l.x_stride = pieces * kPartK * 2 + 64;
+        return 1024 + sums() + rows * (l.x_stride + pieces * 4) + 32 + 2 * kPartK + bars(f.ring) +
+               table_bytes(slots, l.cols);
     };
     auto fits = [&]() { return needs(l.cols) + 2 * box() <= kSmemLimit; };
     auto choose = [&](int cols) {            // the most warps with which so many columns fit
@@ -185,7 +195,8 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     while (!choose(cols) && cols > 1) --cols;
     l.warps = f.warps;
     const int useful = cols == 1 ? kSingleRows : 3 * kMaxCols;
-    l.x_rows = (kSmemLimit - 2 * box() - needs(0)) / (l.x_stride + pieces * 4);
+    const int beside_rows = needs(0);
+    l.x_rows = (kSmemLimit - 2 * box() - beside_rows) / (l.x_stride + pieces * 4);
     if (l.x_rows > useful) l.x_rows = useful;
     if (l.x_rows > x_rows) l.x_rows = x_rows;
     if (l.x_rows < cols) l.x_rows = cols;
@@ -194,12 +205,12 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     if (l.ring < 1) return false;
     const int ring = f.warps * l.ring;
     l.scales = ring * f.box_bytes();
-    l.partial = l.scales + ring * f.box_scale_bytes();
-    l.x = l.partial + partial_bytes(tiles_of(cols), f);
+    l.partial = l.scales + ring * f.scale_bytes();
+    l.x = (l.partial + sums() + 15) & ~15;
     l.x_scale = l.x + l.x_rows * l.x_stride;
     l.zeros = (l.x_scale + l.x_rows * pieces * 4 + 15) & ~15;
     l.bars = l.zeros + 2 * kPartK;
-    l.tables = (l.bars + (ring + 2 * kUnderWay) * 8 + 15) & ~15;
+    l.tables = (l.bars + bars(l.ring) + 15) & ~15;
     l.total = l.tables + table_bytes(slots, cols) + 1024 - 16;
     *out = l;
     return true;
@@ -409,25 +420,6 @@ __device__ __forceinline__ void single_part(uint32_t w_at, const uint8_t* x_at, 
     acc[1] = fmaf(v[3], s_hi.y * sx, acc[1]);
 }
 
-// Wait until the shared counter has reached `target`, with the limits of
-// wait_bounded.  (Counts, not a barrier's phase parity: a warp may pass over
-// several rounds that it takes no part in.)
-__device__ __forceinline__ void wait_count(const volatile int* count, int target,
-                                           const WaitCtx& ctx, uint32_t where) {
-    if (*count < target) {
-        const uint64_t t0 = ptx::globaltimer_ns();
-        for (uint32_t it = 1; *count < target; ++it) {
-            if (*ctx.abort) return;
-            if ((it & 7u) == 0u && ptx::globaltimer_ns() - t0 > ctx.timeout_ns) {
-                *ctx.abort = 1u;
-                record_error(ctx.status, HG_ERR_TIMEOUT, (kRoleMatvec << 24) | where);
-                return;
-            }
-        }
-    }
-    __threadfence_block();
-}
-
 // kTiles: MMAs side by side, eight slots each; 0: a single slot.
 template <bool kSwiglu, int kTiles, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32, 1)
@@ -443,41 +435,29 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     constexpr int kParts = kForm.parts;
     constexpr int kBoxK = kParts * kPartK;
     constexpr int kBoxBytes = kForm.box_bytes();
-    constexpr int kBoxScaleBytes = kForm.box_scale_bytes();
-    constexpr int kScaleLanes = kRows * kParts;              // eight scales a lane
-    static_assert(kScaleLanes <= 32, "a warp copies a box's scales at once");
+    constexpr int kScaleBytes = kForm.scale_bytes();         // of two boxes side by side
+    static_assert(kScaleBytes == 32 * 16, "a warp copies two boxes' scales at once");
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
-    const Tables tb = tables_at(smem + a.l.tables, a.slots, a.l.cols);
+    const Tables tb = tables_at(smem + a.l.tables, smem + a.l.partial, a.slots, a.l.cols);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t bars = base + a.l.bars + 8 * warp * a.l.ring;
-    const uint32_t full = base + a.l.bars + 8 * kWarps * a.l.ring;
-    // of each place of the sums: the rounds that have been joined (single
-    // column), or the parts that have been added
-    volatile int* joined = reinterpret_cast<volatile int*>(smem + a.l.bars + 8 * kWarps * a.l.ring +
-                                                           8 * kUnderWay);
-
-    const uint32_t x_bar = full + 8 * kUnderWay + 4 * kUnderWay;   // behind `joined`
+    const uint32_t left_bar = bars + 8 * (kWarps - warp) * a.l.ring;     // one per warp
+    const uint32_t x_bar = left_bar + 8 * kWarps;
+    // the first box of each warp's range in the run
+    int* bound = reinterpret_cast<int*>(smem + a.l.bars + 8 * (kWarps * a.l.ring + kWarps + 1));
     const int nb = (a.K + kBoxK - 1) / kBoxK;
-    const int sharers = min(nb, kWarps);                     // warps that work on one unit
     const int out_cols = kSwiglu ? a.N / 2 : a.N;
     const int tile_cols = kSwiglu ? kRows / 2 : kRows;       // outputs of a unit
     const int tiles = (out_cols + tile_cols - 1) / tile_cols;
-    // Boxes of a run in order, box b of unit u at (u - run) * nb + b: this warp
-    // takes every kWarps-th.
-    const int step_u = kWarps / nb, step_b = kWarps - step_u * nb;
-    const int first_u = warp / nb, first_b = warp - first_u * nb;
 
     if (lane == 0) {
         for (int i = 0; i < a.l.ring; ++i) ptx::mbar_init(bars + 8 * i, 33);
+        ptx::mbar_init(left_bar + 8 * warp, 1);
         if (warp == 0) {
             ptx::prefetch_tensormap(&map_w);
             s_abort = 0;
             ptx::mbar_init(x_bar, 1);
-            for (int i = 0; i < kUnderWay; ++i) {
-                ptx::mbar_init(full + 8 * i, sharers);
-                joined[i] = 0;
-            }
         }
         ptx::fence_barrier_init();
     }
@@ -520,10 +500,12 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     };
     if (hold_all) load_rows(a.x_rows, [](int held) { return held; });
     // zeros behind the rows, up to the end of their last box (cp.async writes them itself)
-    const int tail = kSingle ? 0 : (2 * kPartK * parts - 2 * a.K) / 16;
-    for (int i = threadIdx.x; i < tail * a.l.x_rows; i += kThreads)
-        *reinterpret_cast<uint4*>(smem + a.l.x + i / tail * a.l.x_stride + 2 * a.K +
-                                  16 * (i % tail)) = make_uint4(0, 0, 0, 0);
+    if constexpr (!kSingle) {
+        const int tail = (2 * kPartK * parts - 2 * a.K) / 16;
+        for (int i = threadIdx.x; i < tail * a.l.x_rows; i += kThreads)
+            *reinterpret_cast<uint4*>(smem + a.l.x + i / tail * a.l.x_stride + 2 * a.K +
+                                      16 * (i % tail)) = make_uint4(0, 0, 0, 0);
+    }
     const int chunks = list_slots<kThreads>(a, tb);          // has block barriers
 
     const int units = chunks * tiles;
@@ -572,20 +554,59 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     };
     if (!hold_all && u0 < u1) load_run(chunk0, run_end(chunk0));
 
+    // The run's boxes, in order, box b of unit u at (u - run) * nb + b, are cut
+    // into equal ranges; with two MMAs a row tile by the times above.
+    auto first_box = [&](int w, int run, int end) {
+        if (kTiles != 2 || chunks > 32)
+            return static_cast<int>(static_cast<long long>(end - run) * nb * w / kWarps);
+        int all = 0, at = run;
+        auto each_chunk = [&](auto f) {
+            at = run;
+            for (int c = run / tiles; at < end; ++c) {
+                const int to = min((c + 1) * tiles, end);
+                if (f(to - at, tb.ncols[c] > kTileCols ? 5 : 4)) return;
+                at = to;
+            }
+        };
+        each_chunk([&](int n, int weight) {
+            all += n * weight;
+            return false;
+        });
+        long long want = static_cast<long long>(all) * nb * w / kWarps;
+        int box = 0;
+        each_chunk([&](int n, int weight) {
+            const long long here = static_cast<long long>(n) * nb * weight;
+            if (want <= here) {
+                box += static_cast<int>((want + weight - 1) / weight);
+                return true;
+            }
+            want -= here;
+            box += n * nb;
+            return false;
+        });
+        return box;
+    };
+
     // What this warp has asked for so far.
     const int groups = a.K / 32;
     const uint32_t ring_w = base + warp * a.l.ring * kBoxBytes;
-    const uint32_t ring_s = base + a.l.scales + warp * a.l.ring * kBoxScaleBytes;
-    int p_u = u0 + first_u, p_b = first_b, p_end = u0 < u1 ? run_end(chunk0) : u0;
+    const uint32_t ring_s = base + a.l.scales + warp * a.l.ring * kScaleBytes;
+    int p_u = 0, p_b = 0, p_left = 0, p_end = u0;            // p_left: boxes of the range
+    int p_slot = -1;                         // of the ring of scales
     int p_chunk = chunk0, p_known = -1, p_n0 = 0, p_expert = 0, p_at = 0, issued = 0;
     const uint8_t* p_scale = nullptr;
     auto issue = [&]() {
-        while (p_u >= p_end) {
+        bool first = false;
+        while (p_left == 0) {
             if (p_end >= u1) return;
-            p_u = p_end + first_u;
-            p_b = first_b;
-            while (p_end >= (p_chunk + 1) * tiles) ++p_chunk;
+            const int run = p_end;
+            while (run >= (p_chunk + 1) * tiles) ++p_chunk;
             p_end = run_end(p_chunk);
+            const int lo = first_box(warp, run, p_end);
+            p_left = first_box(warp + 1, run, p_end) - lo;
+            p_u = run + lo / nb;
+            p_b = lo % nb;
+            first = true;
         }
         if (p_u != p_known) {
             p_known = p_u;
@@ -594,7 +615,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             p_expert = tb.expert[p_chunk];
             // the row whose scales this lane copies; rows past the end of the
             // expert's are not used
-            const int r = lane / kParts % kRows;
+            const int r = lane / kParts;
             const int n = kSwiglu ? min(p_n0 + r % (kRows / 2), out_cols - 1) +
                                         r / (kRows / 2) * out_cols
                                   : min(p_n0 + r, out_cols - 1);
@@ -610,23 +631,27 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 ptx::tma_load_3d(dst + h * (kBoxBytes / kParts), &map_w,
                                  (kParts * p_b + h) * (kPartK / 2), p_n0, z, bar);
         }
-        // eight scales a lane: a row's 256 K, or half of a row's 512 K
-        const int g = 8 * (kParts * p_b + lane % kParts);
-        const uint32_t to = ring_s + p_at * kBoxScaleBytes + 8 * lane;
-        if (lane >= kScaleLanes) {
-        } else if (groups & 7) {             // rows of scales start at multiples of 4 bytes
-            ptx::cp_async_4(to, p_scale + (g < groups ? g : 0), g < groups);
-            ptx::cp_async_4(to + 4, p_scale + (g + 4 < groups ? g + 4 : 0), g + 4 < groups);
-        } else {
-            ptx::cp_async_8(to, p_scale + (g < groups ? g : 0), g < groups);
+        // The scales come for two boxes at once, sixteen a lane: a row's 512 K,
+        // or half of a row's 1024 K.  (Eight at a time, through an L1 that has
+        // little room beside the ring, 4 tokens take 53 us in place of 43.)
+        if (first || p_b % 2 == 0) {
+            if (++p_slot == a.l.ring) p_slot = 0;
+            const int g = 16 * (p_b / 2 * kParts + lane % kParts);
+            const uint32_t to = ring_s + p_slot * kScaleBytes + 16 * lane;
+            if ((groups & 15) == 0) {
+                ptx::cp_async_16(to, p_scale + (g < groups ? g : 0), g < groups);
+            } else {                         // rows of scales start at multiples of 4 bytes
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    ptx::cp_async_4(to + i, p_scale + (g + i < groups ? g + i : 0), g + i < groups);
+            }
         }
         ptx::cp_async_mbar_arrive(bar);
         ++issued;
         if (++p_at == a.l.ring) p_at = 0;
-        p_u += step_u;
-        p_b += step_b;
-        if (p_b >= nb) {
-            p_b -= nb;
+        --p_left;
+        if (++p_b == nb) {
+            p_b = 0;
             ++p_u;
         }
     };
@@ -641,7 +666,6 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 
     const WaitCtx ctx{a.status, &s_abort, a.timeout_ns};
     float* x_scale = reinterpret_cast<float*>(smem + a.l.x_scale);
-    float* partial = reinterpret_cast<float*>(smem + a.l.partial);
     const int q = lane & 3, g8 = lane >> 2;
     // ldmatrix: lane l addresses row l % 8 of matrix l / 8: the MMA's rows 0-7
     // and 8-15 of one group, then of the next; 16-byte chunks are XOR-swizzled
@@ -650,16 +674,16 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     constexpr int kHiBlock = kSwiglu ? kR : 1, kTileBlock = kSwiglu ? 1 : 2;
     const uint32_t lm_row =
         ring_w + ((lane >> 3) & 1) * (kHiBlock * kBlockBytes) + (lane & 7) * 128;
-    constexpr int kScaleRow = 8 * kParts;
-    const uint8_t* my_scales = smem + a.l.scales + warp * a.l.ring * kBoxScaleBytes +
+    constexpr int kScaleRow = 16 * kParts;
+    const uint8_t* my_scales = smem + a.l.scales + warp * a.l.ring * kScaleBytes +
                                g8 * kScaleRow;
-    int at = 0;
-    uint32_t phase = 0, x_phase = 0;
+    int at = 0, slot = -1;
+    uint32_t phase = 0, x_phase = 0, left_phase = 0;
     if (!kSingle && hold_all && u0 >= u1) {  // no work here, but rows are on their way
         wait_bounded(x_bar, x_phase, ctx, kRoleMatvec, 0x300);
         x_phase ^= 1;
     }
-    for (int run = u0, chunk = chunk0, before = 0; run < u1;) {   // before: units of earlier runs
+    for (int run = u0, chunk = chunk0; run < u1;) {
         while (run >= (chunk + 1) * tiles) ++chunk;
         const int end = run_end(chunk);
         if (run > u0) {
@@ -675,6 +699,9 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         }
         each_piece(hold_all ? a.x_rows : run_rows(chunk, end),
                    [&](int held, int part) { scale_piece(a, smem, held, part, parts, lane); });
+        const int lo = first_box(warp, run, end), hi = first_box(warp + 1, run, end);
+        if (lane == 0) bound[warp] = lo;
+        if (threadIdx.x == 0) bound[kWarps] = (end - run) * nb;
         __syncthreads();
         // Where this lane's columns of the current chunk lie; lanes of columns
         // that the chunk does not have read zeros.
@@ -768,14 +795,17 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 }
             }
         };
-        for (int u = run + first_u, b = first_b; u < end;) {
+        bool left = false;                   // whether this warp has left its sums
+        int begun = lo % nb;                 // where its part of unit u begins
+        for (int i = lo, u = run + lo / nb, b = begun; i < hi; ++i) {
             while (u >= (x_chunk + 1) * tiles) next_chunk();
             const bool ok = __all_sync(0xFFFFFFFFu,
                                        wait_bounded(bars + 8 * at, phase, ctx, kRoleMatvec, at));
+            if ((i == lo || b % 2 == 0) && ++slot == a.l.ring) slot = 0;
             if (ok) {
-                const uint8_t* codes = my_scales + at * kBoxScaleBytes;
+                const uint8_t* codes = my_scales + slot * kScaleBytes + b % 2 * (8 * kParts);
                 if (kSingle) {
-#pragma unroll
+#pragma unroll 1                             // fewer instructions to fetch: 20.7 us, else 22.6
                     for (int h = 0; h < kParts; ++h) {
                         const uint8_t* c = codes + 8 * h + 2 * q;
                         single_part(lm_row + at * kBoxBytes + h * (kBoxBytes / kParts),
@@ -796,47 +826,50 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 at = 0;
                 phase ^= 1;
             }
-            const int done = u, boxes_left = nb - 1 - b;     // of unit u
-            const bool last_box = boxes_left == 0;
-            u += step_u;
-            b += step_b;
-            if (b >= nb) {
-                b -= nb;
+            const int done = u;
+            const bool whole = ++b == nb;
+            if (!whole && i + 1 < hi) continue;
+            const bool own = begun == 0;     // this warp has the unit's first box
+            begun = 0;
+            if (whole) {
+                b = 0;
                 ++u;
             }
-            if (u == done) continue;
 
-            // This warp's part of unit `done` is complete: leave it, and if the
-            // unit's last box was here, join the parts and write the outputs.
-            const int n_unit = before + done - run;
-            const int place = n_unit % kUnderWay;
-            const int round = n_unit / kUnderWay;
+            // This warp's part of unit `done` is complete.
+            uint8_t* sums = smem + a.l.partial;
+            // the parts of the warps behind
+            auto each_other = [&](auto f) {
+                if (whole) return;
+                const int unit_end = (done - run + 1) * nb;
+                for (int w = warp + 1; bound[w] < unit_end; ++w) {
+                    if (bound[w + 1] == bound[w]) continue;
+                    wait_bounded(left_bar + 8 * w, left_phase, ctx, kRoleMatvec, 0x200 + w);
+                    f(w);
+                }
+            };
+            auto leave = [&]() {
+                left = true;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(left_bar + 8 * warp);
+            };
             if (kSingle) {
-                // the unit's sharers in the order of their boxes: from w0 on, cyclically
-                const int w0 = warp + 1 - sharers + (warp + 1 < sharers ? kWarps : 0);
-                auto sharer = [&](int j) { return w0 + j - (w0 + j >= kWarps ? kWarps : 0); };
-                wait_count(joined + place, round, ctx, 0x100 + place);
-                float* part = partial + place * kWarps * kRows;
 #pragma unroll
                 for (int o = 1; o <= 2; o <<= 1) {
                     one[0] += __shfl_xor_sync(0xFFFFFFFFu, one[0], o);
                     one[1] += __shfl_xor_sync(0xFFFFFFFFu, one[1], o);
                 }
-                if (q < 2) part[warp * kRows + 8 * q + g8] = q ? one[1] : one[0];
+                const float lo8 = __shfl_sync(0xFFFFFFFFu, one[0], 4 * (lane & 7));
+                const float hi8 = __shfl_sync(0xFFFFFFFFu, one[1], 4 * (lane & 7));
+                float y = lane & 8 ? hi8 : lo8;              // of weight row lane % 16
                 one[0] = one[1] = 0.0f;
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(full + 8 * place);
-                if (!last_box) continue;
-                wait_bounded(full + 8 * place, round & 1, ctx, kRoleMatvec, 0x200 + place);
-                float y = 0.0f;
-#pragma unroll 4
-                for (int j = 0; j < sharers; ++j)
-                    y += part[sharer(j) * kRows + (lane & 15)];
-                __syncwarp();
-                if (lane == 0) {
-                    __threadfence_block();
-                    joined[place] = round + 1;
+                float* sum = reinterpret_cast<float*>(sums) + (lane & 15);
+                if (!own) {
+                    if (lane < 16) sum[warp * kRows] = y;
+                    leave();
+                    continue;
                 }
+                each_other([&](int w) { y += sum[w * kRows]; });
                 const int n = (done - x_chunk * tiles) * tile_cols + lane;
                 if (kSwiglu) {
                     const float up = __shfl_down_sync(0xFFFFFFFFu, y, 8);
@@ -846,60 +879,57 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                     a.out[static_cast<long long>(tb.slot[x_chunk]) * out_cols + n] =
                         __bfloat16_as_ushort(__float2bfloat16_rn(y));
             } else {
-                // The parts are added to one sum in the order of the boxes,
-                // which is that of their arrival, more or less: each warp
-                // waits for its turn.  (A copy per warp would take the room
-                // of two to four warps' rings.)
                 constexpr int kA = kR * kT;
-                ulonglong2* sum = reinterpret_cast<ulonglong2*>(partial) + place * kA * 32 + lane;
-                const int turn = sharers - 1 - boxes_left;
-                wait_count(joined + place, round * sharers + turn, ctx, 0x100 + place);
-                float4 total[kA];
+                ulonglong2* sum = reinterpret_cast<ulonglong2*>(sums) + lane;
+                if (!own) {
 #pragma unroll
-                for (int i = 0; i < kA; ++i) {
-                    uint64_t(&mine)[2] = acc[i / kT][i % kT];
-                    if (turn > 0) {
-                        const ulonglong2 v = sum[i * 32];
-                        mine[0] = ptx::add_f32x2(v.x, mine[0]);
-                        mine[1] = ptx::add_f32x2(v.y, mine[1]);
+                    for (int j = 0; j < kA; ++j) {
+                        uint64_t(&mine)[2] = acc[j / kT][j % kT];
+                        sum[(warp * kA + j) * 32] = make_ulonglong2(mine[0], mine[1]);
+                        mine[0] = mine[1] = 0;
                     }
-                    if (!last_box) sum[i * 32] = make_ulonglong2(mine[0], mine[1]);
-                    const float2 lo = ptx::f32x2_parts(mine[0]), hi = ptx::f32x2_parts(mine[1]);
-                    total[i] = make_float4(lo.x, lo.y, hi.x, hi.y);
-                    mine[0] = mine[1] = 0;
+                    leave();
+                    continue;
                 }
-                __syncwarp();
-                if (lane == 0) {
-                    __threadfence_block();
-                    joined[place] = round * sharers + turn + 1;
+                each_other([&](int w) {
+#pragma unroll
+                    for (int j = 0; j < kA; ++j) {
+                        uint64_t(&mine)[2] = acc[j / kT][j % kT];
+                        const ulonglong2 v = sum[(w * kA + j) * 32];
+                        mine[0] = ptx::add_f32x2(mine[0], v.x);
+                        mine[1] = ptx::add_f32x2(mine[1], v.y);
+                    }
+                });
+                uint16_t* to[2 * kT];        // the lane's columns' outputs
+#pragma unroll
+                for (int c = 0; c < 2 * kT; ++c) {
+                    const int col = min(8 * (c / 2) + 2 * q + c % 2, ncols - 1);
+                    to[c] = a.out + static_cast<long long>(tb.slot[x_chunk * a.l.cols + col]) *
+                                        out_cols;
                 }
-                if (!last_box) continue;
 #pragma unroll
                 for (int j = 0; j < kA; ++j) {
-                    const float y[4] = {total[j].x, total[j].y, total[j].z, total[j].w};
-                    const int n0 = (done - x_chunk * tiles) * tile_cols +
-                                   j / kT * (kSwiglu ? 8 : 16) + g8;
+                    uint64_t(&mine)[2] = acc[j / kT][j % kT];
+                    const float2 lo8 = ptx::f32x2_parts(mine[0]), hi8 = ptx::f32x2_parts(mine[1]);
+                    const float y[4] = {lo8.x, lo8.y, hi8.x, hi8.y};
+                    mine[0] = mine[1] = 0;
+                    const int n = (done - x_chunk * tiles) * tile_cols +
+                                  j / kT * (kSwiglu ? 8 : 16) + g8;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = 8 * (j % kT) + 2 * q + i;
-                        if (c >= ncols) continue;
-                        uint16_t* o = a.out + static_cast<long long>(
-                                                  tb.slot[x_chunk * a.l.cols + c]) * out_cols + n0;
-                        if (kSwiglu) {
-                            if (n0 < out_cols)
-                                o[0] = __bfloat16_as_ushort(
-                                    __float2bfloat16_rn(y[i] / (1.0f + expf(-y[i])) * y[2 + i]));
-                        } else {
-                            if (n0 < out_cols)
-                                o[0] = __bfloat16_as_ushort(__float2bfloat16_rn(y[i]));
-                            if (n0 + 8 < out_cols)
-                                o[8] = __bfloat16_as_ushort(__float2bfloat16_rn(y[2 + i]));
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        if (8 * (j % kT) + 2 * q + c >= ncols) continue;
+                        uint16_t* o = to[2 * (j % kT) + c] + n;
+                        const float v = kSwiglu ? y[c] / (1.0f + expf(-y[c])) * y[2 + c] : y[c];
+                        if (n < out_cols) o[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                        if (!kSwiglu && n + 8 < out_cols)
+                            o[8] = __bfloat16_as_ushort(__float2bfloat16_rn(y[2 + c]));
                     }
                 }
             }
         }
-        before += end - run;
+        // once a run, whether or not there was anything to leave
+        if (!left && lane == 0) ptx::mbar_arrive(left_bar + 8 * warp);
+        left_phase ^= 1;
         run = end;
     }
     // After a wait that gave up, copies may still be in flight: wait for them,
