@@ -36,12 +36,13 @@
 // own rounding.  The sums of a 32-K group come out of the MMA in FP32 and are
 // added up in FP32 times the product of the two scales.
 //
-// Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 20.8
+// Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 20.5
 // us for 107 MB, of which 3.5 pass before the first weights arrive; from there
-// on the weights stream at the measured copy rate.  Down, 6144 x 2048: 13.3 us
-// for 54 MB.  4 tokens, gate/up: 43.1 us for 293 MB; 8 tokens, down: 29.0 us
-// for 194 MB.  13 tokens on 12 experts, 6144 x 3584: 42.7 us for 142 MB, bound by
-// the instructions issued: conversion, MMA and scaling.
+// on the weights stream at the measured copy rate.  Down, 6144 x 2048: 13.2 us
+// for 54 MB.  4 tokens, gate/up: 42.2 us for 293 MB; 8 tokens, down: 29.1 us
+// for 194 MB.  13 tokens on 12 experts, 6144 x 3584: 39.4 us for 142 MB, of which
+// about 7 pass before the first product; then it is bound by the instructions
+// issued: conversion, MMA and scaling.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -82,9 +83,9 @@ struct Form {
 __host__ __device__ constexpr Form form_of(int tiles, int warps) {
     return tiles == 0 ? Form{warps, 1, 2, 2} : Form{warps, 2, 1, 2};
 }
-// The sums that each warp leaves: a float per weight row and column.
+// The sums that each warp but the first may leave: a float per weight row and column.
 __host__ __device__ constexpr int partial_bytes(int tiles, const Form& f) {
-    return f.warps * f.rows() * 4 * (tiles == 0 ? 1 : tiles * kTileCols);
+    return (f.warps - 1) * f.rows() * 4 * (tiles == 0 ? 1 : tiles * kTileCols);
 }
 __host__ __device__ constexpr int tiles_of(int cols) {
     return cols == 1 ? 0 : cols <= kTileCols ? 1 : 2;
@@ -98,8 +99,8 @@ struct __align__(8) Entry {
     uint8_t slots[kMatvecMaxSlots / 32];     // how many it has in each 32 slots
 };
 
-// The slots by expert: an entry per slot or chunk (there are at most as many
-// chunks as slots), and a hash table of the experts.
+// The slots by expert: entries per slot and per chunk, and a hash table of the
+// experts.
 struct Tables {
     int* count;              // [0] chunks, [1] slots without an expert
     int* id;                 // of a slot; -1 without an expert
@@ -118,24 +119,30 @@ __host__ __device__ inline int hash_entries(int slots) {
     return n;
 }
 
-__host__ __device__ inline int table_bytes(int slots, int cols) {
-    const int n = (slots + 3) & ~3;
-    return 16 + n * (3 * 4 + 2 * cols) + (slots > 32 ? kMatvecMaxSlots / 8 : 0);
+// Chunks at most: each expert in use has one that is not full.
+__host__ __device__ inline int max_chunks(int slots, int cols, int E) {
+    const int n = slots / cols + (E < slots ? E : slots);
+    return n < slots ? n : slots;
+}
+
+__host__ __device__ inline int table_bytes(int slots, int cols, int E) {
+    const int n = (slots + 3) & ~3, c = (max_chunks(slots, cols, E) + 3) & ~3;
+    return 16 + 4 * n + c * (2 * 4 + 2 * cols) + (slots > 32 ? kMatvecMaxSlots / 8 : 0);
 }
 
 __host__ __device__ inline int hash_bytes(int slots) {
     return slots > 32 ? static_cast<int>(sizeof(Entry)) * hash_entries(slots) : 0;
 }
 
-__device__ inline Tables tables_at(uint8_t* p, uint8_t* hash, int slots, int cols) {
-    const int n = (slots + 3) & ~3;
+__device__ inline Tables tables_at(uint8_t* p, uint8_t* hash, int slots, int cols, int E) {
+    const int n = (slots + 3) & ~3, c = (max_chunks(slots, cols, E) + 3) & ~3;
     Tables t;
     t.count = reinterpret_cast<int*>(p);
     t.id = t.count + 4;
     t.expert = t.id + n;
-    t.ncols = t.expert + n;
-    t.slot = reinterpret_cast<uint16_t*>(t.ncols + n);
-    t.leads = reinterpret_cast<uint32_t*>(t.slot + n * cols);
+    t.ncols = t.expert + c;
+    t.slot = reinterpret_cast<uint16_t*>(t.ncols + c);
+    t.leads = reinterpret_cast<uint32_t*>(t.slot + c * cols);
     t.hash = reinterpret_cast<Entry*>(hash);
     return t;
 }
@@ -146,7 +153,7 @@ struct Layout {
     int cols;          // most slots of a chunk
     int x_rows;        // input rows held at once
     int x_stride;      // bytes between them
-    int scales, partial, x, x_scale, zeros, bars, tables, total;   // byte offsets
+    int scales, partial, x, x_scale, bars, tables, total;   // byte offsets
 };
 
 // Columns: up to eight (one MMA) where an expert has few slots on average, up
@@ -170,8 +177,8 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
         const int parts = f.parts * kPartK;              // the rows reach to the end of a box
         pieces = (K + parts - 1) / parts * f.parts;
         l.x_stride = pieces * kPartK * 2 + 64;
-        return 1024 + sums() + rows * (l.x_stride + pieces * 4) + 32 + 2 * kPartK + bars(f.ring) +
-               table_bytes(slots, l.cols);
+        return 1024 + sums() + rows * (l.x_stride + pieces * 4) + 32 + bars(f.ring) +
+               table_bytes(slots, l.cols, E);
     };
     auto fits = [&]() { return needs(l.cols) + 2 * box() <= kSmemLimit; };
     auto choose = [&](int cols) {            // the most warps with which so many columns fit
@@ -208,13 +215,23 @@ bool make_layout(int K, int slots, int tokens, int E, int x_rows, Layout* out) {
     l.partial = l.scales + ring * f.scale_bytes();
     l.x = (l.partial + sums() + 15) & ~15;
     l.x_scale = l.x + l.x_rows * l.x_stride;
-    l.zeros = (l.x_scale + l.x_rows * pieces * 4 + 15) & ~15;
-    l.bars = l.zeros + 2 * kPartK;
+    l.bars = (l.x_scale + l.x_rows * pieces * 4 + 15) & ~15;
     l.tables = (l.bars + bars(l.ring) + 15) & ~15;
-    l.total = l.tables + table_bytes(slots, cols) + 1024 - 16;
+    l.total = l.tables + table_bytes(slots, cols, E) + 1024 - 16;
     *out = l;
     return true;
 }
+
+// Division by a number that the host knows, of n in [0, 2^31).
+struct Divisor {
+    uint32_t d, m;                           // m = 2^32 / d, at most 2^32 - 1
+    explicit Divisor(int by = 1)
+        : d(by), m(by == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((1ull << 32) / by)) {}
+    __device__ __forceinline__ int of(int n) const {
+        const uint32_t q = __umulhi(static_cast<uint32_t>(n), m);       // or one less
+        return static_cast<int>(q + (static_cast<uint32_t>(n) - q * d >= d));
+    }
+};
 
 struct KernelArgs {
     const uint16_t* x;
@@ -224,6 +241,7 @@ struct KernelArgs {
     uint32_t* status;
     uint64_t timeout_ns;
     int x_rows, slots_per_row, slots, E, N, K;
+    Divisor boxes, tiles, blocks;            // boxes of a unit, units of a chunk, blocks
     Layout l;
 };
 
@@ -279,7 +297,7 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
         for (int w = 0; w < kMatvecMaxSlots / 32; w += 4)
             *reinterpret_cast<uint32_t*>(t.slots + w) = 0;
     }
-    for (int i = tid; i < a.slots; i += kThreads) tb.ncols[i] = 0;
+    for (int i = tid; i < max_chunks(a.slots, cols, a.E); i += kThreads) tb.ncols[i] = 0;
     if (tid == 0) tb.count[1] = 0;
     __syncthreads();
     // each expert's slots of each 32, by the first lane that has it
@@ -342,41 +360,59 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
 // Input rows come to shared memory as they are and are rewritten in place as
 // scaled FP16, 256 elements of a row at a time, eight a lane: piece p is part
 // p % parts of held row p / parts, and belongs to warp p % warps.  The one to four
-// rows of single columns come by cp.async of the lanes that rewrite them (a
-// dense 500 x 640 takes 3.8 us so, 4.3 with bulk copies), the many rows of the
-// other forms by a bulk copy each (13 tokens on 12 experts: 50.7 against 52.1 us).
-__device__ __forceinline__ void scale_piece(const KernelArgs& a, uint8_t* smem, int held, int part,
-                                            int parts, int lane) {
-    uint4* at = reinterpret_cast<uint4*>(smem + a.l.x + held * a.l.x_stride + part * (2 * kPartK) +
-                                         16 * lane);
-    const uint4 v = *at;
-    constexpr uint32_t kAbs = 0x7FFF7FFFu;   // BF16 magnitudes compare as integers, NaN the largest
-    const uint32_t two = __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs),
-                                  __vmaxu2(v.z & kAbs, v.w & kAbs));
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(two & 0xFFFFu, two >> 16));
-    float f[8];
-    bf16_unpack8(v, f);
-    int be = static_cast<int>(top >> 7);
-    float mult, back;
-    if (be == 255) {
-        // an Inf or NaN decides the sum: the finite elements may be dropped
+// rows of single columns come by cp.async of the lanes that rewrite them (0.5 us
+// less than with bulk copies for a dense 500 x 640), the many rows of the other
+// forms by a bulk copy each (1.4 us less for 13 tokens on 12 experts).  Those are
+// rewritten four pieces a warp at once, which hides the latency of the maximum
+// over the lanes: one at a time takes 13 tokens' 182 pieces 2.5 us longer.
+template <int kPieces>
+__device__ __forceinline__ void scale_pieces(const KernelArgs& a, uint8_t* smem, int first,
+                                             int step, int parts, float per_row, int lane) {
+    uint4* at[kPieces];
+    uint4 v[kPieces];
+    uint32_t top[kPieces];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = isfinite(f[e]) ? 0.0f : f[e];
-        mult = back = 1.0f;
-    } else {
-        be = max(be, 15);                    // both factors stay normal numbers
-        mult = __uint_as_float(static_cast<uint32_t>(268 - be) << 23);   // 2^(14 - (be - 127))
-        back = __uint_as_float(static_cast<uint32_t>(be - 14) << 23);
+    for (int i = 0; i < kPieces; ++i) {
+        const int p = first + i * step;
+        const int held = static_cast<int>((p + 0.5f) * per_row);
+        at[i] = reinterpret_cast<uint4*>(smem + a.l.x + held * a.l.x_stride +
+                                         (p - held * parts) * (2 * kPartK) + 16 * lane);
+        v[i] = *at[i];
     }
-    uint32_t h[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const __half2 p = __floats2half2_rn(f[2 * e] * mult, f[2 * e + 1] * mult);
-        h[e] = *reinterpret_cast<const uint32_t*>(&p);
+    for (int i = 0; i < kPieces; ++i) {
+        // BF16 magnitudes compare as integers, NaN the largest
+        constexpr uint32_t kAbs = 0x7FFF7FFFu;
+        const uint32_t two = __vmaxu2(__vmaxu2(v[i].x & kAbs, v[i].y & kAbs),
+                                      __vmaxu2(v[i].z & kAbs, v[i].w & kAbs));
+        top[i] = __reduce_max_sync(0xFFFFFFFFu, max(two & 0xFFFFu, two >> 16));
     }
-    *at = make_uint4(h[0], h[1], h[2], h[3]);
-    if (lane == 0)
-        reinterpret_cast<float*>(smem + a.l.x_scale)[held * parts + part] = back;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        float f[8];
+        bf16_unpack8(v[i], f);
+        int be = static_cast<int>(top[i] >> 7);
+        float mult, back;
+        if (be == 255) {
+            // an Inf or NaN decides the sum: the finite elements may be dropped
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = isfinite(f[e]) ? 0.0f : f[e];
+            mult = back = 1.0f;
+        } else {
+            be = max(be, 15);                // both factors stay normal numbers
+            // 2^(14 - (be - 127)) and its inverse
+            mult = __uint_as_float(static_cast<uint32_t>(268 - be) << 23);
+            back = __uint_as_float(static_cast<uint32_t>(be - 14) << 23);
+        }
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __half2 p = __floats2half2_rn(f[2 * e] * mult, f[2 * e + 1] * mult);
+            h[e] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        *at[i] = make_uint4(h[0], h[1], h[2], h[3]);
+        if (lane == 0) reinterpret_cast<float*>(smem + a.l.x_scale)[first + i * step] = back;
+    }
 }
 
 // 256 K of 16 weight rows times one column.  Were the column alone in the
@@ -433,23 +469,23 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     constexpr int kR = kForm.row_tiles;
     constexpr int kRows = 16 * kR;
     constexpr int kParts = kForm.parts;
-    constexpr int kBoxK = kParts * kPartK;
     constexpr int kBoxBytes = kForm.box_bytes();
     constexpr int kScaleBytes = kForm.scale_bytes();         // of two boxes side by side
     static_assert(kScaleBytes == 32 * 16, "a warp copies two boxes' scales at once");
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
-    const Tables tb = tables_at(smem + a.l.tables, smem + a.l.partial, a.slots, a.l.cols);
+    const Tables tb = tables_at(smem + a.l.tables, smem + a.l.partial, a.slots, a.l.cols,
+                                a.E);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t bars = base + a.l.bars + 8 * warp * a.l.ring;
     const uint32_t left_bar = bars + 8 * (kWarps - warp) * a.l.ring;     // one per warp
     const uint32_t x_bar = left_bar + 8 * kWarps;
     // the first box of each warp's range in the run
     int* bound = reinterpret_cast<int*>(smem + a.l.bars + 8 * (kWarps * a.l.ring + kWarps + 1));
-    const int nb = (a.K + kBoxK - 1) / kBoxK;
+    const int nb = a.boxes.d;
     const int out_cols = kSwiglu ? a.N / 2 : a.N;
     const int tile_cols = kSwiglu ? kRows / 2 : kRows;       // outputs of a unit
-    const int tiles = (out_cols + tile_cols - 1) / tile_cols;
+    const int tiles = a.tiles.d;
 
     if (lane == 0) {
         for (int i = 0; i < a.l.ring; ++i) ptx::mbar_init(bars + 8 * i, 33);
@@ -461,8 +497,6 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         }
         ptx::fence_barrier_init();
     }
-    if (threadIdx.x < kPartK / 2)
-        reinterpret_cast<uint32_t*>(smem + a.l.zeros)[threadIdx.x] = 0;
     start_dependent();                       // nothing global is read or written before
 
     // x goes ahead of the weights, behind which it would wait for the whole
@@ -509,7 +543,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     const int chunks = list_slots<kThreads>(a, tb);          // has block barriers
 
     const int units = chunks * tiles;
-    const int each = units / static_cast<int>(gridDim.x);
+    const int each = a.blocks.of(units);
     const int left = units - each * static_cast<int>(gridDim.x);
     int u0 = static_cast<int>(blockIdx.x) * each + min(static_cast<int>(blockIdx.x), left);
     int u1 = u0 + each + (static_cast<int>(blockIdx.x) < left);
@@ -531,7 +565,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         u0 = chunks ? unit_at(all * blockIdx.x / gridDim.x) : 0;
         u1 = chunks ? unit_at(all * (blockIdx.x + 1) / gridDim.x) : 0;
     }
-    const int chunk0 = u0 / tiles;
+    const int chunk0 = a.tiles.of(u0);
 
     // A run: the units of as many chunks, from chunk c on, as rows can be held.
     auto run_end = [&](int c) {
@@ -555,35 +589,26 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     if (!hold_all && u0 < u1) load_run(chunk0, run_end(chunk0));
 
     // The run's boxes, in order, box b of unit u at (u - run) * nb + b, are cut
-    // into equal ranges; with two MMAs a row tile by the times above.
-    auto first_box = [&](int w, int run, int end) {
+    // into equal ranges, with two MMAs a row tile by the times above.  The first
+    // box of the range of warp `lane`:
+    auto first_box = [&](int run, int end) {
+        const int w = min(lane, kWarps);
         if (kTiles != 2 || chunks > 32)
             return static_cast<int>(static_cast<long long>(end - run) * nb * w / kWarps);
-        int all = 0, at = run;
-        auto each_chunk = [&](auto f) {
-            at = run;
-            for (int c = run / tiles; at < end; ++c) {
-                const int to = min((c + 1) * tiles, end);
-                if (f(to - at, tb.ncols[c] > kTileCols ? 5 : 4)) return;
-                at = to;
-            }
-        };
-        each_chunk([&](int n, int weight) {
-            all += n * weight;
-            return false;
-        });
-        long long want = static_cast<long long>(all) * nb * w / kWarps;
+        auto weight_of = [&](int c) { return tb.ncols[c] > kTileCols ? 5 : 4; };
+        auto units_of = [&](int c) { return min((c + 1) * tiles, end) - max(c * tiles, run); };
+        const int c0 = a.tiles.of(run);
+        long long all = 0;
+        for (int c = c0; c * tiles < end; ++c) all += units_of(c) * weight_of(c);
+        long long want = all * nb * w / kWarps;
         int box = 0;
-        each_chunk([&](int n, int weight) {
-            const long long here = static_cast<long long>(n) * nb * weight;
-            if (want <= here) {
-                box += static_cast<int>((want + weight - 1) / weight);
-                return true;
-            }
-            want -= here;
-            box += n * nb;
-            return false;
-        });
+        for (int c = c0; c * tiles < end; ++c) {
+            const int weight = weight_of(c);
+            const long long here = static_cast<long long>(units_of(c)) * nb * weight;
+            const long long take = want < here ? want : here;
+            box += static_cast<int>((take + weight - 1) / weight);
+            want -= take;
+        }
         return box;
     };
 
@@ -602,10 +627,13 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             const int run = p_end;
             while (run >= (p_chunk + 1) * tiles) ++p_chunk;
             p_end = run_end(p_chunk);
-            const int lo = first_box(warp, run, p_end);
-            p_left = first_box(warp + 1, run, p_end) - lo;
-            p_u = run + lo / nb;
-            p_b = lo % nb;
+            const int mine = first_box(run, p_end);
+            const int lo = __shfl_sync(0xFFFFFFFFu, mine, warp);
+            p_left = __shfl_sync(0xFFFFFFFFu, mine, warp + 1) - lo;
+            if (p_left == 0) continue;
+            const int units_before = a.boxes.of(lo);
+            p_u = run + units_before;
+            p_b = lo - units_before * nb;
             first = true;
         }
         if (p_u != p_known) {
@@ -665,7 +693,6 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     }
 
     const WaitCtx ctx{a.status, &s_abort, a.timeout_ns};
-    float* x_scale = reinterpret_cast<float*>(smem + a.l.x_scale);
     const int q = lane & 3, g8 = lane >> 2;
     // ldmatrix: lane l addresses row l % 8 of matrix l / 8: the MMA's rows 0-7
     // and 8-15 of one group, then of the next; 16-byte chunks are XOR-swizzled
@@ -697,41 +724,40 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             wait_bounded(x_bar, x_phase, ctx, kRoleMatvec, 0x300);
             x_phase ^= 1;
         }
-        each_piece(hold_all ? a.x_rows : run_rows(chunk, end),
-                   [&](int held, int part) { scale_piece(a, smem, held, part, parts, lane); });
-        const int lo = first_box(warp, run, end), hi = first_box(warp + 1, run, end);
-        if (lane == 0) bound[warp] = lo;
-        if (threadIdx.x == 0) bound[kWarps] = (end - run) * nb;
+        const int pieces = (hold_all ? a.x_rows : run_rows(chunk, end)) * parts;
+        int piece = warp;
+        if constexpr (!kSingle) {
+            for (; piece + 3 * kWarps < pieces; piece += 4 * kWarps)
+                scale_pieces<4>(a, smem, piece, kWarps, parts, 1.0f / parts, lane);
+        }
+        for (; piece < pieces; piece += kWarps)
+            scale_pieces<1>(a, smem, piece, kWarps, parts, 1.0f / parts, lane);
+        const int mine = first_box(run, end);
+        if (warp == 0 && lane <= kWarps) bound[lane] = mine;
         __syncthreads();
+        const int lo = bound[warp], hi = bound[warp + 1];
         // Where this lane's columns of the current chunk lie; lanes of columns
-        // that the chunk does not have read zeros.
+        // that the chunk does not have read its last one, for sums nobody writes.
         int ncols = 0, rows_before = 0, x_chunk = chunk - 1;
-        const uint8_t* x_at[kT];
-        int x_step[kT];
-        const float* s_at[kT][2];
-        int s_step[kT][2];
+        int x_at[kT], s_at[kT][2];           // offsets in shared memory
         auto next_chunk = [&]() {
             rows_before += ncols;
             ncols = tb.ncols[++x_chunk];
             auto held_row = [&](int c) {
+                c = kSingle ? 0 : min(c, ncols - 1);
                 return hold_all ? tb.slot[x_chunk * a.l.cols + c] / a.slots_per_row
                                 : rows_before + c;
             };
-            const uint8_t* zeros = smem + a.l.zeros;
-            const float* no_scale = reinterpret_cast<const float*>(smem + a.l.zeros);
 #pragma unroll
             for (int t = 0; t < kT; ++t) {
-                const int c = kSingle ? 0 : 8 * t + g8;
-                x_step[t] = c < ncols ? 2 * kPartK : 0;
-                x_at[t] = (c < ncols ? smem + a.l.x + held_row(c) * a.l.x_stride : zeros) +
-                          16 * (kSingle ? lane : q);
+                x_at[t] = a.l.x + held_row(8 * t + g8) * a.l.x_stride + 16 * (kSingle ? lane : q);
 #pragma unroll
-                for (int i = 0; i < (kSingle ? 1 : 2); ++i) {
-                    const int d = kSingle ? 0 : 8 * t + 2 * q + i;
-                    s_step[t][i] = d < ncols;
-                    s_at[t][i] = d < ncols ? x_scale + held_row(d) * parts : no_scale;
-                }
+                for (int i = 0; i < (kSingle ? 1 : 2); ++i)
+                    s_at[t][i] = a.l.x_scale + 4 * held_row(8 * t + 2 * q + i) * parts;
             }
+        };
+        auto x_scale = [&](int t, int i, int part) {
+            return *reinterpret_cast<const float*>(smem + s_at[t][i] + 4 * part);
         };
         uint64_t acc[kR][kT][2];             // rows g8 and g8 + 8, each of columns 2q and 2q + 1
 #pragma unroll
@@ -744,7 +770,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             uint64_t sx[kHere];
 #pragma unroll
             for (int t = 0; t < kHere; ++t)
-                sx[t] = ptx::f32x2(s_at[t][0][b * s_step[t][0]], s_at[t][1][b * s_step[t][1]]);
+                sx[t] = ptx::f32x2(x_scale(t, 0, b), x_scale(t, 1, b));
             uint2 code[kR][2];
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
@@ -760,7 +786,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
                     for (int t = 0; t < kHere; ++t)
-                        xf[i][t] = *reinterpret_cast<const uint4*>(x_at[t] + b * x_step[t] +
+                        xf[i][t] = *reinterpret_cast<const uint4*>(smem + x_at[t] + b * (2 * kPartK) +
                                                                    64 * (g + i));
                 }
 #pragma unroll
@@ -796,8 +822,9 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             }
         };
         bool left = false;                   // whether this warp has left its sums
-        int begun = lo % nb;                 // where its part of unit u begins
-        for (int i = lo, u = run + lo / nb, b = begun; i < hi; ++i) {
+        const int u_lo = a.boxes.of(lo);
+        int begun = lo - u_lo * nb;          // where its part of unit u begins
+        for (int i = lo, u = run + u_lo, b = begun; i < hi; ++i) {
             while (u >= (x_chunk + 1) * tiles) next_chunk();
             const bool ok = __all_sync(0xFFFFFFFFu,
                                        wait_bounded(bars + 8 * at, phase, ctx, kRoleMatvec, at));
@@ -809,10 +836,10 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                     for (int h = 0; h < kParts; ++h) {
                         const uint8_t* c = codes + 8 * h + 2 * q;
                         single_part(lm_row + at * kBoxBytes + h * (kBoxBytes / kParts),
-                                    x_at[0] + (kParts * b + h) * (2 * kPartK),
+                                    smem + x_at[0] + (kParts * b + h) * (2 * kPartK),
                                     *reinterpret_cast<const uint16_t*>(c),
                                     *reinterpret_cast<const uint16_t*>(c + 8 * kScaleRow),
-                                    s_at[0][0][kParts * b + h], lane, one);
+                                    x_scale(0, 0, kParts * b + h), lane, one);
                     }
                 } else if (kT == 2 && ncols > kTileCols) {
                     multiply(std::integral_constant<int, kT>(), b, codes);
@@ -865,11 +892,11 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                 one[0] = one[1] = 0.0f;
                 float* sum = reinterpret_cast<float*>(sums) + (lane & 15);
                 if (!own) {
-                    if (lane < 16) sum[warp * kRows] = y;
+                    if (lane < 16) sum[(warp - 1) * kRows] = y;
                     leave();
                     continue;
                 }
-                each_other([&](int w) { y += sum[w * kRows]; });
+                each_other([&](int w) { y += sum[(w - 1) * kRows]; });
                 const int n = (done - x_chunk * tiles) * tile_cols + lane;
                 if (kSwiglu) {
                     const float up = __shfl_down_sync(0xFFFFFFFFu, y, 8);
@@ -885,7 +912,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 #pragma unroll
                     for (int j = 0; j < kA; ++j) {
                         uint64_t(&mine)[2] = acc[j / kT][j % kT];
-                        sum[(warp * kA + j) * 32] = make_ulonglong2(mine[0], mine[1]);
+                        sum[((warp - 1) * kA + j) * 32] = make_ulonglong2(mine[0], mine[1]);
                         mine[0] = mine[1] = 0;
                     }
                     leave();
@@ -895,7 +922,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 #pragma unroll
                     for (int j = 0; j < kA; ++j) {
                         uint64_t(&mine)[2] = acc[j / kT][j % kT];
-                        const ulonglong2 v = sum[(w * kA + j) * 32];
+                        const ulonglong2 v = sum[((w - 1) * kA + j) * 32];
                         mine[0] = ptx::add_f32x2(mine[0], v.x);
                         mine[1] = ptx::add_f32x2(mine[1], v.y);
                     }
@@ -1018,10 +1045,15 @@ cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, 
     k.N = a.N;
     k.K = a.K;
     if (!make_layout(a.K, a.slots, a.tokens, a.E, k.x_rows, &k.l)) return cudaErrorInvalidValue;
-    const int tile_cols = form_of(tiles_of(k.l.cols), k.l.warps).rows() / (a.swiglu ? 2 : 1);
-    const long long tiles = ((a.swiglu ? a.N / 2 : a.N) + tile_cols - 1) / tile_cols;
-    const long long units = tiles * a.slots;
+    const Form form = form_of(tiles_of(k.l.cols), k.l.warps);
+    const int tile_cols = form.rows() / (a.swiglu ? 2 : 1), box_k = form.parts * kPartK;
+    const int tiles = ((a.swiglu ? a.N / 2 : a.N) + tile_cols - 1) / tile_cols;
+    const long long units = static_cast<long long>(tiles) * a.slots;
+    if (units > INT32_MAX) return cudaErrorInvalidValue;     // a result of 64 GB and more
     const int grid = static_cast<int>(units < num_sms ? units : num_sms);
+    k.boxes = Divisor((a.K + box_k - 1) / box_k);
+    k.tiles = Divisor(tiles);
+    k.blocks = Divisor(grid);
     return a.swiglu ? launch_cols<true>(map_w, k, grid, stream)
                     : launch_cols<false>(map_w, k, grid, stream);
 }
