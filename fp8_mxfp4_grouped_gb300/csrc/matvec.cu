@@ -37,10 +37,10 @@
 // added up in FP32 times the product of the two scales.
 //
 // Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 20.5
-// us for 107 MB, of which 3.5 pass before the first weights arrive; from there
-// on the weights stream at the measured copy rate.  Down, 6144 x 2048: 13.2 us
-// for 54 MB.  4 tokens, gate/up: 42.2 us for 293 MB; 8 tokens, down: 29.1 us
-// for 194 MB.  13 tokens on 12 experts, 6144 x 3584: 39.4 us for 142 MB, of which
+// to 21.2 us for 107 MB, of which 3.5 pass before the first weights arrive; from there
+// on the weights stream at the measured copy rate.  Down, 6144 x 2048: 12.9 us
+// for 54 MB.  4 tokens, gate/up: 43.1 us for 293 MB; 8 tokens, down: 29.0 us
+// for 194 MB.  13 tokens on 12 experts, 6144 x 3584: 38.3 us for 142 MB, of which
 // about 7 pass before the first product; then it is bound by the instructions
 // issued: conversion, MMA and scaling.
 #include <cuda_fp16.h>
@@ -242,6 +242,7 @@ struct KernelArgs {
     uint64_t timeout_ns;
     int x_rows, slots_per_row, slots, E, N, K;
     Divisor boxes, tiles, blocks;            // boxes of a unit, units of a chunk, blocks
+    bool wide_scales;                        // rows of scales start at multiples of 16 bytes
     Layout l;
 };
 
@@ -614,6 +615,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
 
     // What this warp has asked for so far.
     const int groups = a.K / 32;
+    const bool wide_scales = a.wide_scales;
     const uint32_t ring_w = base + warp * a.l.ring * kBoxBytes;
     const uint32_t ring_s = base + a.l.scales + warp * a.l.ring * kScaleBytes;
     int p_u = 0, p_b = 0, p_left = 0, p_end = u0;            // p_left: boxes of the range
@@ -666,9 +668,9 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             if (++p_slot == a.l.ring) p_slot = 0;
             const int g = 16 * (p_b / 2 * kParts + lane % kParts);
             const uint32_t to = ring_s + p_slot * kScaleBytes + 16 * lane;
-            if ((groups & 15) == 0) {
+            if (wide_scales) {
                 ptx::cp_async_16(to, p_scale + (g < groups ? g : 0), g < groups);
-            } else {                         // rows of scales start at multiples of 4 bytes
+            } else {                         // at multiples of 4
 #pragma unroll
                 for (int i = 0; i < 16; i += 4)
                     ptx::cp_async_4(to + i, p_scale + (g + i < groups ? g + i : 0), g + i < groups);
@@ -1049,8 +1051,8 @@ cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, 
     const int tile_cols = form.rows() / (a.swiglu ? 2 : 1), box_k = form.parts * kPartK;
     const int tiles = ((a.swiglu ? a.N / 2 : a.N) + tile_cols - 1) / tile_cols;
     const long long units = static_cast<long long>(tiles) * a.slots;
-    if (units > INT32_MAX) return cudaErrorInvalidValue;     // a result of 64 GB and more
     const int grid = static_cast<int>(units < num_sms ? units : num_sms);
+    k.wide_scales = ((reinterpret_cast<uintptr_t>(a.w_scale) | (a.K / 32)) & 15) == 0;
     k.boxes = Divisor((a.K + box_k - 1) / box_k);
     k.tiles = Divisor(tiles);
     k.blocks = Divisor(grid);

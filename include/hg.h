@@ -454,10 +454,12 @@ hg_status hg_swiglu_bwd(const uint16_t* dh_bf16, const uint8_t* z_fp8, const uin
  *             4-byte aligned.
  *   y_bf16    uint16 [M*top_k, N] out.
  * Supported: K % 128 == 0, K <= 32768, M*top_k <= 512, any N and E with
- * E*N and M*top_k*N below 2^31.  Each expert's weights are read once per sixteen slots (fewer
- * for large K), so that beyond some tens of tokens the grouped GEMM is the
- * faster way.  The result does not vary from run to run.  One kernel on
- * `stream`; no host synchronisation.
+ * E*N and M*top_k*N below 2^31.  Each expert's weights are read once per sixteen
+ * slots (fewer for large K), so that beyond some tens of tokens the grouped GEMM
+ * is the faster way.  The result does not vary from run to run; the order in
+ * which the terms of a slot's FP32 sum are added can depend on the other slots.
+ * Scales that start at a multiple of 16 bytes, with K % 512 == 0, are read in
+ * wider pieces.  One kernel on `stream`; no host synchronisation.
  */
 hg_status hg_expert_matvec(const uint16_t* x_bf16, int32_t x_rows, const int32_t* topk_ids,
                            const uint8_t* w_fp4, const uint8_t* w_scale, int32_t M, int32_t top_k,

@@ -463,6 +463,24 @@ def test_expert_matvec_repeats_and_agrees_with_gemm(cuda_lib):
     _close(_f64(y), _f64(g), 2 * BF16 * np.abs(ref) + 4 * K * FP32 * mag)
 
 
+@pytest.mark.parametrize("M,K,offset", [(1, 512, 4), (1, 256, 8), (1, 1024, 12), (9, 512, 4),
+                                        (9, 256, 4), (9, 1536, 8)])
+def test_expert_matvec_scales_at_any_multiple_of_four(cuda_lib, M, K, offset):
+    # a view into a larger tensor: the same bits as from a tensor of its own
+    k, E, N = 3, 4, 72
+    ids = torch.from_numpy(make_routing(M, E, k, "uniform", 5)).cuda()
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).cuda()
+    w, ws = (t.cuda() for t in make_weights(E, N, K, seed=7))
+    inside = torch.empty(ws.numel() + 16, dtype=torch.uint8, device="cuda")
+    inside[offset:offset + ws.numel()] = ws.reshape(-1)
+    view = inside[offset:offset + ws.numel()].view(ws.shape)
+    assert view.data_ptr() % 16 == offset
+    want = cuda_lib.hg_expert_matvec(x, ids, w, ws)
+    assert torch.equal(cuda_lib.hg_expert_matvec(x, ids, w, view), want)
+    ref, mag = L.expert_matvec(_f64(x), ids.cpu().numpy(), w.cpu().numpy(), ws.cpu().numpy())
+    _close(_f64(want), ref, BF16 * np.abs(ref) + 2 * K * FP32 * mag)
+
+
 def test_expert_matvec_weights_beyond_32_bits(cuda_lib):
     E, N, K = 512, 2100, 8192                                # 4.4 GB of codes
     g = torch.Generator(device="cuda")
