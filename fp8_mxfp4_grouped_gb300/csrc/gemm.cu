@@ -266,6 +266,8 @@ __device__ __forceinline__ Unit decode_unit(const Sched& s, int u) {
     return t;
 }
 
+// Four weight scales.  No kernel of the library writes weights, and whatever came
+// before the kernel that this one may overlap has completed.
 __device__ __forceinline__ uint32_t ldg_u32(const uint8_t* p) {
     return __ldg(reinterpret_cast<const uint32_t*>(p));
 }
@@ -318,8 +320,8 @@ template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kCtasPerSm)
 grouped_w4a8_kernel(const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ AMaps map_a,
-                    const uint8_t* __restrict__ a_scale, const uint8_t* __restrict__ w_scale,
-                    const int32_t* __restrict__ offsets, int E, int N, int K, int rows,
+                    const uint8_t* a_scale, const uint8_t* __restrict__ w_scale,
+                    const int32_t* offsets, int E, int N, int K, int rows,
                     int as_rs, int as_ks, uint16_t* __restrict__ out, uint32_t* status,
                     uint64_t timeout_ns) {
     constexpr int kStages = Cfg::kStages;
@@ -388,8 +390,8 @@ grouped_w4a8_kernel(const __grid_constant__ CUtensorMap map_w,
     // Per-expert token tiling, from the expert's own row count.
     const int NT = N / kBW;
     for (int e = threadIdx.x; e < E; e += Cfg::kThreads) {
-        const int lo = offsets[e];
-        const int hi = offsets[e + 1];
+        const int lo = ptx::load(offsets + e);
+        const int hi = ptx::load(offsets + e + 1);
         int r = 0;
         if (lo < 0 || hi < lo || hi > rows) {
             record_error(status, HG_ERR_BAD_OFFSETS, static_cast<uint32_t>(e));
@@ -705,8 +707,8 @@ grouped_w4a8_kernel(const __grid_constant__ CUtensorMap map_w,
                     av[i] = 0x7F7F7F7Fu;
                     if (tok < t.n_mma && r < rows) {
                         av[i] = static_cast<uint32_t>(
-                                    __ldg(a_scale + static_cast<size_t>(r) * as_rs +
-                                          static_cast<size_t>(ks) * as_ks)) *
+                                    ptx::load(a_scale + static_cast<size_t>(r) * as_rs +
+                                              static_cast<size_t>(ks) * as_ks)) *
                                 0x01010101u;
                     }
                 }
@@ -769,8 +771,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, Cfg::
 grouped_w4a8_pair_kernel(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ AMaps map_a,
                          const __grid_constant__ CUtensorMap map_out, int out_tma,
-                         const uint8_t* __restrict__ a_scale, const uint8_t* __restrict__ w_scale,
-                         const int32_t* __restrict__ offsets, int E, int N, int K, int rows,
+                         const uint8_t* a_scale, const uint8_t* __restrict__ w_scale,
+                         const int32_t* offsets, int E, int N, int K, int rows,
                          int as_rs, int as_ks, uint16_t* __restrict__ out, uint32_t* status,
                          uint64_t timeout_ns) {
     constexpr int kStages = Cfg::kStages;
@@ -838,8 +840,8 @@ grouped_w4a8_pair_kernel(const __grid_constant__ CUtensorMap map_w,
     // Per-expert token tiling (tiles rounded to 32 rows: two halves of 16k).
     const int NT = N / (2 * kBW);
     for (int e = threadIdx.x; e < E; e += Cfg::kThreads) {
-        const int lo = offsets[e];
-        const int hi = offsets[e + 1];
+        const int lo = ptx::load(offsets + e);
+        const int hi = ptx::load(offsets + e + 1);
         int r = 0;
         if (lo < 0 || hi < lo || hi > rows) {
             record_error(status, HG_ERR_BAD_OFFSETS, static_cast<uint32_t>(e));
@@ -1172,13 +1174,13 @@ grouped_w4a8_pair_kernel(const __grid_constant__ CUtensorMap map_w,
                         const uint8_t* src = a_scale + static_cast<size_t>(r) * as_rs +
                                              static_cast<size_t>(k4) * as_ks;
                         if (word_loads) {
-                            v = __ldg(reinterpret_cast<const uint32_t*>(src));   // 4 whole stages
+                            v = ptx::load(reinterpret_cast<const uint32_t*>(src));   // 4 whole stages
                         } else {
                             v = 0u;
 #pragma unroll
                             for (int j = 0; j < Cfg::kSfbGroup; ++j) {
                                 const uint32_t byte =
-                                    j < nst ? __ldg(src + static_cast<size_t>(j) * as_ks) : 0x7Fu;
+                                    j < nst ? ptx::load(src + static_cast<size_t>(j) * as_ks) : 0x7Fu;
                                 v |= byte << (8 * j);
                             }
                         }

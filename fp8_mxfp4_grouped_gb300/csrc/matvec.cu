@@ -254,7 +254,7 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
     const int tid = threadIdx.x;
     const int cols = a.l.cols;
     auto expert_of = [&](int s) {
-        const int e = s < a.slots ? __ldg(a.ids + s) : -1;
+        const int e = s < a.slots ? ptx::load(a.ids + s) : -1;
         return e >= 0 && e < a.E ? e : -1;
     };
     if (a.slots <= 32) {                     // one warp sees all slots at once

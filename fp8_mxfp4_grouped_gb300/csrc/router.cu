@@ -57,7 +57,7 @@ struct Row {
     }
     __device__ float read(int i) {
         if (lane + 32 * i >= E) return -CUDART_INF_F;
-        const float l = __ldg(at + lane + 32 * i);
+        const float l = ptx::load(at + lane + 32 * i);
         nan |= isnan(l);
         return isnan(l) ? -CUDART_INF_F : l;
     }
@@ -74,7 +74,7 @@ struct Row {
 
 template <int kHeld>
 __global__ void __launch_bounds__(kThreads)
-router_topk_kernel(const float* __restrict__ logits, int M, int E, int top_k, int renormalize,
+router_topk_kernel(const float* logits, int M, int E, int top_k, int renormalize,
                    int32_t* __restrict__ ids, float* __restrict__ weights) {
     const int lane = threadIdx.x & 31;
     const long long t = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -131,8 +131,8 @@ router_topk_kernel(const float* __restrict__ logits, int M, int E, int top_k, in
 }
 
 __global__ void __launch_bounds__(kThreads)
-router_topk_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
-                       const float* __restrict__ weights, const float* __restrict__ dweights,
+router_topk_bwd_kernel(const float* logits, const int32_t* ids,
+                       const float* weights, const float* dweights,
                        int M, int E, int top_k, int renormalize, float* __restrict__ dlogits) {
     const int lane = threadIdx.x & 31;
     const long long t = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -141,10 +141,10 @@ router_topk_bwd_kernel(const float* __restrict__ logits, const int32_t* __restri
     int id = -1;
     float w = 0.0f, dw = 0.0f;
     if (lane < top_k) {
-        id = __ldg(ids + t * top_k + lane);
+        id = ptx::load(ids + t * top_k + lane);
         if (id >= 0 && id < E) {
-            w = __ldg(weights + t * top_k + lane);
-            dw = __ldg(dweights + t * top_k + lane);
+            w = ptx::load(weights + t * top_k + lane);
+            dw = ptx::load(dweights + t * top_k + lane);
         } else {
             id = -1;
         }
@@ -165,10 +165,17 @@ router_topk_bwd_kernel(const float* __restrict__ logits, const int32_t* __restri
         for (int e = lane; e < E; e += 32) out[e] = 0.0f;
     } else {
         const float* row = logits + t * E;
-        const float top = __ldg(row + first);
+        const float top = ptx::load(row + first);
         const float scale = -__shfl_sync(0xFFFFFFFFu, w, 0) * inner;
-#pragma unroll 4
-        for (int e = lane; e < E; e += 32) out[e] = expf(__ldg(row + e) - top) * scale;
+        for (int e0 = lane; e0 < E; e0 += 128) {             // four loads ahead of their stores
+            float l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[i] = e0 + 32 * i < E ? ptx::load(row + e0 + 32 * i) : top;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (e0 + 32 * i < E) out[e0 + 32 * i] = expf(l[i] - top) * scale;
+            }
+        }
     }
     __syncwarp();                            // the chosen ones' values come last
     if (id >= 0) out[id] = w * rise;

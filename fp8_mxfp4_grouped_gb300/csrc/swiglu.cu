@@ -100,7 +100,7 @@ __device__ __forceinline__ uint2 quantize8(const uint64_t (&f)[4], int half, uin
 
 template <bool kCheckpoint>
 __global__ void __launch_bounds__(kThreads)
-swiglu_quantize_kernel(const uint16_t* __restrict__ z, int rows, int F,
+swiglu_quantize_kernel(const uint16_t* z, int rows, int F,
                        uint8_t* __restrict__ a_fp8, uint8_t* __restrict__ a_scale,
                        uint8_t* __restrict__ z_fp8, uint8_t* __restrict__ z_scale) {
     const int G = F / kGroup;
@@ -115,8 +115,8 @@ swiglu_quantize_kernel(const uint16_t* __restrict__ z, int rows, int F,
     auto load = [&]() {
         if (at.i >= groups) return;
         const uint16_t* p = z + at.i * kGroup + at.r * F + 8 * j;
-        next_g = __ldg(reinterpret_cast<const uint4*>(p));
-        next_u = __ldg(reinterpret_cast<const uint4*>(p + F));
+        next_g = ptx::load(reinterpret_cast<const uint4*>(p));
+        next_u = ptx::load(reinterpret_cast<const uint4*>(p + F));
     };
     load();
     while (at.i - half < groups) {
@@ -150,8 +150,8 @@ swiglu_quantize_kernel(const uint16_t* __restrict__ z, int rows, int F,
 }
 
 __global__ void __launch_bounds__(kThreads)
-swiglu_bwd_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restrict__ z_fp8,
-                  const uint8_t* __restrict__ z_scale, int rows, int F,
+swiglu_bwd_kernel(const uint16_t* dh, const uint8_t* z_fp8,
+                  const uint8_t* z_scale, int rows, int F,
                   uint16_t* __restrict__ dz) {
     const int G = F / kGroup;
     const int j = threadIdx.x & 15;
@@ -165,10 +165,10 @@ swiglu_bwd_kernel(const uint16_t* __restrict__ dh, const uint8_t* __restrict__ z
     for (; at.r < rows; at.next(step, step_r, step_g, G)) {
         const long long z_at = at.i * kGroup + at.r * F + 8 * j;
         const uint8_t* s_at = z_scale + (at.i + at.r * G);
-        const uint4 vd = __ldg(reinterpret_cast<const uint4*>(dh + at.i * kGroup + 8 * j));
-        const uint2 vg = __ldg(reinterpret_cast<const uint2*>(z_fp8 + z_at));
-        const uint2 vu = __ldg(reinterpret_cast<const uint2*>(z_fp8 + z_at + F));
-        const float scale_g = e8m0_value(__ldg(s_at)), scale_u = e8m0_value(__ldg(s_at + G));
+        const uint4 vd = ptx::load(reinterpret_cast<const uint4*>(dh + at.i * kGroup + 8 * j));
+        const uint2 vg = ptx::load(reinterpret_cast<const uint2*>(z_fp8 + z_at));
+        const uint2 vu = ptx::load(reinterpret_cast<const uint2*>(z_fp8 + z_at + F));
+        const float scale_g = e8m0_value(ptx::load(s_at)), scale_u = e8m0_value(ptx::load(s_at + G));
         const uint64_t sg = ptx::f32x2(scale_g, scale_g), su = ptx::f32x2(scale_u, scale_u);
         uint32_t og[4], ou[4];
 #pragma unroll

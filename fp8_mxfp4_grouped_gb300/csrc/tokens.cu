@@ -57,8 +57,8 @@ struct Choices {
                        long long rows) {
         const int lane = threadIdx.x & 31;
         if (lane < n) {
-            row = __ldg(place + first + lane);
-            weight = weights ? __ldg(weights + first + lane) : 1.0f;
+            row = ptx::load(place + first + lane);
+            weight = weights ? ptx::load(weights + first + lane) : 1.0f;
             if (row < 0 || row >= rows) row = -1;
         }
     }
@@ -66,8 +66,8 @@ struct Choices {
 
 template <int kPieces>
 __global__ void __launch_bounds__(kThreads)
-dispatch_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ place,
-                const float* __restrict__ weights, int M, int top_k, int K, int team_warps,
+dispatch_kernel(const uint16_t* x, const int32_t* place,
+                const float* weights, int M, int top_k, int K, int team_warps,
                 uint16_t* __restrict__ rows) {
     const Team team(team_warps);
     start_dependent();
@@ -79,7 +79,7 @@ dispatch_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ plac
         for (int c = 0; c < kPieces; ++c) {
             const int n = team.at(pass, kPieces, c);
             v[c] = make_uint4(0, 0, 0, 0);
-            if (n < K) v[c] = __ldg(reinterpret_cast<const uint4*>(xt + n));
+            if (n < K) v[c] = ptx::load(reinterpret_cast<const uint4*>(xt + n));
         }
         for (int j0 = 0; j0 < top_k; j0 += 32) {
             const Choices mine(place, weights, team.token * top_k + j0, min(32, top_k - j0),
@@ -137,8 +137,8 @@ __device__ __forceinline__ float warp_sum8(const float (&d)[8]) {
 // blocks per SM.
 template <bool kSum, bool kDots, int kPieces, int kFlight, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks)
-token_grad_kernel(const uint16_t* __restrict__ rows, const uint16_t* __restrict__ token,
-                  const int32_t* __restrict__ place, const float* __restrict__ weights, int M,
+token_grad_kernel(const uint16_t* rows, const uint16_t* token,
+                  const int32_t* place, const float* weights, int M,
                   int top_k, int N, int team_warps, uint16_t* __restrict__ out,
                   float* __restrict__ dw) {
     __shared__ float s_part[kWarps * kBatch];
@@ -156,7 +156,7 @@ token_grad_kernel(const uint16_t* __restrict__ rows, const uint16_t* __restrict_
             const int n = team.at(pass, kPieces, c);
             own[c] = make_uint4(0, 0, 0, 0);
             if ((!kSum || kDots) && real && n < N)
-                own[c] = __ldg(reinterpret_cast<const uint4*>(token + team.token * N + n));
+                own[c] = ptx::load(reinterpret_cast<const uint4*>(token + team.token * N + n));
             if (kSum) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
@@ -188,7 +188,7 @@ token_grad_kernel(const uint16_t* __restrict__ rows, const uint16_t* __restrict_
                         const int n = team.at(pass, kPieces, c);
                         v[f][c] = make_uint4(0, 0, 0, 0);
                         if (r[f] >= 0 && n < N)
-                            v[f][c] = __ldg(reinterpret_cast<const uint4*>(
+                            v[f][c] = ptx::load(reinterpret_cast<const uint4*>(
                                 rows + static_cast<long long>(r[f]) * N + n));
                     }
                 }
