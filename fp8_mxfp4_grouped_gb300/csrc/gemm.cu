@@ -279,16 +279,6 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
                  : "memory");
 }
 
-// Bounded wait that ignores the abort flag: used while draining in-flight
-// asynchronous work before the CTA exits.
-__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(bar, parity)) {
-        if (ptx::globaltimer_ns() - t0 > timeout_ns) return false;
-    }
-    return true;
-}
-
 // Load `n` activation rows (a multiple of 16, at most 240) starting at row
 // `row`, K offset `k`, into the swizzled tile at `dst`: one TMA per set bit
 // of n / 16, largest box first, so a tile takes at most four instructions.
@@ -487,7 +477,7 @@ grouped_w4a8_kernel(const __grid_constant__ CUtensorMap map_w,
         // worth of issued loads (all of them on the normal path already).
         const uint32_t first = g > kStages ? g - kStages : 0;
         for (uint32_t gg = first; gg < g; ++gg) {
-            wait_drain(bar_full_tma + 8 * (gg % kStages), (gg / kStages) & 1u, timeout_ns);
+            wait_drain(bar_full_tma + 8 * (gg % kStages), (gg / kStages) & 1u);
         }
     } else if (warp == 1) {
         // ------------------------------------------------- MMA issuer ---
@@ -544,7 +534,7 @@ grouped_w4a8_kernel(const __grid_constant__ CUtensorMap map_w,
         }
         // Everything issued must finish before TMEM is released.
         ptx::tc_commit_elect(bar_done);
-        wait_drain(bar_done, 0u, timeout_ns);
+        wait_drain(bar_done, 0u);
     } else if (warp >= 4 && warp < 4 + kEpiWarps) {
         // ---------------------------------------------------- epilogue --
         const int q = warp & 3;   // TMEM lane quadrant this warp may read
@@ -673,7 +663,7 @@ grouped_w4a8_kernel(const __grid_constant__ CUtensorMap map_w,
         }
         if (kCL > 1 && armed) {
             // gave up while partials were on their way: let them land first
-            wait_drain(bar_rx_full + 8 * q, tc & 1u, timeout_ns);
+            wait_drain(bar_rx_full + 8 * q, tc & 1u);
         }
     } else {
         // ------------------------------------------- scale staging -----
@@ -990,10 +980,10 @@ grouped_w4a8_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         const uint32_t first = g > kStages ? g - kStages : 0;
         for (uint32_t gg = first; gg < g; ++gg) {
             if (leader) {
-                wait_drain(bar_full_tma + 8 * (gg % kStages), (gg / kStages) & 1u, timeout_ns);
+                wait_drain(bar_full_tma + 8 * (gg % kStages), (gg / kStages) & 1u);
             } else {
                 // the leader's commit of stage gg completes phase gg / S
-                wait_drain(bar_empty + 8 * (gg % kStages), (gg / kStages) & 1u, timeout_ns);
+                wait_drain(bar_empty + 8 * (gg % kStages), (gg / kStages) & 1u);
             }
         }
     } else if (warp == 1) {
@@ -1084,7 +1074,7 @@ grouped_w4a8_pair_kernel(const __grid_constant__ CUtensorMap map_w,
             }
             // Everything issued must finish before either CTA releases TMEM.
             ptx::tc_commit_pair_multicast_elect(bar_done, 0x1);
-            wait_drain(bar_done, 0u, timeout_ns);
+            wait_drain(bar_done, 0u);
         }
     } else if (warp >= 4 && warp < 4 + kEpiWarps) {
         // ---------------------------------------------------- epilogue --

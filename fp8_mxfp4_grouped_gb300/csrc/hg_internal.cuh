@@ -69,6 +69,18 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, cons
     }
 }
 
+// Wait for asynchronous work in flight before a CTA gives up what it writes to.
+// It ignores the abort flag, and its limit is its own: the caller's (down to a
+// microsecond) may have run out on copies that are merely not there yet.
+constexpr uint64_t kDrainNs = 1000000000ull;
+
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (ptx::globaltimer_ns() - t0 > kDrainNs) return;
+    }
+}
+
 // ------------------------------------------------- host-side launchers --
 
 // Launch with programmatic dependent launch: blocks may start while the kernel

@@ -716,7 +716,9 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         while (run >= (chunk + 1) * tiles) ++chunk;
         const int end = run_end(chunk);
         if (run > u0) {
-            __syncthreads();                 // everybody is done with the rows before
+            // everybody is done with the rows before; once a wait has given up,
+            // no more are asked for (the row barrier may be in a phase that never ends)
+            if (__syncthreads_or(static_cast<int>(*ctx.abort))) break;
             load_run(chunk, end);
         }
         if (kSingle) {
@@ -961,17 +963,12 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         left_phase ^= 1;
         run = end;
     }
-    // After a wait that gave up, copies may still be in flight: wait for them,
-    // again with a limit, before the shared memory is given back.
+    // After a wait that gave up, copies may still be in flight: they land before
+    // the shared memory is given back.
     if (*ctx.abort) {
-        const uint64_t t0 = ptx::globaltimer_ns();
-        auto drain = [&](uint32_t bar, uint32_t parity) {
-            while (!ptx::mbar_try_wait(bar, parity) && ptx::globaltimer_ns() - t0 < a.timeout_ns) {
-            }
-        };
         for (int i = max(0, issued - a.l.ring); i < issued; ++i)
-            drain(bars + 8 * (i % a.l.ring), (i / a.l.ring) & 1);
-        if (!kSingle) drain(x_bar, x_phase ^ 1);             // the last rows asked for
+            wait_drain(bars + 8 * (i % a.l.ring), (i / a.l.ring) & 1);
+        if (!kSingle) wait_drain(x_bar, x_phase ^ 1);        // the last rows asked for
     }
 }
 
