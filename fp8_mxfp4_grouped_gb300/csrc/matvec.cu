@@ -31,10 +31,13 @@
 // and tcgen05 would want the 16-bit weights written back to shared memory
 // first.  x is BF16, wider than FP16's range: each row's 256 elements of a box
 // are scaled by the power of two that takes their largest magnitude into
-// [2^14, 2^15).  An element keeps its 8 bits down to 2^-31 of that largest,
-// and what lies below is off by 2^-39 of it at most, far below the FP32 sum's
-// own rounding.  The sums of a 32-K group come out of the MMA in FP32 and are
-// added up in FP32 times the product of the two scales.
+// [2^14, 2^15).  An element keeps its 8 bits down to 2^-31 of that largest.  The
+// sums of a 32-K group come out of the MMA in FP32 and are added up in FP32
+// times the two scales, one after the other (their product can leave FP32's range
+// where the term does not).  Where 256 elements span more than that, or are
+// outside 2^+-86 or so, Inf or NaN, the units concerned are computed once more at
+// the end, from memory, x split into levels of 32 powers of two: an element counts
+// in full whatever lies beside it, as the largest may meet a weight of zero.
 //
 // Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 20.5
 // to 21.2 us for 107 MB, of which 3.5 pass before the first weights arrive; from there
@@ -236,6 +239,7 @@ struct Divisor {
 struct KernelArgs {
     const uint16_t* x;
     const int32_t* ids;
+    const uint8_t* w_fp4;
     const uint8_t* w_scale;
     uint16_t* out;
     uint32_t* status;
@@ -366,45 +370,125 @@ __device__ int list_slots(const KernelArgs& a, const Tables& tb) {
 // forms by a bulk copy each (1.4 us less for 13 tokens on 12 experts).  Those are
 // rewritten four pieces a warp at once, which hides the latency of the maximum
 // over the lanes: one at a time takes 13 tokens' 182 pieces 2.5 us longer.
+//
+// What a row's 256 elements of a piece are scaled by follows from `be`, the
+// biased exponent of the largest: an element goes to FP16 times 2^(141 - be), and
+// sums come back times 2^(be - 141).  FP16 holds an element's 8 bits down to 31
+// powers of two below the largest.  Pieces that span more are multiplied in
+// levels: level l has the elements of exponents be - 32 l down to be - 32 l - 31,
+// scaled as if be - 32 l were the largest's.
+constexpr int kFp16Exponent = 141;           // of an element that stays as it is
+constexpr int kLevel = 32;
+constexpr int kLeastExponent = 15;           // both factors are normal numbers from here on
+// A sum of the MMA, 2^-25 to 2^23 or zero, times a factor of up to 2^+-100 is
+// exact and a normal number, and is then multiplied with the weights' scale as it
+// is added.
+constexpr int kQuickExponents = 100;
+__device__ __forceinline__ float to_fp16_range(int be) {
+    return __uint_as_float(static_cast<uint32_t>(kFp16Exponent + 127 - be) << 23);
+}
+// Biased exponent of a magnitude; a subnormal's lowest bit is that of exponent 1.
+__device__ __forceinline__ int exponent_of(uint32_t magnitude) {
+    return max(static_cast<int>(magnitude >> 7), 1);
+}
+__device__ __forceinline__ int level_exponent(int be, int level) {
+    return be == 255 ? kFp16Exponent : max(be - kLevel * level, kLeastExponent);
+}
+// Level `level` of eight elements as FP16, zeros in the others' places.  be = 255:
+// Inf and NaN alone, as they are, which decide a sum.
+__device__ __forceinline__ uint4 level_part(const uint4 v, int be, int level) {
+    const float mult = be == 255 ? 1.0f : to_fp16_range(level_exponent(be, level));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t bits = e ? w[i] >> 16 : w[i] & 0xFFFFu;
+            const int below = be - exponent_of(bits & 0x7FFFu);
+            const bool here = be == 255 ? below == 0 && level == 0 : below >> 5 == level;
+            f[e] = here ? __uint_as_float(bits << 16) * mult : 0.0f;
+        }
+        const __half2 p = __floats2half2_rn(f[0], f[1]);
+        h[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+static_assert(kLevel == 32, "levels are told by a shift of five");
+
+__device__ __forceinline__ uint4* piece_at(const KernelArgs& a, uint8_t* smem, int p, int parts,
+                                           float per_row, int lane) {
+    const int held = static_cast<int>((p + 0.5f) * per_row);
+    return reinterpret_cast<uint4*>(smem + a.l.x + held * a.l.x_stride +
+                                    (p - held * parts) * (2 * kPartK) + 16 * lane);
+}
+__device__ __forceinline__ float* factor_of(const KernelArgs& a, uint8_t* smem, int p) {
+    return reinterpret_cast<float*>(smem + a.l.x_scale) + p;
+}
+// Largest and least magnitude of BF16 elements.  Magnitudes compare as integers,
+// NaN the largest.  For the least, with the highest bit set and less one they are
+// signed numbers in order, but zero, which comes out the largest.
+struct Span {
+    uint32_t top = 0, low = 0x7FFF7FFFu;
+    __device__ __forceinline__ void add(uint32_t two) {
+        top = __vmaxu2(top, two & 0x7FFF7FFFu);
+        low = __vmins2(low, (two | 0x80008000u) - 0x00010001u);
+    }
+    __device__ __forceinline__ void add(const uint4 v) {
+        add(v.x);
+        add(v.y);
+        add(v.z);
+        add(v.w);
+    }
+    __device__ __forceinline__ uint32_t largest() const { return max(top & 0xFFFFu, top >> 16); }
+    __device__ __forceinline__ int least_code() const {
+        return min(static_cast<int>(low << 16) >> 16, static_cast<int>(low) >> 16);
+    }
+    // whether any element but zero is below 2^(exponent - 127), exponent above 0
+    __device__ __forceinline__ bool any_below(int exponent) const {
+        const int bound = static_cast<int>(static_cast<uint32_t>(exponent * 128 - 32769) << 16);
+        return min(static_cast<int>(low << 16), static_cast<int>(low)) < bound;
+    }
+};
+// Whether a lane's elements, with `top` the largest magnitude of the piece, allow
+// it to be a plain one: of zeros, or neither Inf, NaN, extreme nor wide.
+__device__ __forceinline__ bool is_plain(const Span& span, uint32_t top) {
+    constexpr uint32_t kLow = (kFp16Exponent - kQuickExponents) << 7;
+    constexpr uint32_t kHigh = (kFp16Exponent + kQuickExponents + 1) << 7;
+    return top - 1u >= kLow - 1u && top < kHigh &&
+           !span.any_below(static_cast<int>(top >> 7) - (kLevel - 1));
+}
+
+// Rows as they came become scaled FP16 where they lie.  Returns whether this lane
+// has seen anything that makes its piece more than a plain one: Inf, NaN, extreme
+// or wide elements.  (A vote and a branch here would stand in the way of the pieces'
+// overlap: 13 tokens on 12 experts 41.1 us, the flag alone 39.0.)
 template <int kPieces>
-__device__ __forceinline__ void scale_pieces(const KernelArgs& a, uint8_t* smem, int first,
+__device__ __forceinline__ bool scale_pieces(const KernelArgs& a, uint8_t* smem, int first,
                                              int step, int parts, float per_row, int lane) {
     uint4* at[kPieces];
     uint4 v[kPieces];
     uint32_t top[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        const int p = first + i * step;
-        const int held = static_cast<int>((p + 0.5f) * per_row);
-        at[i] = reinterpret_cast<uint4*>(smem + a.l.x + held * a.l.x_stride +
-                                         (p - held * parts) * (2 * kPartK) + 16 * lane);
+        at[i] = piece_at(a, smem, first + i * step, parts, per_row, lane);
         v[i] = *at[i];
     }
+    Span span[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        // BF16 magnitudes compare as integers, NaN the largest
-        constexpr uint32_t kAbs = 0x7FFF7FFFu;
-        const uint32_t two = __vmaxu2(__vmaxu2(v[i].x & kAbs, v[i].y & kAbs),
-                                      __vmaxu2(v[i].z & kAbs, v[i].w & kAbs));
-        top[i] = __reduce_max_sync(0xFFFFFFFFu, max(two & 0xFFFFu, two >> 16));
+        span[i].add(v[i]);
+        top[i] = __reduce_max_sync(0xFFFFFFFFu, span[i].largest());
     }
+    bool plain = true;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
         float f[8];
         bf16_unpack8(v[i], f);
-        int be = static_cast<int>(top[i] >> 7);
-        float mult, back;
-        if (be == 255) {
-            // an Inf or NaN decides the sum: the finite elements may be dropped
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = isfinite(f[e]) ? 0.0f : f[e];
-            mult = back = 1.0f;
-        } else {
-            be = max(be, 15);                // both factors stay normal numbers
-            // 2^(14 - (be - 127)) and its inverse
-            mult = __uint_as_float(static_cast<uint32_t>(268 - be) << 23);
-            back = __uint_as_float(static_cast<uint32_t>(be - 14) << 23);
-        }
+        plain &= is_plain(span[i], top[i]);
+        const int be = max(static_cast<int>(top[i] >> 7), kLeastExponent);
+        const float mult = to_fp16_range(be);
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -412,8 +496,19 @@ __device__ __forceinline__ void scale_pieces(const KernelArgs& a, uint8_t* smem,
             h[e] = *reinterpret_cast<const uint32_t*>(&p);
         }
         *at[i] = make_uint4(h[0], h[1], h[2], h[3]);
-        if (lane == 0) reinterpret_cast<float*>(smem + a.l.x_scale)[first + i * step] = back;
+        if (lane == 0)
+            *factor_of(a, smem, first + i * step) =
+                __uint_as_float(static_cast<uint32_t>(be + 127 - kFp16Exponent) << 23);
     }
+    return !plain;
+}
+
+// acc + d * 2^(code - 127) * 2^(be - 141).  The product of the two powers can
+// lie far outside FP32's range where the term does not: half of its exponent at
+// a time.  Code 255 is NaN.
+__device__ __forceinline__ float add_scaled(float d, uint32_t code, int be, float acc) {
+    const int e = static_cast<int>(code) - 127 + be - kFp16Exponent, half = e >> 1;
+    return fmaf(d * e8m0_value(127 + half), e8m0_value(code == 255u ? 255u : 127 + e - half), acc);
 }
 
 // 256 K of 16 weight rows times one column.  Were the column alone in the
@@ -451,10 +546,10 @@ __device__ __forceinline__ void single_part(uint32_t w_at, const uint8_t* x_at, 
         }
     }
     const float2 s_lo = ptx::e8m0x2_to_f32(code_lo), s_hi = ptx::e8m0x2_to_f32(code_hi);
-    acc[0] = fmaf(v[0], s_lo.x * sx, acc[0]);
-    acc[0] = fmaf(v[1], s_lo.y * sx, acc[0]);
-    acc[1] = fmaf(v[2], s_hi.x * sx, acc[1]);
-    acc[1] = fmaf(v[3], s_hi.y * sx, acc[1]);
+    acc[0] = fmaf(v[0] * sx, s_lo.x, acc[0]);
+    acc[0] = fmaf(v[1] * sx, s_lo.y, acc[0]);
+    acc[1] = fmaf(v[2] * sx, s_hi.x, acc[1]);
+    acc[1] = fmaf(v[3] * sx, s_hi.y, acc[1]);
 }
 
 // kTiles: MMAs side by side, eight slots each; 0: a single slot.
@@ -462,7 +557,7 @@ template <bool kSwiglu, int kTiles, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t s_abort;
+    __shared__ uint32_t s_abort, s_other;
     constexpr bool kSingle = kTiles == 0;
     constexpr int kT = kSingle ? 1 : kTiles;
     constexpr Form kForm = form_of(kTiles, kWarps);
@@ -493,7 +588,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         ptx::mbar_init(left_bar + 8 * warp, 1);
         if (warp == 0) {
             ptx::prefetch_tensormap(&map_w);
-            s_abort = 0;
+            s_abort = s_other = 0;
             ptx::mbar_init(x_bar, 1);
         }
         ptx::fence_barrier_init();
@@ -503,6 +598,8 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     // x goes ahead of the weights, behind which it would wait for the whole
     // ring; where all rows are held, ahead of the ids, too.
     const int parts = kParts * nb;
+    uint32_t x_phase = 0, x_asked = 1;       // of x_bar: the next to wait for, the last asked for
+    bool rows_came = true;
     const bool hold_all = a.x_rows <= a.l.x_rows;
     auto each_piece = [&](int rows, auto f) {
         for (int p = warp, held = 0, part = warp; p < parts * rows; p += kWarps) {
@@ -525,7 +622,9 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             ptx::cp_async_commit();
             return;
         }
-        if (warp != 0) return;
+        // none are asked for in a phase that follows one that did not end
+        if (warp != 0 || !rows_came) return;
+        x_asked = x_phase;
         if (lane == 0) ptx::mbar_arrive_expect_tx(x_bar, rows * 2 * a.K);
         __syncwarp();
         ptx::fence_proxy_async_smem();       // the rows before were rewritten in place
@@ -694,6 +793,115 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             a.out[static_cast<long long>(s) * out_cols + n] = 0;
     }
 
+    // Sixteen weight rows of unit u (row tile r), of chunk c, times eight columns in
+    // levels, from memory: a lane loads the words that ldmatrix would give it.
+    auto rows_in_levels = [&](int u, int r, int c, int t) {
+        const int q = lane & 3, g8 = lane >> 2, ncols = tb.ncols[c];
+        const int n0 = (u - c * tiles) * tile_cols + 8 * (kSwiglu ? r : 2 * r) + g8;
+        auto slot_of = [&](int col) { return tb.slot[c * a.l.cols + min(col, ncols - 1)]; };
+        const uint16_t* row =
+            a.x + static_cast<long long>(slot_of(8 * t + g8) / a.slots_per_row) * a.K + 8 * q;
+        // the lane's two weight rows' first groups
+        const long long base_row = static_cast<long long>(tb.expert[c]) * a.N;
+        const long long lo = (base_row + min(n0, out_cols - 1)) * (a.K / 32);
+        const long long hi = (base_row + (kSwiglu ? out_cols + min(n0, out_cols - 1)
+                                                  : min(n0 + 8, out_cols - 1))) * (a.K / 32);
+        float sum[4] = {};
+#pragma unroll 1
+        for (int part = 0; part * kPartK < a.K; ++part) {
+            const int groups = min(8, a.K / 32 - 8 * part);
+            auto x_of = [&](int g) {
+                return ptx::load(reinterpret_cast<const uint4*>(row + part * kPartK + 32 * g));
+            };
+            Span span;
+#pragma unroll 4
+            for (int g = 0; g < groups; ++g) span.add(x_of(g));
+            uint32_t top = span.largest();
+            int low = span.least_code();
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {               // over the column's four lanes
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                low = min(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
+            }
+            const int be = exponent_of(top);
+            const int mine = be == 255 || top == 0 ? 1 : (be - exponent_of(low + 32769)) / kLevel + 1;
+            const int count = __reduce_max_sync(0xFFFFFFFFu, mine);
+#pragma unroll 1
+            for (int l = 0; l < count; ++l) {
+                // of the columns whose sums the lane holds
+                const int be0 = __shfl_sync(0xFFFFFFFFu, level_exponent(be, l), 8 * q);
+                const int be1 = __shfl_sync(0xFFFFFFFFu, level_exponent(be, l), 8 * q + 4);
+#pragma unroll 4
+                for (int g = 0; g < groups; ++g) {
+                    const uint4 x = level_part(x_of(g), be, l);
+                    uint32_t w_lo[4], w_hi[4];
+                    auto weights = [&](long long first, uint32_t(&w)[4]) {
+                        const long long at = first + 8 * part + g;
+                        ptx::e2m1x8_to_f16(
+                            ptx::load(reinterpret_cast<const uint32_t*>(a.w_fp4 + 16 * at + 4 * q)), w);
+                        return ptx::load(a.w_scale + at);
+                    };
+                    const uint32_t code_lo = weights(lo, w_lo), code_hi = weights(hi, w_hi);
+                    float d[4];
+                    ptx::mma_f16_16816_first(d, w_lo[0], w_hi[0], w_lo[1], w_hi[1], x.x, x.y);
+                    ptx::mma_f16_16816(d, w_lo[2], w_hi[2], w_lo[3], w_hi[3], x.z, x.w);
+                    sum[0] = add_scaled(d[0], code_lo, be0, sum[0]);
+                    sum[1] = add_scaled(d[1], code_lo, be1, sum[1]);
+                    sum[2] = add_scaled(d[2], code_hi, be0, sum[2]);
+                    sum[3] = add_scaled(d[3], code_hi, be1, sum[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int col = 8 * t + 2 * q + i;
+            if (col >= ncols) continue;
+            uint16_t* to = a.out + static_cast<long long>(slot_of(col)) * out_cols + n0;
+            const float y = sum[i], y2 = sum[2 + i];
+            const float v = kSwiglu ? y / (1.0f + expf(-y)) * y2 : y;
+            if (n0 < out_cols) to[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            if (!kSwiglu && n0 + 8 < out_cols) to[8] = __bfloat16_as_ushort(__float2bfloat16_rn(y2));
+        }
+    };
+    // The units of a run again, in levels, where any row of a chunk's eight columns is
+    // not plain.  Which they are is found anew, a row a warp: rows that nobody
+    // multiplies are held, too, and may hold anything.  Rare, and in no hurry: one
+    // such row takes a call of one token, gate/up, from 21 to 180 us, and one of 13
+    // tokens on 12 experts from 40 to 260; one that belongs to no slot from 44 to 54.
+    // After the loop and with little unrolled, since the registers that this asks
+    // for, the loop of the boxes does not get.
+    auto run_in_levels = [&](int run, int end, int chunk) {
+        uint8_t* other = smem + a.l.partial;                 // chunk by chunk, tile by tile
+        const int last = a.tiles.of(end - 1);
+        __syncthreads();                     // outputs and sums: all is done
+        for (int i = threadIdx.x; i < (last + 1 - chunk) * kT; i += kThreads) other[i] = 0;
+        __syncthreads();
+        for (int c = chunk, col = warp; c <= last; col += kWarps) {
+            for (; c <= last && col >= tb.ncols[c]; ++c) col -= tb.ncols[c];
+            if (c > last) break;
+            const uint16_t* row =
+                a.x + static_cast<long long>(tb.slot[c * a.l.cols + col] / a.slots_per_row) * a.K;
+            bool plain = true;
+#pragma unroll 1
+            for (int k = 8 * lane; k - 8 * lane < a.K; k += kPartK) {
+                Span span;
+                if (k < a.K) span.add(ptx::load(reinterpret_cast<const uint4*>(row + k)));
+                plain &= is_plain(span, __reduce_max_sync(0xFFFFFFFFu, span.largest()));
+            }
+            if (!plain) other[(c - chunk) * kT + col / kTileCols] = 1;
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = run * kR + warp, c = chunk; i < end * kR; i += kWarps) {
+            const int u = i / kR;
+            while (u >= (c + 1) * tiles) ++c;
+#pragma unroll 1
+            for (int t = 0; t < kT; ++t) {
+                if (other[(c - chunk) * kT + t]) rows_in_levels(u, i % kR, c, t);
+            }
+        }
+    };
+
     const WaitCtx ctx{a.status, &s_abort, a.timeout_ns};
     const int q = lane & 3, g8 = lane >> 2;
     // ldmatrix: lane l addresses row l % 8 of matrix l / 8: the MMA's rows 0-7
@@ -707,7 +915,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     const uint8_t* my_scales = smem + a.l.scales + warp * a.l.ring * kScaleBytes +
                                g8 * kScaleRow;
     int at = 0, slot = -1;
-    uint32_t phase = 0, x_phase = 0, left_phase = 0;
+    uint32_t phase = 0, left_phase = 0;
     if (!kSingle && hold_all && u0 >= u1) {  // no work here, but rows are on their way
         wait_bounded(x_bar, x_phase, ctx, kRoleMatvec, 0x300);
         x_phase ^= 1;
@@ -716,26 +924,27 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         while (run >= (chunk + 1) * tiles) ++chunk;
         const int end = run_end(chunk);
         if (run > u0) {
-            // everybody is done with the rows before; once a wait has given up,
-            // no more are asked for (the row barrier may be in a phase that never ends)
-            if (__syncthreads_or(static_cast<int>(*ctx.abort))) break;
+            __syncthreads();                 // everybody is done with the rows before
             load_run(chunk, end);
         }
         if (kSingle) {
             ptx::cp_async_wait_all_groups();
             __syncwarp();
         } else {
-            wait_bounded(x_bar, x_phase, ctx, kRoleMatvec, 0x300);
+            rows_came = __any_sync(0xFFFFFFFFu,
+                                   wait_bounded(x_bar, x_phase, ctx, kRoleMatvec, 0x300));
             x_phase ^= 1;
         }
         const int pieces = (hold_all ? a.x_rows : run_rows(chunk, end)) * parts;
         int piece = warp;
+        bool other = false;
         if constexpr (!kSingle) {
             for (; piece + 3 * kWarps < pieces; piece += 4 * kWarps)
-                scale_pieces<4>(a, smem, piece, kWarps, parts, 1.0f / parts, lane);
+                other |= scale_pieces<4>(a, smem, piece, kWarps, parts, 1.0f / parts, lane);
         }
         for (; piece < pieces; piece += kWarps)
-            scale_pieces<1>(a, smem, piece, kWarps, parts, 1.0f / parts, lane);
+            other |= scale_pieces<1>(a, smem, piece, kWarps, parts, 1.0f / parts, lane);
+        if (other) s_other = 1;              // and it stays
         const int mine = first_box(run, end);
         if (warp == 0 && lane <= kWarps) bound[lane] = mine;
         __syncthreads();
@@ -814,12 +1023,10 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
                             float d[4];
                             ptx::mma_f16_16816_first(d, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
                             ptx::mma_f16_16816(d, lo[2], hi[2], lo[3], hi[3], x.z, x.w);
-                            acc[r][t][0] = ptx::fma_f32x2(ptx::f32x2(d[0], d[1]),
-                                                          ptx::mul_f32x2(s_lo, sx[t]),
-                                                          acc[r][t][0]);
-                            acc[r][t][1] = ptx::fma_f32x2(ptx::f32x2(d[2], d[3]),
-                                                          ptx::mul_f32x2(s_hi, sx[t]),
-                                                          acc[r][t][1]);
+                            acc[r][t][0] = ptx::fma_f32x2(
+                                ptx::mul_f32x2(ptx::f32x2(d[0], d[1]), sx[t]), s_lo, acc[r][t][0]);
+                            acc[r][t][1] = ptx::fma_f32x2(
+                                ptx::mul_f32x2(ptx::f32x2(d[2], d[3]), sx[t]), s_hi, acc[r][t][1]);
                         }
                     }
                 }
@@ -961,6 +1168,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         // once a run, whether or not there was anything to leave
         if (!left && lane == 0) ptx::mbar_arrive(left_bar + 8 * warp);
         left_phase ^= 1;
+        if (__builtin_expect(s_other, 0)) run_in_levels(run, end, chunk);
         run = end;
     }
     // After a wait that gave up, copies may still be in flight: they land before
@@ -968,7 +1176,7 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
     if (*ctx.abort) {
         for (int i = max(0, issued - a.l.ring); i < issued; ++i)
             wait_drain(bars + 8 * (i % a.l.ring), (i / a.l.ring) & 1);
-        if (!kSingle) wait_drain(x_bar, x_phase ^ 1);        // the last rows asked for
+        if (!kSingle && warp == 0) wait_drain(x_bar, x_asked);
     }
 }
 
@@ -1033,6 +1241,7 @@ cudaError_t launch_expert_matvec(const MatvecArgs& a, const CUtensorMap& map_w, 
     KernelArgs k;
     k.x = a.x;
     k.ids = a.ids;
+    k.w_fp4 = a.w_fp4;
     k.w_scale = a.w_scale;
     k.out = a.out;
     k.status = a.status;

@@ -1,11 +1,13 @@
 """The MoE layer's steps on the GPU at the ends of their ranges, against their float64
 definitions.  Tolerances are those of test_gpu_moe_layer unless stated at the test.
 """
+import numpy as np
 import pytest
 import torch
 
+from oracle import moe_layer as L
 from synth import make_routing, make_weights
-from tests.test_gpu_moe_layer import _normal
+from tests.test_gpu_moe_layer import BF16, FP32, _check_matvec, _close, _f64, _normal
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +42,139 @@ def test_expert_matvec_survives_a_wait_limit_of_a_microsecond(cuda_lib, M, k, E,
         cuda_lib.lib.hg_set_wait_timeout_us(0)
     assert torch.equal(cuda_lib.hg_expert_matvec(x, ids, w, ws), want)
     assert cuda_lib.hg_get_device_status()[0] == cuda_lib.HG_OK
+
+
+def _ones(N, K):
+    """One expert whose weights are all 1, as (codes, scales)."""
+    return (torch.full((1, N, K // 2), 0x22, dtype=torch.uint8),
+            torch.full((1, N, K // 32), 127, dtype=torch.uint8))
+
+
+def _set_code(w, n, k, code):
+    byte = w[0, n, k // 2]
+    w[0, n, k // 2] = (byte & 0x0F) | (code << 4) if k & 1 else (byte & 0xF0) | code
+
+
+@pytest.mark.parametrize("M", [1, 3, 13])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("power", [24, 31, 32, 39, 40, 62, 64, 100, 127])
+def test_expert_matvec_outlier_that_meets_zero_weights(cuda_lib, M, swiglu, power):
+    # one element of 2^power among elements near 1, or near 2^-power / 2: it
+    # meets zeros, so that the sum is the small elements'
+    N, K, k0 = 40, 640, 77
+    w, ws = _ones(N, K)
+    for n in range(N):
+        _set_code(w, n, k0, 0)
+    x = torch.full((M, K), 2.0 ** -6 if swiglu else 1.0078125)
+    x[:, 256:512] = 1.5 * 2.0 ** -(power // 2)
+    x[:, 300] = 0.0
+    if M > 1:
+        x[1] = 0.25                                         # a row without outliers
+    x[0, k0] = 2.0 ** power
+    x[-1, k0] = -(2.0 ** power)
+    ids = np.zeros((M, 1), dtype=np.int32)
+    _check_matvec(cuda_lib, M, 1, 1, N, K, False, swiglu, ids=ids, x=x.bfloat16(), w=(w, ws))
+
+
+@pytest.mark.parametrize("M,E,per_slot", [(1, 1, False), (2, 1, False), (11, 1, False),
+                                          (4, 3, True)])
+@pytest.mark.parametrize("span", [30, 60, 120])
+def test_expert_matvec_any_range_within_a_row(cuda_lib, M, E, per_slot, span):
+    # element k of every row lies near 2^p_k, p_k over [-span, span]; weight row
+    # n is zero wherever p_k is above a limit of its own, so that each output is
+    # decided by elements of another size
+    N, K = 48, 896
+    rng = np.random.default_rng(span + M)
+    p = rng.integers(-span, span + 1, K)
+    rows = M * 2 if per_slot else M
+    x = torch.from_numpy(rng.choice([-1.0, 1.0], (rows, K)) * rng.uniform(1, 2, (rows, K))
+                         * 2.0 ** p).bfloat16()
+    code = rng.integers(0, 16, (E, N, K))
+    limit = np.linspace(-span + 2, span, N).round()[None, :, None]
+    code[np.broadcast_to(p > limit, code.shape)] = 0
+    w = torch.from_numpy((code[..., 0::2] | code[..., 1::2] << 4).astype(np.uint8))
+    ws = torch.from_numpy(rng.integers(120, 126, (E, N, K // 32)).astype(np.uint8))
+    ids = rng.integers(0, E, (M, 2)).astype(np.int32)
+    _check_matvec(cuda_lib, M, 2, E, N, K, per_slot, False, ids=ids, x=x, w=(w, ws))
+
+
+@pytest.mark.parametrize("M", [1, 5])
+def test_expert_matvec_non_finite_rows_beside_wide_ones(cuda_lib, M):
+    # a row of many powers of two next to one with an Inf or a NaN: each decides
+    # its own outputs (511 rounds to 512)
+    N, K = 18, 512
+    w, ws = _ones(N, K)
+    x = torch.ones(M, K)
+    x[:, 3] = 2.0 ** -50
+    x[0, 300] = float("inf")
+    if M > 1:
+        x[1, 7], x[2, 8] = float("nan"), float("-inf")
+        x[3, 9] = 2.0 ** 90
+    y = cuda_lib.hg_expert_matvec(x.bfloat16().cuda(), torch.zeros(M, 1, dtype=torch.int32).cuda(),
+                                  w.cuda(), ws.cuda()).float().cpu()
+    assert (y[0] == float("inf")).all()
+    if M > 1:
+        assert y[1].isnan().all() and (y[2] == float("-inf")).all()
+        assert (y[3] == 2.0 ** 90).all() and (y[4] == K).all()
+
+
+@pytest.mark.parametrize("M", [1, 3, 12])
+def test_expert_matvec_scales_against_rows(cuda_lib, M):
+    # 256-element pieces of x near 2^e with weight scales near 2^-e, and groups
+    # of zero weights whose scales are anything up to 2^127
+    N, K = 34, 1536
+    rng = np.random.default_rng(M)
+    e = np.array([-120, 124, 60, -60, 125, -118])
+    e = rng.permutation(e)
+    x = torch.from_numpy(rng.standard_normal((M, K)) * 2.0 ** np.repeat(e, 256)).bfloat16()
+    code = rng.integers(0, 16, (1, N, K))
+    s = np.broadcast_to(np.clip(127 - np.repeat(e, 8), 0, 254), (1, N, K // 32)).copy()
+    s += rng.integers(-1, 1, s.shape)
+    none = rng.random(s.shape) < 0.3                        # groups without weights
+    code[np.repeat(none, 32, axis=2)] = 0
+    s[none] = rng.choice([0, 1, 100, 150, 200, 254], int(none.sum()))
+    s = np.clip(s, 0, 254)
+    w = torch.from_numpy((code[..., 0::2] | code[..., 1::2] << 4).astype(np.uint8))
+    ids = np.zeros((M, 1), dtype=np.int32)
+    _check_matvec(cuda_lib, M, 1, 1, N, K, False, False, ids=ids, x=x,
+                  w=(w, torch.from_numpy(s.astype(np.uint8))))
+
+
+@pytest.mark.parametrize("M", [1, 5])
+def test_expert_matvec_zero_weights_under_the_largest_scale(cuda_lib, M):
+    # 0 * 2^127 times a row of 2^15 and more adds nothing
+    N, K = 18, 512
+    w, ws = _ones(N, K)
+    w[:, :, 16:32] = 0                                      # the second group of 32
+    ws[:, :, 1] = 254
+    x = torch.ones(M, K)
+    x[:, 5], x[0, 40] = 2.0 ** 15, 2.0 ** 20
+    ids = np.zeros((M, 1), dtype=np.int32)
+    _check_matvec(cuda_lib, M, 1, 1, N, K, False, False, ids=ids, x=x.bfloat16(), w=(w, ws))
+
+
+@pytest.mark.parametrize("M,k,E,K", [(6, 2, 4, 512), (48, 4, 5, 8192), (3, 1, 2, 384)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_expert_matvec_wide_rows_among_others(cuda_lib, M, k, E, K, swiglu):
+    # some rows hold elements that their largest would swamp, one belongs to no
+    # expert and holds NaN; several runs of units per block in the largest case
+    N = 72
+    rng = np.random.default_rng(M + K)
+    ids = make_routing(M, E, k, "biased", 4)
+    x = rng.standard_normal((M, K))
+    x[::3] *= 2.0 ** rng.integers(-50, 20, (len(x[::3]), K))
+    x[M // 2] = np.nan
+    ids[M // 2] = -1
+    w, ws = make_weights(E, N, K, seed=11)
+    x = torch.from_numpy(x).bfloat16()
+    got = cuda_lib.hg_expert_matvec_swiglu if swiglu else cuda_lib.hg_expert_matvec
+    y = got(x.cuda(), torch.from_numpy(ids).cuda(), w.cuda(), ws.cuda())
+    assert float(y[M // 2 * k:(M // 2 + 1) * k].float().abs().max()) == 0
+    x[M // 2] = 0.0                                         # what the definition is given
+    ref, mag = L.expert_matvec(_f64(x), ids, w.numpy(), ws.numpy())
+    err = 2 * K * FP32 * mag
+    if swiglu:
+        g, u, eg, eu = ref[:, :N // 2], ref[:, N // 2:], err[:, :N // 2], err[:, N // 2:]
+        ref = g * L.sigmoid(g) * u
+        err = 1.1 * eg * (np.abs(u) + eu) + np.abs(g * L.sigmoid(g)) * eu + 2.0 ** -16 * np.abs(ref)
+    _close(_f64(y), ref, BF16 * np.abs(ref) + err + 2.0 ** -134)

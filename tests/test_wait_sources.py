@@ -36,9 +36,10 @@ def test_no_other_wait_polls_a_barrier():
 
 
 def test_nothing_is_asked_for_after_giving_up():
-    # between two runs of units the whole block agrees whether to go on, before
-    # new rows are asked for on a barrier whose phase may never end
+    # input rows are asked for on a barrier with one arrival: not again in a phase
+    # whose end the asking warp has not seen
     code = _code(os.path.join(CSRC, "matvec.cu"))
-    loop = code[code.index("for (int run = u0"):]
-    assert loop.index("__syncthreads_or") < loop.index("load_run(")
-    assert re.search(r"if \(__syncthreads_or\([^;]*abort[^;]*\)\) break;", loop)
+    ask = code[code.index("auto load_rows"):code.index("ptx::mbar_arrive_expect_tx(x_bar")]
+    assert re.search(r"if \([^;]*!rows_came\) return;", ask)
+    assert re.search(r"rows_came = __any_sync\([^;]*wait_bounded\(x_bar", code)
+    assert re.search(r"warp == 0\) wait_drain\(x_bar, x_asked\)", code)
