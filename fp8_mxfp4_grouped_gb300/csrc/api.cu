@@ -602,7 +602,8 @@ hg_status hg_swiglu_quantize(const uint16_t* z_bf16, int32_t rows, int32_t F, ui
                              uint8_t* a_scale, uint8_t* z_fp8, uint8_t* z_scale,
                              hg_stream_t stream) {
     if (rows < 0 || F < 1) return HG_ERR_INVALID_ARG;
-    if (F % 128 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (F % 128 != 0 || static_cast<long long>(rows) * (F / 128) > swiglu_max_groups())
+        return HG_ERR_UNSUPPORTED_SHAPE;
     if ((z_fp8 == nullptr) != (z_scale == nullptr)) return HG_ERR_INVALID_ARG;
     if (rows == 0) return HG_OK;
     if (!z_bf16 || !a_fp8 || !a_scale) return HG_ERR_INVALID_ARG;
@@ -620,7 +621,8 @@ hg_status hg_swiglu_quantize(const uint16_t* z_bf16, int32_t rows, int32_t F, ui
 hg_status hg_swiglu_bwd(const uint16_t* dh_bf16, const uint8_t* z_fp8, const uint8_t* z_scale,
                         int32_t rows, int32_t F, uint16_t* dz_bf16, hg_stream_t stream) {
     if (rows < 0 || F < 1) return HG_ERR_INVALID_ARG;
-    if (F % 128 != 0) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (F % 128 != 0 || static_cast<long long>(rows) * (F / 128) > swiglu_max_groups())
+        return HG_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0) return HG_OK;
     if (!dh_bf16 || !z_fp8 || !z_scale || !dz_bf16) return HG_ERR_INVALID_ARG;
     if (!aligned(dh_bf16, 16) || !aligned(z_fp8, 16) || !aligned(dz_bf16, 16))

@@ -206,6 +206,7 @@ cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, const in
                                const float* weights, int M, int top_k, int N, uint16_t* dy,
                                float* dw, cudaStream_t stream);
 
+int swiglu_max_groups();     // of 128 elements of h
 cudaError_t launch_swiglu_quantize(const uint16_t* z, int rows, int F, uint8_t* a_fp8,
                                    uint8_t* a_scale, uint8_t* z_fp8, uint8_t* z_scale, int num_sms,
                                    cudaStream_t stream);

@@ -411,7 +411,9 @@ hg_status hg_combine_topk_bwd(const uint16_t* dout_bf16, const uint16_t* y_bf16,
  *   a_fp8    uint8 [rows, F] out, 16-byte aligned; a_scale uint8 [rows, F/128] out.
  *   z_fp8    uint8 [rows, 2F] out, 16-byte aligned, and z_scale uint8
  *            [rows, 2F/128] out; both NULL when no backward pass follows.
- * F % 128 == 0.  h is quantised from FP32, without a BF16 rounding between.
+ * F % 128 == 0, rows * F/128 below 2^31 - 2^20.  h is quantised from FP32, without
+ * a BF16 rounding between; where silu(g) alone is below FP32's normal numbers
+ * (g < -87), g and u are taken together, so that h is not.
  * One kernel on `stream`; no host synchronisation.
  */
 hg_status hg_swiglu_quantize(const uint16_t* z_bf16, int32_t rows, int32_t F, uint8_t* a_fp8,
@@ -428,7 +430,8 @@ hg_status hg_swiglu_quantize(const uint16_t* z_bf16, int32_t rows, int32_t F, ui
  *   dh_bf16  uint16 [rows, F] BF16, 16-byte aligned.
  *   z_fp8    uint8 [rows, 2F], 16-byte aligned; z_scale uint8 [rows, 2F/128].
  *   dz_bf16  uint16 [rows, 2F] out, 16-byte aligned.
- * F % 128 == 0.  One kernel on `stream`; no host synchronisation.
+ * F % 128 == 0, rows * F/128 below 2^31 - 2^20.  No factor of a product leaves
+ * FP32's range where the product does not.  One kernel on `stream`; no host synchronisation.
  */
 hg_status hg_swiglu_bwd(const uint16_t* dh_bf16, const uint8_t* z_fp8, const uint8_t* z_scale,
                         int32_t rows, int32_t F, uint16_t* dz_bf16, hg_stream_t stream);

@@ -178,3 +178,57 @@ def test_expert_matvec_wide_rows_among_others(cuda_lib, M, k, E, K, swiglu):
         ref = g * L.sigmoid(g) * u
         err = 1.1 * eg * (np.abs(u) + eu) + np.abs(g * L.sigmoid(g)) * eu + 2.0 ** -16 * np.abs(ref)
     _close(_f64(y), ref, BF16 * np.abs(ref) + err + 2.0 ** -134)
+
+
+# --------------------------------------------------------- SwiGLU ---------
+
+def test_swiglu_quantize_gates_far_below_zero(cuda_lib):
+    # silu(g) leaves FP32's normal numbers below g = -87, u brings h back
+    z = torch.zeros(6, 512)
+    z[:, :256] = -torch.linspace(60.0, 176.0, 256)
+    z[:, 256:] = (2.0 ** torch.tensor([0.0, 60.0, 90.0, 110.0, 120.0, 127.0]))[:, None]
+    z[5, 256::2] *= -1.0
+    z = z.bfloat16()
+    a, s, _, _ = cuda_lib.hg_swiglu_quantize(z.cuda(), False)
+    # exp's argument is off by |g| 2^-24 at most
+    h = L.swiglu(_f64(z))
+    e, amax = L.group_exponents(h)
+    got_e = s.cpu().numpy().astype(np.int64) - 127
+    near = np.abs(amax / np.ldexp(448.0, got_e) - 1) < 2.0 ** -12
+    near |= np.abs(amax / np.ldexp(224.0, got_e) - 1) < 2.0 ** -12
+    # below FP32's smallest normal number h may be 0, and its scale then 2^0
+    assert np.all((got_e == e) | near | (amax < 2.0 ** -126))
+    dec = L.dequantize(a.cpu().numpy(), s.cpu().numpy())
+    low = np.repeat(np.ldexp(1.0, got_e - 10), 128, axis=1)
+    # 2^-126 is FP32's smallest normal number
+    _close(dec, h, np.maximum(2.0 ** -4 * np.abs(h), low) + 2.0 ** -12 * np.abs(h) + 2.0 ** -126)
+
+
+def _swiglu_bwd(cuda_lib, g, u, dh):
+    """Codes and scales of checkpoints of one group each; dz and what it should be."""
+    zf = np.concatenate([g, u], axis=1)
+    q, qs = L.quantize(zf)
+    zf = L.dequantize(q, qs)
+    d = torch.from_numpy(dh).bfloat16()
+    dz = cuda_lib.hg_swiglu_bwd(d.cuda(), torch.from_numpy(q).cuda(), torch.from_numpy(qs).cuda())
+    want = L.swiglu_bwd(_f64(d), zf)
+    F = dh.shape[1]
+    gate, up, s = zf[:, :F], zf[:, F:], L.sigmoid(zf[:, :F])
+    mag = np.concatenate([np.abs(_f64(d) * up) * s * (1 + np.abs(gate) * L.sigmoid(-gate)),
+                          np.abs(_f64(d) * gate) * s], axis=1)
+    return _f64(dz), want, mag
+
+
+@pytest.mark.parametrize("low,high,u,d", [(-170.0, -80.0, 2.0 ** 100, 2.0 ** 20),
+                                          (-170.0, -80.0, 2.0 ** 20, 2.0 ** 100),
+                                          (-120.0, -60.0, 2.0 ** 100, 2.0 ** 90),
+                                          (-80.0, -70.0, 2.0 ** 127, 2.0 ** 80),
+                                          (-300.0, 300.0, 1.0, 1.0),
+                                          (-100.0, -88.0, 2.0 ** -20, 2.0 ** 127)])
+def test_swiglu_bwd_far_below_zero_and_large(cuda_lib, low, high, u, d):
+    # s alone underflows, or dh * u alone overflows, where the gradient does neither
+    g = np.linspace(low, high, 256)[None]
+    sign = np.where(np.arange(256) % 3 == 0, -1.0, 1.0)[None]
+    got, want, mag = _swiglu_bwd(cuda_lib, g, u * sign, d * np.ones((1, 256)))
+    assert np.abs(want).max() < 2.0 ** 127
+    _close(got, want, BF16 * np.abs(want) + 2.0 ** -16 * mag + 2.0 ** -134)
