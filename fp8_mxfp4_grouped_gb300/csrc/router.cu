@@ -130,10 +130,14 @@ router_topk_kernel(const float* logits, int M, int E, int top_k, int renormalize
     }
 }
 
+// dw - c, with c = sum_j w_j dw_j, cancels for the largest weight where that is
+// nearly 1.  There it is taken as dw (1 - w) - sum over the others of w_j dw_j, and
+// 1 - w as the sum of all other probabilities.
+template <int kHeld>
 __global__ void __launch_bounds__(kThreads)
-router_topk_bwd_kernel(const float* logits, const int32_t* ids,
-                       const float* weights, const float* dweights,
-                       int M, int E, int top_k, int renormalize, float* __restrict__ dlogits) {
+router_topk_bwd_kernel(const float* logits, const int32_t* ids, const float* weights,
+                       const float* dweights, int M, int E, int top_k, int renormalize,
+                       float* __restrict__ dlogits) {
     const int lane = threadIdx.x & 31;
     const long long t = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     start_dependent();
@@ -142,43 +146,55 @@ router_topk_bwd_kernel(const float* logits, const int32_t* ids,
     float w = 0.0f, dw = 0.0f;
     if (lane < top_k) {
         id = ptx::load(ids + t * top_k + lane);
-        if (id >= 0 && id < E) {
-            w = ptx::load(weights + t * top_k + lane);
-            dw = ptx::load(dweights + t * top_k + lane);
-        } else {
-            id = -1;
-        }
+        w = ptx::load(weights + t * top_k + lane);
+        dw = ptx::load(dweights + t * top_k + lane);
     }
-    // dw - sum_j w_j dw_j; renormalised weights add up to 1, and sum_j w_j (dw -
-    // dw_j) does not cancel where one weight is nearly all of it
-    float inner = 0.0f, rise = 0.0f;
-    if (renormalize) {
-        for (int j = 0; j < top_k; ++j)
-            rise = fmaf(__shfl_sync(0xFFFFFFFFu, w, j), dw - __shfl_sync(0xFFFFFFFFu, dw, j), rise);
-    } else {
-        inner = warp_sum(w * dw);
-        rise = dw - inner;
+    const float* row = logits + t * E;
+    float l[kHeld ? kHeld : 1];
+    if (!renormalize) {                      // asked for ahead of what the choices decide
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            l[i] = lane + 32 * i < E ? ptx::load(row + lane + 32 * i) : -CUDART_INF_F;
     }
+    if (id < 0 || id >= E) {
+        id = -1;
+        w = dw = 0.0f;
+    }
+    const uint32_t chosen = __ballot_sync(0xFFFFFFFFu, id >= 0);
+    const float others = warp_sum(lane > 0 ? w * dw : 0.0f);
+    const float c = __shfl_sync(0xFFFFFFFFu, w * dw, 0) + others;
+    float rest = lane > 0 ? w : 0.0f;        // probabilities but the largest
     const int first = __shfl_sync(0xFFFFFFFFu, id, 0);
     float* out = dlogits + t * E;
     if (renormalize || first < 0) {
         for (int e = lane; e < E; e += 32) out[e] = 0.0f;
     } else {
-        const float* row = logits + t * E;
-        const float top = ptx::load(row + first);
-        const float scale = -__shfl_sync(0xFFFFFFFFu, w, 0) * inner;
-        for (int e0 = lane; e0 < E; e0 += 128) {             // four loads ahead of their stores
-            float l[4];
+        auto logit = [&](int e) {
+            if (kHeld == 0) return ptx::load(row + e);
+            float v = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) l[i] = e0 + 32 * i < E ? ptx::load(row + e0 + 32 * i) : top;
+            for (int i = 0; i < kHeld; ++i) v = e >> 5 == i ? l[i] : v;
+            return __shfl_sync(0xFFFFFFFFu, v, e & 31);
+        };
+        const float top = logit(first), p_top = __shfl_sync(0xFFFFFFFFu, w, 0);
+        // what comes after the last choice, in the choices' order, is not chosen
+        const int last_e = __shfl_sync(0xFFFFFFFFu, id, 31 - __clz(chosen));
+        const float last = logit(last_e);
+        auto each = [&](int e, float le) {
+            const float p = expf(le - top) * p_top;
+            if (le < last || (le == last && e > last_e)) rest += p;
+            if (e < E) out[e] = -p * c;
+        };
+        if (kHeld) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (e0 + 32 * i < E) out[e0 + 32 * i] = expf(l[i] - top) * scale;
-            }
+            for (int i = 0; i < kHeld; ++i) each(lane + 32 * i, l[i]);
+        } else {
+            for (int e = lane; e < E; e += 32) each(e, ptx::load(row + e));
         }
     }
+    rest = warp_sum(rest);
     __syncwarp();                            // the chosen ones' values come last
-    if (id >= 0) out[id] = w * rise;
+    if (id >= 0) out[id] = w * (lane == 0 ? fmaf(dw, rest, -others) : dw - c);
 }
 
 template <int kHeld>
@@ -214,9 +230,16 @@ cudaError_t launch_router_topk(const float* logits, int M, int E, int top_k, int
 cudaError_t launch_router_topk_bwd(const float* logits, const int32_t* ids, const float* weights,
                                    const float* dweights, int M, int E, int top_k,
                                    int renormalize, float* dlogits, cudaStream_t stream) {
-    const int grid = (M - 1) / (kThreads / 32) + 1;
-    return launch_dependent(router_topk_bwd_kernel, grid, kThreads, 0, stream, logits, ids,
-                            weights, dweights, M, E, top_k, renormalize, dlogits);
+    const int grid = (M - 1) / (kThreads / 32) + 1, held = (E + 31) / 32;
+    const auto kernel = renormalize        ? router_topk_bwd_kernel<0>
+                        : held <= 1        ? router_topk_bwd_kernel<1>
+                        : held <= 2        ? router_topk_bwd_kernel<2>
+                        : held <= 5        ? router_topk_bwd_kernel<5>
+                        : held <= 8        ? router_topk_bwd_kernel<8>
+                        : held <= kMaxHeld ? router_topk_bwd_kernel<kMaxHeld>
+                                           : router_topk_bwd_kernel<0>;
+    return launch_dependent(kernel, grid, kThreads, 0, stream, logits, ids, weights, dweights, M, E,
+                            top_k, renormalize, dlogits);
 }
 
 }  // namespace hg

@@ -232,3 +232,45 @@ def test_swiglu_bwd_far_below_zero_and_large(cuda_lib, low, high, u, d):
     got, want, mag = _swiglu_bwd(cuda_lib, g, u * sign, d * np.ones((1, 256)))
     assert np.abs(want).max() < 2.0 ** 127
     _close(got, want, BF16 * np.abs(want) + 2.0 ** -16 * mag + 2.0 ** -134)
+
+
+# ------------------------------------------------------------ router ------
+
+def _saturated(M, E, seed):
+    """Logits of which one per row is larger than the others by 0 to 40."""
+    l = _normal(seed, M, E)
+    top = torch.randint(0, E, (M,), generator=torch.Generator().manual_seed(seed))
+    l[torch.arange(M), top] = l.amax(1) + torch.linspace(0.0, 40.0, M)
+    return l
+
+
+@pytest.mark.parametrize("E,k", [(64, 8), (16, 1), (160, 6), (600, 4), (8, 8)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_router_gradient_of_saturated_rows(cuda_lib, E, k, renorm):
+    # relative to the gradient's own size, which is that of the small weights
+    # where one is nearly 1: with q_i the other probabilities, dl_j is w_j times
+    # sum_i q_i (dw_j - dw_i), and each factor is off by (E + 64) * 2^-24 of itself
+    M = 41
+    logits = _saturated(M, E, E + k)
+    dw = _normal(E, M, k)
+    ids, w = cuda_lib.hg_router_topk(logits.cuda(), k, renorm)
+    d = cuda_lib.hg_router_topk_bwd(logits.cuda(), ids, w, dw.cuda(), renorm)
+    got, lf, df, chosen = d.double().cpu().numpy(), logits.double().numpy(), dw.double().numpy(), \
+        ids.cpu().numpy()
+    p = np.exp(lf - lf.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    want, mag = np.zeros_like(p), np.zeros_like(p)
+    for t in range(M):
+        q, full = p[t].copy(), np.zeros(E)
+        if renorm:
+            outside = np.ones(E, bool)
+            outside[chosen[t]] = False
+            q[outside] = 0.0
+            q /= q.sum()
+        full[chosen[t]] = df[t]
+        for e in range(E):
+            want[t, e] = q[e] * np.sum(q * (full[e] - full))
+            mag[t, e] = q[e] * np.sum(q * (np.abs(full[e]) + np.abs(full)) * (np.arange(E) != e))
+    _close(got, want, 4 * (E + 64) * FP32 * mag + 2.0 ** -126)
+    # the exact row adds up to 0
+    assert np.all(np.abs(got.sum(1)) <= 4 * (E + 64) * FP32 * mag.sum(1) + E * 2.0 ** -126)
