@@ -133,6 +133,10 @@ router_topk_kernel(const float* logits, int M, int E, int top_k, int renormalize
 // dw - c, with c = sum_j w_j dw_j, cancels for the largest weight where that is
 // nearly 1.  There it is taken as dw (1 - w) - sum over the others of w_j dw_j, and
 // 1 - w as the sum of all other probabilities.
+//
+// A choice whose id has been taken out since the gate (for an expert's capacity,
+// say) has no dw, but its probability still counts: its weight does, and where it
+// was the row's largest, or one before the last, the row's own softmax is taken.
 template <int kHeld>
 __global__ void __launch_bounds__(kThreads)
 router_topk_bwd_kernel(const float* logits, const int32_t* ids, const float* weights,
@@ -156,17 +160,19 @@ router_topk_bwd_kernel(const float* logits, const int32_t* ids, const float* wei
         for (int i = 0; i < kHeld; ++i)
             l[i] = lane + 32 * i < E ? ptx::load(row + lane + 32 * i) : -CUDART_INF_F;
     }
+    float out_of = 0.0f;                     // the weight of a choice taken out
     if (id < 0 || id >= E) {
         id = -1;
+        out_of = w;
         w = dw = 0.0f;
     }
     const uint32_t chosen = __ballot_sync(0xFFFFFFFFu, id >= 0);
-    const float others = warp_sum(lane > 0 ? w * dw : 0.0f);
-    const float c = __shfl_sync(0xFFFFFFFFu, w * dw, 0) + others;
-    float rest = lane > 0 ? w : 0.0f;        // probabilities but the largest
-    const int first = __shfl_sync(0xFFFFFFFFu, id, 0);
+    const int lead = chosen ? __ffs(chosen) - 1 : 0;         // the largest weight's
+    const float others = warp_sum(lane != lead ? w * dw : 0.0f);
+    const float c = __shfl_sync(0xFFFFFFFFu, w * dw, lead) + others;
+    float rest = lane != lead ? w + out_of : 0.0f;           // probabilities but the largest
     float* out = dlogits + t * E;
-    if (renormalize || first < 0) {
+    if (renormalize || !chosen) {
         for (int e = lane; e < E; e += 32) out[e] = 0.0f;
     } else {
         auto logit = [&](int e) {
@@ -176,25 +182,38 @@ router_topk_bwd_kernel(const float* logits, const int32_t* ids, const float* wei
             for (int i = 0; i < kHeld; ++i) v = e >> 5 == i ? l[i] : v;
             return __shfl_sync(0xFFFFFFFFu, v, e & 31);
         };
-        const float top = logit(first), p_top = __shfl_sync(0xFFFFFFFFu, w, 0);
-        // what comes after the last choice, in the choices' order, is not chosen
-        const int last_e = __shfl_sync(0xFFFFFFFFu, id, 31 - __clz(chosen));
-        const float last = logit(last_e);
-        auto each = [&](int e, float le) {
-            const float p = expf(le - top) * p_top;
-            if (le < last || (le == last && e > last_e)) rest += p;
-            if (e < E) out[e] = -p * c;
-        };
-        if (kHeld) {
+        auto each = [&](auto f) {
+            if (kHeld) {
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) each(lane + 32 * i, l[i]);
-        } else {
-            for (int e = lane; e < E; e += 32) each(e, ptx::load(row + e));
+                for (int i = 0; i < kHeld; ++i) f(lane + 32 * i, l[i]);
+            } else {
+                for (int e = lane; e < E; e += 32) f(e, ptx::load(row + e));
+            }
+        };
+        const int last = 31 - __clz(chosen);
+        float top = logit(__shfl_sync(0xFFFFFFFFu, id, lead));
+        float p_top = __shfl_sync(0xFFFFFFFFu, w, lead);
+        if (lead > 0) {                      // the row's largest was taken out
+            float most = -CUDART_INF_F, sum = 0.0f;
+            each([&](int, float le) { most = fmaxf(most, le); });
+            top = warp_max(most);
+            each([&](int, float le) { sum += expf(le - top); });
+            p_top = 1.0f / warp_sum(sum);
         }
+        // what comes after the last choice, in the choices' order, is not chosen;
+        // weights taken out behind it are among that
+        const int last_e = __shfl_sync(0xFFFFFFFFu, id, last);
+        const float least = logit(last_e);
+        if (lane > last) rest -= out_of;
+        each([&](int e, float le) {
+            const float p = expf(le - top) * p_top;
+            if (le < least || (le == least && e > last_e)) rest += p;
+            if (e < E) out[e] = -p * c;
+        });
     }
     rest = warp_sum(rest);
     __syncwarp();                            // the chosen ones' values come last
-    if (id >= 0) out[id] = w * (lane == 0 ? fmaf(dw, rest, -others) : dw - c);
+    if (id >= 0) out[id] = w * (lane == lead ? fmaf(dw, rest, -others) : dw - c);
 }
 
 template <int kHeld>

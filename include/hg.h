@@ -515,8 +515,12 @@ hg_status hg_router_topk(const float* logits, int32_t M, int32_t E, int32_t top_
  *   dlogits[t, e] = [e chosen] w[t, e] * (dweights[t, e] - c)           (renormalize != 0)
  *
  *   logits        float32 [M, E]: the forward input; may be NULL when renormalize != 0.
- *   topk_ids, topk_weights  what hg_router_topk returned for these logits, the
- *                 first choice the largest; ids outside [0, E) take no part.
+ *   topk_ids, topk_weights  what hg_router_topk returned for these logits.  An id
+ *                 may have been taken out since (set outside [0, E), its weight left
+ *                 as it was): its dweights count as 0, the others' weights and their
+ *                 gradients stay those of the whole choice.  With renormalize != 0
+ *                 its own logit's gradient, -w * c, has no place to go to and is left
+ *                 out: 0 is written there.
  *   dweights      float32 [M, top_k]; dlogits float32 [M, E] out (every element).
  * One kernel on `stream`; no host synchronisation.
  */

@@ -274,3 +274,33 @@ def test_router_gradient_of_saturated_rows(cuda_lib, E, k, renorm):
     _close(got, want, 4 * (E + 64) * FP32 * mag + 2.0 ** -126)
     # the exact row adds up to 0
     assert np.all(np.abs(got.sum(1)) <= 4 * (E + 64) * FP32 * mag.sum(1) + E * 2.0 ** -126)
+
+
+@pytest.mark.parametrize("E,k", [(48, 6), (700, 3), (9, 9)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_router_gradient_with_choices_dropped_since(cuda_lib, E, k, renorm):
+    # choices taken out after the gate, the first among them: the others keep
+    # their weights, and the gradient is that of sum over them of w dw
+    M = 24
+    logits = _normal(E, M, E) * 2
+    logits[3] = logits[3] - 200.0 * (torch.arange(E) != 5)    # the rest's weights vanish
+    dw = _normal(E + 1, M, k)
+    ids, w = cuda_lib.hg_router_topk(logits.cuda(), k, renorm)
+    rng = np.random.default_rng(E)
+    keep = rng.random((M, k)) < 0.6
+    keep[:8, 0] = False
+    keep[8] = False
+    kept_ids = np.where(keep, ids.cpu().numpy(), np.where(rng.random((M, k)) < 0.5, -1, E))
+    d = cuda_lib.hg_router_topk_bwd(logits.cuda(), torch.from_numpy(kept_ids.astype(np.int32)).cuda(),
+                                    w, dw.cuda(), renorm).double().cpu().numpy()
+    lf, df, chosen = logits.double().numpy(), dw.double().numpy(), ids.cpu().numpy()
+    for t in range(M):
+        p = np.exp(lf[t] - lf[t].max())
+        p /= p.sum()
+        wt = p[chosen[t]] / (p[chosen[t]].sum() if renorm else 1.0)
+        c = np.sum((wt * df[t])[keep[t]])
+        want = np.zeros(E) if renorm else -p * c
+        at = chosen[t][keep[t]]
+        want[at] += wt[keep[t]] * (df[t][keep[t]] - (c if renorm else 0.0))
+        mag = np.sum(np.abs(wt * df[t])) + np.abs(want)
+        _close(d[t], want, 4 * (E + 64) * FP32 * mag + 2.0 ** -126, t)
