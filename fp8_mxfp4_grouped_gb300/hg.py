@@ -125,18 +125,44 @@ def _stream(stream):
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _handle(stream, like):
-    return _raw_stream(like.get_device()) if stream is None else stream.cuda_stream
+_get_device = torch._C._cuda_getDevice
+
+
+def _device(like, *others):
+    """The GPU that all of these inputs (None aside) are on."""
+    device = like.get_device()
+    assert device >= 0, "tensors must be on a GPU"
+    for t in others:
+        assert t is None or t.get_device() == device, "tensors must be on the same GPU"
+    return device
+
+
+def _run(fn, what, device, stream, *args):
+    """One call of the library on the tensors' GPU, which need not be the current one, on
+    `stream` or that GPU's current stream."""
+    if device != _get_device():
+        with torch.cuda.device(device):
+            return _run(fn, what, device, stream, *args)
+    if stream is None:
+        stream = _raw_stream(device)
+    else:
+        assert stream.device_index == device, "the stream must belong to the tensors' GPU"
+        stream = stream.cuda_stream
+    _check(fn(*args, stream), what)
 
 
 def _out(given, shape, dtype, like, stream):
     """The caller's output tensor, checked, or a new one that belongs to `stream`."""
     if given is not None:
         assert given.dtype == dtype and given.shape == shape and given.is_contiguous()
+        assert given.get_device() == like.get_device(), "tensors must be on the same GPU"
         return given
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
@@ -313,16 +339,16 @@ def hg_dispatch_tokens(x_bf16: torch.Tensor, top_k: int, src_to_sorted: torch.Te
     """rows[src_to_sorted[t*k + j]] = w[t, j] * x[t] (w = 1 without weights), BF16 [M*top_k, K].
     Rows that no entry names are not written."""
     M, K = x_bf16.shape
-    assert x_bf16.dtype == torch.bfloat16 and x_bf16.is_contiguous()
-    assert src_to_sorted.dtype == torch.int32 and src_to_sorted.numel() == M * top_k
+    assert x_bf16.dtype == _BF16 and x_bf16.is_contiguous()
+    assert src_to_sorted.dtype == _I32 and src_to_sorted.numel() == M * top_k
     assert src_to_sorted.is_contiguous()
-    assert topk_weights is None or (topk_weights.dtype == torch.float32 and
+    assert topk_weights is None or (topk_weights.dtype == _F32 and
                                     topk_weights.shape == (M, top_k) and
                                     topk_weights.is_contiguous())
-    out = _out(out, (M * top_k, K), torch.bfloat16, x_bf16, stream)
-    st = lib.hg_dispatch_tokens(_addr(x_bf16), _addr(src_to_sorted), _addr(topk_weights), M, top_k,
-                                K, _addr(out), _handle(stream, x_bf16))
-    _check(st, "hg_dispatch_tokens")
+    device = _device(x_bf16, src_to_sorted, topk_weights)
+    out = _out(out, (M * top_k, K), _BF16, x_bf16, stream)
+    _run(lib.hg_dispatch_tokens, "hg_dispatch_tokens", device, stream, x_bf16.data_ptr(),
+         src_to_sorted.data_ptr(), _addr(topk_weights), M, top_k, K, out.data_ptr())
     return out
 
 
@@ -332,22 +358,22 @@ def hg_dispatch_tokens_bwd(drows: torch.Tensor, top_k: int, src_to_sorted: torch
     dweights is None unless the forward input x_bf16 is given."""
     R, K = drows.shape
     M = src_to_sorted.numel() // top_k
-    assert drows.dtype == torch.bfloat16 and drows.is_contiguous() and R == M * top_k
-    assert src_to_sorted.dtype == torch.int32 and src_to_sorted.numel() == R
+    assert drows.dtype == _BF16 and drows.is_contiguous() and R == M * top_k
+    assert src_to_sorted.dtype == _I32 and src_to_sorted.numel() == R
     assert src_to_sorted.is_contiguous()
-    assert topk_weights is None or (topk_weights.dtype == torch.float32 and
+    assert topk_weights is None or (topk_weights.dtype == _F32 and
                                     topk_weights.shape == (M, top_k) and
                                     topk_weights.is_contiguous())
-    dx = _out(dx, (M, K), torch.bfloat16, drows, stream)
+    device = _device(drows, src_to_sorted, topk_weights, x_bf16)
+    dx = _out(dx, (M, K), _BF16, drows, stream)
     if x_bf16 is not None:
-        assert x_bf16.dtype == torch.bfloat16 and x_bf16.shape == (M, K) and x_bf16.is_contiguous()
-        dweights = _out(dweights, (M, top_k), torch.float32, drows, stream)
+        assert x_bf16.dtype == _BF16 and x_bf16.shape == (M, K) and x_bf16.is_contiguous()
+        dweights = _out(dweights, (M, top_k), _F32, drows, stream)
     else:
         assert dweights is None
-    st = lib.hg_dispatch_tokens_bwd(_addr(drows), _addr(x_bf16), _addr(src_to_sorted),
-                                    _addr(topk_weights), M, top_k, K, _addr(dx), _addr(dweights),
-                                    _handle(stream, drows))
-    _check(st, "hg_dispatch_tokens_bwd")
+    _run(lib.hg_dispatch_tokens_bwd, "hg_dispatch_tokens_bwd", device, stream, drows.data_ptr(),
+         _addr(x_bf16), src_to_sorted.data_ptr(), _addr(topk_weights), M, top_k, K, dx.data_ptr(),
+         _addr(dweights))
     return dx, dweights
 
 
@@ -356,17 +382,17 @@ def hg_combine_topk_bwd(dout: torch.Tensor, y_bf16: torch.Tensor, src_to_sorted:
     """Gradient of hg_combine_topk: (dy [M*top_k, N] BF16, dweights [M, top_k] float32)."""
     M, k = topk_weights.shape
     N = dout.shape[1]
-    assert dout.dtype == torch.bfloat16 and dout.shape == (M, N) and dout.is_contiguous()
-    assert y_bf16.dtype == torch.bfloat16 and y_bf16.shape == (M * k, N) and y_bf16.is_contiguous()
-    assert topk_weights.dtype == torch.float32 and topk_weights.is_contiguous()
-    assert src_to_sorted.dtype == torch.int32 and src_to_sorted.numel() == M * k
+    assert dout.dtype == _BF16 and dout.shape == (M, N) and dout.is_contiguous()
+    assert y_bf16.dtype == _BF16 and y_bf16.shape == (M * k, N) and y_bf16.is_contiguous()
+    assert topk_weights.dtype == _F32 and topk_weights.is_contiguous()
+    assert src_to_sorted.dtype == _I32 and src_to_sorted.numel() == M * k
     assert src_to_sorted.is_contiguous()
-    dy = _out(dy, (M * k, N), torch.bfloat16, dout, stream)
-    dweights = _out(dweights, (M, k), torch.float32, dout, stream)
-    st = lib.hg_combine_topk_bwd(_addr(dout), _addr(y_bf16), _addr(src_to_sorted),
-                                 _addr(topk_weights), M, k, N, _addr(dy), _addr(dweights),
-                                 _handle(stream, dout))
-    _check(st, "hg_combine_topk_bwd")
+    device = _device(dout, y_bf16, topk_weights, src_to_sorted)
+    dy = _out(dy, (M * k, N), _BF16, dout, stream)
+    dweights = _out(dweights, (M, k), _F32, dout, stream)
+    _run(lib.hg_combine_topk_bwd, "hg_combine_topk_bwd", device, stream, dout.data_ptr(),
+         y_bf16.data_ptr(), src_to_sorted.data_ptr(), topk_weights.data_ptr(), M, k, N,
+         dy.data_ptr(), dweights.data_ptr())
     return dy, dweights
 
 
@@ -375,18 +401,18 @@ def hg_swiglu_quantize(z_bf16: torch.Tensor, checkpoint: bool = True, a_fp8=None
     """silu(g) * u of z = (g, u) [rows, 2F] as the next GEMM's (a_fp8, a_scale), and with
     `checkpoint` z itself in 8 bits (z_fp8, z_scale), else None in their places."""
     rows, F2 = z_bf16.shape
-    assert z_bf16.dtype == torch.bfloat16 and z_bf16.is_contiguous() and F2 % 2 == 0
+    assert z_bf16.dtype == _BF16 and z_bf16.is_contiguous() and F2 % 2 == 0
     F = F2 // 2
-    a_fp8 = _out(a_fp8, (rows, F), torch.uint8, z_bf16, stream)
-    a_scale = _out(a_scale, (rows, F // 128), torch.uint8, z_bf16, stream)
+    device = _device(z_bf16)
+    a_fp8 = _out(a_fp8, (rows, F), _U8, z_bf16, stream)
+    a_scale = _out(a_scale, (rows, F // 128), _U8, z_bf16, stream)
     if checkpoint:
-        z_fp8 = _out(z_fp8, (rows, F2), torch.uint8, z_bf16, stream)
-        z_scale = _out(z_scale, (rows, F2 // 128), torch.uint8, z_bf16, stream)
+        z_fp8 = _out(z_fp8, (rows, F2), _U8, z_bf16, stream)
+        z_scale = _out(z_scale, (rows, F2 // 128), _U8, z_bf16, stream)
     else:
         assert z_fp8 is None and z_scale is None
-    st = lib.hg_swiglu_quantize(_addr(z_bf16), rows, F, _addr(a_fp8), _addr(a_scale), _addr(z_fp8),
-                                _addr(z_scale), _handle(stream, z_bf16))
-    _check(st, "hg_swiglu_quantize")
+    _run(lib.hg_swiglu_quantize, "hg_swiglu_quantize", device, stream, z_bf16.data_ptr(), rows, F,
+         a_fp8.data_ptr(), a_scale.data_ptr(), _addr(z_fp8), _addr(z_scale))
     return a_fp8, a_scale, z_fp8, z_scale
 
 
@@ -394,14 +420,14 @@ def hg_swiglu_bwd(dh: torch.Tensor, z_fp8: torch.Tensor, z_scale: torch.Tensor, 
                   stream=None) -> torch.Tensor:
     """Gradient of silu(g) * u from the 8-bit checkpoint of (g, u): dz [rows, 2F] BF16."""
     rows, F = dh.shape
-    assert dh.dtype == torch.bfloat16 and dh.is_contiguous()
-    assert z_fp8.dtype == torch.uint8 and z_fp8.shape == (rows, 2 * F) and z_fp8.is_contiguous()
-    assert z_scale.dtype == torch.uint8 and z_scale.shape == (rows, 2 * F // 128)
+    assert dh.dtype == _BF16 and dh.is_contiguous()
+    assert z_fp8.dtype == _U8 and z_fp8.shape == (rows, 2 * F) and z_fp8.is_contiguous()
+    assert z_scale.dtype == _U8 and z_scale.shape == (rows, 2 * F // 128)
     assert z_scale.is_contiguous()
-    dz = _out(dz, (rows, 2 * F), torch.bfloat16, dh, stream)
-    st = lib.hg_swiglu_bwd(_addr(dh), _addr(z_fp8), _addr(z_scale), rows, F, _addr(dz),
-                           _handle(stream, dh))
-    _check(st, "hg_swiglu_bwd")
+    device = _device(dh, z_fp8, z_scale)
+    dz = _out(dz, (rows, 2 * F), _BF16, dh, stream)
+    _run(lib.hg_swiglu_bwd, "hg_swiglu_bwd", device, stream, dh.data_ptr(), z_fp8.data_ptr(),
+         z_scale.data_ptr(), rows, F, dz.data_ptr())
     return dz
 
 
@@ -409,15 +435,15 @@ def _expert_matvec(fn, what, cols, x_bf16, topk_ids, w_fp4, w_scale, out, stream
     M, k = topk_ids.shape
     E, N, K2 = w_fp4.shape
     K = 2 * K2
-    assert x_bf16.dtype == torch.bfloat16 and x_bf16.is_contiguous() and x_bf16.shape[1] == K
-    assert topk_ids.dtype == torch.int32 and topk_ids.is_contiguous()
-    assert w_fp4.dtype == torch.uint8 and w_fp4.is_contiguous()
-    assert w_scale.dtype == torch.uint8 and w_scale.is_contiguous()
+    assert x_bf16.dtype == _BF16 and x_bf16.is_contiguous() and x_bf16.shape[1] == K
+    assert topk_ids.dtype == _I32 and topk_ids.is_contiguous()
+    assert w_fp4.dtype == _U8 and w_fp4.is_contiguous()
+    assert w_scale.dtype == _U8 and w_scale.is_contiguous()
     assert w_scale.shape == (E, N, K // 32)
-    out = _out(out, (M * k, cols(N)), torch.bfloat16, x_bf16, stream)
-    st = fn(_addr(x_bf16), x_bf16.shape[0], _addr(topk_ids), _addr(w_fp4), _addr(w_scale), M, k, E,
-            N, K, _addr(out), _handle(stream, x_bf16))
-    _check(st, what)
+    device = _device(x_bf16, topk_ids, w_fp4, w_scale)
+    out = _out(out, (M * k, cols(N)), _BF16, x_bf16, stream)
+    _run(fn, what, device, stream, x_bf16.data_ptr(), x_bf16.shape[0], topk_ids.data_ptr(),
+         w_fp4.data_ptr(), w_scale.data_ptr(), M, k, E, N, K, out.data_ptr())
     return out
 
 
@@ -440,12 +466,12 @@ def hg_router_topk(logits: torch.Tensor, top_k: int, renormalize: bool = True, i
                    weights=None, stream=None):
     """(topk_ids int32 [M, top_k], topk_weights float32 [M, top_k]) of float32 logits [M, E]."""
     M, E = logits.shape
-    assert logits.dtype == torch.float32 and logits.is_contiguous()
-    ids = _out(ids, (M, top_k), torch.int32, logits, stream)
-    weights = _out(weights, (M, top_k), torch.float32, logits, stream)
-    st = lib.hg_router_topk(_addr(logits), M, E, top_k, int(renormalize), _addr(ids),
-                            _addr(weights), _handle(stream, logits))
-    _check(st, "hg_router_topk")
+    assert logits.dtype == _F32 and logits.is_contiguous()
+    device = _device(logits)
+    ids = _out(ids, (M, top_k), _I32, logits, stream)
+    weights = _out(weights, (M, top_k), _F32, logits, stream)
+    _run(lib.hg_router_topk, "hg_router_topk", device, stream, logits.data_ptr(), M, E, top_k,
+         int(renormalize), ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -455,15 +481,15 @@ def hg_router_topk_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, topk_weight
     """Gradient of hg_router_topk with respect to the logits: float32 [M, E]."""
     M, E = logits.shape
     k = topk_ids.shape[1]
-    assert logits.dtype == torch.float32 and logits.is_contiguous()
-    assert topk_ids.dtype == torch.int32 and topk_ids.shape == (M, k) and topk_ids.is_contiguous()
+    assert logits.dtype == _F32 and logits.is_contiguous()
+    assert topk_ids.dtype == _I32 and topk_ids.shape == (M, k) and topk_ids.is_contiguous()
     for t in (topk_weights, dweights):
-        assert t.dtype == torch.float32 and t.shape == (M, k) and t.is_contiguous()
-    dlogits = _out(dlogits, (M, E), torch.float32, logits, stream)
-    st = lib.hg_router_topk_bwd(_addr(logits), _addr(topk_ids), _addr(topk_weights),
-                                _addr(dweights), M, E, k, int(renormalize), _addr(dlogits),
-                                _handle(stream, logits))
-    _check(st, "hg_router_topk_bwd")
+        assert t.dtype == _F32 and t.shape == (M, k) and t.is_contiguous()
+    device = _device(logits, topk_ids, topk_weights, dweights)
+    dlogits = _out(dlogits, (M, E), _F32, logits, stream)
+    _run(lib.hg_router_topk_bwd, "hg_router_topk_bwd", device, stream, logits.data_ptr(),
+         topk_ids.data_ptr(), topk_weights.data_ptr(), dweights.data_ptr(), M, E, k,
+         int(renormalize), dlogits.data_ptr())
     return dlogits
 
 
