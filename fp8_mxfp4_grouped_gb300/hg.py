@@ -121,18 +121,19 @@ def _stream(stream):
 
 # The calls of a decoding step take a few microseconds on the GPU: what they do
 # on the host is kept as short.  Addresses go to ctypes as plain integers, and
-# the current stream's handle is asked for without building a Stream.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the current device and its stream's handle are asked for below torch.cuda,
+# where this torch has that (one without CUDA has not).
+def _stream_handle(device):
+    return torch.cuda.current_stream(device).cuda_stream
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_handle)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-_get_device = torch._C._cuda_getDevice
 
 
 def _device(like, *others):

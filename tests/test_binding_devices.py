@@ -3,12 +3,14 @@ on the same one, are refused before the library is entered; a call on another GP
 one is made with that GPU current, on its stream.  No GPU needed: the library's functions are
 replaced by one that records its arguments."""
 import contextlib
+import subprocess
+import sys
 import types
 
 import pytest
 import torch
 
-from tests.test_abi_moe_layer import lib  # noqa: F401  (the fixture)
+from tests.test_abi_moe_layer import ROOT, lib  # noqa: F401  (lib is the fixture)
 
 
 class Recorder:
@@ -124,3 +126,14 @@ def test_cpu_tensors_are_refused(lib):  # noqa: F811
         lib.hg_router_topk(torch.zeros(2, 4), 2)
     with pytest.raises(AssertionError):
         lib.hg_swiglu_quantize(torch.zeros(2, 256, dtype=B), False)
+
+
+def test_import_without_torchs_private_names(lib):  # noqa: F811
+    # a torch built without CUDA has neither
+    code = ("import torch; del torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice; "
+            "from fp8_mxfp4_grouped_gb300 import hg; "
+            "assert hg._raw_stream is hg._stream_handle; "
+            "assert hg._get_device is torch.cuda.current_device; print(hg.lib.hg_version())")
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                          timeout=300)
+    assert done.returncode == 0, done.stderr
