@@ -4,7 +4,8 @@
 * ``train_step``: forward and backward through a layer whose experts are frozen (only what
   lies around them learns: the router, and the layers below through dx).  Activations cross
   the experts in FP8; the SwiGLU's input is kept as an 8-bit checkpoint.
-* ``decode``: the same layer for the few tokens of a decoding step, in four launches.
+* ``decode``: the same layer for the few tokens of a decoding step, in four launches (the
+  numbers of the slots, which never change, are made once by the caller).
 
     python examples/moe_layer.py
 """
@@ -71,12 +72,19 @@ def train_step(x, logits, dout, top_k, experts):
     return (out, *backward(dout, ctx, top_k, experts))
 
 
-def decode(x, logits, top_k, experts):
-    """The layer for a few tokens: no plan, no sorting, BF16 activations throughout."""
+def slot_numbers(tokens, top_k, device="cuda"):
+    """What hg_combine_topk reads where the rows are in slot order."""
+    return torch.arange(tokens * top_k, dtype=torch.int32, device=device)
+
+
+def decode(x, logits, top_k, experts, slots=None):
+    """The layer for a few tokens: no plan, no sorting, BF16 activations throughout.  slots:
+    slot_numbers(M, top_k), made here (a launch more) where they are not given."""
+    if slots is None:
+        slots = slot_numbers(x.shape[0], top_k, x.device)
     ids, weights = hg.hg_router_topk(logits, top_k)
     h = hg.hg_expert_matvec_swiglu(x, ids, *experts.gate_up)
     y = hg.hg_expert_matvec(h, ids, *experts.down)
-    slots = torch.arange(y.shape[0], dtype=torch.int32, device=y.device)   # y is in slot order
     return hg.hg_combine_topk(y, slots, weights)
 
 
@@ -95,7 +103,8 @@ def main():
     drouter = x.float().T @ dlogits
     print("train: out", tuple(out.shape), "dx", tuple(dx.shape), "router gradient norm",
           round(float(drouter.norm()), 4))
-    few = decode(x[:3].contiguous(), x[:3].float() @ router, top_k, experts)
+    few = decode(x[:3].contiguous(), x[:3].float() @ router, top_k, experts,
+                 slot_numbers(3, top_k))
     off = float((few.float() - out[:3].float()).norm() / out[:3].float().norm())
     print("decode: out", tuple(few.shape), "relative difference from the FP8 path", round(off, 4))
     status, detail = hg.hg_get_device_status()
