@@ -51,37 +51,16 @@ __device__ __forceinline__ float warp_abs_max(float v) {
     return m;
 }
 
-// E8M0 code of the scale of a group whose largest magnitude is amax: 127 + e
-// with e the smallest integer such that amax <= 448 * 2^e = 1.75 * 2^(e + 8),
-// clamped to codes from 0 (the carry of the addition is the step from 1.75 to
-// the next power of two); 127 for amax = 0, 255 (NaN) for an Inf or NaN.
+// E8M0 code of the scale of a group whose largest magnitude is amax, from its bits
+// (exact, no floating-point division or logarithm): 127 + e with e the smallest
+// integer such that amax <= 448 * 2^e = 1.75 * 2^(e + 8), clamped to codes from 0
+// (the carry of the addition is the step from 1.75 to the next power of two); 127
+// for amax = 0, 255 (NaN) for an Inf or NaN.
 __device__ __forceinline__ uint32_t e8m0_scale_code(float amax) {
     const uint32_t bits = __float_as_uint(amax) & 0x7FFFFFFFu;
     const int code = static_cast<int>((bits + 0x1FFFFFu) >> 23) - 8;
     if (bits >= 0x7F800000u) return 255u;
     return bits == 0u ? 127u : static_cast<uint32_t>(max(code, 0));
-}
-
-// Smallest e with amax <= 448 * 2^e, from the bits of amax (exact, no
-// floating-point division or logarithm).  amax = f * 2^p with f in [1, 2):
-// amax <= 1.75 * 2^(8+e)  <=>  e >= p - 8 when f <= 1.75, else e >= p - 7.
-__device__ __forceinline__ int scale_exponent(float amax) {
-    if (amax == 0.0f) return 0;
-    const uint32_t bits = __float_as_uint(amax);
-    int p;
-    uint32_t mant;
-    const uint32_t be = (bits >> 23) & 0xFFu;
-    if (be == 0) {                         // subnormal: normalise
-        const uint32_t m = bits & 0x7FFFFFu;
-        const int lz = __clz(m) - 8;       // shift that brings the leading 1 to bit 23
-        p = -126 - lz;
-        mant = (m << lz) & 0x7FFFFFu;
-    } else {
-        p = static_cast<int>(be) - 127;
-        mant = bits & 0x7FFFFFu;
-    }
-    int e = p - 8 + (mant > 0x600000u ? 1 : 0);
-    return e < -127 ? -127 : (e > 127 ? 127 : e);
 }
 
 // The two BF16 values of a 32-bit word (element 2i in the low half).
@@ -117,29 +96,23 @@ struct GroupCodes {
 
 // Lane j of a half-warp holds elements 8j .. 8j+7 of one 128-element group;
 // every lane of the warp must call this (the amax reduction shuffles).
-__device__ __forceinline__ GroupCodes quantize_codes(const float (&f)[8]) {
-    float amax = 0.0f;
-    bool nonfinite = false;
+__device__ __forceinline__ GroupCodes quantize_codes(const uint4 v) {
+    float f[8];
+    bf16_unpack8(v, f);
+    float amax = 0.0f;                             // NaN if any element is
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        amax = fmaxf(amax, fabsf(f[i]));
-        nonfinite |= !isfinite(f[i]);
-    }
+    for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(f[i]));
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        nonfinite |= __shfl_xor_sync(0xFFFFFFFFu, nonfinite ? 1 : 0, o) != 0;
-    }
+    for (int o = 8; o >= 1; o >>= 1)
+        amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     GroupCodes c;
-    if (nonfinite) {
-        c.scale = 0xFF;                            // E8M0 NaN
-        c.lo = c.hi = 0x7F7F7F7Fu;                 // E4M3 NaN
+    c.scale = static_cast<uint8_t>(e8m0_scale_code(amax));
+    if (c.scale == 255u) {                         // an Inf or NaN: all of the group NaN
+        c.lo = c.hi = 0x7F7F7F7Fu;
     } else {
-        const int e = scale_exponent(amax);
-        c.scale = static_cast<uint8_t>(127 + e);
-        // 2^-e from its bits: finite inputs give e <= 120, so the biased
-        // exponent 127 - e stays in [7, 254] (a normal float).
-        const float inv = __int_as_float((127 - e) << 23);
+        // 2^-e from its bits: finite inputs give codes up to 247, so that the
+        // biased exponent 254 - code stays in [7, 254] (a normal float).
+        const float inv = __uint_as_float((254u - c.scale) << 23);
         uint32_t b[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -149,12 +122,6 @@ __device__ __forceinline__ GroupCodes quantize_codes(const float (&f)[8]) {
         c.hi = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
     }
     return c;
-}
-
-__device__ __forceinline__ GroupCodes quantize_codes(const uint4 v) {
-    float f[8];
-    bf16_unpack8(v, f);
-    return quantize_codes(f);
 }
 
 }  // namespace hg

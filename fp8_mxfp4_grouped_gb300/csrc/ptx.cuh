@@ -158,12 +158,6 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool v
                  : "memory");
 }
 
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-                 "r"(valid ? 8u : 0u)
-                 : "memory");
-}
-
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(valid ? 16u : 0u)
