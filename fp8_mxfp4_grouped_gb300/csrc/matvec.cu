@@ -35,9 +35,10 @@
 // sums of a 32-K group come out of the MMA in FP32 and are added up in FP32
 // times the two scales, one after the other (their product can leave FP32's range
 // where the term does not).  Where 256 elements span more than that, or are
-// outside 2^+-86 or so, Inf or NaN, the units concerned are computed once more at
-// the end, from memory, x split into levels of 32 powers of two: an element counts
-// in full whatever lies beside it, as the largest may meet a weight of zero.
+// outside 2^+-86 or so, Inf or NaN, outputs in which that can show are computed
+// once more at the end, from memory, x split into levels of 32 powers of two: an
+// element counts in full whatever lies beside it, as the largest may meet a weight
+// of zero.
 //
 // Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 20.5
 // to 21.2 us for 107 MB, of which 3.5 pass before the first weights arrive; from there
@@ -863,41 +864,107 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
             if (!kSwiglu && n0 + 8 < out_cols) to[8] = __bfloat16_as_ushort(__float2bfloat16_rn(y2));
         }
     };
-    // The units of a run again, in levels, where any row of a chunk's eight columns is
-    // not plain.  Which they are is found anew, a row a warp: rows that nobody
-    // multiplies are held, too, and may hold anything.  Rare, and in no hurry: one
-    // such row takes a call of one token, gate/up, from 21 to 180 us, and one of 13
-    // tokens on 12 experts from 40 to 260; one that belongs to no slot from 44 to 54.
-    // After the loop and with little unrolled, since the registers that this asks
-    // for, the loop of the boxes does not get.
-    auto run_in_levels = [&](int run, int end, int chunk) {
-        uint8_t* other = smem + a.l.partial;                 // chunk by chunk, tile by tile
-        const int last = a.tiles.of(end - 1);
+    // What FP16 cut of a slot's row: a bound on the sum of the errors of its elements;
+    // infinity where the quick result says nothing (Inf, NaN, extreme pieces).
+    auto cut_of = [&](int slot) {
+        const uint16_t* row = a.x + static_cast<long long>(slot / a.slots_per_row) * a.K;
+        float cut = 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < a.K; k += kPartK) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (k + 8 * lane < a.K) v = ptx::load(reinterpret_cast<const uint4*>(row + k + 8 * lane));
+            Span span;
+            span.add(v);
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, span.largest());
+            if (is_plain(span, top)) continue;
+            const int be = exponent_of(top);
+            if (abs(be - kFp16Exponent) > kQuickExponents) {
+                cut = __uint_as_float(0x7F800000u);
+                continue;
+            }
+            // an element is off by half of 2^-24 times 2^(be - 141), or by itself
+            const float most = __uint_as_float(static_cast<uint32_t>(be - 39) << 23);
+            float f[8];
+            bf16_unpack8(v, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (be - exponent_of(__float_as_uint(f[e]) >> 16 & 0x7FFFu) >= kLevel)
+                    cut += fminf(fabsf(f[e]), most);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) cut += __shfl_xor_sync(0xFFFFFFFFu, cut, o);
+        return cut;
+    };
+    // Whether the cuts can show in sixteen rows' outputs (row tile r of unit u, eight
+    // columns): they are 2^-11 of none of them, a quarter of BF16's step, with every
+    // weight taken as 6 times the row's largest scale.
+    auto cuts_show = [&](int u, int r, int c, int t, const float* cut) {
+        const int q = lane & 3, g8 = lane >> 2, ncols = tb.ncols[c];
+        const int n0 = (u - c * tiles) * tile_cols + 16 * r;
+        // two lanes a row look for its largest scale, 4 codes at a time
+        const long long first = (static_cast<long long>(tb.expert[c]) * a.N +
+                                 min(n0 + (lane >> 1), out_cols - 1)) * (a.K / 32);
+        uint32_t even = 0, odd = 0;
+#pragma unroll 1
+        for (int g = 4 * (lane & 1); g < a.K / 32; g += 8) {
+            const uint32_t w = ptx::load(reinterpret_cast<const uint32_t*>(a.w_scale + first + g));
+            even = __vmaxu2(even, w & 0x00FF00FFu);
+            odd = __vmaxu2(odd, w >> 8 & 0x00FF00FFu);
+        }
+        const uint32_t two = __vmaxu2(even, odd);
+        uint32_t code = max(two & 0xFFFFu, two >> 16);
+        code = max(code, __shfl_xor_sync(0xFFFFFFFFu, code, 1));
+        bool show = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float w = 6.0f * e8m0_value(__shfl_sync(0xFFFFFFFFu, code, 2 * (g8 + 8 * h)));
+            const int n = n0 + g8 + 8 * h;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = 8 * t + 2 * q + i;
+                if (col >= ncols || n >= out_cols) continue;
+                const int slot = tb.slot[c * a.l.cols + col];
+                const float y = bf16_lo(ptx::load(a.out + static_cast<long long>(slot) * out_cols + n));
+                const bool hidden = fabsf(y) >= 0x1p11f * cut[slot] * w && isfinite(y);
+                show |= cut[slot] > 0.0f && !hidden;
+            }
+        }
+        return static_cast<bool>(__any_sync(0xFFFFFFFFu, show));
+    };
+    // This block's units again, in levels, where FP16 has cut something off a row
+    // that can show.  Which rows these are is found anew, a row a warp: rows that
+    // nobody multiplies are held, too, and may hold anything.  SwiGLU's outputs do not
+    // tell what can show: there all units of such a row are done again.
+    //
+    // With SwiGLU's outputs of gates beyond +-20 as x, one token's down takes 18 in
+    // place of 13 us, 8 tokens' 41 for 28; where the cuts show in many outputs, some
+    // ten times as long (gate/up of one token with a row that spans too much: 180
+    // us).  At the very end, since the registers that this asks for, the loop of the
+    // boxes does not get.
+    auto units_in_levels = [&]() {
+        float* cut = reinterpret_cast<float*>(smem + a.l.partial);           // by slot
+        const int last = a.tiles.of(u1 - 1);
         __syncthreads();                     // outputs and sums: all is done
-        for (int i = threadIdx.x; i < (last + 1 - chunk) * kT; i += kThreads) other[i] = 0;
-        __syncthreads();
-        for (int c = chunk, col = warp; c <= last; col += kWarps) {
+        for (int c = chunk0, col = warp; c <= last; col += kWarps) {
             for (; c <= last && col >= tb.ncols[c]; ++c) col -= tb.ncols[c];
             if (c > last) break;
-            const uint16_t* row =
-                a.x + static_cast<long long>(tb.slot[c * a.l.cols + col] / a.slots_per_row) * a.K;
-            bool plain = true;
-#pragma unroll 1
-            for (int k = 8 * lane; k - 8 * lane < a.K; k += kPartK) {
-                Span span;
-                if (k < a.K) span.add(ptx::load(reinterpret_cast<const uint4*>(row + k)));
-                plain &= is_plain(span, __reduce_max_sync(0xFFFFFFFFu, span.largest()));
-            }
-            if (!plain) other[(c - chunk) * kT + col / kTileCols] = 1;
+            const int slot = tb.slot[c * a.l.cols + col];
+            const float of_slot = cut_of(slot);
+            if (lane == 0) cut[slot] = of_slot;
         }
         __syncthreads();
 #pragma unroll 1
-        for (int i = run * kR + warp, c = chunk; i < end * kR; i += kWarps) {
+        for (int i = u0 * kR + warp, c = chunk0; i < u1 * kR; i += kWarps) {
             const int u = i / kR;
             while (u >= (c + 1) * tiles) ++c;
 #pragma unroll 1
-            for (int t = 0; t < kT; ++t) {
-                if (other[(c - chunk) * kT + t]) rows_in_levels(u, i % kR, c, t);
+            for (int t = 0; 8 * t < tb.ncols[c]; ++t) {
+                const int col = 8 * t + (lane & 7);
+                const bool any = __any_sync(
+                    0xFFFFFFFFu, col < tb.ncols[c] && cut[tb.slot[c * a.l.cols + col]] > 0.0f);
+                if (any && (kSwiglu || cuts_show(u, i % kR, c, t, cut)))
+                    rows_in_levels(u, i % kR, c, t);
             }
         }
     };
@@ -1168,9 +1235,9 @@ expert_matvec_kernel(const __grid_constant__ CUtensorMap map_w, const KernelArgs
         // once a run, whether or not there was anything to leave
         if (!left && lane == 0) ptx::mbar_arrive(left_bar + 8 * warp);
         left_phase ^= 1;
-        if (__builtin_expect(s_other, 0)) run_in_levels(run, end, chunk);
         run = end;
     }
+    if (u0 < u1 && s_other) units_in_levels();
     // After a wait that gave up, copies may still be in flight: they land before
     // the shared memory is given back.
     if (*ctx.abort) {

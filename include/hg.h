@@ -461,9 +461,12 @@ hg_status hg_swiglu_bwd(const uint16_t* dh_bf16, const uint8_t* z_fp8, const uin
  * slots (fewer for large K), so that beyond some tens of tokens the grouped GEMM
  * is the faster way.  The result does not vary from run to run; the order in
  * which the terms of a slot's FP32 sum are added can depend on the other slots.
- * Every BF16 x and every scale is taken at full precision; rows of which 256
- * consecutive elements span more than 31 powers of two (zeros aside), lie beyond
- * 2^+-86 or hold an Inf or NaN take several times as long.
+ * x may span any range: where 256 consecutive elements of a row span more than 31
+ * powers of two (zeros aside), lie beyond 2^+-86 or hold an Inf or NaN, outputs in
+ * which the quick way's rounding of the smaller elements could show (by 2^-11 of the
+ * output) are computed once more, and the call takes longer: some 40 % for SwiGLU's
+ * outputs as x, several times as long where it shows in many outputs, and with the
+ * SwiGLU epilogue, for which all outputs of such a row are.
  * Scales that start at a multiple of 16 bytes, with K % 512 == 0, are read in
  * wider pieces.  One kernel on `stream`; no host synchronisation.
  */

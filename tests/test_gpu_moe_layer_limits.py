@@ -304,3 +304,21 @@ def test_router_gradient_with_choices_dropped_since(cuda_lib, E, k, renorm):
         want[at] += wt[keep[t]] * (df[t][keep[t]] - (c if renorm else 0.0))
         mag = np.sum(np.abs(wt * df[t])) + np.abs(want)
         _close(d[t], want, 4 * (E + 64) * FP32 * mag + 2.0 ** -126, t)
+
+
+@pytest.mark.parametrize("M", [1, 5, 12])
+@pytest.mark.parametrize("spread", [3, 20])
+def test_expert_matvec_on_activations_of_many_powers(cuda_lib, M, spread):
+    # a SwiGLU's outputs, whose gates far below zero leave e^g: much of a row is far
+    # below its largest, and shows only in outputs that are small themselves
+    k, E, N, K = 2, 3, 1000, 2048
+    g, u = _normal(40 + M, M * k, K) * spread, _normal(41 + M, M * k, K)
+    x = (g * torch.sigmoid(g) * u).bfloat16()
+    ids = make_routing(M, E, k, "biased", 8)
+    w, ws = make_weights(E, N, K, seed=12)
+    w[:, 5:9, :K // 4] = 0                                  # rows that miss a row's largest
+    big = x.float().abs().amax(0) > 2.0 ** -20
+    code = torch.stack([w & 15, w >> 4], dim=-1).view(E, N, K)
+    code[:, 20:24, big] = 0                                 # and some that miss all but the smallest
+    w = (code[..., 0::2] | code[..., 1::2] << 4).contiguous()
+    _check_matvec(cuda_lib, M, k, E, N, K, True, False, ids=ids, x=x, w=(w, ws))
