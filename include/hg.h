@@ -458,8 +458,11 @@ hg_status hg_swiglu_bwd(const uint16_t* dh_bf16, const uint8_t* z_fp8, const uin
  *   y_bf16    uint16 [M*top_k, N] out.
  * Supported: K % 128 == 0, K <= 32768, M*top_k <= 512, any N and E with
  * E*N and M*top_k*N below 2^31.  Each expert's weights are read once per sixteen
- * slots (fewer for large K), so that beyond some tens of tokens the grouped GEMM
- * is the faster way.  The result does not vary from run to run; the order in
+ * slots (fewer for large K).  On a GB300, with 32 experts, top-8, 4096 x 6144 with the
+ * SwiGLU and 6144 x 2048, the two products take 76 us for 8 tokens and 99 for 12, and
+ * the plan, the quantisation and two grouped GEMMs 89 and 90: beyond some 80 slots
+ * on such experts the grouped GEMM is the faster way.
+ * The result does not vary from run to run; the order in
  * which the terms of a slot's FP32 sum are added can depend on the other slots.
  * x may span any range: where 256 consecutive elements of a row span more than 31
  * powers of two (zeros aside), lie beyond 2^+-86 or hold an Inf or NaN, outputs in
