@@ -40,13 +40,14 @@
 // element counts in full whatever lies beside it, as the largest may meet a weight
 // of zero.
 //
-// Measured (E = 32, top-8): gate/up of one token, 4096 x 6144 with SwiGLU, 20.5
-// to 21.2 us for 107 MB, of which 3.5 pass before the first weights arrive; from there
-// on the weights stream at the measured copy rate.  Down, 6144 x 2048: 12.9 us
-// for 54 MB.  4 tokens, gate/up: 43.1 us for 293 MB; 8 tokens, down: 29.0 us
-// for 194 MB.  13 tokens on 12 experts, 6144 x 3584: 38.3 us for 142 MB, of which
-// about 7 pass before the first product; then it is bound by the instructions
-// issued: conversion, MMA and scaling.
+// Measured (E = 32, top-8; bytes of the experts that the timed ids name): gate/up of
+// one token, 4096 x 6144 with SwiGLU, 20.8 to 21.2 us for 107 MB, of which 3.5 pass
+// before the first weights arrive; from there on the weights stream at the measured
+// copy rate.  Down, 6144 x 2048: 13.1 us for 54 MB.  4 tokens, gate/up, 18 experts in
+// use: 42.6 us for 236 MB; 8 tokens, down, 21 experts: 29.4 us for 139 MB.  13 tokens
+// on 12 experts, 6144 x 3584: 39.4 us for 142 MB, of which about 7 pass before the
+// first product; then it is bound by the instructions issued: conversion, MMA and
+// scaling.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -464,7 +465,7 @@ __device__ __forceinline__ bool is_plain(const Span& span, uint32_t top) {
 // Rows as they came become scaled FP16 where they lie.  Returns whether this lane
 // has seen anything that makes its piece more than a plain one: Inf, NaN, extreme
 // or wide elements.  (A vote and a branch here would stand in the way of the pieces'
-// overlap: 13 tokens on 12 experts 41.1 us, the flag alone 39.0.)
+// overlap: 41.1 us for 13 tokens on 12 experts where the flag alone took 39.0.)
 template <int kPieces>
 __device__ __forceinline__ bool scale_pieces(const KernelArgs& a, uint8_t* smem, int first,
                                              int step, int parts, float per_row, int lane) {

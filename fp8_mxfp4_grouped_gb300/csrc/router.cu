@@ -17,9 +17,9 @@
 // instructions count.  The row stays in registers (up to 512 experts); a choice
 // is a warp-wide maximum and a warp-wide minimum of the index, one reduction
 // instruction each, and only the lane that owned it looks at its values again.
-// The gradient needs no softmax of its own: the first choice is the row's
-// largest logit and its weight 1 / sum, so that p_e = exp(l_e - l_first) *
-// w_first.  Gate and gradient of 16384 x 160, top-6, take 15.7 us (22 MB: 3.3 at
+// The gradient needs no softmax of its own, as long as the first choice is there:
+// it is the row's largest logit and its weight 1 / sum, so that p_e = exp(l_e -
+// l_first) * w_first.  Gate and gradient of 16384 x 160, top-6, take 15.8 us (22 MB: 3.3 at
 // the copy rate), bound by the rounds of choice; of 5 x 32, top-8, the gate 2.0.
 #include <math_constants.h>
 

@@ -13,7 +13,7 @@
 // group of 128 belongs to half a warp, eight elements a lane, so that its
 // largest magnitude is a reduction instruction away and nothing is read twice
 // (four elements a lane of a whole warp pay twice for addresses and scales:
-// 390 us for 131072 x 2048 with the checkpoint; this form takes 288, 98 % of
+// 390 us for 131072 x 2048 with the checkpoint; this form takes 287, 98 % of
 // the measured HBM copy rate).  exp is 2^x of the hardware and
 // the reciprocal its approximation: off by some 2^-22 of the value, and by
 // |g| * 2^-24 of it for the rounding of the exponent, against the formats'

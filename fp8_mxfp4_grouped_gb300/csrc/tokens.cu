@@ -283,7 +283,10 @@ Shape grad_shape(int M, int top_k, int N) {
 // blocks: 489 against 504 us for the combine's gradient (M = 16384, N = 6144,
 // top-8), 63 against 77 for the dispatch's without dw (M = 4096), where the sums
 // alone leave registers for a fourth block.  With
-// one choice a second row would be no row.
+// one choice a second row would be no row.  The block counts were found at 6144 columns and
+// a few other widths; they make some forms spill, most of all the dispatch's gradient
+// with dw at three pieces a lane (120 bytes; 2880 or 6144 columns, for fewer tokens than
+// kManyTokens) and the combine's at four (76 bytes; 2048, 4096 or 8192 columns).
 template <bool kSum, bool kDots, int kPieces>
 cudaError_t launch_pieces(const Shape& s, const uint16_t* rows, const uint16_t* token,
                           const int32_t* d2s, const float* weights, int M, int top_k, int N,
