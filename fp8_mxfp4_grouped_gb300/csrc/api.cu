@@ -22,6 +22,16 @@ constexpr int kPlanIdsPerBlock = 2048;
 constexpr int kPlanMaxBlocks = 256;
 constexpr int32_t kMaxRowElements = 1 << 30;     // of a token row: kernels index it with int32
 
+// eps of the norm: 1 / sqrt(eps) and the squares that it is added to stay in FP32's range
+constexpr float kMinEps = 1e-30f;
+constexpr float kMaxEps = 1e30f;
+
+// Weights of whole 32-K groups, whose tiles a grid can number.
+bool weight_shape(int32_t E, int32_t N, int32_t K) {
+    if (K % 32 != 0 || static_cast<long long>(E) * N > 0x7FFFFFFFll) return false;
+    return static_cast<long long>(E) * N * (K / 32) <= 1ll << 36;
+}
+
 struct DeviceInfo {
     bool ready = false;
     int num_sms = 0;
@@ -246,6 +256,83 @@ hg_status out_map(PFN_cuTensorMapEncodeTiled_v12000 encode, uint16_t* out, int32
     return HG_OK;
 }
 
+// The weight gradient's operands and result as matrices [matrices, rows, cols], boxes of
+// `box_rows` x `box_cols`.  Encoded at every call.
+hg_status matrix_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMapDataType type, int bytes,
+                     const void* p, long long matrices, int32_t rows, int32_t cols,
+                     uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle,
+                     CUtensorMap* out) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(matrices)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * bytes,
+                             static_cast<cuuint64_t>(cols) * bytes * rows};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return encode(out, type, 3, const_cast<void*>(p), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scale, bool fp8,
+                        const int32_t* offsets, int32_t E, int32_t N, int32_t K, int32_t rows,
+                        int32_t accumulate, void* dw, int32_t dw_f32, void* workspace,
+                        size_t workspace_bytes, hg_stream_t stream) {
+    if (E < 1 || N < 1 || K < 1 || rows < 0) return HG_ERR_INVALID_ARG;
+    if (E > gemm_max_experts() || N % 8 != 0 || K % (fp8 ? 128 : 8) != 0 || N > kMaxRowElements ||
+        K > kMaxRowElements || !wgrad_fits(E, N, K, rows))
+        return HG_ERR_UNSUPPORTED_SHAPE;
+    if (accumulate && !dw_f32) return HG_ERR_INVALID_ARG;
+    if (!offsets || !dw || (rows > 0 && (!dy || !x || (fp8 && !x_scale))))
+        return HG_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(offsets, 4) || !aligned(dw, 16))
+        return HG_ERR_INVALID_ARG;
+    const size_t need = wgrad_workspace(E, N, K, rows);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return HG_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    st = encoder(&encode);
+    if (st != HG_OK) return st;
+    WgradArgs a{};
+    a.x_scale = x_scale;
+    a.offsets = offsets;
+    a.E = E;
+    a.N = N;
+    a.K = K;
+    a.rows = rows;
+    a.accumulate = accumulate != 0;
+    a.f32 = dw_f32 != 0;
+    a.dw = dw;
+    a.parts = need > 0 ? static_cast<float*>(workspace) : nullptr;
+    a.status = d->status;
+    a.timeout_ns = g_timeout_ns.load();
+    // without rows nothing is loaded, but the maps have to name some memory
+    const int32_t map_rows = rows > 0 ? rows : 1;
+    const bool out_f32 = a.f32 || a.parts;
+    WgradMaps maps;
+    st = matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows > 0 ? dy : dw, 1, map_rows,
+                    N, kWgradRows, 64, CU_TENSOR_MAP_SWIZZLE_128B, &maps.dy);
+    if (st == HG_OK)
+        st = fp8 ? matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows > 0 ? x : dw, 1,
+                              map_rows, K, kWgradRows, 128, CU_TENSOR_MAP_SWIZZLE_NONE, &maps.x)
+                 : matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows > 0 ? x : dw, 1,
+                              map_rows, K, kWgradRows, 64, CU_TENSOR_MAP_SWIZZLE_128B, &maps.x);
+    if (st == HG_OK)
+        st = matrix_map(encode,
+                        out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        out_f32 ? 4 : 2, a.parts ? static_cast<void*>(a.parts) : dw,
+                        static_cast<long long>(E) * (a.parts ? wgrad_splits(E, N, K, rows) : 1), N,
+                        K, 32, out_f32 ? 32 : 64, CU_TENSOR_MAP_SWIZZLE_128B, &maps.out);
+    if (st != HG_OK) return st;
+    return launch_wgrad(a, maps, d->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace hg
 
@@ -277,6 +364,7 @@ hg_status hg_shutdown(void) {
     gemm_reset_caches();
     plan_noalloc_reset();
     matvec_reset_caches();
+    wgrad_reset_caches();
     map_cache_reset();
     return HG_OK;
 }
@@ -560,6 +648,23 @@ hg_status hg_dispatch_tokens(const uint16_t* x_bf16, const int32_t* src_to_sorte
                : HG_ERR_CUDA;
 }
 
+hg_status hg_dispatch_acts(const uint8_t* a_fp8, const uint8_t* a_scale,
+                           const int32_t* src_to_sorted, int32_t M, int32_t top_k, int32_t K,
+                           uint8_t* rows_fp8, uint8_t* rows_scale, hg_stream_t stream) {
+    if (M < 0 || top_k < 1 || K < 1) return HG_ERR_INVALID_ARG;
+    if (K % 128 != 0 || K > kMaxRowElements) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<long long>(M) * top_k > 0x7FFFFFFFll) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return HG_OK;
+    if (!a_fp8 || !a_scale || !src_to_sorted || !rows_fp8 || !rows_scale)
+        return HG_ERR_INVALID_ARG;
+    if (!aligned(a_fp8, 16) || !aligned(rows_fp8, 16) || !aligned(src_to_sorted, 4))
+        return HG_ERR_INVALID_ARG;
+    return launch_dispatch_acts(a_fp8, a_scale, src_to_sorted, M, top_k, K, rows_fp8, rows_scale,
+                                reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
 hg_status hg_dispatch_tokens_bwd(const uint16_t* drows_bf16, const uint16_t* x_bf16,
                                  const int32_t* src_to_sorted, const float* topk_weights,
                                  int32_t M, int32_t top_k, int32_t K, uint16_t* dx_bf16,
@@ -684,6 +789,105 @@ hg_status hg_router_topk_bwd(const float* logits, const int32_t* topk_ids,
                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK
                : HG_ERR_CUDA;
+}
+
+hg_status hg_rmsnorm_quantize(const uint16_t* x_bf16, const uint16_t* residual_bf16,
+                              const uint16_t* gain_bf16, int32_t M, int32_t D, float eps,
+                              uint16_t* sum_bf16, uint16_t* y_bf16, uint8_t* a_fp8,
+                              uint8_t* a_scale, float* rstd, hg_stream_t stream) {
+    if (M < 0 || D < 1 || !(eps >= kMinEps && eps <= kMaxEps)) return HG_ERR_INVALID_ARG;
+    if (D % (a_fp8 ? 128 : 8) != 0 || D > rmsnorm_max_elements()) return HG_ERR_UNSUPPORTED_SHAPE;
+    if ((a_fp8 == nullptr) != (a_scale == nullptr) ||
+        (residual_bf16 == nullptr) != (sum_bf16 == nullptr))
+        return HG_ERR_INVALID_ARG;
+    if (M == 0) return HG_OK;
+    if (!x_bf16 || !gain_bf16) return HG_ERR_INVALID_ARG;
+    if (!aligned(x_bf16, 16) || !aligned(residual_bf16, 16) || !aligned(gain_bf16, 16) ||
+        !aligned(sum_bf16, 16) || !aligned(y_bf16, 16) || !aligned(a_fp8, 16) || !aligned(rstd, 4))
+        return HG_ERR_INVALID_ARG;
+    const RmsnormArgs a{x_bf16,   residual_bf16, gain_bf16, M,       D,   eps,
+                        sum_bf16, y_bf16,        a_fp8,     a_scale, rstd};
+    return launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? HG_OK
+                                                                                    : HG_ERR_CUDA;
+}
+
+size_t hg_rmsnorm_bwd_workspace_bytes(int32_t M, int32_t D) {
+    if (M < 1 || D < 1 || D % 8 != 0 || D > rmsnorm_max_elements()) return 0;
+    return rmsnorm_bwd_workspace(M, D);
+}
+
+hg_status hg_rmsnorm_bwd(const uint16_t* dy_bf16, const uint16_t* dsum_bf16,
+                         const uint16_t* sum_bf16, const uint16_t* gain_bf16, const float* rstd,
+                         int32_t M, int32_t D, uint16_t* dx_bf16, float* dgain, void* workspace,
+                         size_t workspace_bytes, hg_stream_t stream) {
+    if (M < 0 || D < 1) return HG_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > rmsnorm_max_elements()) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(dgain, 4)) return HG_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        if (!dgain) return HG_OK;
+        return cudaMemsetAsync(dgain, 0, sizeof(float) * D, s) == cudaSuccess ? HG_OK : HG_ERR_CUDA;
+    }
+    if (!dy_bf16 || !sum_bf16 || !gain_bf16 || !rstd || !dx_bf16) return HG_ERR_INVALID_ARG;
+    if (!aligned(dy_bf16, 16) || !aligned(dsum_bf16, 16) || !aligned(sum_bf16, 16) ||
+        !aligned(gain_bf16, 16) || !aligned(rstd, 4) || !aligned(dx_bf16, 16))
+        return HG_ERR_INVALID_ARG;
+    if (dgain && (!workspace || workspace_bytes < rmsnorm_bwd_workspace(M, D) ||
+                  !aligned(workspace, 16)))
+        return HG_ERR_INVALID_ARG;
+    const RmsnormBwdArgs a{dy_bf16, dsum_bf16, sum_bf16, gain_bf16, rstd,
+                           M,       D,         dx_bf16,  dgain,     static_cast<float*>(workspace)};
+    return launch_rmsnorm_bwd(a, s) == cudaSuccess ? HG_OK : HG_ERR_CUDA;
+}
+
+hg_status hg_quantize_weights(const void* w, int32_t w_f32, int32_t E, int32_t N, int32_t K,
+                              uint8_t* w_fp4, uint8_t* w_scale, uint8_t* wt_fp4,
+                              uint8_t* wt_scale, hg_stream_t stream) {
+    if (E < 0 || N < 1 || K < 1 || (wt_fp4 == nullptr) != (wt_scale == nullptr))
+        return HG_ERR_INVALID_ARG;
+    if (!weight_shape(E, N, K) || (wt_fp4 && N % 32 != 0)) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (E == 0) return HG_OK;
+    if (!w || !w_fp4 || !w_scale) return HG_ERR_INVALID_ARG;
+    if (!aligned(w, 16) || !aligned(w_fp4, 16) || !aligned(wt_fp4, 16)) return HG_ERR_INVALID_ARG;
+    return launch_quantize_weights(w, w_f32 != 0, E, N, K, w_fp4, w_scale, wt_fp4, wt_scale,
+                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+hg_status hg_dequantize_weights(const uint8_t* w_fp4, const uint8_t* w_scale, int32_t E, int32_t N,
+                                int32_t K, void* w, int32_t w_f32, hg_stream_t stream) {
+    if (E < 0 || N < 1 || K < 1) return HG_ERR_INVALID_ARG;
+    if (!weight_shape(E, N, K)) return HG_ERR_UNSUPPORTED_SHAPE;
+    if (E == 0) return HG_OK;
+    if (!w || !w_fp4 || !w_scale) return HG_ERR_INVALID_ARG;
+    if (!aligned(w, 16) || !aligned(w_fp4, 16)) return HG_ERR_INVALID_ARG;
+    return launch_dequantize_weights(w_fp4, w_scale, E, N, K, w, w_f32 != 0,
+                                     reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HG_OK
+               : HG_ERR_CUDA;
+}
+
+size_t hg_grouped_wgrad_workspace_bytes(int32_t E, int32_t N, int32_t K, int32_t rows) {
+    if (E < 1 || N < 1 || K < 1 || rows < 0) return 0;
+    return wgrad_workspace(E, N, K, rows);
+}
+
+hg_status hg_grouped_wgrad(const uint16_t* dy_bf16, const uint16_t* x_bf16,
+                           const int32_t* expert_offsets, int32_t E, int32_t N, int32_t K,
+                           int32_t rows, int32_t accumulate, void* dw, int32_t dw_f32,
+                           void* workspace, size_t workspace_bytes, hg_stream_t stream) {
+    return grouped_wgrad(dy_bf16, x_bf16, nullptr, false, expert_offsets, E, N, K, rows,
+                         accumulate, dw, dw_f32, workspace, workspace_bytes, stream);
+}
+
+hg_status hg_grouped_wgrad_fp8(const uint16_t* dy_bf16, const uint8_t* a_fp8,
+                               const uint8_t* a_scale, const int32_t* expert_offsets, int32_t E,
+                               int32_t N, int32_t K, int32_t rows, int32_t accumulate, void* dw,
+                               int32_t dw_f32, void* workspace, size_t workspace_bytes,
+                               hg_stream_t stream) {
+    return grouped_wgrad(dy_bf16, a_fp8, a_scale, true, expert_offsets, E, N, K, rows, accumulate,
+                         dw, dw_f32, workspace, workspace_bytes, stream);
 }
 
 hg_status hg_get_device_status(hg_stream_t stream, uint32_t* detail) {

@@ -35,6 +35,7 @@ enum WaitRole : uint32_t {
     kRoleSelftest = 6,
     kRoleRelay = 7,
     kRoleMatvec = 8,
+    kRoleWorker = 9,
 };
 
 struct WaitCtx {
@@ -199,6 +200,9 @@ cudaError_t launch_combine_topk(const uint16_t* y, const int32_t* d2s, const flo
 
 cudaError_t launch_dispatch(const uint16_t* x, const int32_t* d2s, const float* weights, int M,
                             int top_k, int K, uint16_t* rows, cudaStream_t stream);
+cudaError_t launch_dispatch_acts(const uint8_t* a, const uint8_t* scale, const int32_t* d2s, int M,
+                                 int top_k, int K, uint8_t* rows, uint8_t* rows_scale,
+                                 cudaStream_t stream);
 cudaError_t launch_dispatch_bwd(const uint16_t* drows, const uint16_t* x, const int32_t* d2s,
                                 const float* weights, int M, int top_k, int K, uint16_t* dx,
                                 float* dw, cudaStream_t stream);
@@ -242,5 +246,58 @@ cudaError_t launch_router_topk_bwd(const float* logits, const int32_t* ids, cons
                                    const float* dweights, int M, int E, int top_k,
                                    int renormalize, float* dlogits, cudaStream_t stream);
 int router_max_top_k();
+
+struct RmsnormArgs {
+    const uint16_t *x, *residual, *gain;
+    int M, D;
+    float eps;
+    uint16_t *sum, *y;      // y, a_fp8 (with a_scale) and rstd may be null
+    uint8_t *a_fp8, *a_scale;
+    float* rstd;
+};
+struct RmsnormBwdArgs {
+    const uint16_t *dy, *dsum, *sum, *gain;     // dsum may be null
+    const float* rstd;
+    int M, D;
+    uint16_t* dx;
+    float *dgain, *parts;   // dgain may be null; parts: rmsnorm_bwd_workspace
+};
+int rmsnorm_max_elements();
+size_t rmsnorm_bwd_workspace(int M, int D);
+cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream);
+cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, cudaStream_t stream);
+
+// qt, scale_t: null for no transposed copy.
+cudaError_t launch_quantize_weights(const void* w, bool f32, int E, int N, int K, uint8_t* q,
+                                    uint8_t* scale, uint8_t* qt, uint8_t* scale_t,
+                                    cudaStream_t stream);
+cudaError_t launch_dequantize_weights(const uint8_t* q, const uint8_t* scale, int E, int N, int K,
+                                      void* w, bool f32, cudaStream_t stream);
+
+struct WgradArgs {
+    const uint8_t* x_scale;     // with an FP8 x, else null
+    const int32_t* offsets;
+    int E, N, K, rows;
+    bool accumulate, f32;       // f32: dw is FP32, else BF16
+    void* dw;
+    float* parts;               // wgrad_workspace, where the rows are split
+    uint32_t* status;
+    uint64_t timeout_ns;
+};
+// Parts that an expert's rows are split into for these sizes.
+int wgrad_splits(int E, int N, int K, int rows);
+size_t wgrad_workspace(int E, int N, int K, int rows);
+bool wgrad_fits(int E, int N, int K, int rows);     // the grid's numbers and the maps' strides
+// Tensor maps: dy [rows, N] in boxes of kWgradRows rows x 64 columns, x [rows, K] the same
+// (FP8: x 128 columns, no swizzle), and the output (the workspace where the rows are
+// split) [E or parts, N, K] in boxes of 32 rows x 128 bytes, all with the 128-byte swizzle.
+constexpr int kWgradRows = 64;
+struct WgradMaps {
+    CUtensorMap dy, x, out;
+};
+cudaError_t launch_wgrad(const WgradArgs& a, const WgradMaps& maps, int num_sms,
+                         cudaStream_t stream);
+// Forget on which devices the weight gradient's kernels are set up (hg_shutdown).
+void wgrad_reset_caches();
 
 }  // namespace hg

@@ -7,6 +7,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include "ptx.cuh"
+
 namespace hg {
 
 // Value of an E8M0 code: 2^(code - 127); code 255 is NaN.
@@ -122,6 +124,49 @@ __device__ __forceinline__ GroupCodes quantize_codes(const uint4 v) {
         c.hi = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
     }
     return c;
+}
+
+// Eight elements a lane of each half-warp's group -> eight E4M3 codes and the
+// group's scale.  Every lane of the warp takes part.
+__device__ __forceinline__ uint2 quantize8(const uint64_t (&f)[4], int half, uint32_t& scale) {
+    float top = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const float2 v = ptx::f32x2_parts(f[p]);
+        top = max_nan(top, max_nan(fabsf(v.x), fabsf(v.y)));
+    }
+    const float top0 = warp_abs_max(half ? 0.0f : top), top1 = warp_abs_max(half ? top : 0.0f);
+    scale = e8m0_scale_code(half ? top1 : top0);
+    const float inv = scale == 255u ? __uint_as_float(0x7FC00000u)      // every code becomes NaN
+                                    : __uint_as_float((254u - scale) << 23);
+    const uint64_t inv2 = ptx::f32x2(inv, inv);
+    float2 q[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) q[p] = ptx::f32x2_parts(ptx::mul_f32x2(f[p], inv2));
+    return make_uint2(e4m3_pack4(q[0].x, q[0].y, q[1].x, q[1].y),
+                      e4m3_pack4(q[2].x, q[2].y, q[3].x, q[3].y));
+}
+
+// E8M0 code of the scale of 32 weights whose largest magnitude is amax: as above with
+// 6 = 1.5 * 2^2 for E2M1 in the place of 448.
+__device__ __forceinline__ uint32_t e8m0_weight_scale_code(float amax) {
+    const uint32_t bits = __float_as_uint(amax) & 0x7FFFFFFFu;
+    const int code = static_cast<int>((bits + 0x3FFFFFu) >> 23) - 2;
+    if (bits >= 0x7F800000u) return 255u;
+    return bits == 0u ? 127u : static_cast<uint32_t>(max(code, 0));
+}
+
+// Eight floats as E2M1 codes, round to nearest, ties to the even code, the first in
+// the lowest four bits.
+__device__ __forceinline__ uint32_t e2m1_pack8(const float (&f)[8]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+    return w;
 }
 
 }  // namespace hg

@@ -107,27 +107,6 @@ struct Walk {
     }
 };
 
-// Eight elements a lane of each half-warp's group -> eight E4M3 codes and the
-// group's scale.  Every lane of the warp takes part.
-__device__ __forceinline__ uint2 quantize8(const uint64_t (&f)[4], int half, uint32_t& scale) {
-    float top = 0.0f;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const float2 v = ptx::f32x2_parts(f[p]);
-        top = max_nan(top, max_nan(fabsf(v.x), fabsf(v.y)));
-    }
-    const float top0 = warp_abs_max(half ? 0.0f : top), top1 = warp_abs_max(half ? top : 0.0f);
-    scale = e8m0_scale_code(half ? top1 : top0);
-    const float inv = scale == 255u ? __uint_as_float(0x7FC00000u)      // every code becomes NaN
-                                    : __uint_as_float((254u - scale) << 23);
-    const uint64_t inv2 = ptx::f32x2(inv, inv);
-    float2 q[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) q[p] = ptx::f32x2_parts(ptx::mul_f32x2(f[p], inv2));
-    return make_uint2(e4m3_pack4(q[0].x, q[0].y, q[1].x, q[1].y),
-                      e4m3_pack4(q[2].x, q[2].y, q[3].x, q[3].y));
-}
-
 // h of all of this warp's groups that hold a gate below kFar, again.  Out of line:
 // in the loop, or as a loop after it, it costs the kernel up to 9 %.
 __device__ __noinline__ void far_groups(const uint16_t* z, int groups, int F, uint8_t* a_fp8,

@@ -64,6 +64,49 @@ struct Choices {
     }
 };
 
+// 8-bit rows with their scales, as they are: the codes go as 16-bit words, eight a piece,
+// and the lanes take the scales a byte each.
+template <int kPieces>
+__global__ void __launch_bounds__(kThreads)
+dispatch_acts_kernel(const uint8_t* a, const uint8_t* scale, const int32_t* place, int M,
+                     int top_k, int K, int team_warps, uint8_t* __restrict__ rows,
+                     uint8_t* __restrict__ rows_scale) {
+    const Team team(team_warps);
+    start_dependent();
+    if (team.token >= M) return;
+    const int words = K / 2, G = K / 128;
+    for (int pass = 0; pass * team.pass_elements(kPieces) < words; ++pass) {
+        uint4 v[kPieces];
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) {
+            const int n = team.at(pass, kPieces, c);
+            v[c] = make_uint4(0, 0, 0, 0);
+            if (n < words) v[c] = ptx::load(reinterpret_cast<const uint4*>(a + team.token * K + 2 * n));
+        }
+        // a scale for 64 words: at most one a lane and pass
+        const int g0 = pass * team.pass_elements(kPieces) / 64;
+        const int g1 = min(G, g0 + team.pass_elements(kPieces) / 64);
+        static_assert(kMaxPieces * 256 / 64 <= 32, "a scale a lane");
+        const int g = g0 + team.rank;
+        uint32_t sc = 0;
+        if (g < g1) sc = ptx::load(scale + team.token * G + g);
+        for (int j0 = 0; j0 < top_k; j0 += 32) {
+            const Choices mine(place, nullptr, team.token * top_k + j0, min(32, top_k - j0),
+                               static_cast<long long>(M) * top_k);
+            for (int j = j0; j < min(top_k, j0 + 32); ++j) {
+                const long long r = __shfl_sync(0xFFFFFFFFu, mine.row, j - j0);
+                if (r < 0) continue;
+#pragma unroll
+                for (int c = 0; c < kPieces; ++c) {
+                    const int n = team.at(pass, kPieces, c);
+                    if (n < words) *reinterpret_cast<uint4*>(rows + r * K + 2 * n) = v[c];
+                }
+                if (g < g1) rows_scale[r * G + g] = static_cast<uint8_t>(sc);
+            }
+        }
+    }
+}
+
 template <int kPieces>
 __global__ void __launch_bounds__(kThreads)
 dispatch_kernel(const uint16_t* x, const int32_t* place,
@@ -322,6 +365,18 @@ cudaError_t launch_dispatch(const uint16_t* x, const int32_t* d2s, const float* 
                                         : dispatch_kernel<4>;
     return launch_dependent(kernel, s.blocks(M), kThreads, 0, stream, x, d2s, weights, M, top_k, K,
                             s.team_warps, rows);
+}
+
+cudaError_t launch_dispatch_acts(const uint8_t* a, const uint8_t* scale, const int32_t* d2s, int M,
+                                 int top_k, int K, uint8_t* rows, uint8_t* rows_scale,
+                                 cudaStream_t stream) {
+    const Shape s(K / 2);
+    const auto kernel = s.pieces == 1   ? dispatch_acts_kernel<1>
+                        : s.pieces == 2 ? dispatch_acts_kernel<2>
+                        : s.pieces == 3 ? dispatch_acts_kernel<3>
+                                        : dispatch_acts_kernel<4>;
+    return launch_dependent(kernel, s.blocks(M), kThreads, 0, stream, a, scale, d2s, M, top_k, K,
+                            s.team_warps, rows, rows_scale);
 }
 
 cudaError_t launch_dispatch_bwd(const uint16_t* drows, const uint16_t* x, const int32_t* d2s,

@@ -88,6 +88,26 @@ lib.hg_router_topk.restype = ctypes.c_int
 lib.hg_router_topk_bwd.argtypes = [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _p, _p]
 lib.hg_router_topk_bwd.restype = ctypes.c_int
 
+lib.hg_dispatch_acts.argtypes = [_p, _p, _p, _i32, _i32, _i32, _p, _p, _p]
+lib.hg_dispatch_acts.restype = ctypes.c_int
+lib.hg_rmsnorm_quantize.argtypes = [_p, _p, _p, _i32, _i32, ctypes.c_float, _p, _p, _p, _p, _p, _p]
+lib.hg_rmsnorm_quantize.restype = ctypes.c_int
+lib.hg_rmsnorm_bwd_workspace_bytes.argtypes = [_i32, _i32]
+lib.hg_rmsnorm_bwd_workspace_bytes.restype = _sz
+lib.hg_rmsnorm_bwd.argtypes = [_p, _p, _p, _p, _p, _i32, _i32, _p, _p, _p, _sz, _p]
+lib.hg_rmsnorm_bwd.restype = ctypes.c_int
+lib.hg_quantize_weights.argtypes = [_p, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p]
+lib.hg_quantize_weights.restype = ctypes.c_int
+lib.hg_dequantize_weights.argtypes = [_p, _p, _i32, _i32, _i32, _p, _i32, _p]
+lib.hg_dequantize_weights.restype = ctypes.c_int
+lib.hg_grouped_wgrad_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
+lib.hg_grouped_wgrad_workspace_bytes.restype = _sz
+lib.hg_grouped_wgrad.argtypes = [_p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p, _i32, _p, _sz, _p]
+lib.hg_grouped_wgrad.restype = ctypes.c_int
+lib.hg_grouped_wgrad_fp8.argtypes = [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p, _i32, _p,
+                                     _sz, _p]
+lib.hg_grouped_wgrad_fp8.restype = ctypes.c_int
+
 HG_OK = 0
 HG_ERR_INVALID_ARG = 1
 HG_ERR_UNSUPPORTED_SHAPE = 2
@@ -492,6 +512,182 @@ def hg_router_topk_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, topk_weight
          topk_ids.data_ptr(), topk_weights.data_ptr(), dweights.data_ptr(), M, E, k,
          int(renormalize), dlogits.data_ptr())
     return dlogits
+
+
+def hg_dispatch_acts(a_fp8: torch.Tensor, a_scale: torch.Tensor, top_k: int,
+                     src_to_sorted: torch.Tensor, out_fp8=None, out_scale=None, stream=None):
+    """(a_fp8 [M*top_k, K], a_scale [M*top_k, K/128]) in the plan's order, of 8-bit tokens
+    (a_fp8 [M, K], a_scale [M, K/128]).  Rows that no entry names are not written."""
+    M, K = a_fp8.shape
+    assert a_fp8.dtype == _U8 and a_fp8.is_contiguous()
+    assert a_scale.dtype == _U8 and a_scale.shape == (M, K // 128) and a_scale.is_contiguous()
+    assert src_to_sorted.dtype == _I32 and src_to_sorted.numel() == M * top_k
+    assert src_to_sorted.is_contiguous()
+    device = _device(a_fp8, a_scale, src_to_sorted)
+    out_fp8 = _out(out_fp8, (M * top_k, K), _U8, a_fp8, stream)
+    out_scale = _out(out_scale, (M * top_k, K // 128), _U8, a_fp8, stream)
+    _run(lib.hg_dispatch_acts, "hg_dispatch_acts", device, stream, a_fp8.data_ptr(),
+         a_scale.data_ptr(), src_to_sorted.data_ptr(), M, top_k, K, out_fp8.data_ptr(),
+         out_scale.data_ptr())
+    return out_fp8, out_scale
+
+
+def hg_rmsnorm_quantize(x_bf16: torch.Tensor, gain: torch.Tensor, residual=None,
+                        eps: float = 1e-6, plain: bool = True, codes: bool = True,
+                        checkpoint: bool = True, y=None, a_fp8=None, a_scale=None, summed=None,
+                        rstd=None, stream=None):
+    """Root-mean-square norm of s = x + residual (of x without a residual), times gain [D]:
+    (y, a_fp8, a_scale, summed, rstd) with y BF16 [M, D] (`plain`), the same in 8 bits
+    (`codes`), s as BF16 (with a residual) and 1/rms [M] for hg_rmsnorm_bwd (`checkpoint`);
+    None in the places of what is not asked for."""
+    M, D = x_bf16.shape
+    assert x_bf16.dtype == _BF16 and x_bf16.is_contiguous()
+    assert gain.dtype == _BF16 and gain.shape == (D,) and gain.is_contiguous()
+    device = _device(x_bf16, gain, residual)
+    if residual is not None:
+        assert residual.dtype == _BF16 and residual.shape == (M, D) and residual.is_contiguous()
+        summed = _out(summed, (M, D), _BF16, x_bf16, stream)
+    else:
+        assert summed is None
+    if plain:
+        y = _out(y, (M, D), _BF16, x_bf16, stream)
+    else:
+        assert y is None
+    if codes:
+        a_fp8 = _out(a_fp8, (M, D), _U8, x_bf16, stream)
+        a_scale = _out(a_scale, (M, D // 128), _U8, x_bf16, stream)
+    else:
+        assert a_fp8 is None and a_scale is None
+    if checkpoint:
+        rstd = _out(rstd, (M,), _F32, x_bf16, stream)
+    else:
+        assert rstd is None
+    _run(lib.hg_rmsnorm_quantize, "hg_rmsnorm_quantize", device, stream, x_bf16.data_ptr(),
+         _addr(residual), gain.data_ptr(), M, D, eps, _addr(summed), _addr(y), _addr(a_fp8),
+         _addr(a_scale), _addr(rstd))
+    return y, a_fp8, a_scale, summed, rstd
+
+
+def _workspace(given, need, like, stream):
+    """The caller's workspace, checked, or a new one of `need` bytes; None where none is needed."""
+    if given is not None:
+        assert given.is_contiguous() and given.numel() * given.element_size() >= need
+        assert given.get_device() == like.get_device(), "tensors must be on the same GPU"
+        return given, given.numel() * given.element_size()
+    return (_out(None, (need,), _U8, like, stream) if need else None), need
+
+
+def hg_rmsnorm_bwd_workspace_bytes(M: int, D: int) -> int:
+    return int(lib.hg_rmsnorm_bwd_workspace_bytes(M, D))
+
+
+def hg_rmsnorm_bwd(dy: torch.Tensor, summed: torch.Tensor, gain: torch.Tensor,
+                   rstd: torch.Tensor, dsum=None, want_dgain: bool = True, dx=None, dgain=None,
+                   workspace=None, stream=None):
+    """Gradient of hg_rmsnorm_quantize: (dx [M, D] BF16, of x and of the residual alike, dgain
+    [D] float32, or None without `want_dgain`).  summed: what the norm was taken of; dsum: what
+    reaches it by other ways."""
+    M, D = dy.shape
+    for t in (dy, summed, dsum):
+        assert t is None or (t.dtype == _BF16 and t.shape == (M, D) and t.is_contiguous())
+    assert gain.dtype == _BF16 and gain.shape == (D,) and gain.is_contiguous()
+    assert rstd.dtype == _F32 and rstd.shape == (M,) and rstd.is_contiguous()
+    device = _device(dy, summed, gain, rstd, dsum)
+    dx = _out(dx, (M, D), _BF16, dy, stream)
+    size = 0
+    if want_dgain:
+        dgain = _out(dgain, (D,), _F32, dy, stream)
+        need = lib.hg_rmsnorm_bwd_workspace_bytes(M, D)
+        workspace, size = _workspace(workspace, need, dy, stream)
+    else:
+        assert dgain is None
+    _run(lib.hg_rmsnorm_bwd, "hg_rmsnorm_bwd", device, stream, dy.data_ptr(), _addr(dsum),
+         summed.data_ptr(), gain.data_ptr(), rstd.data_ptr(), M, D, dx.data_ptr(), _addr(dgain),
+         _addr(workspace), size)
+    return dx, dgain
+
+
+def hg_quantize_weights(w: torch.Tensor, transposed: bool = False, w_fp4=None, w_scale=None,
+                        wt_fp4=None, wt_scale=None, stream=None):
+    """BF16 or float32 weights [E, N, K] as the GEMM's: (w_fp4 [E, N, K/2], w_scale [E, N, K/32],
+    wt_fp4 [E, K, N/2], wt_scale [E, K, N/32]); the last two, the weights of the transposed
+    product, only with `transposed`, else None."""
+    E, N, K = w.shape
+    assert w.dtype in (_BF16, _F32) and w.is_contiguous()
+    device = _device(w)
+    w_fp4 = _out(w_fp4, (E, N, K // 2), _U8, w, stream)
+    w_scale = _out(w_scale, (E, N, K // 32), _U8, w, stream)
+    if transposed:
+        wt_fp4 = _out(wt_fp4, (E, K, N // 2), _U8, w, stream)
+        wt_scale = _out(wt_scale, (E, K, N // 32), _U8, w, stream)
+    else:
+        assert wt_fp4 is None and wt_scale is None
+    _run(lib.hg_quantize_weights, "hg_quantize_weights", device, stream, w.data_ptr(),
+         int(w.dtype == _F32), E, N, K, w_fp4.data_ptr(), w_scale.data_ptr(), _addr(wt_fp4),
+         _addr(wt_scale))
+    return w_fp4, w_scale, wt_fp4, wt_scale
+
+
+def hg_dequantize_weights(w_fp4: torch.Tensor, w_scale: torch.Tensor, dtype=torch.bfloat16,
+                          out=None, stream=None) -> torch.Tensor:
+    """The numbers [E, N, K] that 4-bit weights stand for, as BF16 or float32."""
+    E, N, K2 = w_fp4.shape
+    assert dtype in (_BF16, _F32)
+    assert w_fp4.dtype == _U8 and w_fp4.is_contiguous()
+    assert w_scale.dtype == _U8 and w_scale.shape == (E, N, K2 // 16) and w_scale.is_contiguous()
+    device = _device(w_fp4, w_scale)
+    out = _out(out, (E, N, 2 * K2), dtype, w_fp4, stream)
+    _run(lib.hg_dequantize_weights, "hg_dequantize_weights", device, stream, w_fp4.data_ptr(),
+         w_scale.data_ptr(), E, N, 2 * K2, out.data_ptr(), int(dtype == _F32))
+    return out
+
+
+def hg_grouped_wgrad_workspace_bytes(E: int, N: int, K: int, rows: int) -> int:
+    return int(lib.hg_grouped_wgrad_workspace_bytes(E, N, K, rows))
+
+
+def _grouped_wgrad(fn, what, dy, x, x_scale, expert_offsets, dtype, dw, accumulate, workspace,
+                   stream):
+    rows, N = dy.shape
+    K = x.shape[1]
+    E = expert_offsets.numel() - 1
+    assert dy.dtype == _BF16 and dy.is_contiguous()
+    assert x.shape[0] == rows and x.is_contiguous()
+    assert expert_offsets.dtype == _I32 and expert_offsets.is_contiguous()
+    if dw is not None:
+        dtype = dw.dtype
+    assert dtype in (_BF16, _F32)
+    assert not accumulate or dw is not None, "accumulate adds to a dw that is given"
+    device = _device(dy, x, x_scale, expert_offsets)
+    dw = _out(dw, (E, N, K), dtype, dy, stream)
+    need = lib.hg_grouped_wgrad_workspace_bytes(E, N, K, rows)
+    workspace, size = _workspace(workspace, need, dy, stream)
+    args = (dy.data_ptr(), x.data_ptr(), *(() if x_scale is None else (x_scale.data_ptr(),)))
+    _run(fn, what, device, stream, *args, expert_offsets.data_ptr(), E, N, K, rows,
+         int(accumulate), dw.data_ptr(), int(dtype == _F32), _addr(workspace), size)
+    return dw
+
+
+def hg_grouped_wgrad(dy: torch.Tensor, x_bf16: torch.Tensor, expert_offsets: torch.Tensor,
+                     dtype=torch.float32, dw=None, accumulate: bool = False, workspace=None,
+                     stream=None) -> torch.Tensor:
+    """dw[e] (+)= dy[off[e]:off[e+1]]^T x[off[e]:off[e+1]]: [E, N, K] of BF16 dy [rows, N] and
+    x [rows, K], in `dtype` (float32 or BF16) or the type of a given dw."""
+    assert x_bf16.dtype == _BF16
+    return _grouped_wgrad(lib.hg_grouped_wgrad, "hg_grouped_wgrad", dy, x_bf16, None,
+                          expert_offsets, dtype, dw, accumulate, workspace, stream)
+
+
+def hg_grouped_wgrad_fp8(dy: torch.Tensor, a_fp8: torch.Tensor, a_scale: torch.Tensor,
+                         expert_offsets: torch.Tensor, dtype=torch.float32, dw=None,
+                         accumulate: bool = False, workspace=None, stream=None) -> torch.Tensor:
+    """hg_grouped_wgrad with x as the forward product had it: E4M3 codes [rows, K] and E8M0
+    scales [rows, K/128]."""
+    rows, K = a_fp8.shape
+    assert a_fp8.dtype == _U8
+    assert a_scale.dtype == _U8 and a_scale.shape == (rows, K // 128) and a_scale.is_contiguous()
+    return _grouped_wgrad(lib.hg_grouped_wgrad_fp8, "hg_grouped_wgrad_fp8", dy, a_fp8, a_scale,
+                          expert_offsets, dtype, dw, accumulate, workspace, stream)
 
 
 def hg_get_device_status(stream=None):

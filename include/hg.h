@@ -323,8 +323,8 @@ hg_status hg_combine_topk(const uint16_t* y_bf16, const int32_t* src_to_sorted,
 /* ----------------------------------- tokens by expert, and gradients -- */
 
 /*
- * This section and the three after it hold the operators of an MoE layer
- * around the plan and the GEMM.  Each call is one kernel, launched with
+ * This section and the six after it hold the operators of an MoE layer
+ * around the plan and the GEMM.  Each call is one kernel (or the two it names), launched with
  * programmatic dependent launch: its blocks may start while the kernel before
  * on `stream` drains, and read and write nothing until that has completed, so
  * stream order holds as with a plain launch.  All of them can be captured
@@ -350,6 +350,25 @@ hg_status hg_combine_topk(const uint16_t* y_bf16, const int32_t* src_to_sorted,
 hg_status hg_dispatch_tokens(const uint16_t* x_bf16, const int32_t* src_to_sorted,
                              const float* topk_weights, int32_t M, int32_t top_k, int32_t K,
                              uint16_t* rows_bf16, hg_stream_t stream);
+
+/*
+ * 8-bit token rows with their scales copied into the plan's sorted order, as they
+ * are (from hg_rmsnorm_quantize, say; hg_quantize_scatter_acts makes them from BF16
+ * on the way):
+ *
+ *   rows_fp8[src_to_sorted[t*top_k + j], :] = a_fp8[t, :], rows_scale the same
+ *
+ *   a_fp8          uint8 [M, K], 16-byte aligned; a_scale uint8 [M, K/128].
+ *   src_to_sorted  int32 [M*top_k] from hg_plan_expert_offsets; entries outside
+ *                  [0, M*top_k) are skipped (ids the plan dropped are -1).
+ *   rows_fp8       uint8 [M*top_k, K] out, 16-byte aligned; rows_scale uint8
+ *                  [M*top_k, K/128] out; rows no entry names are not written.
+ * K % 128 == 0, K <= 2^30.  Every token is read once.  One kernel on `stream`; no host
+ * synchronisation.
+ */
+hg_status hg_dispatch_acts(const uint8_t* a_fp8, const uint8_t* a_scale,
+                           const int32_t* src_to_sorted, int32_t M, int32_t top_k, int32_t K,
+                           uint8_t* rows_fp8, uint8_t* rows_scale, hg_stream_t stream);
 
 /*
  * Gradient of hg_dispatch_tokens (and of hg_quantize_scatter_acts, taken as
@@ -535,6 +554,140 @@ hg_status hg_router_topk_bwd(const float* logits, const int32_t* topk_ids,
                              int32_t E, int32_t top_k, int32_t renormalize, float* dlogits,
                              hg_stream_t stream);
 
+/* --------------------------------------------- gradient of the weights -- */
+
+/*
+ * Gradient of the experts' weights for out = x W^T by rows sorted by expert, the rows
+ * of expert e being [off[e], off[e+1]):
+ *
+ *   dw[e, n, k] = (accumulate ? dw[e, n, k] : 0) + sum_r dy[r, n] * x[r, k]
+ *
+ *   dy_bf16         uint16 [rows, N] BF16, 16-byte aligned.
+ *   x_bf16          uint16 [rows, K] BF16, 16-byte aligned.
+ *   expert_offsets  int32 [E+1] device, as for hg_grouped_w4a8_gemm.
+ *   dw              FP32 (dw_f32 != 0) or BF16 [E, N, K], 16-byte aligned.  An expert
+ *                   without rows gets zeros, or keeps its dw when accumulating.
+ *                   accumulate needs an FP32 dw; sums that are FP32's subnormals may
+ *                   count as 0 there.
+ *   workspace       device scratch of hg_grouped_wgrad_workspace_bytes(E, N, K, rows)
+ *                   bytes, 16-byte aligned (NULL where that is 0): few tiles of dw are
+ *                   cut along the rows, and the parts added in order by a second kernel.
+ *                   One call at a time may use it.
+ * N % 8 == 0, K % 8 == 0, E in [1, 512].  Rows outside [off[0], off[E]) are not read
+ * into any sum, whatever they hold.  Sums are FP32; the result does not vary from run to
+ * run.  Offsets that are not monotone or exceed rows are detected on the device: the
+ * affected experts count as having no rows, and HG_ERR_BAD_OFFSETS is recorded for
+ * hg_get_device_status.  One or two kernels on `stream`, launched with programmatic
+ * dependent launch as the section above says; no host synchronisation.
+ */
+size_t hg_grouped_wgrad_workspace_bytes(int32_t E, int32_t N, int32_t K, int32_t rows);
+hg_status hg_grouped_wgrad(const uint16_t* dy_bf16, const uint16_t* x_bf16,
+                           const int32_t* expert_offsets, int32_t E, int32_t N, int32_t K,
+                           int32_t rows, int32_t accumulate, void* dw, int32_t dw_f32,
+                           void* workspace, size_t workspace_bytes, hg_stream_t stream);
+
+/*
+ * The same with x as the forward product had it:
+ *
+ *   a_fp8    uint8 [rows, K] E4M3 codes, 16-byte aligned; a_scale uint8 [rows, K/128].
+ * K % 128 == 0.  Codes times scales are taken as BF16, which is exact within BF16's
+ * range.  Scale code 255 is NaN; NaN codes under another scale are not supported inputs,
+ * as for the GEMM.
+ */
+hg_status hg_grouped_wgrad_fp8(const uint16_t* dy_bf16, const uint8_t* a_fp8,
+                               const uint8_t* a_scale, const int32_t* expert_offsets, int32_t E,
+                               int32_t N, int32_t K, int32_t rows, int32_t accumulate, void* dw,
+                               int32_t dw_f32, void* workspace, size_t workspace_bytes,
+                               hg_stream_t stream);
+
+/* ---------------------------------------------------- 4-bit weights -- */
+
+/*
+ * BF16 or FP32 weights as the GEMM's MXFP4 weights, and in the same pass as the weights
+ * of the transposed product, for the gradient of the activations.  Per group of 32
+ * weights, along K for (w_fp4, w_scale) and along N for (wt_fp4, wt_scale):
+ *
+ *   e     = the smallest integer with amax <= 6 * 2^e (amax = 0 gives e = 0), in [-127, 127]
+ *   scale = 127 + e (E8M0); code = E2M1 round-to-nearest of w / 2^e, ties to the even code
+ *
+ * A group holding an Inf or NaN gets scale code 255 (NaN) and element codes 0.
+ *
+ *   w         FP32 (w_f32 != 0) or BF16 [E, N, K], 16-byte aligned.
+ *   w_fp4     uint8 [E, N, K/2] out, 16-byte aligned; w_scale uint8 [E, N, K/32] out.
+ *   wt_fp4    uint8 [E, K, N/2] out, 16-byte aligned, and wt_scale uint8 [E, K, N/32]
+ *             out; both NULL for no transposed copy.
+ * K % 32 == 0, with the transposed copy N % 32 == 0 (hg_grouped_w4a8_gemm takes multiples
+ * of 128); E*N below 2^31.  One kernel on `stream`, launched with programmatic dependent
+ * launch; no host synchronisation.
+ */
+hg_status hg_quantize_weights(const void* w, int32_t w_f32, int32_t E, int32_t N, int32_t K,
+                              uint8_t* w_fp4, uint8_t* w_scale, uint8_t* wt_fp4,
+                              uint8_t* wt_scale, hg_stream_t stream);
+
+/*
+ * 4-bit weights as numbers: w[e, n, k] = E2M1(code) * 2^(scale - 127), NaN for scale code
+ * 255; Inf where that passes the range of w's type, otherwise exact.
+ *
+ *   w   FP32 (w_f32 != 0) or BF16 [E, N, K] out, 16-byte aligned; w_fp4 16-byte aligned.
+ * K % 32 == 0, E*N below 2^31.  One kernel on `stream`; no host synchronisation.
+ */
+hg_status hg_dequantize_weights(const uint8_t* w_fp4, const uint8_t* w_scale, int32_t E, int32_t N,
+                                int32_t K, void* w, int32_t w_f32, hg_stream_t stream);
+
+/* ---------------------------------------------------------------- norm -- */
+
+/*
+ * Root-mean-square norm of the residual stream, with the addition before it:
+ *
+ *   s[m, :] = bf16_rne( x[m, :] + residual[m, :] )       (FP32 sum; s = x without a residual)
+ *   r[m]    = 1 / sqrt( mean(s[m, :]^2) + eps )
+ *   v[m, d] = s[m, d] * r[m] * gain[d]                   (FP32)
+ *   y = bf16_rne(v);  (a_fp8, a_scale) = v in E4M3 with one E8M0 scale per 128 elements, by
+ *   the rule of hg_quantize_gather_acts, from FP32 without a BF16 rounding between.
+ *
+ *   x_bf16         uint16 [M, D]; residual_bf16 uint16 [M, D], or NULL; gain_bf16 uint16 [D];
+ *                  all 16-byte aligned.
+ *   eps            in [1e-30, 1e30].
+ *   sum_bf16       uint16 [M, D] out, 16-byte aligned: s, with a residual; else NULL.  May
+ *                  be x_bf16 or residual_bf16 itself.
+ *   y_bf16         uint16 [M, D] out, 16-byte aligned, or NULL.  May be x_bf16 when there
+ *                  is a residual and sum_bf16 is not x_bf16.
+ *   a_fp8          uint8 [M, D] out, 16-byte aligned, and a_scale uint8 [M, D/128] out; or
+ *                  both NULL.
+ *   rstd           float32 [M] out: r, for hg_rmsnorm_bwd; or NULL.
+ * D % 8 == 0 (with codes D % 128 == 0), D <= 16384.  The row of a token that holds an Inf
+ * has r = 0, one that holds a NaN r = NaN.  One kernel on `stream`; no host synchronisation.
+ */
+hg_status hg_rmsnorm_quantize(const uint16_t* x_bf16, const uint16_t* residual_bf16,
+                              const uint16_t* gain_bf16, int32_t M, int32_t D, float eps,
+                              uint16_t* sum_bf16, uint16_t* y_bf16, uint8_t* a_fp8,
+                              uint8_t* a_scale, float* rstd, hg_stream_t stream);
+
+/*
+ * Gradient of hg_rmsnorm_quantize (the codes taken as the identity), with n = s r and
+ * u[m, d] = r[m] * dy[m, d] * gain[d]:
+ *
+ *   dx[m, d] = bf16_rne( dsum[m, d] + u[m, d] - n[m, d] * mean(u[m, :] n[m, :]) )
+ *   dgain[d] = sum_m dy[m, d] * n[m, d]                  (FP32)
+ *
+ * dx is the gradient of x and of the residual alike; dsum is what reaches s by other ways.
+ *
+ *   dy_bf16    uint16 [M, D]; dsum_bf16 uint16 [M, D], or NULL; sum_bf16 uint16 [M, D]: s
+ *              (x without a residual); gain_bf16 uint16 [D]; all 16-byte aligned.
+ *   rstd       float32 [M] from hg_rmsnorm_quantize.
+ *   dx_bf16    uint16 [M, D] out, 16-byte aligned.  May be dy_bf16, dsum_bf16 or sum_bf16.
+ *   dgain      float32 [D] out, or NULL.
+ *   workspace  with dgain: device scratch of hg_rmsnorm_bwd_workspace_bytes(M, D) bytes,
+ *              16-byte aligned; else NULL.  One call at a time may use it.
+ * D % 8 == 0, D <= 16384.  One kernel on `stream`, with dgain two; the result does not vary
+ * from run to run.  No host synchronisation.
+ */
+size_t hg_rmsnorm_bwd_workspace_bytes(int32_t M, int32_t D);
+hg_status hg_rmsnorm_bwd(const uint16_t* dy_bf16, const uint16_t* dsum_bf16,
+                         const uint16_t* sum_bf16, const uint16_t* gain_bf16, const float* rstd,
+                         int32_t M, int32_t D, uint16_t* dx_bf16, float* dgain, void* workspace,
+                         size_t workspace_bytes, hg_stream_t stream);
+
 /* ------------------------------------------------- from host buffers -- */
 
 /*
@@ -605,7 +758,8 @@ hg_status hg_get_device_status(hg_stream_t stream, uint32_t* detail);
 hg_status hg_selftest_wait_timeout(uint32_t timeout_us, hg_stream_t stream);
 
 /*
- * Per-wait limit of the GEMM's and the few-token product's waits in microseconds (default
+ * Per-wait limit of the waits of the GEMM, the few-token product and the gradient of the weights
+ * in microseconds (default
  * 1000000).  Host-side setting, applied to later launches.  0 restores the
  * default.
  */

@@ -32,6 +32,8 @@ Modules:
 
 * ``moe_layer`` -- dispatch and combine with gradients, SwiGLU with its 8-bit
   checkpoint, the few-token expert product, the router's gate, in float64.
+* ``expert_training`` -- the gradient of the weights, MXFP4 quantisation and
+  back, the RMS norm with its gradient, 8-bit rows by expert, in float64.
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against facts
 fixed independently of this code (exhaustive decode against closed forms and
