@@ -44,27 +44,31 @@ constexpr int kChunk = 8;
 
 template <bool kFp8>
 struct Cfg {
-    static constexpr int kWorkers = kFp8 ? 4 : 1;
+    static constexpr int kWorkers = kFp8 ? 4 : 1;        // warps that work on one stage
+    static constexpr int kGroups = kFp8 ? 2 : 1;         // of them, taking stages in turn
     static constexpr int kFirstWorker = kFp8 ? 12 : 2;
-    static constexpr int kThreads = 32 * (kFp8 ? 16 : 12);
-    static constexpr int kStages = kFp8 ? 4 : 5;
-    static constexpr int kOutBufs = 2;                   // per epilogue warp
+    static constexpr int kThreads = 32 * (kFp8 ? 20 : 12);
+    static constexpr int kStages = kFp8 ? 4 : 6;
     static constexpr int kRaw = kFp8 ? kWgradRows * kHalf : 0;
+    static constexpr int kFactors = kFp8 ? (2 * kWgradRows + 4) * 4 : 0;
     static constexpr int kTx = kOperand + (kFp8 ? kRaw : kOperand);
     static constexpr int kOffA = 0;
     static constexpr int kOffB = kOffA + kStages * kOperand;
     static constexpr int kOffRaw = kOffB + kStages * kOperand;
     static constexpr int kOffOut = kOffRaw + kStages * kRaw;
-    static constexpr int kOffBar = kOffOut + kEpiWarps * kOutBufs * kOutBuf;
+    static constexpr int kOffFactors = kOffOut + kEpiWarps * kOutBuf;
+    static constexpr int kOffBar = kOffFactors + kStages * kFactors;
     static constexpr int kOffMisc = kOffBar + 8 * (3 * kStages + 5);
     static constexpr int kSmem = kOffMisc + 16 + 1024;   // with room to align to 1024
     static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
     // registers of a thread by role: their sum over the warpgroups is the launch's
-    static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
-    static constexpr int kControlRegs = kFp8 ? 56 : 88;
-    static constexpr int kEpiRegs = kFp8 ? 176 : 208;
-    static constexpr int kWorkerRegs = kFp8 ? 104 : 0;
-    static_assert(kControlRegs + 2 * kEpiRegs + kWorkerRegs <= kLaunchRegs * kThreads / 128, "");
+    static constexpr int kLaunchRegs = kFp8 ? 96 : 168;
+    static constexpr int kControlRegs = kFp8 ? 48 : 88;
+    static constexpr int kEpiRegs = kFp8 ? 168 : 208;
+    static constexpr int kWorkerRegs = kFp8 ? 48 : 0;
+    static_assert(kControlRegs + 2 * kEpiRegs + kGroups * kWorkerRegs <=
+                      kLaunchRegs * kThreads / 128,
+                  "setmaxnreg takes only what the launch has");
 };
 
 struct Shape {
@@ -75,13 +79,14 @@ struct Shape {
 struct Unit {
     int e, n0, k0, split, row0, rows;
     bool bad;
+    // u may be past the last unit: any expert's offsets are read then
     __device__ __forceinline__ Unit(const Shape& s, const int32_t* offsets, int u) {
         const int tn = u % s.tiles_n;
         u /= s.tiles_n;
         const int tk = u % s.tiles_k;
         u /= s.tiles_k;
         split = u % s.splits;
-        e = u / s.splits;
+        e = min(u / s.splits, s.E - 1);
         n0 = tn * kTile;
         k0 = tk * kTile;
         const int lo = ptx::load(offsets + e), hi = ptx::load(offsets + e + 1);
@@ -99,11 +104,25 @@ struct Unit {
     }
 };
 
-// Four E4M3 codes as BF16 pairs times 2^-120 (the exponent's bias is off by as much).
-__device__ __forceinline__ void e4m3_as_bf16(uint32_t w, uint32_t (&h)[2]) {
-    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
-    h[0] = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u);
-    h[1] = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+// Eight E4M3 codes as BF16 times f, a pair of BF16 2^120 times the scale: shifted into place
+// a code is its value times 2^-120 (the exponents' biases differ by as much; subnormal codes
+// become subnormal numbers).  The four words' steps stand in turn, so that none waits for
+// the one before.
+__device__ __forceinline__ uint4 e4m3x8_to_bf16(uint2 v, uint32_t f) {
+    uint4 o;
+    asm("{\n\t.reg .b32 a, b, c, d, p, q, r, s;\n\t"
+        "prmt.b32 a, %4, 0, 0x1404;\n\tprmt.b32 b, %4, 0, 0x3424;\n\t"
+        "prmt.b32 c, %5, 0, 0x1404;\n\tprmt.b32 d, %5, 0, 0x3424;\n\t"
+        "shr.b32 p, a, 4;\n\tshr.b32 q, b, 4;\n\tshr.b32 r, c, 4;\n\tshr.b32 s, d, 4;\n\t"
+        "and.b32 p, p, 0x07F007F0;\n\tand.b32 q, q, 0x07F007F0;\n\t"
+        "and.b32 r, r, 0x07F007F0;\n\tand.b32 s, s, 0x07F007F0;\n\t"
+        "lop3.b32 p, a, 0x80008000, p, 0xEA;\n\tlop3.b32 q, b, 0x80008000, q, 0xEA;\n\t"
+        "lop3.b32 r, c, 0x80008000, r, 0xEA;\n\tlop3.b32 s, d, 0x80008000, s, 0xEA;\n\t"
+        "mul.rn.bf16x2 %0, p, %6;\n\tmul.rn.bf16x2 %1, q, %6;\n\t"
+        "mul.rn.bf16x2 %2, r, %6;\n\tmul.rn.bf16x2 %3, s, %6;\n\t}"
+        : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+        : "r"(v.x), "r"(v.y), "r"(f));
+    return o;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -116,15 +135,6 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
                  "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
 // Clear rows [first, last) of an operand's stage (whole warp).
 __device__ __forceinline__ void clear_rows(uint32_t operand, int first, int last) {
     for (int i = threadIdx.x & 31; i < (last - first) * 16; i += 32) {
@@ -161,7 +171,7 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const ui
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_full + 8 * s, kFp8 ? 2 : 1);
             ptx::mbar_init(bar_ready + 8 * s, 2 * C::kWorkers);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
@@ -205,8 +215,10 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const ui
         const uint64_t policy = ptx::policy_evict_last();    // read again by other tiles
         uint32_t g = 0;
         bool ok = true;
+        Unit next(shape, offsets, first);
         for (int u = first; ok && u < units; u += pairs) {
-            const Unit t(shape, offsets, u);
+            const Unit t = next;
+            next = Unit(shape, offsets, u + pairs);
             if (t.bad && lane == 0) record_error(status, HG_ERR_BAD_OFFSETS, t.e);
             const int n = t.n0 + static_cast<int>(rank) * kHalf;
             const int k = t.k0 + static_cast<int>(rank) * kHalf;
@@ -244,8 +256,10 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const ui
             const uint32_t idesc = ptx::idesc_bf16_mnmajor(kTile, kTile);
             uint32_t g = 0, tc = 0;
             bool ok = true;
+            Unit next(shape, offsets, first);
             for (int u = first; ok && u < units; u += pairs) {
-                const Unit t(shape, offsets, u);
+                const Unit t = next;
+                next = Unit(shape, offsets, u + pairs);
                 const int stages = t.stages();
                 for (int s = 0; s < stages; ++s, ++g) {
                     const uint32_t b = tc & 1u, slot = g % kStages;
@@ -283,11 +297,10 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const ui
         constexpr int kCols = kF32 ? 32 : 64;            // 128 bytes of output
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t tempty = ptx::mapa_shared(bar_tempty, 0);
-        const uint32_t stage = sbase + C::kOffOut + (warp - 4) * C::kOutBufs * kOutBuf;
-        const uint32_t mine = lane * 128;
+        const uint32_t buf = sbase + C::kOffOut + (warp - 4) * kOutBuf;
         const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * kEpiCols;
         const bool add = accumulate && !parts;
-        uint32_t tc = 0, slab = 0;
+        uint32_t tc = 0;
         bool ok = true;
         for (int u = first; ok && u < units; u += pairs) {
             const Unit t(shape, offsets, u);
@@ -302,17 +315,20 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const ui
                 const uint32_t b = tc & 1u;
                 if (!(ok = wait(bar_tfull + 8 * b, (tc >> 1) & 1u, kRoleEpilogue, b))) break;
                 ptx::tc_fence_after();
+                if (s == 0) {
 #pragma unroll
-                for (int c = 0; c < kEpiCols; c += 32) {
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(from + b * kTile + c, v);
+                    for (int c = 0; c < kEpiCols; c += 16)
+                        ptx::tmem_ld_32x32b_x16(from + b * kTile + c,
+                                                reinterpret_cast<uint32_t(&)[16]>(sum[c]));
                     ptx::tmem_ld_wait();
-                    if (s == 0) {
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[c + i] = __uint_as_float(v[i]);
-                    } else {
+                    for (int c = 0; c < kEpiCols; c += 16) {
+                        uint32_t v[16];
+                        ptx::tmem_ld_32x32b_x16(from + b * kTile + c, v);
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(v[i]);
+                        for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
                     }
                 }
                 ptx::tc_fence_before();
@@ -326,18 +342,20 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const ui
 #pragma unroll
             for (int c = 0; c < kEpiCols; c += kCols) {
                 if (n >= shape.N || k + c >= shape.K) continue;
-                uint32_t v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = kF32 ? __float_as_uint(sum[c + i])
-                                : bf16_pack(sum[c + 2 * i % kCols], sum[c + 2 * i % kCols + 1]);
-                const uint32_t buf = stage + slab % C::kOutBufs * kOutBuf;
-                if (lane == 0) ptx::bulk_wait_group_read<C::kOutBufs - 1>();
+                if (lane == 0) ptx::bulk_wait_group_read<0>();
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sts_v4(buf + mine + ((i ^ (lane & 7)) << 4), v[4 * i], v[4 * i + 1],
-                           v[4 * i + 2], v[4 * i + 3]);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t to = buf + lane * 128 + ((i ^ (lane & 7)) << 4);
+                    const float* v = sum + c + i * (kCols / 8);
+                    if constexpr (kF32) {
+                        sts_v4(to, __float_as_uint(v[0]), __float_as_uint(v[1]),
+                               __float_as_uint(v[2]), __float_as_uint(v[3]));
+                    } else {
+                        sts_v4(to, bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3]),
+                               bf16_pack(v[4], v[5]), bf16_pack(v[6], v[7]));
+                    }
+                }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -348,91 +366,137 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const ui
                     }
                     ptx::bulk_commit_group();
                 }
-                ++slab;
             }
         }
         // every store has completed before the CTA can exit
         if (lane == 0) ptx::bulk_wait_group_all();
         __syncwarp();
-    } else if (warp >= C::kFirstWorker && warp < C::kFirstWorker + C::kWorkers) {
-        // ----------------------------------------------------- workers --
-        const int w = warp - C::kFirstWorker;
-        const uint32_t ready = ptx::mapa_shared(bar_ready, 0);
-        const int groups = shape.K / kHalf;              // scales of a row (FP8)
+    } else if (kFp8 && warp == 2) {
+        // ------------------------------------------------------ scales --
+        // One factor a row for the workers: 2^120 times the row's scale as a pair of BF16, in
+        // two factors where BF16 ends, and 0 for rows that are not the unit's.  The scales of
+        // four stages are asked for while those of the four before are handed over.
+        const int groups = shape.K / kHalf;
+        uint32_t* factors = reinterpret_cast<uint32_t*>(base + C::kOffFactors);
+        int u = first, s = 0;                            // the next stage to ask for
+        Unit t(shape, offsets, u);
+        constexpr uint32_t kNone = 256u;
+        uint32_t now[8], later[8];
+        auto ask = [&](uint32_t (&code)[8]) {            // how many stages were left
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                code[2 * i] = code[2 * i + 1] = kNone;
+                while (u < units && s >= t.stages()) {
+                    u += pairs;
+                    s = 0;
+                    t = Unit(shape, offsets, u);
+                }
+                if (u >= units) continue;
+                const int group = (t.k0 >> 7) + static_cast<int>(rank);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = s * kWgradRows + 32 * h + lane;
+                    if (r < t.rows && group < groups)
+                        code[2 * i + h] =
+                            ptx::load(x_scale + static_cast<long long>(t.row0 + r) * groups + group);
+                }
+                ++s;
+                ++n;
+            }
+            return n;
+        };
+        int n = ask(now);
         uint32_t g = 0;
         bool ok = true;
+        while (ok && n > 0) {
+            const int more = ask(later);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i >= n) break;
+                const uint32_t slot = g % kStages;
+                if (!(ok = wait(bar_empty + 8 * slot, ((g / kStages) & 1u) ^ 1u, kRoleScale, slot)))
+                    break;
+                uint32_t* to = factors + slot * (C::kFactors / 4);
+                bool wide = false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t code = now[2 * i + h];
+                    const uint32_t one = code == 255u ? 0x7FC0u : (min(code, 134u) + 120u) << 7;
+                    const bool over = code > 134u && code < 255u;
+                    const uint32_t two = (over ? code - 7u : 127u) << 7;
+                    to[32 * h + lane] = code == kNone ? 0u : one * 0x10001u;
+                    to[kWgradRows + 32 * h + lane] = two * 0x10001u;
+                    wide |= over;
+                }
+                wide = __any_sync(0xFFFFFFFFu, wide);
+                if (lane == 0) to[2 * kWgradRows] = wide;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_full + 8 * slot);
+                ++g;
+            }
+            n = more;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) now[i] = later[i];
+        }
+    } else if (warp >= C::kFirstWorker && warp < C::kFirstWorker + C::kWorkers * C::kGroups) {
+        // ----------------------------------------------------- workers --
+        const int w = (warp - C::kFirstWorker) % C::kWorkers;
+        const uint32_t turn = (warp - C::kFirstWorker) / C::kWorkers;
+        const uint32_t ready = ptx::mapa_shared(bar_ready, 0);
+        // FP8: this warp's 16 rows of a stage two at a time, a lane eight codes of one
+        const int row0 = kMmaRows * w + (lane >> 4);
+        const uint32_t from = row0 * kHalf + (lane & 15) * 8;
+        const uint32_t to = ((lane >> 3) & 1) * kPanel + row0 * 128;
+        uint32_t g = 0;
+        bool ok = true;
+        Unit next(shape, offsets, first);
         for (int u = first; ok && u < units; u += pairs) {
-            const Unit t(shape, offsets, u);
-            const int group = (t.k0 >> 7) + static_cast<int>(rank);
-            for (int s = 0; s < t.stages(); ++s, ++g) {
+            const Unit t = next;
+            next = Unit(shape, offsets, u + pairs);
+            const int stages = t.stages();
+            for (int s = 0; s < stages; ++s, ++g) {
+                if (C::kGroups > 1 && g % C::kGroups != turn) continue;
                 const uint32_t slot = g % kStages;
                 const uint32_t a = sbase + C::kOffA + slot * kOperand;
-                const uint32_t b = sbase + C::kOffB + slot * kOperand;
                 const int valid = t.valid(s);
                 const int used = (valid + kMmaRows - 1) / kMmaRows * kMmaRows;
+                if (!(ok = wait(bar_full + 8 * slot, (g / kStages) & 1u, kRoleWorker, slot))) break;
                 if constexpr (kFp8) {
-                    // this warp's 16 rows, four at a time, eight lanes a row
-                    const int r0 = kMmaRows * w + (lane >> 3), c = lane & 7;
-                    uint32_t code[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + 4 * i;
-                        code[i] = 127u;
-                        if (r < valid && group < groups)
-                            code[i] = ptx::load(
-                                x_scale + static_cast<long long>(t.row0 + s * kWgradRows + r) *
-                                              groups + group);
-                    }
-                    if (!(ok = wait(bar_full + 8 * slot, (g / kStages) & 1u, kRoleWorker, slot)))
-                        break;
                     if (kMmaRows * w < used) {
-                        const uint32_t raw = sbase + C::kOffRaw + slot * C::kRaw;
+                        const uint8_t* raw = base + C::kOffRaw + slot * C::kRaw + from;
+                        uint8_t* out = base + C::kOffB + slot * kOperand + to;
+                        const uint32_t* factor = reinterpret_cast<const uint32_t*>(
+                                                     base + C::kOffFactors + slot * C::kFactors) + row0;
+                        const bool wide = factor[2 * kWgradRows - row0] != 0u;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = r0 + 4 * i;
-                            const uint4 v = lds_v4(raw + r * kHalf + 16 * c);
-                            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                            // 2^120 times the scale, in two factors where BF16 ends
-                            const uint32_t one = code[i] == 255u ? 0x7FC0u
-                                                                 : (min(code[i], 134u) + 120u) << 7;
-                            const uint32_t f1 = one * 0x10001u;
-                            const bool wide = code[i] > 134u;
-                            const uint32_t f2 = ((max(code[i], 134u) - 7u) << 7) * 0x10001u;
-                            uint32_t out[8];
+                        for (int i0 = 0; i0 < 8; i0 += 4) {
+                            uint2 v[4];
+                            uint32_t f[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t h[2];
-                                e4m3_as_bf16(in[j], h);
-                                out[2 * j] = mul_bf16x2(h[0], f1);
-                                out[2 * j + 1] = mul_bf16x2(h[1], f1);
+                            for (int i = 0; i < 4; ++i) {
+                                v[i] = *reinterpret_cast<const uint2*>(raw + 2 * (i0 + i) * kHalf);
+                                f[i] = factor[2 * (i0 + i)];
                             }
-                            if (wide) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) out[j] = mul_bf16x2(out[j], f2);
+                            for (int i = 0; i < 4; ++i) {
+                                uint4 o = e4m3x8_to_bf16(v[i], f[i]);
+                                if (wide) {
+                                    const uint32_t f2 = factor[kWgradRows + 2 * (i0 + i)];
+                                    o = make_uint4(mul_bf16x2(o.x, f2), mul_bf16x2(o.y, f2),
+                                                   mul_bf16x2(o.z, f2), mul_bf16x2(o.w, f2));
+                                }
+                                // row 2i + lane / 16 of 16, its chunk swizzled by the row mod 8
+                                const int chunk = (lane & 7) ^ ((2 * i + (lane >> 4)) & 7);
+                                *reinterpret_cast<uint4*>(out + 256 * (i0 + i) + (chunk << 4)) = o;
                             }
-                            if (r >= valid) {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) out[j] = 0u;
-                            }
-                            // two 16-byte chunks; lanes of the second panel start with the
-                            // odd one, so that a row's eight lanes meet all banks
-                            const uint32_t to = b + (c >> 2) * kPanel + r * 128;
-                            const int chunk = 2 * (c & 3), odd = c >> 2;
-                            const uint32_t* p = out;
-                            const int c0 = (chunk + odd) ^ (r & 7), c1 = (chunk + 1 - odd) ^ (r & 7);
-                            sts_v4(to + (c0 << 4), odd ? p[4] : p[0], odd ? p[5] : p[1],
-                                   odd ? p[6] : p[2], odd ? p[7] : p[3]);
-                            sts_v4(to + (c1 << 4), odd ? p[0] : p[4], odd ? p[1] : p[5],
-                                   odd ? p[2] : p[6], odd ? p[3] : p[7]);
                         }
-                        const int from = max(valid, kMmaRows * w);
-                        clear_rows(a, from, max(from, min(used, kMmaRows * (w + 1))));
+                        if (valid < kMmaRows * (w + 1))
+                            clear_rows(a, max(valid, kMmaRows * w), min(used, kMmaRows * (w + 1)));
                     }
-                } else {
-                    if (!(ok = wait(bar_full + 8 * slot, (g / kStages) & 1u, kRoleWorker, slot)))
-                        break;
+                } else if (valid < used) {
                     clear_rows(a, valid, used);
-                    clear_rows(b, valid, used);
+                    clear_rows(sbase + C::kOffB + slot * kOperand, valid, used);
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
