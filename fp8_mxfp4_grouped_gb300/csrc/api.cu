@@ -32,6 +32,11 @@ bool weight_shape(int32_t E, int32_t N, int32_t K) {
     return static_cast<long long>(E) * N * (K / 32) <= 1ll << 36;
 }
 
+// An FP8 operand of the weight gradient as BF16.
+size_t wgrad_decoded_bytes(int32_t K, int32_t rows) {
+    return sizeof(uint16_t) * static_cast<size_t>(K) * static_cast<size_t>(rows);
+}
+
 struct DeviceInfo {
     bool ready = false;
     int num_sms = 0;
@@ -256,12 +261,11 @@ hg_status out_map(PFN_cuTensorMapEncodeTiled_v12000 encode, uint16_t* out, int32
     return HG_OK;
 }
 
-// The weight gradient's operands and result as matrices [matrices, rows, cols], boxes of
-// `box_rows` x `box_cols`.  Encoded at every call.
+// The weight gradient's operands and result as matrices [matrices, rows, cols], 128-byte
+// swizzle, boxes of `box_rows` x `box_cols`.  Encoded at every call.
 hg_status matrix_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMapDataType type, int bytes,
                      const void* p, long long matrices, int32_t rows, int32_t cols,
-                     uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle,
-                     CUtensorMap* out) {
+                     uint32_t box_rows, uint32_t box_cols, CUtensorMap* out) {
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                           static_cast<cuuint64_t>(matrices)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * bytes,
@@ -269,12 +273,14 @@ hg_status matrix_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMapDataTy
     cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return encode(out, type, 3, const_cast<void*>(p), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? HG_OK
                : HG_ERR_CUDA;
 }
 
+// x: BF16, or (with its scales) FP8 codes, which are decoded into the workspace.
 hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scale, bool fp8,
                         const int32_t* offsets, int32_t E, int32_t N, int32_t K, int32_t rows,
                         int32_t accumulate, void* dw, int32_t dw_f32, void* workspace,
@@ -288,7 +294,8 @@ hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scal
         return HG_ERR_INVALID_ARG;
     if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(offsets, 4) || !aligned(dw, 16))
         return HG_ERR_INVALID_ARG;
-    const size_t need = wgrad_workspace(E, N, K, rows);
+    const size_t parts = wgrad_parts_bytes(E, N, K, rows);      // a multiple of 16
+    const size_t need = parts + (fp8 ? wgrad_decoded_bytes(K, rows) : 0);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return HG_ERR_INVALID_ARG;
     DeviceInfo* d = nullptr;
@@ -298,7 +305,12 @@ hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scal
     st = encoder(&encode);
     if (st != HG_OK) return st;
     WgradArgs a{};
-    a.x_scale = x_scale;
+    if (fp8) {
+        a.codes = static_cast<const uint8_t*>(x);
+        a.code_scale = x_scale;
+        a.x = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + parts);
+        x = a.x;
+    }
     a.offsets = offsets;
     a.E = E;
     a.N = N;
@@ -307,7 +319,7 @@ hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scal
     a.accumulate = accumulate != 0;
     a.f32 = dw_f32 != 0;
     a.dw = dw;
-    a.parts = need > 0 ? static_cast<float*>(workspace) : nullptr;
+    a.parts = parts > 0 ? static_cast<float*>(workspace) : nullptr;
     a.status = d->status;
     a.timeout_ns = g_timeout_ns.load();
     // without rows nothing is loaded, but the maps have to name some memory
@@ -315,18 +327,16 @@ hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scal
     const bool out_f32 = a.f32 || a.parts;
     WgradMaps maps;
     st = matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows > 0 ? dy : dw, 1, map_rows,
-                    N, kWgradRows, 64, CU_TENSOR_MAP_SWIZZLE_128B, &maps.dy);
+                    N, kWgradRows, 64, &maps.dy);
     if (st == HG_OK)
-        st = fp8 ? matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows > 0 ? x : dw, 1,
-                              map_rows, K, kWgradRows, 128, CU_TENSOR_MAP_SWIZZLE_NONE, &maps.x)
-                 : matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows > 0 ? x : dw, 1,
-                              map_rows, K, kWgradRows, 64, CU_TENSOR_MAP_SWIZZLE_128B, &maps.x);
+        st = matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows > 0 ? x : dw, 1, map_rows,
+                        K, kWgradRows, 64, &maps.x);
     if (st == HG_OK)
         st = matrix_map(encode,
                         out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                         out_f32 ? 4 : 2, a.parts ? static_cast<void*>(a.parts) : dw,
                         static_cast<long long>(E) * (a.parts ? wgrad_splits(E, N, K, rows) : 1), N,
-                        K, 32, out_f32 ? 32 : 64, CU_TENSOR_MAP_SWIZZLE_128B, &maps.out);
+                        K, 32, out_f32 ? 32 : 64, &maps.out);
     if (st != HG_OK) return st;
     return launch_wgrad(a, maps, d->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK
@@ -870,7 +880,12 @@ hg_status hg_dequantize_weights(const uint8_t* w_fp4, const uint8_t* w_scale, in
 
 size_t hg_grouped_wgrad_workspace_bytes(int32_t E, int32_t N, int32_t K, int32_t rows) {
     if (E < 1 || N < 1 || K < 1 || rows < 0) return 0;
-    return wgrad_workspace(E, N, K, rows);
+    return wgrad_parts_bytes(E, N, K, rows);
+}
+
+size_t hg_grouped_wgrad_fp8_workspace_bytes(int32_t E, int32_t N, int32_t K, int32_t rows) {
+    if (E < 1 || N < 1 || K < 1 || rows < 0) return 0;
+    return wgrad_parts_bytes(E, N, K, rows) + wgrad_decoded_bytes(K, rows);
 }
 
 hg_status hg_grouped_wgrad(const uint16_t* dy_bf16, const uint16_t* x_bf16,

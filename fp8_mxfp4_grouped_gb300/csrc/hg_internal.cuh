@@ -275,22 +275,23 @@ cudaError_t launch_dequantize_weights(const uint8_t* q, const uint8_t* scale, in
                                       void* w, bool f32, cudaStream_t stream);
 
 struct WgradArgs {
-    const uint8_t* x_scale;     // with an FP8 x, else null
+    const uint8_t *codes, *code_scale;  // an FP8 x, to be decoded into x; else null
+    uint16_t* x;
     const int32_t* offsets;
     int E, N, K, rows;
     bool accumulate, f32;       // f32: dw is FP32, else BF16
     void* dw;
-    float* parts;               // wgrad_workspace, where the rows are split
+    float* parts;               // wgrad_parts_bytes, where the rows are split
     uint32_t* status;
     uint64_t timeout_ns;
 };
 // Parts that an expert's rows are split into for these sizes.
 int wgrad_splits(int E, int N, int K, int rows);
-size_t wgrad_workspace(int E, int N, int K, int rows);
+size_t wgrad_parts_bytes(int E, int N, int K, int rows);
 bool wgrad_fits(int E, int N, int K, int rows);     // the grid's numbers and the maps' strides
-// Tensor maps: dy [rows, N] in boxes of kWgradRows rows x 64 columns, x [rows, K] the same
-// (FP8: x 128 columns, no swizzle), and the output (the workspace where the rows are
-// split) [E or parts, N, K] in boxes of 32 rows x 128 bytes, all with the 128-byte swizzle.
+// Tensor maps: dy [rows, N] and x [rows, K] in boxes of kWgradRows rows x 64 columns, and the
+// output (the parts where the rows are split) [E or parts, N, K] in boxes of 32 rows x 128
+// bytes, all with the 128-byte swizzle.
 constexpr int kWgradRows = 64;
 struct WgradMaps {
     CUtensorMap dy, x, out;

@@ -102,6 +102,8 @@ lib.hg_dequantize_weights.argtypes = [_p, _p, _i32, _i32, _i32, _p, _i32, _p]
 lib.hg_dequantize_weights.restype = ctypes.c_int
 lib.hg_grouped_wgrad_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
 lib.hg_grouped_wgrad_workspace_bytes.restype = _sz
+lib.hg_grouped_wgrad_fp8_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
+lib.hg_grouped_wgrad_fp8_workspace_bytes.restype = _sz
 lib.hg_grouped_wgrad.argtypes = [_p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p, _i32, _p, _sz, _p]
 lib.hg_grouped_wgrad.restype = ctypes.c_int
 lib.hg_grouped_wgrad_fp8.argtypes = [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p, _i32, _p,
@@ -646,6 +648,10 @@ def hg_grouped_wgrad_workspace_bytes(E: int, N: int, K: int, rows: int) -> int:
     return int(lib.hg_grouped_wgrad_workspace_bytes(E, N, K, rows))
 
 
+def hg_grouped_wgrad_fp8_workspace_bytes(E: int, N: int, K: int, rows: int) -> int:
+    return int(lib.hg_grouped_wgrad_fp8_workspace_bytes(E, N, K, rows))
+
+
 def _grouped_wgrad(fn, what, dy, x, x_scale, expert_offsets, dtype, dw, accumulate, workspace,
                    stream):
     rows, N = dy.shape
@@ -660,7 +666,8 @@ def _grouped_wgrad(fn, what, dy, x, x_scale, expert_offsets, dtype, dw, accumula
     assert not accumulate or dw is not None, "accumulate adds to a dw that is given"
     device = _device(dy, x, x_scale, expert_offsets)
     dw = _out(dw, (E, N, K), dtype, dy, stream)
-    need = lib.hg_grouped_wgrad_workspace_bytes(E, N, K, rows)
+    need = (lib.hg_grouped_wgrad_workspace_bytes if x_scale is None else
+            lib.hg_grouped_wgrad_fp8_workspace_bytes)(E, N, K, rows)
     workspace, size = _workspace(workspace, need, dy, stream)
     args = (dy.data_ptr(), x.data_ptr(), *(() if x_scale is None else (x_scale.data_ptr(),)))
     _run(fn, what, device, stream, *args, expert_offsets.data_ptr(), E, N, K, rows,

@@ -577,7 +577,7 @@ hg_status hg_router_topk_bwd(const float* logits, const int32_t* topk_ids,
  * into any sum, whatever they hold.  Sums are FP32; the result does not vary from run to
  * run.  Offsets that are not monotone or exceed rows are detected on the device: the
  * affected experts count as having no rows, and HG_ERR_BAD_OFFSETS is recorded for
- * hg_get_device_status.  One or two kernels on `stream`, launched with programmatic
+ * hg_get_device_status.  One to three kernels on `stream`, launched with programmatic
  * dependent launch as the section above says; no host synchronisation.
  */
 size_t hg_grouped_wgrad_workspace_bytes(int32_t E, int32_t N, int32_t K, int32_t rows);
@@ -590,10 +590,12 @@ hg_status hg_grouped_wgrad(const uint16_t* dy_bf16, const uint16_t* x_bf16,
  * The same with x as the forward product had it:
  *
  *   a_fp8    uint8 [rows, K] E4M3 codes, 16-byte aligned; a_scale uint8 [rows, K/128].
- * K % 128 == 0.  Codes times scales are taken as BF16, which is exact within BF16's
- * range.  Scale code 255 is NaN; NaN codes under another scale are not supported inputs,
- * as for the GEMM.
+ * K % 128 == 0.  Codes times scales become BF16 in the workspace first, by a kernel more,
+ * which is exact within BF16's range; the workspace has
+ * hg_grouped_wgrad_fp8_workspace_bytes(E, N, K, rows) bytes.  Scale code 255 and the codes
+ * 0x7F and 0xFF are NaN.
  */
+size_t hg_grouped_wgrad_fp8_workspace_bytes(int32_t E, int32_t N, int32_t K, int32_t rows);
 hg_status hg_grouped_wgrad_fp8(const uint16_t* dy_bf16, const uint8_t* a_fp8,
                                const uint8_t* a_scale, const int32_t* expert_offsets, int32_t E,
                                int32_t N, int32_t K, int32_t rows, int32_t accumulate, void* dw,

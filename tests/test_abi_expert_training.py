@@ -34,7 +34,8 @@ def test_grouped_wgrad(lib, fp8):  # noqa: F811
              "ws", "bytes"]
     call = _caller(getattr(lib.lib, "hg_grouped_wgrad_fp8" if fp8 else "hg_grouped_wgrad"), names,
                    dict(dy=0x1000, x=0x2000, s=0x3000, off=0x4000, E=4, N=64, K=256, rows=100,
-                        acc=0, dw=0x5000, f32=1, ws=0, bytes=0))
+                        acc=0, dw=0x5000, f32=1, ws=0x6000 if fp8 else 0,
+                        bytes=2 * 256 * 100 if fp8 else 0))
     _refuses(call, [dict(E=0), dict(N=0), dict(K=0), dict(rows=-1), dict(dy=0), dict(x=0),
                     dict(off=0), dict(dw=0), dict(dy=0x1008), dict(x=0x2008), dict(off=0x4002),
                     dict(dw=0x5008), dict(acc=1, f32=0), *([dict(s=0)] if fp8 else []),
@@ -44,8 +45,8 @@ def test_grouped_wgrad(lib, fp8):  # noqa: F811
                     dict(E=1, N=256, K=256, rows=1 << 16, ws=0x6004, bytes=1 << 30)],
              [dict(E=513), dict(N=60), dict(K=260), dict(N=(1 << 30) + 8), dict(K=(1 << 30) + 128),
               dict(E=512, N=1 << 30, K=1 << 20), dict(N=1 << 30, rows=1 << 20)])
-    if fp8:
-        assert call(K=264) == SHAPE
+    if fp8:                                               # the decoded rows need a workspace
+        _refuses(call, [dict(ws=0), dict(bytes=2 * 256 * 100 - 1), dict(ws=0x6008)], [dict(K=264)])
 
 
 def test_grouped_wgrad_workspace(lib):  # noqa: F811
@@ -55,6 +56,10 @@ def test_grouped_wgrad_workspace(lib):  # noqa: F811
     need = f(1, 256, 512, 1 << 16)
     assert need > 0 and need % (4 * 256 * 512) == 0
     assert f(0, 256, 256, 1 << 16) == 0 and f(1, 256, 256, -1) == 0
+    fp8 = lib.hg_grouped_wgrad_fp8_workspace_bytes        # the same and the decoded rows
+    for E, K, rows in ((32, 6144, 16384), (1, 512, 1 << 16), (3, 128, 0)):
+        assert fp8(E, 256, K, rows) == f(E, 256, K, rows) + 2 * K * rows
+    assert fp8(1, 256, 256, -1) == 0
 
 
 def test_quantize_weights(lib):  # noqa: F811
@@ -145,9 +150,9 @@ CALLS = {
                               [((2, 64, 48), U8), ((2, 64, 3), U8), ((2, 64, 96), B)]),
     "hg_grouped_wgrad": (lambda f, t: f(*t[:3], dw=t[3], workspace=t[4]),
                          [((9, 64), B), ((9, 72), B), ((3,), I32), ((2, 64, 72), F32), ((4,), U8)]),
-    "hg_grouped_wgrad_fp8": (lambda f, t: f(*t[:4], dw=t[4], accumulate=True),
+    "hg_grouped_wgrad_fp8": (lambda f, t: f(*t[:4], dw=t[4], accumulate=True, workspace=t[5]),
                              [((9, 64), B), ((9, 128), U8), ((9, 1), U8), ((3,), I32),
-                              ((2, 64, 128), F32)]),
+                              ((2, 64, 128), F32), ((9 * 128 * 2,), U8)]),
 }
 
 
@@ -200,6 +205,10 @@ def test_a_workspace_too_small_is_refused(hg, monkeypatch):  # noqa: F811
     call, tensors = CALLS["hg_rmsnorm_bwd"]
     with pytest.raises(AssertionError):
         call(hg.hg_rmsnorm_bwd, [OnGpu(*t, 0) for t in tensors[:-1]] + [OnGpu((64,), U8, 0)])
+    call, tensors = CALLS["hg_grouped_wgrad_fp8"]
+    monkeypatch.setattr(hg.lib, "hg_grouped_wgrad_fp8", record)
+    with pytest.raises(AssertionError):
+        call(hg.hg_grouped_wgrad_fp8, [OnGpu(*t, 0) for t in tensors[:-1]] + [OnGpu((64,), U8, 0)])
     with pytest.raises(AssertionError):                     # nothing to add to
         hg.hg_grouped_wgrad(*[OnGpu(*t, 0) for t in CALLS["hg_grouped_wgrad"][1][:3]],
                             accumulate=True)

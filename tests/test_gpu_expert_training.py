@@ -145,9 +145,8 @@ def test_wgrad_neighbours_do_not_mix(cuda_lib):
 def test_wgrad_fp8_every_code_and_scale(cuda_lib):
     """One row: dw is the row itself, every code under every scale that BF16 holds."""
     hg = cuda_lib
-    codes = [c for c in range(256) if c & 0x7F != 0x7F]
     K = 256
-    row = torch.tensor(codes + [0] * (K - len(codes)), dtype=torch.uint8)
+    row = torch.arange(K, dtype=torch.uint8)              # NaN among them
     off, dy = _offsets([1]).cuda(), torch.zeros(1, 8).bfloat16()
     dy[0, 0] = 1.0
     for scale in (0, 1, 9, 10, 60, 126, 127, 128, 133, 134, 135, 136, 200, 245, 246, 255):
