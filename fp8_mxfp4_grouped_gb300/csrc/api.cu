@@ -261,16 +261,11 @@ hg_status out_map(PFN_cuTensorMapEncodeTiled_v12000 encode, uint16_t* out, int32
     return HG_OK;
 }
 
-// The weight gradient's operands and result as matrices [matrices, rows, cols], 128-byte
-// swizzle, boxes of `box_rows` x `box_cols`.  Encoded at every call.
-hg_status matrix_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMapDataType type, int bytes,
-                     const void* p, long long matrices, int32_t rows, int32_t cols,
-                     uint32_t box_rows, uint32_t box_cols, CUtensorMap* out) {
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                          static_cast<cuuint64_t>(matrices)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * bytes,
-                             static_cast<cuuint64_t>(cols) * bytes * rows};
-    cuuint32_t box[3] = {box_cols, box_rows, 1};
+// Three dimensions, the innermost of which is contiguous; 128-byte swizzle.  The maps of the
+// weight gradient, encoded at every call.
+hg_status map_3d(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMapDataType type, const void* p,
+                 const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                 const cuuint32_t (&box)[3], CUtensorMap* out) {
     cuuint32_t estr[3] = {1, 1, 1};
     return encode(out, type, 3, const_cast<void*>(p), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -278,6 +273,30 @@ hg_status matrix_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMapDataTy
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? HG_OK
                : HG_ERR_CUDA;
+}
+
+// An operand [rows, cols] BF16 as wgrad_panels has it, in both heights of boxes.
+hg_status operand_maps(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* p, int32_t rows,
+                       int32_t cols, CUtensorMap (&out)[2]) {
+    const cuuint64_t r = static_cast<cuuint64_t>(rows), c = static_cast<cuuint64_t>(cols);
+    const bool whole = wgrad_panels(cols) == 2;
+    for (int i = 0; i < 2; ++i) {
+        const hg_status st = map_3d(
+            encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, {whole ? 64 : c, r, whole ? c / 64 : 1},
+            {2 * c, whole ? 128 : 2 * c * r},
+            {64, static_cast<cuuint32_t>(i ? kWgradRows : kWgradRows / 2), whole ? 2u : 1u}, &out[i]);
+        if (st != HG_OK) return st;
+    }
+    return HG_OK;
+}
+
+// The result, [matrices, rows, cols].
+hg_status result_map(PFN_cuTensorMapEncodeTiled_v12000 encode, bool f32, const void* p,
+                     long long matrices, int32_t rows, int32_t cols, CUtensorMap* out) {
+    const cuuint64_t r = static_cast<cuuint64_t>(rows), row = static_cast<cuuint64_t>(cols) * (f32 ? 4 : 2);
+    return map_3d(encode, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p,
+                  {static_cast<cuuint64_t>(cols), r, static_cast<cuuint64_t>(matrices)},
+                  {row, row * r}, {f32 ? 32u : 64u, 32, 1}, out);
 }
 
 // x: BF16, or (with its scales) FP8 codes, which are decoded into the workspace.
@@ -326,17 +345,12 @@ hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scal
     const int32_t map_rows = rows > 0 ? rows : 1;
     const bool out_f32 = a.f32 || a.parts;
     WgradMaps maps;
-    st = matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows > 0 ? dy : dw, 1, map_rows,
-                    N, kWgradRows, 64, &maps.dy);
+    st = operand_maps(encode, rows > 0 ? dy : dw, map_rows, N, maps.dy);
+    if (st == HG_OK) st = operand_maps(encode, rows > 0 ? x : dw, map_rows, K, maps.x);
     if (st == HG_OK)
-        st = matrix_map(encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows > 0 ? x : dw, 1, map_rows,
-                        K, kWgradRows, 64, &maps.x);
-    if (st == HG_OK)
-        st = matrix_map(encode,
-                        out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        out_f32 ? 4 : 2, a.parts ? static_cast<void*>(a.parts) : dw,
+        st = result_map(encode, out_f32, a.parts ? static_cast<void*>(a.parts) : dw,
                         static_cast<long long>(E) * (a.parts ? wgrad_splits(E, N, K, rows) : 1), N,
-                        K, 32, out_f32 ? 32 : 64, &maps.out);
+                        K, &maps.out);
     if (st != HG_OK) return st;
     return launch_wgrad(a, maps, d->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HG_OK

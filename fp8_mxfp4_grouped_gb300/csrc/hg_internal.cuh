@@ -289,12 +289,14 @@ struct WgradArgs {
 int wgrad_splits(int E, int N, int K, int rows);
 size_t wgrad_parts_bytes(int E, int N, int K, int rows);
 bool wgrad_fits(int E, int N, int K, int rows);     // the grid's numbers and the maps' strides
-// Tensor maps: dy [rows, N] and x [rows, K] in boxes of kWgradRows rows x 64 columns, and the
-// output (the parts where the rows are split) [E or parts, N, K] in boxes of 32 rows x 128
-// bytes, all with the 128-byte swizzle.
-constexpr int kWgradRows = 64;
+// Tensor maps, all with the 128-byte swizzle: dy [rows, N] and x [rows, K] in boxes of
+// half of kWgradRows rows and of all x wgrad_panels panels of 64 columns, as [rows, N] or as
+// [N/64, rows, 64]; the output (the parts where the rows are split) [E or parts, N, K] in boxes of 32 rows x
+// 128 bytes.
+constexpr int kWgradRows = 128;
+int wgrad_panels(int cols);
 struct WgradMaps {
-    CUtensorMap dy, x, out;
+    CUtensorMap dy[2], x[2], out;
 };
 cudaError_t launch_wgrad(const WgradArgs& a, const WgradMaps& maps, int num_sms,
                          cudaStream_t stream);

@@ -37,18 +37,16 @@ constexpr int kTile = 256;                   // dw rows and columns of a pair's 
 constexpr int kHalf = 128;                   // dy columns and x columns that a CTA loads
 constexpr int kEpiWarps = 8;                 // four lane quarters x two halves of the columns
 constexpr int kEpiCols = kTile * 4 / kEpiWarps;
-constexpr int kPanel = kWgradRows * 128;     // bytes of 64 rows x 64 16-bit columns
-constexpr int kOperand = 2 * kPanel;         // a CTA's part of an operand's stage
+constexpr int kOperand = kWgradRows * kHalf * 2;         // bytes of a CTA's part of a stage
 constexpr int kOutBuf = 32 * 128;            // a warp's 32 rows x 128 bytes of output
 constexpr int kTmemCols = 512;               // two accumulators of 256 columns
 constexpr int kMmaRows = 16;                 // K of an MMA
 
 // Stages of an accumulator: 512 rows.
-constexpr int kChunk = 8;
+constexpr int kChunk = 512 / kWgradRows;
 
 constexpr int kThreads = 384;
-constexpr int kStages = 6;
-constexpr int kTx = 4 * kOperand;            // bytes of a stage in both CTAs
+constexpr int kStages = 3;
 constexpr int kOffA = 0;
 constexpr int kOffB = kOffA + kStages * kOperand;
 constexpr int kOffOut = kOffB + kStages * kOperand;
@@ -59,6 +57,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
 
 struct Shape {
     int E, N, K, rows, splits, tiles_n, tiles_k;
+    int dy_panels, x_panels;                 // of 64 columns in a box: 1 or 2
 };
 
 // A unit of work: the tile's place, and the rows that are summed.
@@ -88,6 +87,10 @@ struct Unit {
     __device__ __forceinline__ bool mixed(int stage) const {
         return rows - stage * kWgradRows < kWgradRows && rows % kMmaRows != 0;
     }
+    // rows that a stage has room for: half of the boxes' where no more are left
+    __device__ __forceinline__ int room(int stage) const {
+        return valid(stage) > kWgradRows / 2 ? kWgradRows : kWgradRows / 2;
+    }
     // rows of a stage that belong to the unit
     __device__ __forceinline__ int valid(int stage) const {
         return min(kWgradRows, rows - stage * kWgradRows);
@@ -100,11 +103,26 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
                  "r"(d)
                  : "memory");
 }
-// Clear rows [first, last) of an operand's stage (whole warp).
-__device__ __forceinline__ void clear_rows(uint32_t operand, int first, int last) {
-    for (int i = threadIdx.x & 31; i < (last - first) * 16; i += 32) {
-        const int r = first + (i >> 4), panel = (i >> 3) & 1;
-        sts_v4(operand + panel * kPanel + r * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+
+// Clear rows [first, last) of an operand's stage with room for `room` (whole warp).
+__device__ __forceinline__ void clear_rows(uint32_t operand, int room, int first, int last) {
+    operand += first * 128;
+    for (int i = threadIdx.x & 31; i < (last - first) * 16; i += 32)
+        sts_v4(operand + ((i >> 3) & 1) * room * 128 + (i >> 4) * 128 + (i & 7) * 16, 0u, 0u, 0u,
+               0u);
+}
+
+// A CTA's 128 columns of a stage, counted on a barrier of either CTA: two panels of 64
+// columns, one behind the other.
+__device__ __forceinline__ void load_stage(uint32_t to, const CUtensorMap (&maps)[2], int panels,
+                                           int room, int col, int row, uint32_t bar,
+                                           uint64_t policy) {
+    const CUtensorMap* map = &maps[room == kWgradRows];
+    if (panels == 2) {
+        ptx::tma_load_3d_pair_elect(to, map, 0, row, col / 64, bar, policy);
+    } else {
+        ptx::tma_load_3d_pair_elect(to, map, col, row, 0, bar, policy);
+        ptx::tma_load_3d_pair_elect(to + room * 128, map, col + 64, row, 0, bar, policy);
     }
 }
 
@@ -153,8 +171,10 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
         ptx::tmem_relinquish_pair();
     }
     if (warp == 0 && lane == 0) {
-        ptx::prefetch_tensormap(&maps.dy);
-        ptx::prefetch_tensormap(&maps.x);
+        for (int i = 0; i < 2; ++i) {
+            ptx::prefetch_tensormap(&maps.dy[i]);
+            ptx::prefetch_tensormap(&maps.x[i]);
+        }
         ptx::prefetch_tensormap(&maps.out);
     }
     // Nothing above reads global memory.
@@ -193,21 +213,18 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
                                 slot)))
                     break;
                 const int row = t.row0 + s * kWgradRows;
+                const int room = t.room(s), bytes = 2 * room * kHalf * 2;     // of this CTA
                 uint32_t bar = full + 8 * slot;
                 if (t.mixed(s)) {
                     bar = last + 8 * slot;
-                    ptx::mbar_arrive_expect_tx_elect(bar_last + 8 * slot, kTx / 2);
+                    ptx::mbar_arrive_expect_tx_elect(bar_last + 8 * slot, bytes);
                 } else if (leader) {
-                    ptx::mbar_arrive_expect_tx_elect(bar_full + 8 * slot, kTx);
+                    ptx::mbar_arrive_expect_tx_elect(bar_full + 8 * slot, 2 * bytes);
                 }
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    ptx::tma_load_3d_pair_elect(sbase + kOffA + slot * kOperand + p * kPanel,
-                                                &maps.dy, n + 64 * p, row, 0, bar, policy);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    ptx::tma_load_3d_pair_elect(sbase + kOffB + slot * kOperand + p * kPanel,
-                                                &maps.x, k + 64 * p, row, 0, bar, policy);
+                load_stage(sbase + kOffA + slot * kOperand, maps.dy, shape.dy_panels, room, n, row,
+                           bar, policy);
+                load_stage(sbase + kOffB + slot * kOperand, maps.x, shape.x_panels, room, k, row,
+                           bar, policy);
             }
         }
         // No copy may land, and no release of a stage arrive, after the CTA has gone: what the
@@ -237,9 +254,9 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
                         break;
                     ptx::tc_fence_after();
                     const uint64_t a =
-                        ptx::desc_mnmajor_sw128(sbase + kOffA + slot * kOperand, kPanel);
+                        ptx::desc_mnmajor_sw128(sbase + kOffA + slot * kOperand, t.room(s) * 128);
                     const uint64_t x =
-                        ptx::desc_mnmajor_sw128(sbase + kOffB + slot * kOperand, kPanel);
+                        ptx::desc_mnmajor_sw128(sbase + kOffB + slot * kOperand, t.room(s) * 128);
                     const int steps = (t.valid(s) + kMmaRows - 1) / kMmaRows;
                     for (int i = 0; i < steps; ++i) {
                         // 16 rows of 128 bytes on, in the descriptor's 16-byte units
@@ -352,8 +369,8 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
                 const int valid = t.valid(s);
                 const int used = (valid + kMmaRows - 1) / kMmaRows * kMmaRows;
                 if (!(ok = wait(bar_last + 8 * slot, parity, kRoleWorker, slot))) break;
-                clear_rows(sbase + kOffA + slot * kOperand, valid, used);
-                clear_rows(sbase + kOffB + slot * kOperand, valid, used);
+                clear_rows(sbase + kOffA + slot * kOperand, t.room(s), valid, used);
+                clear_rows(sbase + kOffB + slot * kOperand, t.room(s), valid, used);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (leader && !(ok = wait(bar_clear + 8 * slot, parity, kRoleWorker, 0x100u | slot)))
@@ -484,6 +501,10 @@ void wgrad_reset_caches() {
     for (auto& pairs : g_pairs) pairs.store(0);
 }
 
+// Whole panels of 64 columns go two in a box (else a box's columns would run into the next
+// row): a copy costs the engine some 80 cycles beside its bytes.
+int wgrad_panels(int cols) { return cols % 64 == 0 ? 2 : 1; }
+
 // With fewer tiles than pairs the rows are split, as long as a part has some 512 rows.
 int wgrad_splits(int E, int N, int K, int rows) {
     constexpr long long kPairs = 76, kLeast = 512;
@@ -519,8 +540,9 @@ cudaError_t launch_wgrad(const WgradArgs& a, const WgradMaps& maps, int num_sms,
                                a.rows, a.K, a.x);
         if (err != cudaSuccess) return err;
     }
-    const Shape s{a.E, a.N, a.K, a.rows, wgrad_splits(a.E, a.N, a.K, a.rows), tiles(a.N),
-                  tiles(a.K)};
+    const Shape s{a.E,        a.N,        a.K,
+                  a.rows,     wgrad_splits(a.E, a.N, a.K, a.rows),
+                  tiles(a.N), tiles(a.K), wgrad_panels(a.N), wgrad_panels(a.K)};
     const long long units = static_cast<long long>(s.E) * s.splits * s.tiles_n * s.tiles_k;
     const int grid = 2 * static_cast<int>(units < pairs ? units : pairs);
     err = launch_dependent(a.f32 || a.parts ? wgrad_kernel<true> : wgrad_kernel<false>, grid,
