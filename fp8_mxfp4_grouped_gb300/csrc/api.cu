@@ -389,6 +389,7 @@ hg_status hg_shutdown(void) {
     plan_noalloc_reset();
     matvec_reset_caches();
     wgrad_reset_caches();
+    rmsnorm_reset_caches();
     map_cache_reset();
     return HG_OK;
 }
@@ -859,8 +860,11 @@ hg_status hg_rmsnorm_bwd(const uint16_t* dy_bf16, const uint16_t* dsum_bf16,
     if (dgain && (!workspace || workspace_bytes < rmsnorm_bwd_workspace(M, D) ||
                   !aligned(workspace, 16)))
         return HG_ERR_INVALID_ARG;
-    const RmsnormBwdArgs a{dy_bf16, dsum_bf16, sum_bf16, gain_bf16, rstd,
-                           M,       D,         dx_bf16,  dgain,     static_cast<float*>(workspace)};
+    DeviceInfo* d = nullptr;
+    const hg_status st = device_info(&d);
+    if (st != HG_OK) return st;
+    const RmsnormBwdArgs a{dy_bf16, dsum_bf16, sum_bf16, gain_bf16, rstd, M, D, dx_bf16, dgain,
+                           static_cast<float*>(workspace), d->status, g_timeout_ns.load()};
     return launch_rmsnorm_bwd(a, s) == cudaSuccess ? HG_OK : HG_ERR_CUDA;
 }
 

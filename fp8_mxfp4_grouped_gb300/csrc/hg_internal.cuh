@@ -36,6 +36,7 @@ enum WaitRole : uint32_t {
     kRoleRelay = 7,
     kRoleMatvec = 8,
     kRoleWorker = 9,
+    kRoleNorm = 10,
 };
 
 struct WaitCtx {
@@ -261,9 +262,13 @@ struct RmsnormBwdArgs {
     int M, D;
     uint16_t* dx;
     float *dgain, *parts;   // dgain may be null; parts: rmsnorm_bwd_workspace
+    uint32_t* status;
+    uint64_t timeout_ns;
 };
 int rmsnorm_max_elements();
 size_t rmsnorm_bwd_workspace(int M, int D);
+// Forget on which devices the norm's gradient is set up (hg_shutdown).
+void rmsnorm_reset_caches();
 cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream);
 cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, cudaStream_t stream);
 

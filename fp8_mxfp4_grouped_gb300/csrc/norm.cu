@@ -14,6 +14,8 @@
 // that holds it in registers, up to four pieces of eight elements a lane, so that
 // everything is read once; a half-warp's sixteen pieces are one 128-element group of
 // the scales.
+#include <atomic>
+
 #include "hg_internal.cuh"
 #include "numeric.cuh"
 
@@ -148,98 +150,152 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* gain
     }
 }
 
-// Blocks of the gradient's grid: two a SM.  Each team takes every so-manieth row and
-// keeps its columns' part of dgain in registers; the parts go to the workspace, a row a
-// team, and are added in the order of the teams.
-constexpr int kBwdBlocks = 2 * 152;
+// The gradient: a block takes groups of consecutive rows in turn, some 8192 elements of each
+// array a group, which bulk copies bring into one half of its shared memory while the other
+// half is worked on.  Rows stay there for their second pass; a thread keeps its columns'
+// gains and its part of dgain in registers.  The parts of a block's teams are added up, then
+// written to the workspace, a row a block, and joined in the order of the blocks.
+constexpr int kGroupElements = 8192;
+constexpr int kBwdBlocks = 2 * 152;          // two a SM, of up to eight warps
 
 template <int kPieces>
 __global__ void __launch_bounds__(kMaxTeamWarps * 32)
 rmsnorm_bwd_kernel(const uint16_t* dy, const uint16_t* dsum, const uint16_t* sum,
                    const uint16_t* gain, const float* rstd, int M, int D, int team_warps,
-                   uint16_t* dx, float* parts) {
+                   int group_rows, uint16_t* dx, float* parts, uint32_t* status,
+                   uint64_t timeout_ns) {
+    extern __shared__ __align__(16) uint8_t smem[];      // two halves of dy, sum and dsum
     __shared__ float part[2][kMaxTeamWarps];
+    __shared__ __align__(8) uint64_t s_bar[2];
+    __shared__ uint32_t s_abort;
     const Team team(team_warps);
-    const int teams = gridDim.x * team.per_block;
-    const int first = blockIdx.x * team.per_block + team.in_block;
+    const uint32_t bars = ptx::smem_u32(s_bar);
+    if (threadIdx.x == 0) {
+        for (int h = 0; h < 2; ++h) ptx::mbar_init(bars + 8 * h, 1);
+        s_abort = 0u;
+        ptx::fence_barrier_init();
+    }
+    __syncthreads();
     start_dependent();
-    if (first >= M) return;
-    float dg[kPieces][8] = {};
-    int turn = 0;
-    for (long long row = first; row < M; row += teams, turn ^= 1) {
-        uint4 vd[kPieces], vs[kPieces];
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-            const int n = team.at(c);
-            vd[c] = vs[c] = make_uint4(0, 0, 0, 0);
-            if (n >= D) continue;
-            vd[c] = ptx::load(reinterpret_cast<const uint4*>(dy + row * D + n));
-            vs[c] = ptx::load(reinterpret_cast<const uint4*>(sum + row * D + n));
-        }
-        const float r = ptx::load(rstd + row);
-        float dot = 0.0f;
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-            const int n = team.at(c);
-            float d[8], s[8], g[8];
-            bf16_unpack8(vd[c], d);
-            bf16_unpack8(vs[c], s);
-            uint4 vg = make_uint4(0, 0, 0, 0);
-            if (n < D) vg = ptx::load(reinterpret_cast<const uint4*>(gain + n));
-            bf16_unpack8(vg, g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float norm = s[i] * r;
-                dg[c][i] = fmaf(d[i], norm, dg[c][i]);
-                dot = fmaf(d[i] * r * g[i], norm, dot);
-            }
-        }
-        const float mean = team_sum(team, dot, part[turn]) / static_cast<float>(D);
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-            const int n = team.at(c);
-            if (n >= D) continue;
-            float d[8], s[8], g[8], o[8] = {};
-            bf16_unpack8(vd[c], d);
-            bf16_unpack8(vs[c], s);
-            bf16_unpack8(ptx::load(reinterpret_cast<const uint4*>(gain + n)), g);
-            if (dsum) bf16_unpack8(ptx::load(reinterpret_cast<const uint4*>(dsum + row * D + n)), o);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] += fmaf(-s[i] * r, mean, d[i] * r * g[i]);
-            *reinterpret_cast<uint4*>(dx + row * D + n) = bf16_pack8(o);
+    const int arrays = dsum ? 3 : 2;
+    const int array_bytes = group_rows * D * 2;
+    const int groups = (M - 1) / group_rows + 1;
+    const WaitCtx ctx{status, &s_abort, timeout_ns};
+    auto load = [&](int group, int half) {
+        const long long row = static_cast<long long>(group) * group_rows;
+        const uint32_t bytes = static_cast<uint32_t>(min(static_cast<long long>(group_rows), M - row)) * D * 2;
+        const uint16_t* from[3] = {dy, sum, dsum};
+        ptx::mbar_arrive_expect_tx(bars + 8 * half, bytes * arrays);
+        for (int i = 0; i < arrays; ++i)
+            ptx::bulk_load(ptx::smem_u32(smem) + (half * 3 + i) * array_bytes, from[i] + row * D,
+                           bytes, bars + 8 * half);
+    };
+    if (threadIdx.x == 0) {
+        for (int h = 0; h < 2; ++h) {
+            const long long group = blockIdx.x + static_cast<long long>(h) * gridDim.x;
+            if (group < groups) load(static_cast<int>(group), h);
         }
     }
+    uint4 g16[kPieces];
+    float dg[kPieces][8] = {};
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+        const int n = team.at(c);
+        g16[c] = make_uint4(0, 0, 0, 0);
+        if (n < D) g16[c] = ptx::load(reinterpret_cast<const uint4*>(gain + n));
+    }
+    int turn = 0, step = 0;
+    long long group = blockIdx.x;
+    for (; group < groups; group += gridDim.x, ++step) {
+        const int half = step & 1;
+        const long long row0 = group * group_rows;
+        const int rows = static_cast<int>(min(static_cast<long long>(group_rows), M - row0));
+        const bool came = wait_bounded(bars + 8 * half, (step >> 1) & 1u, ctx, kRoleNorm, half);
+        if (__syncthreads_or(!came)) break;
+        const uint8_t* base = smem + half * 3 * array_bytes;
+        for (int j = team.in_block; j < rows; j += team.per_block, turn ^= 1) {
+            const float r = ptx::load(rstd + row0 + j);
+            const uint16_t* at = reinterpret_cast<const uint16_t*>(base) + j * D;
+            float dot = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c) {
+                const int n = team.at(c);
+                if (n >= D) continue;
+                float d[8], s[8], g[8];
+                bf16_unpack8(*reinterpret_cast<const uint4*>(at + n), d);
+                bf16_unpack8(*reinterpret_cast<const uint4*>(at + array_bytes / 2 + n), s);
+                bf16_unpack8(g16[c], g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float norm = s[i] * r;
+                    dg[c][i] = fmaf(d[i], norm, dg[c][i]);
+                    dot = fmaf(d[i] * r * g[i], norm, dot);
+                }
+            }
+            const float mean = team_sum(team, dot, part[turn]) / static_cast<float>(D);
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c) {
+                const int n = team.at(c);
+                if (n >= D) continue;
+                float d[8], s[8], g[8], o[8] = {};
+                bf16_unpack8(*reinterpret_cast<const uint4*>(at + n), d);
+                bf16_unpack8(*reinterpret_cast<const uint4*>(at + array_bytes / 2 + n), s);
+                bf16_unpack8(g16[c], g);
+                if (dsum) bf16_unpack8(*reinterpret_cast<const uint4*>(at + array_bytes + n), o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] += fmaf(-s[i] * r, mean, d[i] * r * g[i]);
+                *reinterpret_cast<uint4*>(dx + (row0 + j) * D + n) = bf16_pack8(o);
+            }
+        }
+        __syncthreads();                                 // this half has been read
+        if (threadIdx.x == 0 && group + 2ll * gridDim.x < groups)
+            load(static_cast<int>(group + 2ll * gridDim.x), half);
+    }
+    if (s_abort) {                                       // copies in flight land first
+        for (int i = 0; i < 2; ++i, ++step)
+            if (threadIdx.x == 0 && blockIdx.x + static_cast<long long>(step) * gridDim.x < groups)
+                wait_drain(bars + 8 * (step & 1), (step >> 1) & 1u);
+        return;
+    }
     if (!parts) return;
+    float* sums = reinterpret_cast<float*>(smem);        // [teams, D]; nothing is in flight
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
         const int n = team.at(c);
         if (n >= D) continue;
-        float4* to = reinterpret_cast<float4*>(parts + static_cast<long long>(first) * D + n);
+        float4* to = reinterpret_cast<float4*>(
+            team.per_block > 1 ? sums + team.in_block * D + n
+                               : parts + static_cast<long long>(blockIdx.x) * D + n);
         to[0] = make_float4(dg[c][0], dg[c][1], dg[c][2], dg[c][3]);
         to[1] = make_float4(dg[c][4], dg[c][5], dg[c][6], dg[c][7]);
     }
+    if (team.per_block == 1) return;
+    __syncthreads();
+    for (int n = threadIdx.x; n < D; n += blockDim.x) {
+        float v = sums[n];
+        for (int t = 1; t < team.per_block; ++t) v += sums[t * D + n];
+        parts[static_cast<long long>(blockIdx.x) * D + n] = v;
+    }
 }
 
-// dgain[n] = sum over the teams' parts, in an order that depends on the sizes alone.
-constexpr int kJoinWarps = 8;
+// dgain[n] = sum over the blocks' parts, in an order that depends on the sizes alone.
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(kJoinWarps * 32)
-rmsnorm_join_kernel(const float* parts, int teams, int D, float* dgain) {
-    __shared__ float s[kJoinWarps][32];
+rmsnorm_join_kernel(const float* parts, int blocks, int D, float* dgain) {
+    __shared__ float s[kJoinWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = blockIdx.x * 32 + lane;
     start_dependent();
     float v = 0.0f;
     if (n < D) {
-#pragma unroll 4
-        for (int t = warp; t < teams; t += kJoinWarps)
-            v += ptx::load(parts + static_cast<long long>(t) * D + n);
+#pragma unroll 10
+        for (int b = warp; b < blocks; b += kJoinWarps)
+            v += ptx::load(parts + static_cast<long long>(b) * D + n);
     }
     s[warp][lane] = v;
     __syncthreads();
-    if (warp > 0 || n >= D) return;
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) v += s[w][lane];
-    dgain[n] = v;
+    v = warp_sum(s[lane][warp]);                         // of column `warp`
+    if (lane == 0 && blockIdx.x * 32 + warp < D) dgain[blockIdx.x * 32 + warp] = v;
 }
 
 // Warps per row, pieces per lane and threads per block for rows of D elements.
@@ -254,10 +310,24 @@ struct Shape {
     int teams_per_block() const { return threads / (32 * team_warps); }
 };
 
-int bwd_teams(int M, int D) {
-    const int most = kBwdBlocks * Shape(D).teams_per_block();
-    return M < most ? M : most;
-}
+// The gradient's grid: groups of whole teams' rows, shorter where there would be fewer
+// groups than blocks.
+struct BwdShape {
+    int group_rows, blocks;
+    size_t smem;
+    BwdShape(int M, int D) {
+        const Shape s(D);
+        const int teams = s.teams_per_block();
+        const int most = s.team_warps > kWarps ? kBwdBlocks / 2 : kBwdBlocks;
+        const int fair = ((M - 1) / most / teams + 1) * teams;
+        group_rows = kGroupElements / D / teams * teams;
+        if (group_rows < teams) group_rows = teams;
+        if (group_rows > fair) group_rows = fair;
+        const int groups = (M - 1) / group_rows + 1;
+        blocks = groups < most ? groups : most;
+        smem = 6ull * group_rows * D * sizeof(uint16_t);     // and room for the teams' sums
+    }
+};
 
 template <int kPieces>
 cudaError_t launch_fwd(const Shape& s, const RmsnormArgs& a, cudaStream_t stream) {
@@ -268,16 +338,29 @@ cudaError_t launch_fwd(const Shape& s, const RmsnormArgs& a, cudaStream_t stream
                             a.rstd);
 }
 
+// Devices (a bit each) on which a gradient's kernel may use its shared memory, by pieces.
+std::atomic<uint64_t> g_ready[kMaxPieces + 1];
+constexpr int kBwdSmem = 6 * kMaxTeamWarps * 32 * kMaxPieces * 8 * 2;
+
 template <int kPieces>
 cudaError_t launch_bwd(const Shape& s, const RmsnormBwdArgs& a, cudaStream_t stream) {
-    const int teams = bwd_teams(a.M, a.D), per_block = s.teams_per_block();
-    const cudaError_t err = launch_dependent(
-        rmsnorm_bwd_kernel<kPieces>, (teams + per_block - 1) / per_block, s.threads, 0, stream,
-        a.dy, a.dsum, a.sum, a.gain, a.rstd, a.M, a.D, s.team_warps, a.dx,
-        a.dgain ? a.parts : nullptr);
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(g_ready[kPieces].load() & bit)) {
+        err = cudaFuncSetAttribute(rmsnorm_bwd_kernel<kPieces>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+        if (err != cudaSuccess) return err;
+        g_ready[kPieces].fetch_or(bit);
+    }
+    const BwdShape b(a.M, a.D);
+    err = launch_dependent(rmsnorm_bwd_kernel<kPieces>, b.blocks, s.threads, b.smem, stream, a.dy,
+                           a.dsum, a.sum, a.gain, a.rstd, a.M, a.D, s.team_warps, b.group_rows,
+                           a.dx, a.dgain ? a.parts : nullptr, a.status, a.timeout_ns);
     if (err != cudaSuccess || !a.dgain) return err;
     return launch_dependent(rmsnorm_join_kernel, (a.D + 31) / 32, kJoinWarps * 32, 0, stream,
-                            a.parts, teams, a.D, a.dgain);
+                            a.parts, b.blocks, a.D, a.dgain);
 }
 
 }  // namespace
@@ -285,7 +368,11 @@ cudaError_t launch_bwd(const Shape& s, const RmsnormBwdArgs& a, cudaStream_t str
 int rmsnorm_max_elements() { return kMaxTeamWarps * 32 * kMaxPieces * 8; }
 
 size_t rmsnorm_bwd_workspace(int M, int D) {
-    return static_cast<size_t>(bwd_teams(M, D)) * static_cast<size_t>(D) * sizeof(float);
+    return static_cast<size_t>(BwdShape(M, D).blocks) * static_cast<size_t>(D) * sizeof(float);
+}
+
+void rmsnorm_reset_caches() {
+    for (auto& ready : g_ready) ready.store(0);
 }
 
 cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream) {

@@ -760,8 +760,8 @@ hg_status hg_get_device_status(hg_stream_t stream, uint32_t* detail);
 hg_status hg_selftest_wait_timeout(uint32_t timeout_us, hg_stream_t stream);
 
 /*
- * Per-wait limit of the waits of the GEMM, the few-token product and the gradient of the weights
- * in microseconds (default
+ * Per-wait limit of the waits of the GEMM, the few-token product and the gradients of the weights
+ * and of the norm in microseconds (default
  * 1000000).  Host-side setting, applied to later launches.  0 restores the
  * default.
  */
