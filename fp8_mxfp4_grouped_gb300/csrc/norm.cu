@@ -35,9 +35,19 @@ struct Team {
           in_block(threadIdx.x / (32 * team_warps)),
           per_block(blockDim.x / (32 * team_warps)) {}
     __device__ __forceinline__ int at(int c) const { return 8 * (rank + 32 * warps * c); }
-    // A barrier of the team's own: other teams of the block may be at other rows.
+    // A barrier of the team's own: other teams of the block may be at other rows.  (Barriers by
+    // number: one in a register would take all sixteen of the SM's per block.)
     __device__ __forceinline__ void sync() const {
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + in_block), "r"(32 * warps) : "memory");
+        switch (in_block) {
+            case 0: named_sync<1>(); break;
+            case 1: named_sync<2>(); break;
+            case 2: named_sync<3>(); break;
+            default: named_sync<4>(); break;             // teams of two warps: four a block
+        }
+    }
+    template <int kName>
+    __device__ __forceinline__ void named_sync() const {
+        asm volatile("bar.sync %0, %1;" ::"n"(kName), "r"(32 * warps) : "memory");
     }
 };
 
@@ -83,8 +93,8 @@ __device__ __noinline__ float wide_rstd(const Team team, const uint16_t* row, in
 
 constexpr float kWide = 1e37f;               // sums of squares from here on are done again
 
-template <int kPieces>
-__global__ void __launch_bounds__(kMaxTeamWarps * 32)
+template <int kPieces, bool kResidual>
+__global__ void __launch_bounds__(kMaxTeamWarps * 32, kResidual ? 2 : 3)
 rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* gain, int M, int D,
                float eps, int team_warps, uint16_t* sum, uint16_t* y, uint8_t* a_fp8,
                uint8_t* a_scale, float* rstd) {
@@ -101,14 +111,14 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* gain
         s[c] = add[c] = make_uint4(0, 0, 0, 0);
         if (n >= D) continue;
         s[c] = ptx::load(reinterpret_cast<const uint4*>(x + row * D + n));
-        if (residual) add[c] = ptx::load(reinterpret_cast<const uint4*>(residual + row * D + n));
+        if (kResidual) add[c] = ptx::load(reinterpret_cast<const uint4*>(residual + row * D + n));
     }
     float squares = 0.0f;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
         float f[8];
         bf16_unpack8(s[c], f);
-        if (residual) {
+        if (kResidual) {
             float g[8];
             bf16_unpack8(add[c], g);
 #pragma unroll
@@ -123,7 +133,7 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* gain
     }
     squares = team_sum(team, squares, part);
     const float r = squares < kWide ? 1.0f / sqrtf(squares / static_cast<float>(D) + eps)
-                                    : wide_rstd(team, (residual ? sum : x) + row * D, D, eps, wide_part);
+                                    : wide_rstd(team, (kResidual ? sum : x) + row * D, D, eps, wide_part);
     if (rstd && team.rank == 0) rstd[row] = r;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
@@ -333,7 +343,7 @@ template <int kPieces>
 cudaError_t launch_fwd(const Shape& s, const RmsnormArgs& a, cudaStream_t stream) {
     const int teams = s.teams_per_block();
     const int grid = static_cast<int>((static_cast<long long>(a.M) + teams - 1) / teams);
-    return launch_dependent(rmsnorm_kernel<kPieces>, grid, s.threads, 0, stream, a.x, a.residual,
+    return launch_dependent(a.residual ? rmsnorm_kernel<kPieces, true> : rmsnorm_kernel<kPieces, false>, grid, s.threads, 0, stream, a.x, a.residual,
                             a.gain, a.M, a.D, a.eps, s.team_warps, a.sum, a.y, a.a_fp8, a.a_scale,
                             a.rstd);
 }
