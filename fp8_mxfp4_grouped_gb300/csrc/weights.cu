@@ -16,50 +16,89 @@ namespace {
 constexpr int kGroup = 32;
 constexpr int kThreads = 256;
 
-// Eight consecutive weights in FP32.
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
-    bf16_unpack8(ptx::load(reinterpret_cast<const uint4*>(p)), f);
-}
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint4 v = ptx::load(reinterpret_cast<const uint4*>(p) + h);
-        f[4 * h] = __uint_as_float(v.x);
-        f[4 * h + 1] = __uint_as_float(v.y);
-        f[4 * h + 2] = __uint_as_float(v.z);
-        f[4 * h + 3] = __uint_as_float(v.w);
-    }
-}
-
 // 1 / scale; finite groups have codes up to 253.
 __device__ __forceinline__ float inverse(uint32_t code) {
     return __uint_as_float((254u - code) << 23);
 }
+// (of code 255: any BF16, and nothing beyond its bits)
+__device__ __forceinline__ uint32_t inverse_bf16(uint32_t code) {
+    return ((254u - code) << 7) & 0xFFFFu;
+}
 
-// Codes of eight of a group's weights and the group's scale; the group's largest
-// magnitude is amax (NaN if any weight is).
-__device__ __forceinline__ uint32_t codes8(const float (&f)[8], float amax, uint32_t& scale) {
-    scale = e8m0_weight_scale_code(amax);
-    if (scale == 255u) return 0u;
-    const float inv = inverse(scale);
-    float q[8];
+// Eight consecutive weights, FP32 or BF16.  Largest magnitudes of BF16 are taken on pairs of
+// them as they are: without its sign a BF16's bits are ordered as its value is, and a NaN
+// comes after Inf.  Products with a scale's inverse are exact but for what lies far below
+// the smallest code, in either type.
+template <class T>
+struct Eight;
+
+template <>
+struct Eight<float> {
+    float f[8];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = f[i] * inv;
-    return e2m1_pack8(q);
-}
-
-__device__ __forceinline__ float amax8(const float (&f)[8]) {
-    float m = 0.0f;
+        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+    }
+    __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
-    return m;
+        for (int h = 0; h < 2; ++h) {
+            const uint4 v = ptx::load(reinterpret_cast<const uint4*>(p) + h);
+            f[4 * h] = __uint_as_float(v.x);
+            f[4 * h + 1] = __uint_as_float(v.y);
+            f[4 * h + 2] = __uint_as_float(v.z);
+            f[4 * h + 3] = __uint_as_float(v.w);
+        }
+    }
+    __device__ __forceinline__ void store(uint32_t* to) const {
+        reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ float amax() const {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+        m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));      // four lanes hold a group
+        return max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    }
+    __device__ __forceinline__ uint32_t codes(uint32_t scale) const {
+        if (scale == 255u) return 0u;
+        const float inv = inverse(scale);
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = f[i] * inv;
+        return e2m1_pack8(q);
+    }
+};
+
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) {
+    return __vmaxu2(m, w & 0x7FFF7FFFu);
 }
 
-// Four lanes hold a group.
-__device__ __forceinline__ float quad_max(float m) {
-    m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    return max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-}
+template <>
+struct Eight<uint16_t> {
+    uint4 v;
+    __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const uint16_t* p) {
+        v = ptx::load(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void store(uint32_t* to) const { *reinterpret_cast<uint4*>(to) = v; }
+    __device__ __forceinline__ float amax() const {
+        uint32_t m = abs_max2(abs_max2(0u, v.x), v.y);
+        m = abs_max2(abs_max2(m, v.z), v.w);
+        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        return bf16_lo(max(m & 0xFFFFu, m >> 16));
+    }
+    __device__ __forceinline__ uint32_t codes(uint32_t scale) const {
+        if (scale == 255u) return 0u;
+        const uint32_t inv = inverse_bf16(scale) * 0x10001u;
+        float q[8];
+        bf16_unpack8(make_uint4(mul_bf16x2(v.x, inv), mul_bf16x2(v.y, inv), mul_bf16x2(v.z, inv),
+                                mul_bf16x2(v.w, inv)),
+                     q);
+        return e2m1_pack8(q);
+    }
+};
 
 // Along K alone the rows of all experts are one run of groups: eight weights a lane,
 // kBatch of them in flight.
@@ -71,21 +110,19 @@ quantize_weights_kernel(const T* w, long long pieces, uint8_t* q, uint8_t* scale
     start_dependent();
     const int lane = threadIdx.x & 31;
     const long long warp = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    float f[kBatch][8];
+    Eight<T> f[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
         const long long p = (warp * kBatch + b) * 32 + lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[b][i] = 0.0f;
-        if (p < pieces) load8(w + 8 * p, f[b]);
+        f[b].clear();
+        if (p < pieces) f[b].load(w + 8 * p);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
         const long long p = (warp * kBatch + b) * 32 + lane;
-        uint32_t code;
-        const uint32_t c = codes8(f[b], quad_max(amax8(f[b])), code);
+        const uint32_t code = e8m0_weight_scale_code(f[b].amax());
         if (p >= pieces) continue;
-        reinterpret_cast<uint32_t*>(q)[p] = c;
+        reinterpret_cast<uint32_t*>(q)[p] = f[b].codes(code);
         if ((lane & 3) == 0) scale[p / 4] = static_cast<uint8_t>(code);
     }
 }
@@ -106,93 +143,139 @@ struct Tile {
     }
 };
 
-__device__ __forceinline__ void word_values(uint32_t w, float (&v)[2], const uint16_t*) {
-    v[0] = bf16_lo(w);
-    v[1] = bf16_hi(w);
+// The 32 words of a column of FP32, or of two columns of BF16: codes and scales.
+__device__ __forceinline__ void column_codes(const uint32_t (&w)[kGroup], uint4 (&codes)[1],
+                                             uint32_t (&scale)[1]) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) amax = max_nan(amax, fabsf(__uint_as_float(w[i])));
+    scale[0] = e8m0_weight_scale_code(amax);
+    const float inv = inverse(scale[0]);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = __uint_as_float(w[8 * i + j]) * inv;
+        c[i] = scale[0] == 255u ? 0u : e2m1_pack8(q);
+    }
+    codes[0] = make_uint4(c[0], c[1], c[2], c[3]);
 }
-__device__ __forceinline__ void word_values(uint32_t w, float (&v)[2], const float*) {
-    v[0] = __uint_as_float(w);
+__device__ __forceinline__ void column_codes(const uint32_t (&w)[kGroup], uint4 (&codes)[2],
+                                             uint32_t (&scale)[2]) {
+    uint32_t amax = 0u;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) amax = abs_max2(amax, w[i]);
+    scale[0] = e8m0_weight_scale_code(bf16_lo(amax));
+    scale[1] = e8m0_weight_scale_code(bf16_hi(amax));
+    const uint32_t inv = inverse_bf16(scale[0]) | (inverse_bf16(scale[1]) << 16);
+    uint32_t c[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo[8], hi[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t q = mul_bf16x2(w[8 * i + j], inv);
+            lo[j] = bf16_lo(q);
+            hi[j] = bf16_hi(q);
+        }
+        c[0][i] = scale[0] == 255u ? 0u : e2m1_pack8(lo);
+        c[1][i] = scale[1] == 255u ? 0u : e2m1_pack8(hi);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) codes[h] = make_uint4(c[h][0], c[h][1], c[h][2], c[h][3]);
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 quantize_weights_both_kernel(const T* w, int N, int K, int tiles_n, int tiles_k, uint8_t* q,
                              uint8_t* scale, uint8_t* qt, uint8_t* scale_t) {
     using Tl = Tile<T>;
     __shared__ __align__(16) uint32_t s[kTileRows * 64];
     start_dependent();
-    const long long tile = blockIdx.x;
-    const int tn = static_cast<int>(tile % tiles_n);
-    const int tk = static_cast<int>(tile / tiles_n % tiles_k);
-    const long long e = tile / tiles_n / tiles_k;
+    const int tn = blockIdx.x % tiles_n, tk = blockIdx.x / tiles_n % tiles_k;
+    const long long e = blockIdx.x / tiles_n / tiles_k;
     const int n0 = tn * kTileRows, k0 = tk * Tl::kCols;
-    const T* we = w + e * N * K;
     constexpr int kRowsAtOnce = kThreads / Tl::kPieces, kSteps = kTileRows / kRowsAtOnce;
     const int piece = threadIdx.x % Tl::kPieces, r0 = threadIdx.x / Tl::kPieces;
     const int k = k0 + 8 * piece;
+    const long long first = (e * N + n0 + r0) * K + k;
 #pragma unroll
     for (int b0 = 0; b0 < kSteps; b0 += kBatch) {
-        float f[kBatch][8];
+        Eight<T> f[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int n = n0 + r0 + (b0 + b) * kRowsAtOnce;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[b][i] = 0.0f;
-            if (n < N && k < K) load8(we + static_cast<long long>(n) * K + k, f[b]);
+            const int r = (b0 + b) * kRowsAtOnce;
+            f[b].clear();
+            if (n0 + r0 + r < N && k < K) f[b].load(w + first + static_cast<long long>(r) * K);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + (b0 + b) * kRowsAtOnce, n = n0 + r;
-            uint32_t code;
-            const uint32_t c = codes8(f[b], quad_max(amax8(f[b])), code);
-            if (n < N && k < K) {
-                const long long at = (e * N + n) * K + k;
-                *reinterpret_cast<uint32_t*>(q + at / 2) = c;
+            const int r = (b0 + b) * kRowsAtOnce;
+            const uint32_t code = e8m0_weight_scale_code(f[b].amax());
+            if (n0 + r0 + r < N && k < K) {
+                const long long at = first + static_cast<long long>(r) * K;
+                *reinterpret_cast<uint32_t*>(q + at / 2) = f[b].codes(code);
                 if (piece % 4 == 0) scale[at / kGroup] = static_cast<uint8_t>(code);
             }
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<uint4*>(&s[Tl::word(r, 4 * piece)]) = bf16_pack8(f[b]);
-            } else {
-                *reinterpret_cast<float4*>(&s[Tl::word(r, 8 * piece)]) =
-                    make_float4(f[b][0], f[b][1], f[b][2], f[b][3]);
-                *reinterpret_cast<float4*>(&s[Tl::word(r, 8 * piece + 4)]) =
-                    make_float4(f[b][4], f[b][5], f[b][6], f[b][7]);
-            }
+            f[b].store(&s[Tl::word(r0 + r, 4 * piece * sizeof(T) / 2)]);
         }
     }
     __syncthreads();
     // lane = (group of rows, word): four lanes write 64 bytes of a column's codes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane & 3, word = 8 * warp + (lane >> 2);
-    const int n = n0 + g * kGroup;
-    if (n >= N) return;
+    const int n = n0 + g * kGroup, col = k0 + word * Tl::kPerWord;
+    if (n >= N || col >= K) return;
+    uint32_t v[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) v[i] = s[Tl::word(g * kGroup + i, word)];
+    uint4 codes[Tl::kPerWord];
+    uint32_t code[Tl::kPerWord];
+    column_codes(v, codes, code);
 #pragma unroll
     for (int h = 0; h < Tl::kPerWord; ++h) {
-        const int col = k0 + word * Tl::kPerWord + h;
-        if (col >= K) return;
-        float f[4][8], amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-            float v[2];
-            word_values(s[Tl::word(g * kGroup + i, word)], v, w);
-            f[i / 8][i % 8] = v[h];
-            amax = max_nan(amax, fabsf(v[h]));
-        }
-        uint32_t code = 0, c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = codes8(f[i], amax, code);
-        const long long at = (e * K + col) * N + n;
-        *reinterpret_cast<uint4*>(qt + at / 2) = make_uint4(c[0], c[1], c[2], c[3]);
-        scale_t[at / kGroup] = static_cast<uint8_t>(code);
+        const long long at = (e * K + col + h) * N + n;
+        *reinterpret_cast<uint4*>(qt + at / 2) = codes[h];
+        scale_t[at / kGroup] = static_cast<uint8_t>(code[h]);
     }
 }
 
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) = bf16_pack8(f);
+// Eight E2M1 values in FP16 times a scale's.
+__device__ __forceinline__ void decode(uint32_t (&h)[4], float value, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        f[2 * i] = v.x * value;
+        f[2 * i + 1] = v.y * value;
+    }
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+
+// A warp's 256 consecutive weights from the lanes' eight codes each and their scales, of the
+// lanes with `mine`.  Every lane takes part.
+__device__ __forceinline__ void store256(uint16_t* w, uint32_t codes, float value, bool mine) {
+    uint32_t h[4];
+    ptx::e2m1x8_to_f16(codes, h);
+    float f[8];
+    decode(h, value, f);
+    if (mine) reinterpret_cast<uint4*>(w)[threadIdx.x & 31] = bf16_pack8(f);
+}
+// FP32: a lane's eight would be 32 bytes, of which an instruction stores 16: the lanes
+// exchange halves, so that 32 lanes store 512 consecutive bytes twice.
+__device__ __forceinline__ void store256(float* w, uint32_t codes, float value, bool mine) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int from = 16 * j + lane / 2;
+        const uint32_t c = __shfl_sync(0xFFFFFFFFu, codes, from);
+        const float v = __shfl_sync(0xFFFFFFFFu, value, from);
+        const bool there = __shfl_sync(0xFFFFFFFFu, mine, from);
+        uint32_t h[4];
+        ptx::e2m1x8_to_f16(lane & 1 ? c >> 16 : c & 0xFFFFu, h);
+        float f[8];
+        decode(h, v, f);
+        if (there) reinterpret_cast<float4*>(w)[32 * j + lane] = make_float4(f[0], f[1], f[2], f[3]);
+    }
 }
 
 // Eight codes a lane, kBatch times.
@@ -213,19 +296,8 @@ dequantize_weights_kernel(const uint8_t* q, const uint8_t* scale, long long piec
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-        const long long p = (warp * kBatch + b) * 32 + lane;
-        if (p >= pieces) continue;
-        const float value = e8m0_value(code[b]);
-        uint32_t h[4];
-        ptx::e2m1x8_to_f16(c[b], h);
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-            f[2 * i] = v.x * value;
-            f[2 * i + 1] = v.y * value;
-        }
-        store8(w + 8 * p, f);
+        const long long p0 = (warp * kBatch + b) * 32;
+        store256(w + 8 * p0, c[b], e8m0_value(code[b]), p0 + lane < pieces);
     }
 }
 
