@@ -25,10 +25,10 @@ __device__ __forceinline__ uint32_t inverse_bf16(uint32_t code) {
     return ((254u - code) << 7) & 0xFFFFu;
 }
 
-// Eight consecutive weights, FP32 or BF16.  Largest magnitudes of BF16 are taken on pairs of
-// them as they are: without its sign a BF16's bits are ordered as its value is, and a NaN
-// comes after Inf.  Products with a scale's inverse are exact but for what lies far below
-// the smallest code, in either type.
+// Eight consecutive weights, FP32 or BF16.  BF16 are taken two at a time where they can be,
+// and away from the pipe of the integer instructions, comparisons and conversions, which
+// bounds the kernel that quantises in both orientations: 32 x 4096 x 6144 in 615 us with
+// every weight widened, 511 so.
 template <class T>
 struct Eight;
 
@@ -70,8 +70,20 @@ struct Eight<float> {
     }
 };
 
-__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) {
-    return __vmaxu2(m, w & 0x7FFF7FFFu);
+// Larger magnitudes of pairs, whatever their signs; NaN if either is.
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+// The two of a word times the two of another, in FP32, -0 staying -0.
+__device__ __forceinline__ float2 scaled2(uint32_t w, uint32_t by) {
+    float2 f;
+    asm("{\n\t.reg .b16 lo, hi, i, j;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b32 {i, j}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, lo, i, 0f80000000;\n\tfma.rn.f32.bf16 %1, hi, j, 0f80000000;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(w), "r"(by));
+    return f;
 }
 
 template <>
@@ -83,19 +95,21 @@ struct Eight<uint16_t> {
     }
     __device__ __forceinline__ void store(uint32_t* to) const { *reinterpret_cast<uint4*>(to) = v; }
     __device__ __forceinline__ float amax() const {
-        uint32_t m = abs_max2(abs_max2(0u, v.x), v.y);
-        m = abs_max2(abs_max2(m, v.z), v.w);
-        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        return bf16_lo(max(m & 0xFFFFu, m >> 16));
+        uint32_t m = abs_max2(abs_max2(v.x, v.y), abs_max2(v.z, v.w));
+        m = abs_max2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = abs_max2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) & 0x7FFF7FFFu;
+        return bf16_lo(max(m & 0xFFFFu, m >> 16));       // ordered as their bits are, NaN last
     }
     __device__ __forceinline__ uint32_t codes(uint32_t scale) const {
         if (scale == 255u) return 0u;
-        const uint32_t inv = inverse_bf16(scale) * 0x10001u;
+        const uint32_t inv = inverse_bf16(scale) * 0x10001u, w[4] = {v.x, v.y, v.z, v.w};
         float q[8];
-        bf16_unpack8(make_uint4(mul_bf16x2(v.x, inv), mul_bf16x2(v.y, inv), mul_bf16x2(v.z, inv),
-                                mul_bf16x2(v.w, inv)),
-                     q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = scaled2(w[i], inv);
+            q[2 * i] = f.x;
+            q[2 * i + 1] = f.y;
+        }
         return e2m1_pack8(q);
     }
 };
@@ -163,10 +177,10 @@ __device__ __forceinline__ void column_codes(const uint32_t (&w)[kGroup], uint4 
 }
 __device__ __forceinline__ void column_codes(const uint32_t (&w)[kGroup], uint4 (&codes)[2],
                                              uint32_t (&scale)[2]) {
-    uint32_t amax = 0u;
+    uint32_t amax = w[0];
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) amax = abs_max2(amax, w[i]);
-    scale[0] = e8m0_weight_scale_code(bf16_lo(amax));
+    for (int i = 1; i < kGroup; ++i) amax = abs_max2(amax, w[i]);
+    scale[0] = e8m0_weight_scale_code(bf16_lo(amax));    // which does not ask for the sign
     scale[1] = e8m0_weight_scale_code(bf16_hi(amax));
     const uint32_t inv = inverse_bf16(scale[0]) | (inverse_bf16(scale[1]) << 16);
     uint32_t c[2][4];
@@ -175,9 +189,9 @@ __device__ __forceinline__ void column_codes(const uint32_t (&w)[kGroup], uint4 
         float lo[8], hi[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t q = mul_bf16x2(w[8 * i + j], inv);
-            lo[j] = bf16_lo(q);
-            hi[j] = bf16_hi(q);
+            const float2 q = scaled2(w[8 * i + j], inv);
+            lo[j] = q.x;
+            hi[j] = q.y;
         }
         c[0][i] = scale[0] == 255u ? 0u : e2m1_pack8(lo);
         c[1][i] = scale[1] == 255u ? 0u : e2m1_pack8(hi);
