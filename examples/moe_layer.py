@@ -4,6 +4,9 @@
 * ``train_step``: forward and backward through a layer whose experts are frozen (only what
   lies around them learns: the router, and the layers below through dx).  Activations cross
   the experts in FP8; the SwiGLU's input is kept as an 8-bit checkpoint.
+* ``train_block``: the layer behind its norm, with the residual stream, and the experts learn
+  too: gradients of their weights from the FP8 activations that the forward pass kept, and
+  ``Experts.quantize`` writes updated master weights over the 4-bit ones.
 * ``decode``: the same layer for the few tokens of a decoding step, in four launches (the
   numbers of the slots, which never change, are made once by the caller).
 
@@ -18,7 +21,6 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from fp8_mxfp4_grouped_gb300 import hg  # noqa: E402
-from synth import quantize_weights  # noqa: E402
 
 
 @dataclass
@@ -33,28 +35,39 @@ class Experts:
 
     @staticmethod
     def from_float(gate_up: torch.Tensor, down: torch.Tensor) -> "Experts":
-        """gate_up [E, 2F, D], down [E, D, F], float32."""
-        return Experts(quantize_weights(gate_up), quantize_weights(down),
-                       quantize_weights(gate_up.transpose(1, 2).contiguous()),
-                       quantize_weights(down.transpose(1, 2).contiguous()))
+        """gate_up [E, 2F, D], down [E, D, F], float32 or BF16."""
+        g, d = (hg.hg_quantize_weights(w, transposed=True) for w in (gate_up, down))
+        return Experts(g[:2], d[:2], g[2:], d[2:])
+
+    def quantize(self, gate_up: torch.Tensor, down: torch.Tensor):
+        """The same weights after an update, over the ones that are there."""
+        hg.hg_quantize_weights(gate_up, True, *self.gate_up, *self.gate_up_t)
+        hg.hg_quantize_weights(down, True, *self.down, *self.down_t)
 
 
-def forward(x, logits, top_k, experts, keep=True):
-    """x [M, D] BF16, logits [M, E] float32 -> out [M, D] BF16 and what the backward needs."""
+def forward(x, logits, top_k, experts, keep=True, acts=None):
+    """x [M, D] BF16, logits [M, E] float32 -> out [M, D] BF16 and what the backward needs.
+    acts: x as FP8 codes with scales, where the norm before has made them."""
     E = logits.shape[1]
     ids, weights = hg.hg_router_topk(logits, top_k)
     offsets, _, place = hg.hg_plan_expert_offsets(ids, E)
-    a, a_scale = hg.hg_quantize_scatter_acts(x, top_k, place)
+    if acts is None:
+        a, a_scale = hg.hg_quantize_scatter_acts(x, top_k, place)
+    else:
+        a, a_scale = hg.hg_dispatch_acts(*acts, top_k, place)
     z = hg.hg_grouped_w4a8_gemm(a, a_scale, *experts.gate_up, offsets)
     h, h_scale, z8, z8_scale = hg.hg_swiglu_quantize(z, checkpoint=keep)
     y = hg.hg_grouped_w4a8_gemm(h, h_scale, *experts.down, offsets)
     out = hg.hg_combine_topk(y, place, weights)
-    return out, (logits, ids, weights, offsets, place, z8, z8_scale, y) if keep else None
+    if not keep:
+        return out, None
+    return out, (logits, ids, weights, offsets, place, z8, z8_scale, y, (a, a_scale), (h, h_scale))
 
 
-def backward(dout, ctx, top_k, experts):
-    """(dx [M, D] BF16, dlogits [M, E] float32) of dout [M, D] BF16."""
-    logits, ids, weights, offsets, place, z8, z8_scale, y = ctx
+def backward(dout, ctx, top_k, experts, weight_grads=False):
+    """(dx [M, D] BF16, dlogits [M, E] float32) of dout [M, D] BF16, and with weight_grads the
+    gradients of gate_up [E, 2F, D] and down [E, D, F] in float32."""
+    logits, ids, weights, offsets, place, z8, z8_scale, y, acts, hidden = ctx
     rows = torch.arange(y.shape[0], dtype=torch.int32, device=y.device)
     dy, dweights = hg.hg_combine_topk_bwd(dout, y, place, weights)
     q, s = hg.hg_quantize_scatter_acts(dy, 1, rows)
@@ -64,12 +77,28 @@ def backward(dout, ctx, top_k, experts):
     dxs = hg.hg_grouped_w4a8_gemm(q, s, *experts.gate_up_t, offsets)
     dx, _ = hg.hg_dispatch_tokens_bwd(dxs, top_k, place)
     dlogits = hg.hg_router_topk_bwd(logits, ids, weights, dweights)
-    return dx, dlogits
+    if not weight_grads:
+        return dx, dlogits
+    return dx, dlogits, (hg.hg_grouped_wgrad_fp8(dz, *acts, offsets),
+                         hg.hg_grouped_wgrad_fp8(dy, *hidden, offsets))
 
 
 def train_step(x, logits, dout, top_k, experts):
     out, ctx = forward(x, logits, top_k, experts)
     return (out, *backward(dout, ctx, top_k, experts))
+
+
+def train_block(x, residual, gain, router, dout, top_k, experts):
+    """One training step of s = x + residual, y = s + layer(norm(s) * gain): x, residual and dout
+    [M, D] BF16, gain [D] BF16, router [D, E] float32.  Returns y, the gradient of x (and of
+    residual, which is the same), of gain, of router, and of the experts' weights."""
+    n, a, a_scale, s, rstd = hg.hg_rmsnorm_quantize(x, gain, residual=residual)
+    out, ctx = forward(n, n.float() @ router, top_k, experts, acts=(a, a_scale))
+    dn, dlogits, dexperts = backward(dout, ctx, top_k, experts, weight_grads=True)
+    drouter = n.float().T @ dlogits
+    dn = (dn.float() + dlogits @ router.T).bfloat16()
+    dx, dgain = hg.hg_rmsnorm_bwd(dn, s, gain, rstd, dsum=dout)
+    return s + out, dx, dgain, drouter, dexperts
 
 
 def slot_numbers(tokens, top_k, device="cuda"):
@@ -96,7 +125,8 @@ def main():
     def normal(*shape):
         return torch.randn(*shape, generator=gen, device="cuda")
 
-    experts = Experts.from_float(normal(E, 2 * F, D) / D ** 0.5, normal(E, D, F) / F ** 0.5)
+    masters = [normal(E, 2 * F, D) / D ** 0.5, normal(E, D, F) / F ** 0.5]
+    experts = Experts.from_float(*masters)
     router = normal(D, E) / D ** 0.5
     x, dout = normal(512, D).bfloat16(), normal(512, D).bfloat16()
     out, dx, dlogits = train_step(x, x.float() @ router, dout, top_k, experts)
@@ -107,6 +137,14 @@ def main():
                  slot_numbers(3, top_k))
     off = float((few.float() - out[:3].float()).norm() / out[:3].float().norm())
     print("decode: out", tuple(few.shape), "relative difference from the FP8 path", round(off, 4))
+    gain = (1 + 0.1 * normal(D)).bfloat16()
+    y, _, dgain, _, dexperts = train_block(x, (3 * normal(512, D)).bfloat16(), gain, router, dout,
+                                           top_k, experts)
+    for w, dw in zip(masters, dexperts):
+        w.sub_(1e-3 * dw)
+    experts.quantize(*masters)
+    print("block: y", tuple(y.shape), "gain gradient norm", round(float(dgain.norm()), 4),
+          "expert gradient norms", *(round(float(g.norm()), 2) for g in dexperts))
     status, detail = hg.hg_get_device_status()
     if status != hg.HG_OK:
         raise SystemExit(f"device status {status} detail {detail}")
