@@ -160,16 +160,20 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* gain
     }
 }
 
-// The gradient: a block takes groups of consecutive rows in turn, some 8192 elements of each
+// The gradient: a block takes groups of consecutive rows in turn, some 6144 elements of each
 // array a group, which bulk copies bring into one half of its shared memory while the other
 // half is worked on.  Rows stay there for their second pass; a thread keeps its columns'
 // gains and its part of dgain in registers.  The parts of a block's teams are added up, then
 // written to the workspace, a row a block, and joined in the order of the blocks.
-constexpr int kGroupElements = 8192;
-constexpr int kBwdBlocks = 2 * 152;          // two a SM, of up to eight warps
+constexpr int kGroupElements = 6144;
 
-template <int kPieces>
-__global__ void __launch_bounds__(kMaxTeamWarps * 32)
+// Blocks of an SM that there are registers for.
+constexpr int bwd_blocks(int threads, int pieces) {
+    return threads > kWarps * 32 ? 1 : pieces < kMaxPieces ? 3 : 2;
+}
+
+template <int kPieces, int kThreads>
+__global__ void __launch_bounds__(kThreads, bwd_blocks(kThreads, kPieces))
 rmsnorm_bwd_kernel(const uint16_t* dy, const uint16_t* dsum, const uint16_t* sum,
                    const uint16_t* gain, const float* rstd, int M, int D, int team_warps,
                    int group_rows, uint16_t* dx, float* parts, uint32_t* status,
@@ -321,21 +325,24 @@ struct Shape {
 };
 
 // The gradient's grid: groups of whole teams' rows, shorter where there would be fewer
-// groups than blocks.
-struct BwdShape {
+// groups than blocks, and as many blocks as 152 SMs hold at once.
+constexpr size_t kSmSmem = 228 * 1024, kBlockSmem = 2048;      // of an SM; beside the groups
+struct BwdShape : Shape {
     int group_rows, blocks;
     size_t smem;
-    BwdShape(int M, int D) {
-        const Shape s(D);
-        const int teams = s.teams_per_block();
-        const int most = s.team_warps > kWarps ? kBwdBlocks / 2 : kBwdBlocks;
-        const int fair = ((M - 1) / most / teams + 1) * teams;
+    BwdShape(int M, int D) : Shape(D) {
+        const int teams = teams_per_block();
         group_rows = kGroupElements / D / teams * teams;
         if (group_rows < teams) group_rows = teams;
+        const auto bytes = [&] { return 6ull * group_rows * D * sizeof(uint16_t); };
+        int per_sm = bwd_blocks(threads, pieces);
+        if (per_sm > static_cast<int>(kSmSmem / (bytes() + kBlockSmem)))
+            per_sm = static_cast<int>(kSmSmem / (bytes() + kBlockSmem));
+        const int most = 152 * per_sm, fair = ((M - 1) / most / teams + 1) * teams;
         if (group_rows > fair) group_rows = fair;
         const int groups = (M - 1) / group_rows + 1;
         blocks = groups < most ? groups : most;
-        smem = 6ull * group_rows * D * sizeof(uint16_t);     // and room for the teams' sums
+        smem = bytes();                      // and room for the teams' sums
     }
 };
 
@@ -348,29 +355,30 @@ cudaError_t launch_fwd(const Shape& s, const RmsnormArgs& a, cudaStream_t stream
                             a.rstd);
 }
 
-// Devices (a bit each) on which a gradient's kernel may use its shared memory, by pieces.
-std::atomic<uint64_t> g_ready[kMaxPieces + 1];
-constexpr int kBwdSmem = 6 * kMaxTeamWarps * 32 * kMaxPieces * 8 * 2;
+// Devices (a bit each) on which a gradient's kernel may use its shared memory, by pieces and
+// whether a team has sixteen warps.
+std::atomic<uint64_t> g_ready[kMaxPieces + 1][2];
 
-template <int kPieces>
-cudaError_t launch_bwd(const Shape& s, const RmsnormBwdArgs& a, cudaStream_t stream) {
+template <int kPieces, int kThreads>
+cudaError_t launch_bwd(const BwdShape& s, const RmsnormBwdArgs& a, cudaStream_t stream) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
+    const auto kernel = rmsnorm_bwd_kernel<kPieces, kThreads>;
+    std::atomic<uint64_t>& ready = g_ready[kPieces][kThreads > kWarps * 32];
     const uint64_t bit = 1ull << (dev & 63);
-    if (!(g_ready[kPieces].load() & bit)) {
-        err = cudaFuncSetAttribute(rmsnorm_bwd_kernel<kPieces>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    if (!(ready.load() & bit)) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   6 * kMaxTeamWarps * 32 * kMaxPieces * 8 * 2);
         if (err != cudaSuccess) return err;
-        g_ready[kPieces].fetch_or(bit);
+        ready.fetch_or(bit);
     }
-    const BwdShape b(a.M, a.D);
-    err = launch_dependent(rmsnorm_bwd_kernel<kPieces>, b.blocks, s.threads, b.smem, stream, a.dy,
-                           a.dsum, a.sum, a.gain, a.rstd, a.M, a.D, s.team_warps, b.group_rows,
-                           a.dx, a.dgain ? a.parts : nullptr, a.status, a.timeout_ns);
+    err = launch_dependent(kernel, s.blocks, s.threads, s.smem, stream, a.dy, a.dsum, a.sum, a.gain,
+                           a.rstd, a.M, a.D, s.team_warps, s.group_rows, a.dx,
+                           a.dgain ? a.parts : nullptr, a.status, a.timeout_ns);
     if (err != cudaSuccess || !a.dgain) return err;
     return launch_dependent(rmsnorm_join_kernel, (a.D + 31) / 32, kJoinWarps * 32, 0, stream,
-                            a.parts, b.blocks, a.D, a.dgain);
+                            a.parts, s.blocks, a.D, a.dgain);
 }
 
 }  // namespace
@@ -382,7 +390,8 @@ size_t rmsnorm_bwd_workspace(int M, int D) {
 }
 
 void rmsnorm_reset_caches() {
-    for (auto& ready : g_ready) ready.store(0);
+    for (auto& pieces : g_ready)
+        for (auto& ready : pieces) ready.store(0);
 }
 
 cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream) {
@@ -395,12 +404,18 @@ cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, cudaStream_t stream) {
-    const Shape s(a.D);
-    const auto launch = s.pieces == 1   ? launch_bwd<1>
-                        : s.pieces == 2 ? launch_bwd<2>
-                        : s.pieces == 3 ? launch_bwd<3>
-                                        : launch_bwd<4>;
-    return launch(s, a, stream);
+    constexpr int kSmall = kWarps * 32, kLarge = kMaxTeamWarps * 32;
+    const BwdShape s(a.M, a.D);
+    if (s.threads == kSmall) {
+        const auto launch = s.pieces == 1   ? launch_bwd<1, kSmall>
+                            : s.pieces == 2 ? launch_bwd<2, kSmall>
+                            : s.pieces == 3 ? launch_bwd<3, kSmall>
+                                            : launch_bwd<4, kSmall>;
+        return launch(s, a, stream);
+    }
+    // more than 8192 elements: at least three pieces a lane
+    return s.pieces == 3 ? launch_bwd<3, kLarge>(s, a, stream)
+                         : launch_bwd<4, kLarge>(s, a, stream);
 }
 
 }  // namespace hg
