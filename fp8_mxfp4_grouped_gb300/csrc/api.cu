@@ -275,19 +275,13 @@ hg_status map_3d(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMapDataType t
                : HG_ERR_CUDA;
 }
 
-// An operand [rows, cols] BF16 as wgrad_panels has it, in both heights of boxes.
-hg_status operand_maps(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* p, int32_t rows,
-                       int32_t cols, CUtensorMap (&out)[2]) {
+// An operand [rows, cols] BF16 as wgrad_panels has it.
+hg_status operand_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* p, int32_t rows,
+                      int32_t cols, CUtensorMap* out) {
     const cuuint64_t r = static_cast<cuuint64_t>(rows), c = static_cast<cuuint64_t>(cols);
     const bool whole = wgrad_panels(cols) == 2;
-    for (int i = 0; i < 2; ++i) {
-        const hg_status st = map_3d(
-            encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, {whole ? 64 : c, r, whole ? c / 64 : 1},
-            {2 * c, whole ? 128 : 2 * c * r},
-            {64, static_cast<cuuint32_t>(i ? kWgradRows : kWgradRows / 2), whole ? 2u : 1u}, &out[i]);
-        if (st != HG_OK) return st;
-    }
-    return HG_OK;
+    return map_3d(encode, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, {whole ? 64 : c, r, whole ? c / 64 : 1},
+                  {2 * c, whole ? 128 : 2 * c * r}, {64, kWgradRows, whole ? 2u : 1u}, out);
 }
 
 // The result, [matrices, rows, cols].
@@ -345,8 +339,8 @@ hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scal
     const int32_t map_rows = rows > 0 ? rows : 1;
     const bool out_f32 = a.f32 || a.parts;
     WgradMaps maps;
-    st = operand_maps(encode, rows > 0 ? dy : dw, map_rows, N, maps.dy);
-    if (st == HG_OK) st = operand_maps(encode, rows > 0 ? x : dw, map_rows, K, maps.x);
+    st = operand_map(encode, rows > 0 ? dy : dw, map_rows, N, &maps.dy);
+    if (st == HG_OK) st = operand_map(encode, rows > 0 ? x : dw, map_rows, K, &maps.x);
     if (st == HG_OK)
         st = result_map(encode, out_f32, a.parts ? static_cast<void*>(a.parts) : dw,
                         static_cast<long long>(E) * (a.parts ? wgrad_splits(E, N, K, rows) : 1), N,

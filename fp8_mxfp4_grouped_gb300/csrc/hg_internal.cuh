@@ -295,13 +295,13 @@ int wgrad_splits(int E, int N, int K, int rows);
 size_t wgrad_parts_bytes(int E, int N, int K, int rows);
 bool wgrad_fits(int E, int N, int K, int rows);     // the grid's numbers and the maps' strides
 // Tensor maps, all with the 128-byte swizzle: dy [rows, N] and x [rows, K] in boxes of
-// half of kWgradRows rows and of all x wgrad_panels panels of 64 columns, as [rows, N] or as
-// [N/64, rows, 64]; the output (the parts where the rows are split) [E or parts, N, K] in boxes of 32 rows x
+// kWgradRows rows x wgrad_panels panels of 64 columns, as [rows, N] or as [N/64, rows, 64];
+// the output (the parts where the rows are split) [E or parts, N, K] in boxes of 32 rows x
 // 128 bytes.
 constexpr int kWgradRows = 128;
 int wgrad_panels(int cols);
 struct WgradMaps {
-    CUtensorMap dy[2], x[2], out;
+    CUtensorMap dy, x, out;
 };
 cudaError_t launch_wgrad(const WgradArgs& a, const WgradMaps& maps, int num_sms,
                          cudaStream_t stream);

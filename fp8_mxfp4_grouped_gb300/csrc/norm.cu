@@ -14,6 +14,13 @@
 // that holds it in registers, up to four pieces of eight elements a lane, so that
 // everything is read once; a half-warp's sixteen pieces are one 128-element group of
 // the scales.
+//
+// Measured: 16384 x 6144 with a residual and all outputs 131 us for 907 MB (6.9 TB/s; a
+// persistent grid that asks for the next row ahead 149), the FP8 output alone 73 us, BF16 alone
+// 68; the gradient of 8199 x 6144 with the residual's 70 us for 403 MB (5.7 TB/s), of 16384 x 6144
+// 127 us (6.3 TB/s), of which some 6 us join the parts of dgain.  With the rows in registers, and
+// loads that waited for the row before, the gradient took 106 us at 8199 x 6144 and 78 at
+// 16384 x 1024 (now 31).
 #include <atomic>
 
 #include "hg_internal.cuh"

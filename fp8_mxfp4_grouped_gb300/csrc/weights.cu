@@ -6,7 +6,10 @@
 //   e = smallest integer with amax <= 6 * 2^e (0 for amax = 0), in [-127, 127]
 //   code = nearest E2M1 value of w / 2^e, ties to the even code; scale = 127 + e
 //
-// Both directions are bound by memory.
+// Along K alone and back it is bound by memory: 32 x 4096 x 6144 from BF16 278 us (7.3 TB/s),
+// from FP32 494; back to BF16 292 us, to FP32 525 (7.0 TB/s).  In both orientations 428 us from
+// BF16 (5.8 TB/s; the ALU pipe is busy for 59 % of the time) and 691 from FP32 (5.9): the tiles
+// of a persistent grid copied ahead into shared memory took 630 and 736.
 #include "hg_internal.cuh"
 #include "numeric.cuh"
 

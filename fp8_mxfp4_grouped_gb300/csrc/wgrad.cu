@@ -8,7 +8,7 @@
 //
 // A CTA pair computes 256 x 256 of one expert's dw with tcgen05 cta_group::2 MMAs (M = 256,
 // N = 256, K = 16 rows).  The rows of dy and x are the K of the product, so that both
-// operands lie in memory with K as the slow axis: TMA boxes of 64 rows x 64 columns are
+// operands lie in memory with K as the slow axis: TMA boxes of 128 rows x 64 columns are
 // MN-major panels as they are.  Roles in a CTA: warp 0 TMA producer, warp 1 TMEM
 // allocation and (in the even CTA) MMA issue, warp 2 the last stage of an expert, warps
 // 4-11 epilogue.  An expert's last stage can hold rows of the next expert: warp 2 clears
@@ -25,6 +25,16 @@
 // 2^-24 of itself with each MMA, 9e-7 of a sum of positive terms over 512 rows and 1.8e-4
 // over 32768.  After kChunk stages the epilogue therefore takes an accumulator over into
 // its registers, where sums round.
+//
+// What bounds it: for long sums the tensor cores (4 x 4096 x 4096 over 32768 rows, BF16, 597 us,
+// 1840 TFLOP/s); for experts of some 512 rows the SMs' ports to the L2, where the copies' requests
+// and the stores of dw add up (32 x 4096 x 6144 in FP32 over 16384 rows 793 us, 834 to 848 from
+// FP8; the port is busy for 74 % of the time, 49 % with dw, the tensor cores for 48 %, HBM for
+// 57 %).  Copies alone take 396 us there, the stores 494, both 709; the MMAs at the rate of
+// long sums would take 454.  Tried and not kept: stores by the threads instead of TMA (955 us, from
+// registers 890), 16 KB store boxes (809), two store buffers a warp for a stage less (867), dy
+// kept in shared memory for several tiles with x in the two remaining slots (1040: too few
+// bytes of x in flight), the tiles walked along k (795), pairs started apart in time (no change).
 #include <atomic>
 
 #include "hg_internal.cuh"
@@ -37,7 +47,8 @@ constexpr int kTile = 256;                   // dw rows and columns of a pair's 
 constexpr int kHalf = 128;                   // dy columns and x columns that a CTA loads
 constexpr int kEpiWarps = 8;                 // four lane quarters x two halves of the columns
 constexpr int kEpiCols = kTile * 4 / kEpiWarps;
-constexpr int kOperand = kWgradRows * kHalf * 2;         // bytes of a CTA's part of a stage
+constexpr int kPanel = kWgradRows * 128;     // bytes of a stage of 64 16-bit columns
+constexpr int kOperand = 2 * kPanel;         // a CTA's part of an operand's stage
 constexpr int kOutBuf = 32 * 128;            // a warp's 32 rows x 128 bytes of output
 constexpr int kTmemCols = 512;               // two accumulators of 256 columns
 constexpr int kMmaRows = 16;                 // K of an MMA
@@ -87,10 +98,6 @@ struct Unit {
     __device__ __forceinline__ bool mixed(int stage) const {
         return rows - stage * kWgradRows < kWgradRows && rows % kMmaRows != 0;
     }
-    // rows that a stage has room for: half of the boxes' where no more are left
-    __device__ __forceinline__ int room(int stage) const {
-        return valid(stage) > kWgradRows / 2 ? kWgradRows : kWgradRows / 2;
-    }
     // rows of a stage that belong to the unit
     __device__ __forceinline__ int valid(int stage) const {
         return min(kWgradRows, rows - stage * kWgradRows);
@@ -104,25 +111,22 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
                  : "memory");
 }
 
-// Clear rows [first, last) of an operand's stage with room for `room` (whole warp).
-__device__ __forceinline__ void clear_rows(uint32_t operand, int room, int first, int last) {
+// Clear rows [first, last) of an operand's stage (whole warp).
+__device__ __forceinline__ void clear_rows(uint32_t operand, int first, int last) {
     operand += first * 128;
     for (int i = threadIdx.x & 31; i < (last - first) * 16; i += 32)
-        sts_v4(operand + ((i >> 3) & 1) * room * 128 + (i >> 4) * 128 + (i & 7) * 16, 0u, 0u, 0u,
-               0u);
+        sts_v4(operand + ((i >> 3) & 1) * kPanel + (i >> 4) * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
 }
 
 // A CTA's 128 columns of a stage, counted on a barrier of either CTA: two panels of 64
 // columns, one behind the other.
-__device__ __forceinline__ void load_stage(uint32_t to, const CUtensorMap (&maps)[2], int panels,
-                                           int room, int col, int row, uint32_t bar,
-                                           uint64_t policy) {
-    const CUtensorMap* map = &maps[room == kWgradRows];
+__device__ __forceinline__ void load_stage(uint32_t to, const CUtensorMap* map, int panels, int col,
+                                           int row, uint32_t bar, uint64_t policy) {
     if (panels == 2) {
         ptx::tma_load_3d_pair_elect(to, map, 0, row, col / 64, bar, policy);
     } else {
         ptx::tma_load_3d_pair_elect(to, map, col, row, 0, bar, policy);
-        ptx::tma_load_3d_pair_elect(to + room * 128, map, col + 64, row, 0, bar, policy);
+        ptx::tma_load_3d_pair_elect(to + kPanel, map, col + 64, row, 0, bar, policy);
     }
 }
 
@@ -171,10 +175,8 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
         ptx::tmem_relinquish_pair();
     }
     if (warp == 0 && lane == 0) {
-        for (int i = 0; i < 2; ++i) {
-            ptx::prefetch_tensormap(&maps.dy[i]);
-            ptx::prefetch_tensormap(&maps.x[i]);
-        }
+        ptx::prefetch_tensormap(&maps.dy);
+        ptx::prefetch_tensormap(&maps.x);
         ptx::prefetch_tensormap(&maps.out);
     }
     // Nothing above reads global memory.
@@ -213,18 +215,17 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
                                 slot)))
                     break;
                 const int row = t.row0 + s * kWgradRows;
-                const int room = t.room(s), bytes = 2 * room * kHalf * 2;     // of this CTA
                 uint32_t bar = full + 8 * slot;
                 if (t.mixed(s)) {
                     bar = last + 8 * slot;
-                    ptx::mbar_arrive_expect_tx_elect(bar_last + 8 * slot, bytes);
+                    ptx::mbar_arrive_expect_tx_elect(bar_last + 8 * slot, 2 * kOperand);
                 } else if (leader) {
-                    ptx::mbar_arrive_expect_tx_elect(bar_full + 8 * slot, 2 * bytes);
+                    ptx::mbar_arrive_expect_tx_elect(bar_full + 8 * slot, 4 * kOperand);
                 }
-                load_stage(sbase + kOffA + slot * kOperand, maps.dy, shape.dy_panels, room, n, row,
-                           bar, policy);
-                load_stage(sbase + kOffB + slot * kOperand, maps.x, shape.x_panels, room, k, row,
-                           bar, policy);
+                load_stage(sbase + kOffA + slot * kOperand, &maps.dy, shape.dy_panels, n, row, bar,
+                           policy);
+                load_stage(sbase + kOffB + slot * kOperand, &maps.x, shape.x_panels, k, row, bar,
+                           policy);
             }
         }
         // No copy may land, and no release of a stage arrive, after the CTA has gone: what the
@@ -254,9 +255,9 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
                         break;
                     ptx::tc_fence_after();
                     const uint64_t a =
-                        ptx::desc_mnmajor_sw128(sbase + kOffA + slot * kOperand, t.room(s) * 128);
+                        ptx::desc_mnmajor_sw128(sbase + kOffA + slot * kOperand, kPanel);
                     const uint64_t x =
-                        ptx::desc_mnmajor_sw128(sbase + kOffB + slot * kOperand, t.room(s) * 128);
+                        ptx::desc_mnmajor_sw128(sbase + kOffB + slot * kOperand, kPanel);
                     const int steps = (t.valid(s) + kMmaRows - 1) / kMmaRows;
                     for (int i = 0; i < steps; ++i) {
                         // 16 rows of 128 bytes on, in the descriptor's 16-byte units
@@ -369,8 +370,8 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
                 const int valid = t.valid(s);
                 const int used = (valid + kMmaRows - 1) / kMmaRows * kMmaRows;
                 if (!(ok = wait(bar_last + 8 * slot, parity, kRoleWorker, slot))) break;
-                clear_rows(sbase + kOffA + slot * kOperand, t.room(s), valid, used);
-                clear_rows(sbase + kOffB + slot * kOperand, t.room(s), valid, used);
+                clear_rows(sbase + kOffA + slot * kOperand, valid, used);
+                clear_rows(sbase + kOffB + slot * kOperand, valid, used);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (leader && !(ok = wait(bar_clear + 8 * slot, parity, kRoleWorker, 0x100u | slot)))
@@ -502,12 +503,15 @@ void wgrad_reset_caches() {
 }
 
 // Whole panels of 64 columns go two in a box (else a box's columns would run into the next
-// row): a copy costs the engine some 80 cycles beside its bytes.
+// row): a copy costs the engine some 80 cycles beside its bytes.  32 x 4096 x 6144, 16384
+// rows: 793 us, with a box a panel 803.
 int wgrad_panels(int cols) { return cols % 64 == 0 ? 2 : 1; }
 
-// With fewer tiles than pairs the rows are split, as long as a part has some 512 rows.
+// With fewer tiles than pairs the rows are split, as long as a part has some 2048 rows: dense
+// 1024 x 1024 over 32768 rows 55 us in four parts, 157 in one; over 4096 rows 20 in two,
+// 25 in one; over 2048 rows 18 to 22 in two or four, 17 in one, since joining is a launch more.
 int wgrad_splits(int E, int N, int K, int rows) {
-    constexpr long long kPairs = 76, kLeast = 512;
+    constexpr long long kPairs = 76, kLeast = 2048;
     const long long t = static_cast<long long>(E) * tiles(N) * tiles(K);
     const long long by_rows = rows / (kLeast * E);
     const long long s = kPairs / t < by_rows ? kPairs / t : by_rows;

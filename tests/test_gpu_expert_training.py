@@ -64,12 +64,12 @@ def _decode(codes, scale):
 
 # ------------------------------------------------- gradient of the weights --
 
-# (rows of the experts, N, K): one row; stages of 64 rows and MMAs of 16 just missed and just
+# (rows of the experts, N, K): one row; stages of 128 rows and MMAs of 16 just missed and just
 # passed; experts without rows at either end and in the middle; one column block; tiles of 256
-# missed and passed; an expert of more than one chunk of 512 rows; parts of 512 rows and more
+# missed and passed; an expert of more than one chunk of 512 rows; rows that are cut into parts
 WGRAD = [([1], 8, 128), ([0], 264, 128), ([0, 5, 0, 0, 17, 0], 72, 256), ([64], 256, 256),
          ([63, 65, 16, 15], 264, 384), ([1, 127, 128, 129], 520, 128), ([512, 513], 248, 640),
-         ([1300, 3, 700], 136, 256), ([2048], 200, 384), ([3000, 90], 64, 128)]
+         ([1300, 3, 700], 136, 256), ([4200], 200, 384), ([8200, 90], 64, 128)]
 
 
 @pytest.mark.parametrize("x", ["bf16", "fp8"])
@@ -101,7 +101,7 @@ def test_wgrad(cuda_lib, counts, N, K, out, x):
     assert hg.hg_get_device_status()[0] == hg.HG_OK
 
 
-@pytest.mark.parametrize("counts,N,K", [([3, 0, 70], 40, 128), ([2100], 256, 128)])
+@pytest.mark.parametrize("counts,N,K", [([3, 0, 70], 40, 128), ([4130], 256, 128)])
 @pytest.mark.parametrize("x", ["bf16", "fp8"])
 def test_wgrad_accumulates(cuda_lib, counts, N, K, x):
     hg = cuda_lib
@@ -159,7 +159,7 @@ def test_wgrad_fp8_every_code_and_scale(cuda_lib):
 
 def test_wgrad_repeats_bit_for_bit(cuda_lib):
     hg = cuda_lib
-    for counts, N, K in (([700, 20, 1100], 264, 520), ([4000], 128, 256)):
+    for counts, N, K in (([700, 20, 1100], 264, 520), ([4150], 128, 256)):
         dy, x = _normal(1, sum(counts), N).bfloat16().cuda(), _normal(2, sum(counts), K).bfloat16()
         off, x = _offsets(counts).cuda(), x.cuda()
         first = hg.hg_grouped_wgrad(dy, x, off)
