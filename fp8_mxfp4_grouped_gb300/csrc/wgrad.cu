@@ -438,11 +438,15 @@ constexpr int kDecodeThreads = 256;
 __global__ void __launch_bounds__(kDecodeThreads)
 wgrad_decode_kernel(const uint8_t* a, const uint8_t* scale, const int32_t* offsets, int E, int rows,
                     int K, uint16_t* x) {
+    __shared__ int s_rows;
+    if (threadIdx.x == 0) s_rows = 0;
+    __syncthreads();
     start_dependent();
-    const int row_pieces = K / 16;
-    // rows behind the last expert's are in no sum
-    const long long pieces =
-        static_cast<long long>(min(max(ptx::load(offsets + E), 0), rows)) * row_pieces;
+    // rows behind the last expert's are in no sum (the last offset need not be the largest)
+    for (int e = threadIdx.x; e <= E; e += kDecodeThreads)
+        atomicMax(&s_rows, min(ptx::load(offsets + e), rows));
+    __syncthreads();
+    const long long pieces = static_cast<long long>(s_rows) * (K / 16);
     const long long step = static_cast<long long>(gridDim.x) * kDecodeThreads;
     for (long long p = static_cast<long long>(blockIdx.x) * kDecodeThreads + threadIdx.x; p < pieces;
          p += step) {
@@ -526,7 +530,8 @@ size_t wgrad_parts_bytes(int E, int N, int K, int rows) {
 bool wgrad_fits(int E, int N, int K, int rows) {
     const long long units = static_cast<long long>(wgrad_splits(E, N, K, rows)) * E * tiles(N);
     const long long longest = 4ll * (N > K ? N : K);     // bytes of a row of any operand, at most
-    return units <= 0x7FFFFFFFll / tiles(K) &&
+    constexpr long long kMost = 0x7FFF0000ll;            // with room to go on past the last
+    return rows <= kMost && units <= kMost / tiles(K) &&
            longest * (rows > N ? rows : N) < 1ll << 40;  // a tensor map's stride
 }
 

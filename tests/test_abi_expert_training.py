@@ -44,7 +44,8 @@ def test_grouped_wgrad(lib, fp8):  # noqa: F811
                     dict(E=1, N=256, K=256, rows=1 << 16, ws=0x6000, bytes=1000),
                     dict(E=1, N=256, K=256, rows=1 << 16, ws=0x6004, bytes=1 << 30)],
              [dict(E=513), dict(N=60), dict(K=260), dict(N=(1 << 30) + 8), dict(K=(1 << 30) + 128),
-              dict(E=512, N=1 << 30, K=1 << 20), dict(N=1 << 30, rows=1 << 20)])
+              dict(E=512, N=1 << 30, K=1 << 20), dict(N=1 << 30, rows=1 << 20),
+              dict(rows=(1 << 31) - 1, ws=0x6000, bytes=1 << 60)])
     if fp8:                                               # the decoded rows need a workspace
         _refuses(call, [dict(ws=0), dict(bytes=2 * 256 * 100 - 1), dict(ws=0x6008)], [dict(K=264)])
 

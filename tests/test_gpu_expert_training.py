@@ -171,12 +171,18 @@ def test_wgrad_bad_offsets(cuda_lib):
     hg = cuda_lib
     rows, N, K = 100, 64, 128
     dy, x = _normal(1, rows, N).bfloat16(), _normal(2, rows, K).bfloat16()
+    a, s = _codes(3, rows, K, 120, 130)
     assert hg.hg_get_device_status()[0] == hg.HG_OK
-    for off in ([0, 40, 20, 100], [0, 40, 101, 100], [-1, 40, 60, 100]):
-        dw = hg.hg_grouped_wgrad(dy.cuda(), x.cuda(), torch.tensor(off, dtype=torch.int32).cuda())
-        want, mag = T.wgrad(_f64(dy), _f64(x), off)
-        _close(_f64(dw), want, 2 * (rows + 1) * FP32 * mag, off)
-        assert hg.hg_get_device_status()[0] == hg.HG_ERR_BAD_OFFSETS
+    for off in ([0, 40, 20, 100], [0, 40, 101, 100], [-1, 40, 60, 100], [0, 90, 20, 19],
+                [0, 2 ** 31 - 1, -2 ** 31, 100]):
+        at = torch.tensor(off, dtype=torch.int32).cuda()
+        for call, xv in ((lambda: hg.hg_grouped_wgrad(dy.cuda(), x.cuda(), at), _f64(x)),
+                         (lambda: hg.hg_grouped_wgrad_fp8(dy.cuda(), a.cuda(), s.cuda(), at),
+                          _decode(a, s))):
+            dw = call()
+            want, mag = T.wgrad(_f64(dy), xv, off)
+            _close(_f64(dw), want, 2 * (rows + 1) * FP32 * mag, off)
+            assert hg.hg_get_device_status()[0] == hg.HG_ERR_BAD_OFFSETS
 
 
 def test_wgrad_no_rows(cuda_lib):
