@@ -32,6 +32,12 @@ bool weight_shape(int32_t E, int32_t N, int32_t K) {
     return static_cast<long long>(E) * N * (K / 32) <= 1ll << 36;
 }
 
+// What the weight gradient takes.
+bool wgrad_shape(int32_t E, int32_t N, int32_t K, int32_t rows, bool fp8) {
+    return E <= gemm_max_experts() && N % 8 == 0 && K % (fp8 ? 128 : 8) == 0 &&
+           N <= kMaxRowElements && K <= kMaxRowElements && wgrad_fits(E, N, K, rows);
+}
+
 // An FP8 operand of the weight gradient as BF16.
 size_t wgrad_decoded_bytes(int32_t K, int32_t rows) {
     return sizeof(uint16_t) * static_cast<size_t>(K) * static_cast<size_t>(rows);
@@ -299,9 +305,7 @@ hg_status grouped_wgrad(const uint16_t* dy, const void* x, const uint8_t* x_scal
                         int32_t accumulate, void* dw, int32_t dw_f32, void* workspace,
                         size_t workspace_bytes, hg_stream_t stream) {
     if (E < 1 || N < 1 || K < 1 || rows < 0) return HG_ERR_INVALID_ARG;
-    if (E > gemm_max_experts() || N % 8 != 0 || K % (fp8 ? 128 : 8) != 0 || N > kMaxRowElements ||
-        K > kMaxRowElements || !wgrad_fits(E, N, K, rows))
-        return HG_ERR_UNSUPPORTED_SHAPE;
+    if (!wgrad_shape(E, N, K, rows, fp8)) return HG_ERR_UNSUPPORTED_SHAPE;
     if (accumulate && !dw_f32) return HG_ERR_INVALID_ARG;
     if (!offsets || !dw || (rows > 0 && (!dy || !x || (fp8 && !x_scale))))
         return HG_ERR_INVALID_ARG;
@@ -891,12 +895,12 @@ hg_status hg_dequantize_weights(const uint8_t* w_fp4, const uint8_t* w_scale, in
 }
 
 size_t hg_grouped_wgrad_workspace_bytes(int32_t E, int32_t N, int32_t K, int32_t rows) {
-    if (E < 1 || N < 1 || K < 1 || rows < 0) return 0;
+    if (E < 1 || N < 1 || K < 1 || rows < 0 || !wgrad_shape(E, N, K, rows, false)) return 0;
     return wgrad_parts_bytes(E, N, K, rows);
 }
 
 size_t hg_grouped_wgrad_fp8_workspace_bytes(int32_t E, int32_t N, int32_t K, int32_t rows) {
-    if (E < 1 || N < 1 || K < 1 || rows < 0) return 0;
+    if (E < 1 || N < 1 || K < 1 || rows < 0 || !wgrad_shape(E, N, K, rows, true)) return 0;
     return wgrad_parts_bytes(E, N, K, rows) + wgrad_decoded_bytes(K, rows);
 }
 

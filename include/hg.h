@@ -572,7 +572,7 @@ hg_status hg_router_topk_bwd(const float* logits, const int32_t* topk_ids,
  *   workspace       device scratch of hg_grouped_wgrad_workspace_bytes(E, N, K, rows)
  *                   bytes, 16-byte aligned (NULL where that is 0): few tiles of dw are
  *                   cut along the rows, and the parts added in order by a second kernel.
- *                   One call at a time may use it.
+ *                   One call at a time may use it.  Shapes that the call refuses need 0.
  * N % 8 == 0, K % 8 == 0, E in [1, 512].  Rows outside [off[0], off[E]) are not read
  * into any sum, whatever they hold.  Sums are FP32; the result does not vary from run to
  * run.  Offsets that are not monotone or exceed rows are detected on the device: the

@@ -61,6 +61,12 @@ def test_grouped_wgrad_workspace(lib):  # noqa: F811
     for E, K, rows in ((32, 6144, 16384), (1, 512, 1 << 16), (3, 128, 0)):
         assert fp8(E, 256, K, rows) == f(E, 256, K, rows) + 2 * K * rows
     assert fp8(1, 256, 256, -1) == 0
+    # shapes that the call refuses, one of which has 2^64 tiles
+    most = (1 << 31) - 1
+    for shape in ((1 << 18, most, most, 100), (most, most, most, most), (1, 260, 256, 100),
+                  (513, 256, 256, 100), (1, 1 << 30, 256, 1 << 20)):
+        assert f(*shape) == 0 and fp8(*shape) == 0, shape
+    assert fp8(1, 256, 264, 100) == 0
 
 
 def test_quantize_weights(lib):  # noqa: F811
