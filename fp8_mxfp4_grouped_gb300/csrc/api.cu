@@ -20,15 +20,18 @@ constexpr int kMaxDevices = 64;
 constexpr int kPlanMaxThreads = 512;
 constexpr int kPlanIdsPerBlock = 2048;
 constexpr int kPlanMaxBlocks = 256;
-constexpr int32_t kMaxRowElements = 1 << 30;     // of a token row: kernels index it with int32
+constexpr int32_t kMaxRowElements = 1 << 30;     // of a row: kernels index it with int32
 
 // eps of the norm: 1 / sqrt(eps) and the squares that it is added to stay in FP32's range
 constexpr float kMinEps = 1e-30f;
 constexpr float kMaxEps = 1e30f;
 
-// Weights of whole 32-K groups, whose tiles a grid can number.
+// Weights of whole 32-K groups, whose tiles a grid and whose columns an int32 can number, those
+// past a last tile's end too.
 bool weight_shape(int32_t E, int32_t N, int32_t K) {
-    if (K % 32 != 0 || static_cast<long long>(E) * N > 0x7FFFFFFFll) return false;
+    if (K % 32 != 0 || N > kMaxRowElements || K > kMaxRowElements ||
+        static_cast<long long>(E) * N > 0x7FFFFFFFll)
+        return false;
     return static_cast<long long>(E) * N * (K / 32) <= 1ll << 36;
 }
 

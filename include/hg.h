@@ -619,8 +619,8 @@ hg_status hg_grouped_wgrad_fp8(const uint16_t* dy_bf16, const uint8_t* a_fp8,
  *   wt_fp4    uint8 [E, K, N/2] out, 16-byte aligned, and wt_scale uint8 [E, K, N/32]
  *             out; both NULL for no transposed copy.
  * K % 32 == 0, with the transposed copy N % 32 == 0 (hg_grouped_w4a8_gemm takes multiples
- * of 128); E*N below 2^31.  One kernel on `stream`, launched with programmatic dependent
- * launch; no host synchronisation.
+ * of 128); N and K up to 2^30, E*N below 2^31.  One kernel on `stream`, launched with
+ * programmatic dependent launch; no host synchronisation.
  */
 hg_status hg_quantize_weights(const void* w, int32_t w_f32, int32_t E, int32_t N, int32_t K,
                               uint8_t* w_fp4, uint8_t* w_scale, uint8_t* wt_fp4,
@@ -631,7 +631,7 @@ hg_status hg_quantize_weights(const void* w, int32_t w_f32, int32_t E, int32_t N
  * 255; Inf where that passes the range of w's type, otherwise exact.
  *
  *   w   FP32 (w_f32 != 0) or BF16 [E, N, K] out, 16-byte aligned; w_fp4 16-byte aligned.
- * K % 32 == 0, E*N below 2^31.  One kernel on `stream`; no host synchronisation.
+ * K % 32 == 0; N and K up to 2^30, E*N below 2^31.  One kernel on `stream`; no host synchronisation.
  */
 hg_status hg_dequantize_weights(const uint8_t* w_fp4, const uint8_t* w_scale, int32_t E, int32_t N,
                                 int32_t K, void* w, int32_t w_f32, hg_stream_t stream);

@@ -75,7 +75,9 @@ def test_quantize_weights(lib):  # noqa: F811
                    dict(w=0x1000, f32=1, E=2, N=64, K=96, q=0x2000, s=0x3000, qt=0x4000, st=0x5000))
     _refuses(call, [dict(E=-1), dict(N=0), dict(K=0), dict(w=0), dict(q=0), dict(s=0), dict(qt=0),
                     dict(st=0), dict(w=0x1008), dict(q=0x2008), dict(qt=0x4008)],
-             [dict(K=40), dict(N=40), dict(E=1 << 20, N=1 << 12), dict(E=1 << 10, N=1 << 20, K=1 << 14)])
+             [dict(K=40), dict(N=40), dict(E=1 << 20, N=1 << 12), dict(E=1 << 10, N=1 << 20, K=1 << 14),
+              # columns and rows that a last tile would number past 2^31
+              dict(E=1, N=32, K=(1 << 31) - 32), dict(E=1, N=(1 << 31) - 32, K=32)])
     assert call(E=0, w=0, q=0, s=0, qt=0, st=0) == OK
 
 
@@ -83,7 +85,8 @@ def test_dequantize_weights(lib):  # noqa: F811
     call = _caller(lib.lib.hg_dequantize_weights, ["q", "s", "E", "N", "K", "w", "f32"],
                    dict(q=0x2000, s=0x3000, E=2, N=5, K=96, w=0x1000, f32=0))
     _refuses(call, [dict(E=-1), dict(N=0), dict(K=0), dict(w=0), dict(q=0), dict(s=0),
-                    dict(w=0x1008), dict(q=0x2008)], [dict(K=40), dict(E=1 << 20, N=1 << 12)])
+                    dict(w=0x1008), dict(q=0x2008)], [dict(K=40), dict(E=1 << 20, N=1 << 12),
+                                                 dict(E=1, N=32, K=(1 << 31) - 32)])
     assert call(E=0, w=0, q=0, s=0) == OK
 
 
