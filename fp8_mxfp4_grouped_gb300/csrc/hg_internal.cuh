@@ -76,11 +76,13 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, cons
 // microsecond) may have run out on copies that are merely not there yet.
 constexpr uint64_t kDrainNs = 1000000000ull;
 
-__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
+// Returns whether the phase completed; false: the whole limit has passed.
+__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (!ptx::mbar_try_wait(bar, parity)) {
-        if (ptx::globaltimer_ns() - t0 > kDrainNs) return;
+        if (ptx::globaltimer_ns() - t0 > kDrainNs) return false;
     }
+    return true;
 }
 
 // ------------------------------------------------- host-side launchers --

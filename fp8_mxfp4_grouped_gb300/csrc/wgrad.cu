@@ -230,13 +230,11 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
                            policy);
             }
         }
-        // No copy may land, and no release of a stage arrive, after the CTA has gone: what the
-        // MMAs have released has landed, and after a wait that gave up one drain's limit is
-        // time enough for what has not been.
-        for (uint32_t gg = g > kStages ? g - kStages : 0; gg < g; ++gg) {
-            wait_drain(bar_empty + 8 * (gg % kStages), (gg / kStages) & 1u);
-            if (*wctx.abort) break;
-        }
+        // No copy may land, and no release of a stage arrive, after the CTA has gone.  What the
+        // MMAs have released has landed.  What they will not release, since a wait gave up, has
+        // landed once a drain has waited for its whole limit: those behind it need no other.
+        for (uint32_t gg = g > kStages ? g - kStages : 0; gg < g; ++gg)
+            if (!wait_drain(bar_empty + 8 * (gg % kStages), (gg / kStages) & 1u)) break;
     } else if (warp == 1) {
         // ------------------------------------------------- MMA issuer ---
         if (leader) {

@@ -43,3 +43,24 @@ def test_nothing_is_asked_for_after_giving_up():
     assert re.search(r"if \([^;]*!rows_came\) return;", ask)
     assert re.search(r"rows_came = __any_sync\([^;]*wait_bounded\(x_bar", code)
     assert re.search(r"warp == 0\) wait_drain\(x_bar, x_asked\)", code)
+
+
+def test_draining_goes_on_until_a_limit_has_passed():
+    # copies behind one that has landed may still be in flight: a loop over several drains ends
+    # early only by a drain that has waited for its whole limit, never by the abort flag
+    drain = _body(_code(os.path.join(CSRC, "hg_internal.cuh")), "wait_drain")
+    assert re.search(r"> kDrainNs\) return false;\s*}\s*return true;", drain)
+    loops = 0
+    for path in glob.glob(os.path.join(CSRC, "*.cu")):
+        code = _code(path)
+        for drained in re.finditer(r"\bwait_drain\(", code):
+            lines = code[:drained.start()].split("\n")
+            if not any(re.search(r"\bfor \(", x) for x in lines[-4:]):
+                continue
+            loops += 1
+            rest = code[drained.start():]
+            after = rest[rest.index(";") + 1:][:80].strip()
+            assert not re.match(r"if \([^;]*abort", after), path
+            if re.match(r"[^;]*break;", rest):
+                assert lines[-1].strip() == "if (!", path
+    assert loops >= 5
