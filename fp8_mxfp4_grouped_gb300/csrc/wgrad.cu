@@ -352,6 +352,10 @@ wgrad_kernel(const __grid_constant__ WgradMaps maps, const Shape shape, const in
                 }
             }
         }
+        // After giving up, the MMAs may still hand over this accumulator and the next one: those
+        // arrivals come before the CTA goes, or not at all.
+        for (uint32_t i = 0; !ok && i < 2; ++i)
+            if (!wait_drain(bar_tfull + 8 * ((tc + i) & 1u), ((tc + i) >> 1) & 1u)) break;
         // every store has completed before the CTA can exit
         if (lane == 0) ptx::bulk_wait_group_all();
         __syncwarp();

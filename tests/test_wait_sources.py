@@ -64,3 +64,12 @@ def test_draining_goes_on_until_a_limit_has_passed():
             if re.match(r"[^;]*break;", rest):
                 assert lines[-1].strip() == "if (!", path
     assert loops >= 5
+
+
+def test_weight_gradient_waits_for_arrivals_after_giving_up():
+    # the issuer's commits arrive on both CTAs: the odd one, which does not see the issuer's own
+    # barrier, stays until the accumulators that it no longer waits for have been handed over
+    code = _code(os.path.join(CSRC, "wgrad.cu"))
+    epilogue = code[code.index("kRoleEpilogue"):code.index("bulk_wait_group_all")]
+    assert re.search(r"!ok && i < 2; \+\+i\)\s*if \(!wait_drain\(bar_tfull \+ 8 \* \(\(tc \+ i\) & 1u\), "
+                     r"\(\(tc \+ i\) >> 1\) & 1u\)\) break;", epilogue)
