@@ -336,6 +336,7 @@ struct Shape {
 constexpr size_t kSmSmem = 228 * 1024, kBlockSmem = 2048;      // of an SM; beside the groups
 struct BwdShape : Shape {
     int group_rows, blocks;
+    int parts;                               // room for parts: the most blocks of up to M rows
     size_t smem;
     BwdShape(int M, int D) : Shape(D) {
         const int teams = teams_per_block();
@@ -349,6 +350,8 @@ struct BwdShape : Shape {
         if (group_rows > fair) group_rows = fair;
         const int groups = (M - 1) / group_rows + 1;
         blocks = groups < most ? groups : most;
+        const int shortest = (M - 1) / teams + 1;        // groups of M rows, a row a team
+        parts = shortest < most ? shortest : most;
         smem = bytes();                      // and room for the teams' sums
     }
 };
@@ -392,8 +395,10 @@ cudaError_t launch_bwd(const BwdShape& s, const RmsnormBwdArgs& a, cudaStream_t 
 
 int rmsnorm_max_elements() { return kMaxTeamWarps * 32 * kMaxPieces * 8; }
 
+// The blocks themselves fall where a group's rows rise: the workspace of a batch has to do for
+// smaller ones too.
 size_t rmsnorm_bwd_workspace(int M, int D) {
-    return static_cast<size_t>(BwdShape(M, D).blocks) * static_cast<size_t>(D) * sizeof(float);
+    return static_cast<size_t>(BwdShape(M, D).parts) * static_cast<size_t>(D) * sizeof(float);
 }
 
 void rmsnorm_reset_caches() {

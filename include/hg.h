@@ -572,7 +572,8 @@ hg_status hg_router_topk_bwd(const float* logits, const int32_t* topk_ids,
  *   workspace       device scratch of hg_grouped_wgrad_workspace_bytes(E, N, K, rows)
  *                   bytes, 16-byte aligned (NULL where that is 0): few tiles of dw are
  *                   cut along the rows, and the parts added in order by a second kernel.
- *                   One call at a time may use it.  Shapes that the call refuses need 0.
+ *                   One call at a time may use it.  What is enough for `rows` rows is
+ *                   enough for fewer.  Shapes that the call refuses need 0.
  * N % 8 == 0, K % 8 == 0, E in [1, 512].  Rows outside [off[0], off[E]) are not read
  * into any sum, whatever they hold.  Sums are FP32; the result does not vary from run to
  * run.  Offsets that are not monotone or exceed rows are detected on the device: the
@@ -680,7 +681,8 @@ hg_status hg_rmsnorm_quantize(const uint16_t* x_bf16, const uint16_t* residual_b
  *   dx_bf16    uint16 [M, D] out, 16-byte aligned.  May be dy_bf16, dsum_bf16 or sum_bf16.
  *   dgain      float32 [D] out, or NULL.
  *   workspace  with dgain: device scratch of hg_rmsnorm_bwd_workspace_bytes(M, D) bytes,
- *              16-byte aligned; else NULL.  One call at a time may use it.
+ *              16-byte aligned; else NULL.  One call at a time may use it.  What is enough
+ *              for M rows is enough for fewer.
  * D % 8 == 0, D <= 16384.  One kernel on `stream`, with dgain two; the result does not vary
  * from run to run.  No host synchronisation.
  */
