@@ -45,8 +45,9 @@ class Experts:
         hg.hg_quantize_weights(down, True, *self.down, *self.down_t)
 
 
-def forward(x, logits, top_k, experts, keep=True, acts=None):
-    """x [M, D] BF16, logits [M, E] float32 -> out [M, D] BF16 and what the backward needs.
+def forward(x, logits, top_k, experts, keep=True, acts=None, weight_grads=False):
+    """x [M, D] BF16, logits [M, E] float32 -> out [M, D] BF16 and what the backward needs, with
+    weight_grads the products' FP8 inputs too (M * top_k * (D + F) bytes).
     acts: x as FP8 codes with scales, where the norm before has made them."""
     E = logits.shape[1]
     ids, weights = hg.hg_router_topk(logits, top_k)
@@ -61,13 +62,15 @@ def forward(x, logits, top_k, experts, keep=True, acts=None):
     out = hg.hg_combine_topk(y, place, weights)
     if not keep:
         return out, None
-    return out, (logits, ids, weights, offsets, place, z8, z8_scale, y, (a, a_scale), (h, h_scale))
+    inputs = ((a, a_scale), (h, h_scale)) if weight_grads else None
+    return out, (logits, ids, weights, offsets, place, z8, z8_scale, y, inputs)
 
 
 def backward(dout, ctx, top_k, experts, weight_grads=False):
     """(dx [M, D] BF16, dlogits [M, E] float32) of dout [M, D] BF16, and with weight_grads the
     gradients of gate_up [E, 2F, D] and down [E, D, F] in float32."""
-    logits, ids, weights, offsets, place, z8, z8_scale, y, acts, hidden = ctx
+    logits, ids, weights, offsets, place, z8, z8_scale, y, inputs = ctx
+    assert inputs or not weight_grads, "the forward pass has not kept the products' inputs"
     rows = torch.arange(y.shape[0], dtype=torch.int32, device=y.device)
     dy, dweights = hg.hg_combine_topk_bwd(dout, y, place, weights)
     q, s = hg.hg_quantize_scatter_acts(dy, 1, rows)
@@ -79,6 +82,7 @@ def backward(dout, ctx, top_k, experts, weight_grads=False):
     dlogits = hg.hg_router_topk_bwd(logits, ids, weights, dweights)
     if not weight_grads:
         return dx, dlogits
+    acts, hidden = inputs
     return dx, dlogits, (hg.hg_grouped_wgrad_fp8(dz, *acts, offsets),
                          hg.hg_grouped_wgrad_fp8(dy, *hidden, offsets))
 
@@ -93,7 +97,7 @@ def train_block(x, residual, gain, router, dout, top_k, experts):
     [M, D] BF16, gain [D] BF16, router [D, E] float32.  Returns y, the gradient of x (and of
     residual, which is the same), of gain, of router, and of the experts' weights."""
     n, a, a_scale, s, rstd = hg.hg_rmsnorm_quantize(x, gain, residual=residual)
-    out, ctx = forward(n, n.float() @ router, top_k, experts, acts=(a, a_scale))
+    out, ctx = forward(n, n.float() @ router, top_k, experts, acts=(a, a_scale), weight_grads=True)
     dn, dlogits, dexperts = backward(dout, ctx, top_k, experts, weight_grads=True)
     drouter = n.float().T @ dlogits
     dn = (dn.float() + dlogits @ router.T).bfloat16()
