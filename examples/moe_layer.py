@@ -23,6 +23,14 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from fp8_mxfp4_grouped_gb300 import hg  # noqa: E402
 
 
+def _quantize(w, *out):
+    """Both orientations of float weights of any strides and type; BF16 as they are, others through
+    float32."""
+    w = w.cuda() if w.device.type == "cpu" else w
+    w = w if w.dtype == torch.bfloat16 else w.float()
+    return hg.hg_quantize_weights(w.contiguous(), True, *out)
+
+
 @dataclass
 class Experts:
     """MXFP4 weights [E, out, in/2] with E8M0 scales [E, out, in/32]: gate rows then up rows,
@@ -35,14 +43,14 @@ class Experts:
 
     @staticmethod
     def from_float(gate_up: torch.Tensor, down: torch.Tensor) -> "Experts":
-        """gate_up [E, 2F, D], down [E, D, F], float32 or BF16."""
-        g, d = (hg.hg_quantize_weights(w, transposed=True) for w in (gate_up, down))
+        """gate_up [E, 2F, D], down [E, D, F]."""
+        g, d = _quantize(gate_up), _quantize(down)
         return Experts(g[:2], d[:2], g[2:], d[2:])
 
     def quantize(self, gate_up: torch.Tensor, down: torch.Tensor):
         """The same weights after an update, over the ones that are there."""
-        hg.hg_quantize_weights(gate_up, True, *self.gate_up, *self.gate_up_t)
-        hg.hg_quantize_weights(down, True, *self.down, *self.down_t)
+        _quantize(gate_up, *self.gate_up, *self.gate_up_t)
+        _quantize(down, *self.down, *self.down_t)
 
 
 def forward(x, logits, top_k, experts, keep=True, acts=None, weight_grads=False):
