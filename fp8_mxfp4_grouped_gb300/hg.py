@@ -658,7 +658,7 @@ def _grouped_wgrad(fn, what, dy, x, x_scale, expert_offsets, dtype, dw, accumula
     K = x.shape[1]
     E = expert_offsets.numel() - 1
     assert dy.dtype == _BF16 and dy.is_contiguous()
-    assert x.shape[0] == rows and x.is_contiguous()
+    assert x.shape == (rows, K) and x.is_contiguous()
     assert expert_offsets.dtype == _I32 and expert_offsets.is_contiguous()
     if dw is not None:
         dtype = dw.dtype
