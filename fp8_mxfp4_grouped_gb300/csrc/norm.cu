@@ -10,17 +10,22 @@
 //   dx    = dsum + u - n mean(u n)              (for x and for the residual alike)
 //   dgain = sum over the rows of dy n
 //
-// All of it is bound by memory.  A row is the work of a team of 1, 2, 4, 8 or 16 warps
-// that holds it in registers, up to four pieces of eight elements a lane, so that
-// everything is read once; a half-warp's sixteen pieces are one 128-element group of
-// the scales.
+// A row is the work of a team of 1, 2, 4, 8 or 16 warps that takes it into registers, up to
+// four pieces of eight elements a lane, so that everything is read once; a half-warp's
+// sixteen pieces are one 128-element group of the scales.
 //
-// Measured: 16384 x 6144 with a residual and all outputs 131 us for 907 MB (6.9 TB/s; a
-// persistent grid that asks for the next row ahead 149), the FP8 output alone 73 us, BF16 alone
-// 68; the gradient of 8199 x 6144 with the residual's 70 us for 403 MB (5.7 TB/s), of 16384 x 6144
-// 127 us (6.3 TB/s), of which some 6 us join the parts of dgain.  With the rows in registers, and
-// loads that waited for the row before, the gradient took 106 us at 8199 x 6144 and 78 at
-// 16384 x 1024 (now 31).
+// Long rows with a residual, and their gradient, are bound by memory: 16384 x 6144 with all
+// outputs 131 us for 907 MB (6.9 TB/s; a persistent grid that asks for the next row ahead 149),
+// the gradient with the residual's 125 us for 805 MB (6.4 TB/s), of 8199 x 6144 69 us (5.9),
+// of which some 6 us join the parts of dgain.  Those 6 us show in short rows: the gradient of
+// 16384 x 1024 takes 30 us for a floor of 20.  With the rows in registers, and loads that waited
+// for the row before, the gradient took 106 us at 8199 x 6144 and 78 at 16384 x 1024.
+//
+// One output without a residual is not: BF16 67 us for 403 MB (6.0 TB/s), FP8, a quarter less,
+// 72 us (4.2 TB/s).  A block has one row and loads, sums, quantises and stores it one after the
+// other, with six rows on an SM; three blocks of up to 512 threads leave 40 registers a thread, of
+// which rows of two to four pieces spill 24, 40 and 72 bytes (with a residual: 64 registers, 12
+// bytes at four pieces).
 #include <atomic>
 
 #include "hg_internal.cuh"
@@ -139,8 +144,9 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* gain
         for (int i = 0; i < 8; ++i) squares = fmaf(f[i], f[i], squares);
     }
     squares = team_sum(team, squares, part);
-    const float r = squares < kWide ? 1.0f / sqrtf(squares / static_cast<float>(D) + eps)
-                                    : wide_rstd(team, (kResidual ? sum : x) + row * D, D, eps, wide_part);
+    const float r = squares < kWide
+                        ? 1.0f / sqrtf(squares / static_cast<float>(D) + eps)
+                        : wide_rstd(team, (kResidual ? sum : x) + row * D, D, eps, wide_part);
     if (rstd && team.rank == 0) rstd[row] = r;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
@@ -204,7 +210,8 @@ rmsnorm_bwd_kernel(const uint16_t* dy, const uint16_t* dsum, const uint16_t* sum
     const WaitCtx ctx{status, &s_abort, timeout_ns};
     auto load = [&](int group, int half) {
         const long long row = static_cast<long long>(group) * group_rows;
-        const uint32_t bytes = static_cast<uint32_t>(min(static_cast<long long>(group_rows), M - row)) * D * 2;
+        const int rows = static_cast<int>(min(static_cast<long long>(group_rows), M - row));
+        const uint32_t bytes = static_cast<uint32_t>(rows) * D * 2;
         const uint16_t* from[3] = {dy, sum, dsum};
         ptx::mbar_arrive_expect_tx(bars + 8 * half, bytes * arrays);
         for (int i = 0; i < arrays; ++i)
@@ -360,9 +367,9 @@ template <int kPieces>
 cudaError_t launch_fwd(const Shape& s, const RmsnormArgs& a, cudaStream_t stream) {
     const int teams = s.teams_per_block();
     const int grid = static_cast<int>((static_cast<long long>(a.M) + teams - 1) / teams);
-    return launch_dependent(a.residual ? rmsnorm_kernel<kPieces, true> : rmsnorm_kernel<kPieces, false>, grid, s.threads, 0, stream, a.x, a.residual,
-                            a.gain, a.M, a.D, a.eps, s.team_warps, a.sum, a.y, a.a_fp8, a.a_scale,
-                            a.rstd);
+    const auto kernel = a.residual ? rmsnorm_kernel<kPieces, true> : rmsnorm_kernel<kPieces, false>;
+    return launch_dependent(kernel, grid, s.threads, 0, stream, a.x, a.residual, a.gain, a.M, a.D,
+                            a.eps, s.team_warps, a.sum, a.y, a.a_fp8, a.a_scale, a.rstd);
 }
 
 // Devices (a bit each) on which a gradient's kernel may use its shared memory, by pieces and

@@ -64,8 +64,8 @@ struct Choices {
     }
 };
 
-// 8-bit rows with their scales, as they are (16384 x 6144, top-8, 137 us for 914 MB): the codes go as 16-bit words, eight a piece,
-// and the lanes take the scales a byte each.
+// 8-bit rows with their scales, as they are (16384 x 6144, top-8, 136 us for 914 MB): the codes
+// go as 16-bit words, eight a piece, and the lanes take the scales a byte each.
 template <int kPieces>
 __global__ void __launch_bounds__(kThreads)
 dispatch_acts_kernel(const uint8_t* a, const uint8_t* scale, const int32_t* place, int M,
@@ -81,7 +81,8 @@ dispatch_acts_kernel(const uint8_t* a, const uint8_t* scale, const int32_t* plac
         for (int c = 0; c < kPieces; ++c) {
             const int n = team.at(pass, kPieces, c);
             v[c] = make_uint4(0, 0, 0, 0);
-            if (n < words) v[c] = ptx::load(reinterpret_cast<const uint4*>(a + team.token * K + 2 * n));
+            if (n < words)
+                v[c] = ptx::load(reinterpret_cast<const uint4*>(a + team.token * K + 2 * n));
         }
         // a scale for 64 words: at most one a lane and pass
         const int g0 = pass * team.pass_elements(kPieces) / 64;

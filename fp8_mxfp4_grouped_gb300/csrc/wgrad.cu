@@ -27,16 +27,22 @@
 // its registers, where sums round.
 //
 // What bounds it: for long sums the tensor cores (4 x 4096 x 4096 over 32768 rows, BF16, 597 us,
-// 1840 TFLOP/s); for experts of some 512 rows the SMs' ports to the L2, where the copies' requests
-// and the stores of dw add up (32 x 4096 x 6144 in FP32 over 16384 rows 793 us, 834 to 848 from
-// FP8; the port is busy for 74 % of the time, 49 % with dw, the tensor cores for 48 %, HBM for
-// 57 %).  Copies alone take 396 us there, the stores 494, both 709; the MMAs at the rate of
-// long sums would take 454.  Tried and not kept: stores by the threads instead of TMA (955 us, from
+// 1840 TFLOP/s).  For experts of some 512 rows nothing that was measured is full: 8 x 4096 x 6144
+// in FP32 of 512 rows each keep the SMs' ports to the L2 busy for 74 % of the time (49 % with the
+// stores of dw), HBM for 57 %, the L2 for 52 % and the tensor cores for 48 %.  32 x 4096 x 6144
+// over 16384 rows, BF16 x, take 794 us with skewed routing (512 rows each 715 to 731), 836 from FP8
+// (764 to 769).  Copies alone take 396 us there, the stores 494, both 709, which is neither the
+// larger nor the sum; the MMAs at the rate of long sums would take 454.  How the rows fall on the
+// pairs counts too: 10 % with these many tiles, and with few the fullest expert's tiles decide
+// (8 x 1024 x 512 over 32768 rows 57 us against 30 with equal experts, a floor of 18), since a
+// tile is one pair's and wgrad_splits knows the average expert only.
+//
+// Tried and not kept, at the 794 us: stores by the threads instead of TMA (955 us, from
 // registers 890), 16 KB store boxes (809), two store buffers a warp for a stage less (867), dy
 // kept in shared memory for several tiles with x in the two remaining slots (1040: too few
 // bytes of x in flight), the tiles walked along k (795), pairs started apart in time (no
-// change), 256 x 512 a pair for experts of up to 1024 rows and two passes for longer ones (skewed
-// routing 866 against 793; 32 x 4096 x 2048 of 200 rows each 117 against 131).
+// change), 256 x 512 a pair for experts of up to 1024 rows and two passes for longer ones (869;
+// 512 rows each 700 against 714; 32 x 4096 x 2048 to BF16 of 200 rows each 123 against 130).
 #include <atomic>
 
 #include "hg_internal.cuh"
@@ -515,7 +521,8 @@ void wgrad_reset_caches() {
 // rows: 793 us, with a box a panel 803.
 int wgrad_panels(int cols) { return cols % 64 == 0 ? 2 : 1; }
 
-// With fewer tiles than pairs the rows are split, as long as a part has some 2048 rows: dense
+// With fewer tiles than pairs (76, those of a whole GPU) the rows are split, as long as a part has
+// some 2048 rows: dense
 // 1024 x 1024 over 32768 rows 55 us in four parts, 157 in one; over 4096 rows 20 in two,
 // 25 in one; over 2048 rows 18 to 22 in two or four, 17 in one, since joining is a launch more.
 int wgrad_splits(int E, int N, int K, int rows) {

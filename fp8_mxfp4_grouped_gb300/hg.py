@@ -689,7 +689,8 @@ def hg_grouped_wgrad_fp8(dy: torch.Tensor, a_fp8: torch.Tensor, a_scale: torch.T
                          expert_offsets: torch.Tensor, dtype=torch.float32, dw=None,
                          accumulate: bool = False, workspace=None, stream=None) -> torch.Tensor:
     """hg_grouped_wgrad with x as the forward product had it: E4M3 codes [rows, K] and E8M0
-    scales [rows, K/128]."""
+    scales [rows, K/128].  It takes 2 * K * rows bytes of workspace, allocated at every call that
+    gives none."""
     rows, K = a_fp8.shape
     assert a_fp8.dtype == _U8
     assert a_scale.dtype == _U8 and a_scale.shape == (rows, K // 128) and a_scale.is_contiguous()
